@@ -1,6 +1,7 @@
 /*
- * libbitlinear — ternary (BitNet b1.58) and sign-only (OneBit) linear layers for
- * AMD Instinct MI355X (gfx950), as a C ABI over hand-written HIP kernels.
+ * libbitlinear — ternary (BitNet b1.58) and sign-only (OneBit) linear layers, and 8-bit
+ * floating point ones with the routing to experts built on them, for AMD Instinct MI355X
+ * (gfx950), as a C ABI over hand-written HIP kernels.
  *
  * Sources (cited by page title and section):
  *  [b158]   "微软、国科大开启1Bit时代：大模型转三进制，速度快4倍能耗降至1/41" — BitNet b1.58
@@ -346,6 +347,86 @@ int bl_residual_binarize(const float* W, int64_t N, int64_t K, void* planes_o, f
 int bl_residual_linear(const uint16_t* x, const void* planes_o, const float* alpha_o,
                        const void* planes_r, const float* alpha_r, int64_t M, int64_t N, int64_t K,
                        float* y, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- 8-bit floating point linear layers and experts ----------------------------------------- */
+
+/* Conventions of this section, beside those at the top:
+ *  - Codes are e4m3 bytes (OCP: 4 exponent bits, 3 mantissa bits, largest 448, no infinity,
+ *    0x7F and 0xFF NaN). A weight [N, K] is row-major codes with one fp32 scale for each
+ *    block of 128 x 128, scales [ceil(N/128), ceil(K/128)] row-major; the last block of
+ *    either axis may be smaller. Activations [M, K] have one scale per row and 128 inputs,
+ *    scales block by block: [ceil(K/128), M].
+ *  - K % 16 == 0, every other size may be odd. 1 <= M <= 2^20, N and K <= 2^24.
+ *  - x and y hold `dtype` values (enum bl_dtype) and their rows are ldx / ldy elements apart
+ *    (at least the row's length). x, codes and ws are 16-byte aligned, and so is every row of
+ *    x; scales are 4-byte aligned, y and its rows by the size of its type.
+ *  - The workspace needs no fill and holds nothing between calls. */
+enum bl_dtype { BL_F16 = 0, BL_BF16 = 1, BL_F32 = 2 };
+enum bl_score { BL_SCORE_SOFTMAX = 0, BL_SCORE_SIGMOID = 1 };
+
+/* Block quantiser of a weight W fp32 [N, K] (contiguous):
+ *   a = max(max |W| over the block, 2^-100);  code = e4m3(fl32(W * fl32(448 fl32(1 / a))));
+ *   scale = fl32(a / 448),
+ * round to nearest even. A block that holds NaN gets scale NaN and NaN codes; one that holds
+ * infinities (and no NaN) gets scale inf, NaN codes for them and zeros for the rest. */
+int bl_fp8_quant_weight(const float* W, int64_t N, int64_t K, uint8_t* codes, float* scales,
+                        void* stream);
+
+/* Block quantiser of activations: as bl_fp8_quant_weight with a block of one row and 128
+ * inputs. gated != 0: a row of x is [gate | up], 2 K values, and what is quantised is
+ * silu(gate) * up = gate / (1 + exp(-gate)) * up, computed in fp32. Outputs: codes q [M, K],
+ * scales fp32 [ceil(K/128), M]. */
+int bl_quant_act_fp8(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, int gated,
+                     uint8_t* q, float* scales, void* stream);
+
+/* Block-scaled product of codes:
+ *   y[m, n] = sum_b scales_x[b, m] scales_w[n / 128, b] sum_{k in block b} q[m, k] w[n, k],
+ * rounded once to ydtype. Both sums are fp32 sums in a fixed order for a given shape. */
+int bl_fp8_linear(const uint8_t* q, const float* scales_x, int64_t M, int64_t K, const uint8_t* w,
+                  const float* scales_w, int64_t N, void* y, int ydtype, int64_t ldy,
+                  void* stream);
+
+/* The whole linear layer from unquantised activations: bl_quant_act_fp8 (not gated), then
+ * bl_fp8_linear; same result. Uses ws (bl_fp8_workspace_bytes(M, K)). */
+size_t bl_fp8_workspace_bytes(int64_t M, int64_t K);
+int bl_fp8_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* w,
+                   const float* scales_w, int64_t N, void* y, int ydtype, int64_t ldy, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/* Routing of M rows of logits [M, E] (dtype, rows ld elements apart) to k experts each.
+ *  - Scores p: softmax over the row's experts, or sigmoid(logit) = 1 / (1 + exp(-logit)). An
+ *    expert whose logit is -inf or NaN is left out (of the softmax too) and never chosen; a
+ *    logit of +inf counts as the largest finite fp32 value.
+ *  - Choice values: p + bias[e] with a bias (fp32 [E]), else p (softmax: compared by the
+ *    logits, whose order it keeps). An expert whose choice value is -inf or NaN is not chosen.
+ *  - groups > 1 (at most 64, a divisor of E): group i holds experts i E/groups ... A group
+ *    ranks by its best choice value (softmax) or the sum of its best two (sigmoid; of its only
+ *    one where it has no second); only the `kept` best groups stay, ties to the lowest group.
+ *  - The k largest choice values, in falling order, ties to the lowest expert; a slot that no
+ *    expert is left for holds index -1 and weight 0.
+ *  - weight = p (without the bias), divided by its row's sum if renorm != 0 (0 where the sum
+ *    is 0), times factor.
+ * 1 <= E <= 2048, 1 <= k <= min(64, E / groups * kept), 1 <= kept <= groups. Outputs: weight
+ * fp32 [M, k], index int32 [M, k]. */
+int bl_route_experts(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
+                     const float* bias, int score, int groups, int kept, int64_t k, int renorm,
+                     float factor, float* weight, int32_t* index, void* stream);
+
+/* The experts' gated products ("mixture of experts" feed-forward):
+ *   y[m] = sum_j weight[m, j] * D_e(silu(G_e(x[m])) * U_e(x[m])),   e = index[m, j],
+ * each of G, U, D a block-scaled linear layer with its input quantised as by
+ * bl_quant_act_fp8. x [M, H]; index int32 [M, k], weight fp32 [M, k]; a slot whose index is
+ * outside [0, E) adds nothing (a row without any gives zeros). wgu codes [E, 2, I, H] (gate,
+ * up) with scales [E, 2, ceil(I/128), ceil(H/128)]; wd codes [E, H, I] with scales
+ * [E, ceil(H/128), ceil(I/128)]. H and I are multiples of 16; 1 <= E <= 4096,
+ * 1 <= k <= 64, M k <= 2^20. A token's slots are added in fp32 in their order. Uses ws
+ * (bl_fp8_experts_workspace_bytes). */
+size_t bl_fp8_experts_workspace_bytes(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I);
+int bl_fp8_experts(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
+                   const int32_t* index, const float* weight, int64_t k, const uint8_t* wgu,
+                   const float* scales_gu, const uint8_t* wd, const float* scales_d, int64_t E,
+                   int64_t I, void* y, int ydtype, int64_t ldy, void* ws, size_t ws_bytes,
+                   void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,5 +1,6 @@
-"""Python binding of libbitlinear: BitNet b1.58 ternary, OneBit sign-only and
-residual-binarised linear layers on MI355X (gfx950).
+"""Python binding of libbitlinear: BitNet b1.58 ternary, OneBit sign-only,
+residual-binarised and 8-bit floating point linear layers, expert routing and experts'
+products on MI355X (gfx950).
 
 Every function here only marshals arguments: it checks tensor dtypes, devices and
 contiguity, allocates outputs with torch (device memory is PyTorch's job) and calls the
@@ -35,6 +36,7 @@ class BitLinearError(RuntimeError):
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_INT = ctypes.c_int
 _SIGS = {
     "bl_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "bl_last_error": (ctypes.c_char_p, []),
@@ -67,6 +69,17 @@ _SIGS = {
     "bl_bitlinear_forward_stack": (ctypes.c_int, [_P, _I64, _I64, _P, _SZ, _P]),
     "bl_stack_status": (ctypes.c_int, [_P, _P]),
     "bl_bitlinear_forward_gemv_noalloc": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I64, _I64, _P, _P]),
+    "bl_fp8_quant_weight": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
+    "bl_quant_act_fp8": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P]),
+    "bl_fp8_linear": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _I64, _P]),
+    "bl_fp8_workspace_bytes": (_SZ, [_I64, _I64]),
+    "bl_fp8_forward": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _P, _I64, _P, _INT, _I64, _P,
+                                      _SZ, _P]),
+    "bl_route_experts": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _INT, _INT, _INT, _I64,
+                                        _INT, ctypes.c_float, _P, _P, _P]),
+    "bl_fp8_experts_workspace_bytes": (_SZ, [_I64] * 5),
+    "bl_fp8_experts": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _I64,
+                                      _I64, _P, _INT, _I64, _P, _SZ, _P]),
 }
 
 
@@ -512,6 +525,173 @@ def bl_stack_status(plan) -> int:
     if st < 0:
         raise BitLinearError(6, "bl_stack_status", _lib)
     return st
+
+
+# ------------------------------------------------------------------------------------------
+# 8-bit floating point linear layers and experts
+# ------------------------------------------------------------------------------------------
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_F8 = torch.float8_e4m3fn
+
+
+def _dtype(dtype, name):
+    if dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float16, bfloat16 or float32, got {dtype}")
+    return _DTYPES[dtype]
+
+
+def _row_stride(t, name):
+    """Elements between the rows of a 2-d tensor with contiguous rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.shape[1] if t.shape[0] == 1 else t.stride(0)
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _out(out, shape, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _shape(out, shape, "out")
+    return out
+
+
+def _scratch(nbytes, device, what):
+    """Scratch of one call. It comes from torch's allocator on the current stream, so calls on
+    different streams never share it."""
+    if nbytes == 0:
+        raise ValueError(f"invalid shape {what}")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def bl_fp8_quant_weight(W):
+    """fp32 W [N, K] -> (e4m3 codes [N, K], scales fp32 [ceil(N/128), ceil(K/128)])."""
+    _need(W, torch.float32, "W")
+    d = _dev(W)
+    N, K = W.shape
+    codes = torch.empty((N, K), dtype=_F8, device=d)
+    scales = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=d)
+    _check(_lib.bl_fp8_quant_weight(_ptr(W), N, K, _ptr(codes), _ptr(scales), _stream(d)),
+           "bl_fp8_quant_weight")
+    return codes, scales
+
+
+def bl_quant_act_fp8(x, gated: bool = False):
+    """x [M, K] (gated: [M, 2 K] = [gate | up], quantised as silu(gate) * up) in fp16, bf16 or
+    fp32 -> (e4m3 codes [M, K], scales fp32 [ceil(K/128), M]). Rows may be strided."""
+    dt, ld = _dtype(x.dtype, "x"), _row_stride(x, "x")
+    d = _dev(x)
+    M, K = x.shape
+    if gated:
+        if K % 2:
+            raise ValueError(f"a gated row holds 2 K values, got {K}")
+        K //= 2
+    q = torch.empty((M, K), dtype=_F8, device=d)
+    scales = torch.empty((_blocks(K), M), dtype=torch.float32, device=d)
+    _check(_lib.bl_quant_act_fp8(_ptr(x), dt, M, K, ld, int(gated), _ptr(q), _ptr(scales), _stream(d)),
+           "bl_quant_act_fp8")
+    return q, scales
+
+
+def _check_weight(w, scales, lead, name):
+    _need(w, _F8, name)
+    _need(scales, torch.float32, f"the scales of {name}")
+    if w.dim() != 2 + lead:
+        raise ValueError(f"{name} must have {2 + lead} dimensions, got {w.dim()}")
+    _shape(scales, (*w.shape[:lead], _blocks(w.shape[-2]), _blocks(w.shape[-1])), f"the scales of {name}")
+
+
+def bl_fp8_linear(q, scales_x, w, scales_w, out_dtype=torch.float32, out=None):
+    """e4m3 q [M, K] and scales from bl_quant_act_fp8, w [N, K] and scales as from
+    bl_fp8_quant_weight -> y [M, N] in out_dtype. out: y, its rows may be strided."""
+    _need(q, _F8, "q")
+    _need(scales_x, torch.float32, "scales_x")
+    _check_weight(w, scales_w, 0, "w")
+    d = _dev(q, scales_x, w, scales_w, out)
+    M, K = q.shape
+    N = w.shape[0]
+    _shape(w, (N, K), "w")
+    _shape(scales_x, (_blocks(K), M), "scales_x")
+    y = _out(out, (M, N), out_dtype, d)
+    _check(_lib.bl_fp8_linear(_ptr(q), _ptr(scales_x), M, K, _ptr(w), _ptr(scales_w), N, _ptr(y),
+                              _dtype(y.dtype, "out"), _row_stride(y, "out"), _stream(d)),
+           "bl_fp8_linear")
+    return y
+
+
+def bl_fp8_forward(x, w, scales_w, out_dtype=torch.float32, out=None):
+    """x [M, K] in fp16, bf16 or fp32 (rows may be strided) -> y [M, N] in out_dtype: quantise,
+    then the block-scaled product."""
+    dt, ld = _dtype(x.dtype, "x"), _row_stride(x, "x")
+    _check_weight(w, scales_w, 0, "w")
+    d = _dev(x, w, scales_w, out)
+    M, K = x.shape
+    N = w.shape[0]
+    _shape(w, (N, K), "w")
+    y = _out(out, (M, N), out_dtype, d)
+    ws = _scratch(_lib.bl_fp8_workspace_bytes(M, K), d, f"M={M} K={K}")
+    _check(_lib.bl_fp8_forward(_ptr(x), dt, M, K, ld, _ptr(w), _ptr(scales_w), N, _ptr(y),
+                               _dtype(y.dtype, "out"), _row_stride(y, "out"), _ptr(ws), ws.numel(),
+                               _stream(d)), "bl_fp8_forward")
+    return y
+
+
+def bl_route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int = 1,
+                     kept_groups: int = 1, renorm: bool = True, factor: float = 1.0):
+    """logits [M, E] in fp16, bf16 or fp32 (rows may be strided) -> (weight fp32 [M, k], index
+    int32 [M, k]); see the header for scores, bias, groups and what is masked out."""
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    dt, ld = _dtype(logits.dtype, "logits"), _row_stride(logits, "logits")
+    d = _dev(logits, bias)
+    M, E = logits.shape
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        _shape(bias, (E,), "bias")
+    weight = torch.empty((M, max(k, 0)), dtype=torch.float32, device=d)
+    index = torch.empty((M, max(k, 0)), dtype=torch.int32, device=d)
+    _check(_lib.bl_route_experts(_ptr(logits), dt, M, E, ld, _ptr(bias), _SCORES[score], groups,
+                                 kept_groups, k, int(renorm), factor, _ptr(weight), _ptr(index),
+                                 _stream(d)), "bl_route_experts")
+    return weight, index
+
+
+def bl_fp8_experts(x, index, weight, wgu, scales_gu, wd, scales_d, out_dtype=None, out=None):
+    """x [M, H], index int32 [M, k] and weight fp32 [M, k] as from bl_route_experts, gate and up
+    codes wgu [E, 2, I, H], down codes wd [E, H, I], each with its scales per block of 128 x 128
+    -> y [M, H] in out_dtype (x's type by default): the weighted sum of each token's experts."""
+    dt, ld = _dtype(x.dtype, "x"), _row_stride(x, "x")
+    _need(index, torch.int32, "index")
+    _need(weight, torch.float32, "weight")
+    _check_weight(wgu, scales_gu, 2, "wgu")
+    _check_weight(wd, scales_d, 1, "wd")
+    d = _dev(x, index, weight, wgu, scales_gu, wd, scales_d, out)
+    M, H = x.shape
+    E, two, inner, _ = wgu.shape
+    _shape(wgu, (E, 2, inner, H), "wgu")
+    _shape(wd, (E, H, inner), "wd")
+    if index.dim() != 2 or index.shape[0] != M:
+        raise ValueError(f"index must be [M, k] with M = {M}")
+    k = index.shape[1]
+    _shape(weight, (M, k), "weight")
+    y = _out(out, (M, H), out_dtype or x.dtype, d)
+    ws = _scratch(_lib.bl_fp8_experts_workspace_bytes(M, H, k, E, inner), d,
+                  f"M={M} H={H} k={k} E={E} I={inner}")
+    _check(_lib.bl_fp8_experts(_ptr(x), dt, M, H, ld, _ptr(index), _ptr(weight), k, _ptr(wgu),
+                               _ptr(scales_gu), _ptr(wd), _ptr(scales_d), E, inner, _ptr(y),
+                               _dtype(y.dtype, "out"), _row_stride(y, "out"), _ptr(ws), ws.numel(),
+                               _stream(d)), "bl_fp8_experts")
+    return y
 
 
 __all__ = [n for n in list(globals()) if n.startswith("bl_")] + [

@@ -41,7 +41,8 @@ EXTRA = {"mf_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 SOURCES = ["api.hip", "pack.hip", "quant.hip", "gemv.hip", "gemm.hip", "onebit.hip", "svid.hip",
            "stack.hip",
-           "residual.hip", "tern_mfma.hip", "mf_decode.hip"]
+           "residual.hip", "tern_mfma.hip", "mf_decode.hip", "fp8_quant.hip", "fp8_linear.hip",
+           "fp8_experts.hip", "route.hip"]
 
 
 def _run(cmd):

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "bl_internal.h"
+#include "fp8_internal.h"
 
 namespace bl {
 namespace {
@@ -40,6 +41,62 @@ constexpr int64_t kMaxStack = 4096;               // linears in one stack plan
 
 inline bool dims_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 1 && N >= 1 && K >= 1 && M <= kMaxDim && N <= kMaxDim && K <= kMaxDim;
+}
+
+// ---- 8-bit floating point section ----
+constexpr int64_t kMaxFp8Rows = int64_t(1) << 20;   // rows (and expert slots) of one call
+constexpr int64_t kMaxFp8Dim = int64_t(1) << 24;
+
+inline bool fp8_dims_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && N >= 1 && K >= 1 && M <= kMaxFp8Rows && N <= kMaxFp8Dim && K <= kMaxFp8Dim &&
+         K % 16 == 0;
+}
+inline bool dtype_ok(int dtype) { return dtype == BL_F16 || dtype == BL_BF16 || dtype == BL_F32; }
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// Bytes from the first to past the last value of M rows of n values, ld apart.
+inline size_t rows_bytes(int64_t M, int64_t n, int64_t ld, int dtype) {
+  return (static_cast<size_t>(M - 1) * ld + n) * dtype_bytes(dtype);
+}
+struct Span {
+  const void* p;
+  size_t n;
+};
+// Whether one of the outputs overlaps an input or another output.
+template <int NO, int NI>
+bool any_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (const Span& in : ins)
+      if (overlap(outs[i].p, outs[i].n, in.p, in.n)) return true;
+    for (int j = i + 1; j < NO; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
+  }
+  return false;
+}
+// Type, stride and alignment of rows of n values that are read 16 bytes at a time.
+int check_rows_in(const void* x, int dtype, int64_t n, int64_t ld) {
+  if (!dtype_ok(dtype)) return BL_ERR_ARG;
+  if (ld < n || ld > kMaxDim) return BL_ERR_SHAPE;
+  if (!aligned16(x) || (ld * dtype_bytes(dtype)) % 16) return BL_ERR_ALIGN;
+  return BL_OK;
+}
+// Type, stride and alignment of rows of n values that are read or written value by value.
+int check_rows_out(const void* y, int dtype, int64_t n, int64_t ld) {
+  if (!dtype_ok(dtype)) return BL_ERR_ARG;
+  if (ld < n || ld > kMaxDim) return BL_ERR_SHAPE;
+  return aligned_to(y, dtype_bytes(dtype)) ? BL_OK : BL_ERR_ALIGN;
+}
+struct Fp8Ws {
+  size_t sx_off, total;       // codes [M, K] at 0, scales [KB, M]
+};
+Fp8Ws fp8_ws(int64_t M, int64_t K) {
+  Fp8Ws w{};
+  w.sx_off = round256(static_cast<size_t>(M) * K);
+  w.total = w.sx_off + round256(static_cast<size_t>(M) * fp8_blocks(K) * 4);
+  return w;
+}
+bool experts_dims_ok(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
+  return fp8_dims_ok(M, I, H) && I % 16 == 0 && I <= kMaxFp8Dim / 2 && k >= 1 && k <= 64 &&
+         E >= 1 && E <= 4096 && M * k <= kMaxFp8Rows;
 }
 
 }  // namespace
@@ -634,6 +691,133 @@ int bl_residual_linear(const uint16_t* x, const void* planes_o, const float* alp
                                              reinterpret_cast<uint32_t*>(w + L.cnt_off),
                                              static_cast<hipStream_t>(stream)),
                       "bl_residual_linear");
+}
+
+
+int bl_fp8_quant_weight(const float* W, int64_t N, int64_t K, uint8_t* codes, float* scales,
+                        void* stream) {
+  if (!W || !codes || !scales) return BL_ERR_NULL;
+  if (!fp8_dims_ok(1, N, K) || fp8_blocks(N) * fp8_blocks(K) >= (int64_t(1) << 31)) return BL_ERR_SHAPE;
+  if (!aligned16(W) || !aligned16(codes) || !aligned_to(scales, 4)) return BL_ERR_ALIGN;
+  const size_t n = static_cast<size_t>(N) * K;
+  const Span outs[] = {{codes, n}, {scales, static_cast<size_t>(fp8_blocks(N)) * fp8_blocks(K) * 4}};
+  const Span ins[] = {{W, n * 4}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  return check_launch(launch_fp8_quant_weight(W, N, K, codes, scales, static_cast<hipStream_t>(stream)),
+                      "bl_fp8_quant_weight");
+}
+
+int bl_quant_act_fp8(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, int gated,
+                     uint8_t* q, float* scales, void* stream) {
+  if (!x || !q || !scales) return BL_ERR_NULL;
+  if (!fp8_dims_ok(M, 1, K) || M * fp8_blocks(K) >= (int64_t(1) << 34)) return BL_ERR_SHAPE;
+  const int64_t width = gated ? 2 * K : K;
+  if (int st = check_rows_in(x, dtype, width, ldx)) return st;
+  if (!aligned16(q) || !aligned_to(scales, 4)) return BL_ERR_ALIGN;
+  const Span outs[] = {{q, static_cast<size_t>(M) * K}, {scales, static_cast<size_t>(M) * fp8_blocks(K) * 4}};
+  const Span ins[] = {{x, rows_bytes(M, width, ldx, dtype)}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  return check_launch(launch_fp8_quant_act(x, dtype, M, K, ldx, gated != 0, nullptr, q, scales,
+                                           static_cast<hipStream_t>(stream)),
+                      "bl_quant_act_fp8");
+}
+
+int bl_fp8_linear(const uint8_t* q, const float* scales_x, int64_t M, int64_t K, const uint8_t* w,
+                  const float* scales_w, int64_t N, void* y, int ydtype, int64_t ldy,
+                  void* stream) {
+  if (!q || !scales_x || !w || !scales_w || !y) return BL_ERR_NULL;
+  if (!fp8_dims_ok(M, N, K)) return BL_ERR_SHAPE;
+  if (int st = check_rows_out(y, ydtype, N, ldy)) return st;
+  if (!aligned16(q) || !aligned16(w) || !aligned_to(scales_x, 4) || !aligned_to(scales_w, 4))
+    return BL_ERR_ALIGN;
+  const Span outs[] = {{y, rows_bytes(M, N, ldy, ydtype)}};
+  const Span ins[] = {{q, static_cast<size_t>(M) * K},
+                      {scales_x, static_cast<size_t>(M) * fp8_blocks(K) * 4},
+                      {w, static_cast<size_t>(N) * K},
+                      {scales_w, static_cast<size_t>(fp8_blocks(N)) * fp8_blocks(K) * 4}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  return check_launch(launch_fp8_linear(Fp8LinearArgs{q, scales_x, w, scales_w, M, N, K, y, ldy, ydtype},
+                                        static_cast<hipStream_t>(stream)),
+                      "bl_fp8_linear");
+}
+
+size_t bl_fp8_workspace_bytes(int64_t M, int64_t K) {
+  return fp8_dims_ok(M, 1, K) ? fp8_ws(M, K).total : 0;
+}
+
+int bl_fp8_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* w,
+                   const float* scales_w, int64_t N, void* y, int ydtype, int64_t ldy, void* ws,
+                   size_t ws_bytes, void* stream) {
+  if (!x || !w || !scales_w || !y) return BL_ERR_NULL;
+  if (!fp8_dims_ok(M, N, K) || M * fp8_blocks(K) >= (int64_t(1) << 34)) return BL_ERR_SHAPE;
+  if (int st = check_rows_in(x, dtype, K, ldx)) return st;
+  if (int st = check_rows_out(y, ydtype, N, ldy)) return st;
+  const Fp8Ws L = fp8_ws(M, K);
+  if (!ws || ws_bytes < L.total) return BL_ERR_WORKSPACE;
+  if (!aligned16(w) || !aligned_to(scales_w, 4) || !aligned16(ws)) return BL_ERR_ALIGN;
+  const Span outs[] = {{y, rows_bytes(M, N, ldy, ydtype)}, {ws, L.total}};
+  const Span ins[] = {{x, rows_bytes(M, K, ldx, dtype)},
+                      {w, static_cast<size_t>(N) * K},
+                      {scales_w, static_cast<size_t>(fp8_blocks(N)) * fp8_blocks(K) * 4}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  auto* q = static_cast<uint8_t*>(ws);
+  auto* sx = reinterpret_cast<float*>(static_cast<char*>(ws) + L.sx_off);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = launch_fp8_quant_act(x, dtype, M, K, ldx, 0, nullptr, q, sx, s);
+  if (e != hipSuccess) return hip_fail(e, "bl_fp8_forward (quantise)");
+  return check_launch(launch_fp8_linear(Fp8LinearArgs{q, sx, w, scales_w, M, N, K, y, ldy, ydtype}, s),
+                      "bl_fp8_forward");
+}
+
+int bl_route_experts(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
+                     const float* bias, int score, int groups, int kept, int64_t k, int renorm,
+                     float factor, float* weight, int32_t* index, void* stream) {
+  if (!logits || !weight || !index) return BL_ERR_NULL;
+  if (M < 1 || M > kMaxDim || E < 1 || E > 2048) return BL_ERR_SHAPE;
+  if (score != BL_SCORE_SOFTMAX && score != BL_SCORE_SIGMOID) return BL_ERR_ARG;
+  if (groups < 1 || groups > 64 || E % groups || kept < 1 || kept > groups || k < 1 || k > 64 ||
+      k > E / groups * kept)
+    return BL_ERR_ARG;
+  if (int st = check_rows_out(logits, dtype, E, ld)) return st;
+  if (!aligned_to(weight, 4) || !aligned_to(index, 4) || !aligned_to(bias, 4)) return BL_ERR_ALIGN;
+  const size_t ob = static_cast<size_t>(M) * k * 4;
+  const Span outs[] = {{weight, ob}, {index, ob}};
+  const Span ins[] = {{logits, rows_bytes(M, E, ld, dtype)}, {bias, bias ? static_cast<size_t>(E) * 4 : 0}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  return check_launch(launch_route(RouteArgs{logits, dtype, M, E, ld, bias, score == BL_SCORE_SIGMOID, groups,
+                                             kept, static_cast<int>(k), renorm, factor, weight, index},
+                                   static_cast<hipStream_t>(stream)),
+                      "bl_route_experts");
+}
+
+size_t bl_fp8_experts_workspace_bytes(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
+  return experts_dims_ok(M, H, k, E, I) ? experts_ws(M, H, k, E, I).total : 0;
+}
+
+int bl_fp8_experts(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
+                   const int32_t* index, const float* weight, int64_t k, const uint8_t* wgu,
+                   const float* scales_gu, const uint8_t* wd, const float* scales_d, int64_t E,
+                   int64_t I, void* y, int ydtype, int64_t ldy, void* ws, size_t ws_bytes,
+                   void* stream) {
+  if (!x || !index || !weight || !wgu || !scales_gu || !wd || !scales_d || !y) return BL_ERR_NULL;
+  if (!experts_dims_ok(M, H, k, E, I)) return BL_ERR_SHAPE;
+  if (int st = check_rows_in(x, dtype, H, ldx)) return st;
+  if (int st = check_rows_out(y, ydtype, H, ldy)) return st;
+  const ExpertsWs L = experts_ws(M, H, k, E, I);
+  if (!ws || ws_bytes < L.total) return BL_ERR_WORKSPACE;
+  if (!aligned16(wgu) || !aligned16(wd) || !aligned16(ws) || !aligned_to(scales_gu, 4) ||
+      !aligned_to(scales_d, 4) || !aligned_to(index, 4) || !aligned_to(weight, 4))
+    return BL_ERR_ALIGN;
+  const size_t slots = static_cast<size_t>(M) * k * 4, n = static_cast<size_t>(E) * I * H;
+  const size_t blocks = static_cast<size_t>(E) * fp8_blocks(I) * fp8_blocks(H) * 4;
+  const Span outs[] = {{y, rows_bytes(M, H, ldy, ydtype)}, {ws, L.total}};
+  const Span ins[] = {{x, rows_bytes(M, H, ldx, dtype)}, {index, slots}, {weight, slots}, {wgu, 2 * n},
+                      {scales_gu, 2 * blocks}, {wd, n}, {scales_d, blocks}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  return check_launch(launch_fp8_experts(Fp8ExpertsArgs{x, dtype, M, H, ldx, index, weight, k, wgu, scales_gu,
+                                                        wd, scales_d, E, I, y, ydtype, ldy},
+                                         static_cast<char*>(ws), static_cast<hipStream_t>(stream)),
+                      "bl_fp8_experts");
 }
 
 }  // extern "C"

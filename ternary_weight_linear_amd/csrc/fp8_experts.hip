@@ -1,0 +1,162 @@
+// The experts' gated products (bl_fp8_experts): sort the (token, slot) pairs by expert,
+// quantise x, multiply by the gate and up matrices, quantise silu(gate) * up, multiply by the
+// down matrix, and add each token's slots with their weights.
+#include "fp8_mfma.h"
+
+namespace bl {
+namespace {
+
+constexpr int kSortThreads = 1024;
+
+// One workgroup: counts per expert, their running sum, the sorted rows and the tiles of at
+// most `tile` rows. Slots whose index is outside [0, E) get no row. The order of the rows
+// within an expert may differ from run to run; no output depends on it, since each row is
+// multiplied by itself.
+__global__ __launch_bounds__(kSortThreads) void experts_sort_kernel(
+    const int32_t* __restrict__ index, int P, int E, int tile, int32_t* __restrict__ head,
+    int32_t* __restrict__ pair, int32_t* __restrict__ tiles) {
+  extern __shared__ int cnt[];              // [E] counts, then [E] next positions
+  __shared__ int scan[2][kSortThreads];
+  int* next = cnt + E;
+  for (int e = threadIdx.x; e < E; e += kSortThreads) cnt[e] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < P; i += kSortThreads) {
+    const int e = index[i];
+    if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+  }
+  __syncthreads();
+  // each thread sums its run of experts, then a scan over the threads
+  const int per = (E + kSortThreads - 1) / kSortThreads;
+  const int e0 = threadIdx.x * per;
+  int rows = 0, nt = 0;
+  for (int e = e0; e < min(e0 + per, E); ++e) {
+    rows += cnt[e];
+    nt += (cnt[e] + tile - 1) / tile;
+  }
+  scan[0][threadIdx.x] = rows;
+  scan[1][threadIdx.x] = nt;
+  __syncthreads();
+  for (int off = 1; off < kSortThreads; off <<= 1) {
+    int r = 0, t = 0;
+    if (static_cast<int>(threadIdx.x) >= off) {
+      r = scan[0][threadIdx.x - off];
+      t = scan[1][threadIdx.x - off];
+    }
+    __syncthreads();
+    scan[0][threadIdx.x] += r;
+    scan[1][threadIdx.x] += t;
+    __syncthreads();
+  }
+  int row = scan[0][threadIdx.x] - rows, at = scan[1][threadIdx.x] - nt;
+  for (int e = e0; e < min(e0 + per, E); ++e) {
+    next[e] = row;
+    for (int r = 0; r < cnt[e]; r += tile, ++at) {
+      tiles[4 * at] = e;
+      tiles[4 * at + 1] = row + r;
+      tiles[4 * at + 2] = min(tile, cnt[e] - r);
+    }
+    row += cnt[e];
+  }
+  if (threadIdx.x == kSortThreads - 1) {
+    head[0] = scan[0][threadIdx.x];
+    head[1] = scan[1][threadIdx.x];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < P; i += kSortThreads) {
+    const int e = index[i];
+    if (e >= 0 && e < E) pair[atomicAdd(&next[e], 1)] = i;
+  }
+}
+
+// y[m, n] = sum_j weight[m, j] part[m k + j, n], slots in their order.
+__global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a,
+                                                              const float* __restrict__ part) {
+  const int64_t m = blockIdx.x;
+  for (int64_t n = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x; n < a.H; n += 256 * gridDim.y) {
+    float sum = 0.0f;
+    for (int64_t j = 0; j < a.k; ++j) {
+      const int e = a.index[m * a.k + j];
+      if (e >= 0 && e < a.E) sum += a.weight[m * a.k + j] * part[(m * a.k + j) * a.H + n];
+    }
+    store_as(a.y, a.ydtype, m * a.ldy + n, sum);
+  }
+}
+
+template <int MT>
+void start_product(const ProductArgs& p, int64_t tiles, hipStream_t s) {
+  fp8_stream_kernel<MT><<<dim3(static_cast<uint32_t>((p.a.N + 15) / 16), static_cast<uint32_t>(tiles)), 512, 0, s>>>(p);
+}
+
+}  // namespace
+
+int64_t experts_max_tiles(int64_t P, int64_t E, int tile) { return P / tile + (P < E ? P : E); }
+
+ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
+  ExpertsWs w{};
+  const int64_t P = M * k, HB = fp8_blocks(H), IB = fp8_blocks(I);
+  size_t off = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t at = off;
+    off += (static_cast<size_t>(bytes) + 255) & ~size_t(255);
+    return at;
+  };
+  w.q_off = take(M * H);
+  w.sx_off = take(M * HB * 4);
+  w.head_off = take(16);
+  w.pair_off = take(P * 4);
+  w.tile_off = take(experts_max_tiles(P, E, 16) * 16);
+  w.gu_off = take(P * 2 * I * 4);
+  w.hq_off = take(P * I);
+  w.hs_off = take(P * IB * 4);
+  w.part_off = take(P * H * 4);
+  w.total = off;
+  return w;
+}
+
+hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) {
+  const ExpertsWs L = experts_ws(a.M, a.H, a.k, a.E, a.I);
+  const int64_t P = a.M * a.k, HB = fp8_blocks(a.H), IB = fp8_blocks(a.I);
+  auto* q = reinterpret_cast<uint8_t*>(ws + L.q_off);
+  auto* sx = reinterpret_cast<float*>(ws + L.sx_off);
+  auto* head = reinterpret_cast<int32_t*>(ws + L.head_off);
+  auto* pair = reinterpret_cast<int32_t*>(ws + L.pair_off);
+  auto* tiles = reinterpret_cast<int32_t*>(ws + L.tile_off);
+  auto* gu = reinterpret_cast<float*>(ws + L.gu_off);
+  auto* hq = reinterpret_cast<uint8_t*>(ws + L.hq_off);
+  auto* hs = reinterpret_cast<float*>(ws + L.hs_off);
+  auto* part = reinterpret_cast<float*>(ws + L.part_off);
+  const bool small = P <= 16 * a.E;
+  const int tile = small ? 16 : 64;
+  const int64_t nt = experts_max_tiles(P, a.E, tile);
+
+  hipError_t e = launch_fp8_quant_act(a.x, a.xdtype, a.M, a.H, a.ldx, 0, nullptr, q, sx, s);
+  if (e != hipSuccess) return e;
+  experts_sort_kernel<<<1, kSortThreads, static_cast<size_t>(a.E) * 8, s>>>(
+      a.index, static_cast<int>(P), static_cast<int>(a.E), tile, head, pair, tiles);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  for (int half = 0; half < 2; ++half) {
+    ProductArgs p{};
+    p.a = Fp8LinearArgs{q, sx, a.wgu + half * a.I * a.H, a.sgu + half * IB * HB, a.M, a.I, a.H, gu + half * a.I, 2 * a.I, BL_F32};
+    p.map = RowMap{tiles, head + 1, pair, static_cast<int>(a.k), 0};
+    p.w_stride = 2 * a.I * a.H;
+    p.sw_stride = 2 * IB * HB;
+    if (small) start_product<1>(p, nt, s);
+    else start_product<4>(p, nt, s);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  e = launch_fp8_quant_act(gu, BL_F32, P, a.I, 2 * a.I, 1, head, hq, hs, s);
+  if (e != hipSuccess) return e;
+  ProductArgs p{};
+  p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, BL_F32};
+  p.map = RowMap{tiles, head + 1, pair, 0, 1};
+  p.w_stride = a.H * a.I;
+  p.sw_stride = HB * IB;
+  if (small) start_product<1>(p, nt, s);
+  else start_product<4>(p, nt, s);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const uint32_t cols = static_cast<uint32_t>((a.H + 255) / 256);
+  experts_combine_kernel<<<dim3(static_cast<uint32_t>(a.M), cols < 16 ? cols : 16), 256, 0, s>>>(a, part);
+  return hipGetLastError();
+}
+
+}  // namespace bl

@@ -1,0 +1,143 @@
+// Block quantisers to e4m3: activations (one scale per row and 128 inputs) and weights (one
+// scale per 128 x 128 block).
+//
+//   a = max(max |v| over the block, 2^-100),  q = e4m3(fl32(v * r)),  r = fl32(448 fl32(1 / a)),
+//   scale = fl32(a / 448).
+//
+// |v r| <= 448 (1 + 2^-20), which rounds to 448, so no code overflows (1 / a is subnormal for
+// a > 2^126, and still right to 21 bits). The
+// maximum is taken over the bit patterns of |v| as unsigned integers: there NaN > inf > every
+// finite value, so a block that holds NaN gets scale NaN and NaN codes.
+#include "fp8_internal.h"
+
+namespace bl {
+namespace {
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// What values are multiplied by before they are rounded to codes. IEEE steps: they decide codes.
+__device__ __forceinline__ float code_factor(float a) { return kFp8Max * (1.0f / a); }
+
+// Eight consecutive values at p (16-byte aligned).
+template <int DT>
+__device__ __forceinline__ void load8(const typename Elem<DT>::type* p, float (&v)[8]) {
+  if constexpr (DT == BL_F32) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = to_float<DT>(static_cast<uint16_t>(w[j] & 0xFFFFu));
+      v[2 * j + 1] = to_float<DT>(static_cast<uint16_t>(w[j] >> 16));
+    }
+  }
+}
+
+__device__ __forceinline__ uint2 pack8(const float (&v)[8], float r) {
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * r, v[1] * r, lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * r, v[3] * r, lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * r, v[5] * r, hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * r, v[7] * r, hi, true);
+  return make_uint2(static_cast<uint32_t>(lo), static_cast<uint32_t>(hi));
+}
+
+// Sixteen lanes per block of 128, eight values each: one 16-byte load per lane, a maximum over
+// the sixteen lanes, one 8-byte store. The block index runs over inputs first.
+template <int DT, bool GATED>
+__global__ __launch_bounds__(256) void fp8_quant_act_kernel(
+    const typename Elem<DT>::type* __restrict__ x, int64_t M, int64_t K, int64_t KB, int64_t ldx,
+    const int32_t* __restrict__ rows_used, uint8_t* __restrict__ q, float* __restrict__ scale) {
+  const int64_t blk = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const int j = threadIdx.x & 15;
+  const int64_t m = blk / KB, kb = blk % KB;
+  if (m >= (rows_used ? *rows_used : M)) return;
+  const int64_t k = kb * kFp8Block + j * 8;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (k < K) {
+    load8<DT>(x + m * ldx + k, v);
+    if constexpr (GATED) {
+      float u[8];
+      load8<DT>(x + m * ldx + K + k, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], u[i]);
+    }
+  }
+  uint32_t a = kFp8FloorBits;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[i]));
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), off)));
+  const float am = __uint_as_float(a);
+  if (k < K) *reinterpret_cast<uint2*>(q + m * K + k) = pack8(v, code_factor(am));
+  if (j == 0) scale[kb * M + m] = am / kFp8Max;
+}
+
+// One workgroup per 128 x 128 block: thread t holds rows t / 16 + 16 i, inputs 8 (t % 16) ...
+__global__ __launch_bounds__(256) void fp8_quant_weight_kernel(const float* __restrict__ W,
+                                                               int64_t N, int64_t K, int64_t KB,
+                                                               uint8_t* __restrict__ codes,
+                                                               float* __restrict__ scale) {
+  __shared__ uint32_t red[4];
+  const int64_t nb = blockIdx.x / KB, kb = blockIdx.x % KB;
+  const int r = threadIdx.x >> 4;
+  const int64_t k = kb * kFp8Block + (threadIdx.x & 15) * 8;
+  float v[8][8];
+  uint32_t a = kFp8FloorBits;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t n = nb * kFp8Block + r + 16 * i;
+    if (n < N && k < K) load8<BL_F32>(W + n * K + k, v[i]);
+    else
+      for (int e = 0; e < 8; ++e) v[i][e] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = max(a, abs_bits(v[i][e]));
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), off)));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = a;
+  __syncthreads();
+  const float am = __uint_as_float(max(max(red[0], red[1]), max(red[2], red[3])));
+  const float rcp = code_factor(am);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t n = nb * kFp8Block + r + 16 * i;
+    if (n < N && k < K) *reinterpret_cast<uint2*>(codes + n * K + k) = pack8(v[i], rcp);
+  }
+  if (threadIdx.x == 0) scale[nb * KB + kb] = am / kFp8Max;
+}
+
+template <int DT>
+void start_quant(const void* x, int64_t M, int64_t K, int64_t ldx, int gated,
+                 const int32_t* rows_used, uint8_t* q, float* scale, hipStream_t s) {
+  using T = typename Elem<DT>::type;
+  const int64_t KB = fp8_blocks(K);
+  const dim3 grid(static_cast<uint32_t>((M * KB + 15) / 16));
+  if (gated)
+    fp8_quant_act_kernel<DT, true><<<grid, 256, 0, s>>>(static_cast<const T*>(x), M, K, KB, ldx, rows_used, q, scale);
+  else
+    fp8_quant_act_kernel<DT, false><<<grid, 256, 0, s>>>(static_cast<const T*>(x), M, K, KB, ldx, rows_used, q, scale);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quant_act(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx,
+                                int gated, const int32_t* rows_used, uint8_t* q, float* scale,
+                                hipStream_t s) {
+  if (dtype == BL_F16) start_quant<BL_F16>(x, M, K, ldx, gated, rows_used, q, scale, s);
+  else if (dtype == BL_BF16) start_quant<BL_BF16>(x, M, K, ldx, gated, rows_used, q, scale, s);
+  else start_quant<BL_F32>(x, M, K, ldx, gated, rows_used, q, scale, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_quant_weight(const float* W, int64_t N, int64_t K, uint8_t* codes,
+                                   float* scale, hipStream_t s) {
+  const int64_t NB = fp8_blocks(N), KB = fp8_blocks(K);
+  fp8_quant_weight_kernel<<<static_cast<uint32_t>(NB * KB), 256, 0, s>>>(W, N, K, KB, codes, scale);
+  return hipGetLastError();
+}
+
+}  // namespace bl
