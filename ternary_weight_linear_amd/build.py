@@ -36,8 +36,11 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 
 # Per-source extras. mf_decode.hip: matrix-core accumulators in ordinary VGPRs (with the
 # default AGPR form the compiler copies them between register files around the loop's
-# uniform branches, ~20 extra ops per batch of tiles).
-EXTRA = {"mf_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# uniform branches, ~20 extra ops per batch of tiles). fp8_*.hip: each block's product is
+# scaled by the VALU, which reads no AGPRs.
+EXTRA = {"mf_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "fp8_linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "fp8_experts.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 SOURCES = ["api.hip", "pack.hip", "quant.hip", "gemv.hip", "gemm.hip", "onebit.hip", "svid.hip",
            "stack.hip",

@@ -1,0 +1,230 @@
+// Tiled block-scaled product for many rows: operands staged through LDS.
+#pragma once
+
+#include "fp8_mfma.h"
+
+namespace bl {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// Offsets from here on are outside every buffer below: a load there gives zeros.
+constexpr uint32_t kOutside = 0x80000000u;
+
+// A buffer of 2 GiB at `base` (wave-uniform): the accesses are kept inside the operand by the
+// row clamps, the buffer's own bound only turns the offset kOutside into zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_buffer(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(kOutside), 0x00020000);
+}
+
+// 16 bytes per lane from base + offset + k0 into LDS at `to` + 16 lane.
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, uint32_t k0, uint8_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16,
+                                           static_cast<int>(offset), static_cast<int>(k0), 0, 0);
+}
+
+template <int BN_, int BM_, int GN_, int GM_, bool EXACT_>
+struct GemmShape {
+  static constexpr int BN = BN_, BM = BM_;          // tile: rows of w, rows of q
+  static constexpr int GN = GN_, GM = GM_;          // waves along each
+  static constexpr int WAVES = GN * GM, THREADS = 64 * WAVES;
+  static constexpr int TN = BN / GN / 16, TM = BM / GM / 16;
+  static constexpr bool EXACT = EXACT_;             // fp16 operands
+  static constexpr int CA = BN / 8 / WAVES, CB = BM / 8 / WAVES;   // copies per wave and block
+};
+
+template <bool EXACT>
+struct OperandT { using type = i32x8; };
+template <>
+struct OperandT<true> { using type = FragH; };
+
+// The fragment of 16 rows whose first byte for this lane is at `at` of a staged tile; the
+// second 16 codes are in the piece four further on, which the XOR order puts 64 bytes away.
+template <bool EXACT>
+__device__ __forceinline__ typename OperandT<EXACT>::type read_operand(const uint8_t* tile, uint32_t lo, uint32_t hi) {
+  Frag f;
+  f.lo = *reinterpret_cast<const u32x4*>(tile + lo);
+  f.hi = *reinterpret_cast<const u32x4*>(tile + hi);
+  if constexpr (EXACT) return to_half(f);
+  else return i32x8{(int)f.lo.x, (int)f.lo.y, (int)f.lo.z, (int)f.lo.w, (int)f.hi.x, (int)f.hi.y, (int)f.hi.z, (int)f.hi.w};
+}
+
+__device__ __forceinline__ f32x4 block_dot(const i32x8& a, const i32x8& b) {
+  const f32x4 c = {0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+template <class S>
+__global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int tiles_n, int tiles_m) {
+  // one array per operand and stage: the compiler can then tell that the copies into one
+  // stage do not touch what is being read
+  __shared__ uint8_t bufA0[S::BN * 128], bufA1[S::BN * 128], bufB0[S::BM * 128], bufB1[S::BM * 128];
+  const Fp8LinearArgs& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, u = lane & 15;
+  const int wn = (wave % S::GN) * (S::BN / S::GN), wm = (wave / S::GN) * (S::BM / S::GM);
+
+  int id = blockIdx.x;
+  const int total = tiles_n * tiles_m;
+  // XCD x takes a contiguous run of tiles
+  {
+    const int per = (total + 7) / 8, rest = total % 8 ? total % 8 : 8;   // first `rest` XCDs have `per`
+    const int xcd = id & 7, i = id >> 3;
+    id = xcd < rest ? xcd * per + i : rest * per + (xcd - rest) * (per - 1) + i;
+  }
+  // bands of 8 tiles of q, within a band q runs first
+  const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n;
+  const int bm = min(8, tiles_m - band * 8);
+  const int tm = band * 8 + in % bm, tn = in / bm;
+
+  const int64_t n0 = static_cast<int64_t>(tn) * S::BN;
+  int64_t first = static_cast<int64_t>(tm) * S::BM;
+  int rows = 0, expert = 0;
+  if (p.map.tiles) {
+    if (tm >= *p.map.n_tiles) return;
+    expert = p.map.tiles[4 * tm];
+    first = p.map.tiles[4 * tm + 1];
+    rows = p.map.tiles[4 * tm + 2];
+  } else {
+    rows = static_cast<int>(a.M - first < S::BM ? a.M - first : S::BM);
+  }
+  const int64_t K = a.K, KB = (K + kFp8Block - 1) / kFp8Block;
+
+  // staging: copy i of this wave fills rows 8 (i WAVES + wave) + lane / 8 of a tile; position
+  // lane % 8 of a row holds the 16 codes of piece (lane % 8) ^ (row % 8)
+  const int piece = (lane & 7) ^ (lane >> 3);
+  uint32_t oa[S::CA], ob[S::CB];
+  const auto ba = make_buffer(a.w + expert * p.w_stride + n0 * K);
+  const auto bb = make_buffer(p.map.gather_div > 0 ? a.q : a.q + first * K);
+#pragma unroll
+  for (int i = 0; i < S::CA; ++i) {
+    const int n = min(8 * (i * S::WAVES + wave) + (lane >> 3), static_cast<int>(min<int64_t>(a.N - 1 - n0, S::BN)));
+    oa[i] = static_cast<uint32_t>(n) * static_cast<uint32_t>(K) + 16 * piece;
+  }
+#pragma unroll
+  for (int i = 0; i < S::CB; ++i) {
+    int r = min(8 * (i * S::WAVES + wave) + (lane >> 3), rows - 1);
+    if (p.map.gather_div > 0) r = p.map.pair[first + r] / p.map.gather_div;
+    ob[i] = static_cast<uint32_t>(r) * static_cast<uint32_t>(K) + 16 * piece;
+  }
+  const int kb_cut = K % kFp8Block ? static_cast<int>(KB) - 1 : -1;   // the block that K ends in
+  const bool out = (KB - 1) * kFp8Block + 16 * piece >= K;
+  auto stage = [&](int kb, uint8_t* ta, uint8_t* tb) __attribute__((always_inline)) {
+    const bool skip = out && kb == kb_cut;
+    const uint32_t k0 = static_cast<uint32_t>(kb) * kFp8Block;
+#pragma unroll
+    for (int i = 0; i < S::CA; ++i)
+      copy_to_lds(ba, skip ? kOutside : oa[i], k0, ta + 1024 * (i * S::WAVES + wave));
+#pragma unroll
+    for (int i = 0; i < S::CB; ++i)
+      copy_to_lds(bb, skip ? kOutside : ob[i], k0, tb + 1024 * (i * S::WAVES + wave));
+  };
+
+  uint32_t ox[S::TM];
+#pragma unroll
+  for (int j = 0; j < S::TM; ++j) {
+    int64_t at = first + min(wm + 16 * j + u, rows - 1);
+    if (p.map.gather_div > 0) at = p.map.pair[at] / p.map.gather_div;
+    ox[j] = 4 * static_cast<uint32_t>(at);
+  }
+  // the wave's weight rows lie in one block of 128 (BN / GN divides 128)
+  const float* sw = a.sw + expert * p.sw_stride + min<int64_t>((n0 + wn) / kFp8Block, (a.N - 1) / kFp8Block) * KB;
+
+  const uint32_t in_row = u * 128 + 16 * (g ^ (u & 7));
+  const uint32_t wa = wn * 128 + in_row, wa2 = wn * 128 + (in_row ^ 64);
+  const uint32_t qa = wm * 128 + in_row, qa2 = wm * 128 + (in_row ^ 64);
+  struct Scales {
+    float x[S::TM], w;
+  };
+  f32x4 acc[S::TN][S::TM] = {};
+  // One block of inputs. While the matrix cores multiply weight fragment i by the TM fragments
+  // of q, the products of fragment i - 1 are scaled and added (VALU) and fragment i + 1 is read.
+  auto compute = [&](const uint8_t* ta, const uint8_t* tb, const Scales& sc) __attribute__((always_inline)) {
+    float f[S::TM];
+#pragma unroll
+    for (int j = 0; j < S::TM; ++j) f[j] = sc.x[j] * sc.w;
+    typename OperandT<S::EXACT>::type b[S::TM], w[2];
+    f32x4 part[2][S::TM];
+    w[0] = read_operand<S::EXACT>(ta, wa, wa2);
+#pragma unroll
+    for (int j = 0; j < S::TM; ++j) b[j] = read_operand<S::EXACT>(tb + 2048 * j, qa, qa2);
+#pragma unroll
+    for (int i = 0; i <= S::TN; ++i) {
+      if (i + 1 < S::TN) w[(i + 1) & 1] = read_operand<S::EXACT>(ta + 2048 * (i + 1), wa, wa2);
+#pragma unroll
+      for (int j = 0; j < S::TM; ++j) {
+        if (i < S::TN) part[i & 1][j] = block_dot(w[i & 1], b[j]);
+        if (i > 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i - 1][j][e] = fmaf(part[(i - 1) & 1][j][e], f[j], acc[i - 1][j][e]);
+          asm volatile("" : "+v"(acc[i - 1][j]));   // the sum is formed here, not sunk to its next use
+        }
+      }
+      // both LDS reads first, then each matrix instruction beside four FMAs of the one before
+      if (i + 1 < S::TN) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+      for (int j = 0; j < S::TM; ++j) {
+        if (i < S::TN) __builtin_amdgcn_sched_group_barrier(0x008, S::EXACT ? 4 : 1, 0);
+        if (i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto scales = [&](int kb, Scales& sc) __attribute__((always_inline)) {
+    sc.w = sw[kb];
+    const auto sx = make_buffer(a.sx + kb * a.M);
+#pragma unroll
+    for (int j = 0; j < S::TM; ++j)
+      sc.x[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sx, static_cast<int>(ox[j]), 0, 0));
+  };
+  // every copy of this wave has landed, then every wave's
+  auto arrive = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);             // vmcnt(0)
+    __syncthreads();
+  };
+
+  const int blocks = static_cast<int>(KB);
+  Scales f0, f1;
+  stage(0, bufA0, bufB0);
+  scales(0, f0);
+  for (int kb = 0; kb + 1 < blocks; kb += 2) {
+    arrive();
+    stage(kb + 1, bufA1, bufB1);
+    scales(kb + 1, f1);
+    compute(bufA0, bufB0, f0);
+    arrive();
+    const int next = min(kb + 2, blocks - 1);     // past the end the last block again, never read
+    stage(next, bufA0, bufB0);
+    scales(next, f0);
+    compute(bufA1, bufB1, f1);
+  }
+  arrive();                                       // no copy outlives the workgroup
+  if (blocks & 1) compute(bufA0, bufB0, f0);
+
+#pragma unroll
+  for (int j = 0; j < S::TM; ++j) {
+    const int r = wm + 16 * j + u;
+    if (r >= rows) continue;
+    int64_t at = first + r;
+    if (p.map.scatter) at = p.map.pair[at];
+#pragma unroll
+    for (int i = 0; i < S::TN; ++i) {
+      const int64_t n = n0 + wn + 16 * i + 4 * g;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < a.N) store_as(a.y, a.ydtype, at * a.ldy + n + e, acc[i][j][e]);
+    }
+  }
+}
+
+template <class S>
+hipError_t start_gemm(const ProductArgs& p, int64_t tiles_m, hipStream_t s) {
+  const int64_t tiles_n = (p.a.N + S::BN - 1) / S::BN;
+  fp8_gemm_kernel<S><<<dim3(static_cast<uint32_t>(tiles_n * tiles_m)), S::THREADS, 0, s>>>(
+      p, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace bl
