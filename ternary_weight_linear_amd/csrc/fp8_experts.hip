@@ -1,7 +1,7 @@
 // The experts' gated products (bl_fp8_experts): sort the (token, slot) pairs by expert,
 // quantise x, multiply by the gate and up matrices, quantise silu(gate) * up, multiply by the
 // down matrix, and add each token's slots with their weights.
-#include "fp8_mfma.h"
+#include "fp8_gemm.h"
 
 namespace bl {
 namespace {
@@ -125,8 +125,14 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   auto* hq = reinterpret_cast<uint8_t*>(ws + L.hq_off);
   auto* hs = reinterpret_cast<float*>(ws + L.hs_off);
   auto* part = reinterpret_cast<float*>(ws + L.part_off);
-  const bool small = P <= 16 * a.E;
-  const int tile = small ? 16 : 64;
+  // fp16 operands where the hidden layer's or the result's type would show the e4m3
+  // instruction's sums (its error, 1.4e-5 of a block's, moves a few hidden codes: 1/2 of
+  // bf16's rounding of the result, 4 times fp16's)
+  const bool exact = a.xdtype != BL_BF16, exact_down = a.ydtype == BL_F32;
+  // rows per tile, by the average rows of an expert; the tiled kernel's offsets are 32 bits
+  const bool tiled = P > 48 * a.E && a.M * a.H < (int64_t(1) << 31) && 2 * a.I * a.H < (int64_t(1) << 31) &&
+                     256 * a.I < (int64_t(1) << 31);
+  const int tile = !tiled ? (P <= 16 * a.E ? 16 : 64) : P <= 192 * a.E || exact || exact_down ? 128 : 256;
   const int64_t nt = experts_max_tiles(P, a.E, tile);
 
   hipError_t e = launch_fp8_quant_act(a.x, a.xdtype, a.M, a.H, a.ldx, 0, nullptr, q, sx, s);
@@ -134,26 +140,44 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   experts_sort_kernel<<<1, kSortThreads, static_cast<size_t>(a.E) * 8, s>>>(
       a.index, static_cast<int>(P), static_cast<int>(a.E), tile, head, pair, tiles);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  for (int half = 0; half < 2; ++half) {
+  if (tile <= 64) {
+    for (int half = 0; half < 2; ++half) {
+      ProductArgs p{};
+      p.a = Fp8LinearArgs{q, sx, a.wgu + half * a.I * a.H, a.sgu + half * IB * HB, a.M, a.I, a.H, gu + half * a.I, 2 * a.I, BL_F32};
+      p.map = RowMap{tiles, head + 1, pair, static_cast<int>(a.k), 0};
+      p.w_stride = 2 * a.I * a.H;
+      p.sw_stride = 2 * IB * HB;
+      if (tile == 16) start_product<1>(p, nt, s);
+      else start_product<4>(p, nt, s);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    e = launch_fp8_quant_act(gu, BL_F32, P, a.I, 2 * a.I, 1, head, hq, hs, s);
+  } else {
     ProductArgs p{};
-    p.a = Fp8LinearArgs{q, sx, a.wgu + half * a.I * a.H, a.sgu + half * IB * HB, a.M, a.I, a.H, gu + half * a.I, 2 * a.I, BL_F32};
+    p.a = Fp8LinearArgs{q, sx, a.wgu, a.sgu, a.M, a.I, a.H, nullptr, 0, BL_F32};
     p.map = RowMap{tiles, head + 1, pair, static_cast<int>(a.k), 0};
     p.w_stride = 2 * a.I * a.H;
     p.sw_stride = 2 * IB * HB;
-    if (small) start_product<1>(p, nt, s);
-    else start_product<4>(p, nt, s);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    p.hq = hq;
+    p.hs = hs;
+    p.h_rows = P;
+    e = exact         ? start_gemm<GemmShape<256, 128, 2, 4, true, true>>(p, nt, s)
+        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, false, true>>(p, nt, s)
+                      : start_gemm<GemmShape<256, 256, 2, 4, false, true>>(p, nt, s);
   }
-  e = launch_fp8_quant_act(gu, BL_F32, P, a.I, 2 * a.I, 1, head, hq, hs, s);
   if (e != hipSuccess) return e;
   ProductArgs p{};
   p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, BL_F32};
   p.map = RowMap{tiles, head + 1, pair, 0, 1};
   p.w_stride = a.H * a.I;
   p.sw_stride = HB * IB;
-  if (small) start_product<1>(p, nt, s);
-  else start_product<4>(p, nt, s);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (tile == 16) start_product<1>(p, nt, s);
+  else if (tile == 64) start_product<4>(p, nt, s);
+  else
+    e = exact_down    ? start_gemm<GemmShape<256, 128, 2, 4, true>>(p, nt, s)
+        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, false>>(p, nt, s)
+                      : start_gemm<GemmShape<256, 256, 2, 4, false>>(p, nt, s);
+  if (e != hipSuccess || (e = hipGetLastError()) != hipSuccess) return e;
   const uint32_t cols = static_cast<uint32_t>((a.H + 255) / 256);
   experts_combine_kernel<<<dim3(static_cast<uint32_t>(a.M), cols < 16 ? cols : 16), 256, 0, s>>>(a, part);
   return hipGetLastError();

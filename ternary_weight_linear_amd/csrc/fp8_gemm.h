@@ -23,13 +23,18 @@ __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
                                            static_cast<int>(offset), static_cast<int>(k0), 0, 0);
 }
 
-template <int BN_, int BM_, int GN_, int GM_, bool EXACT_>
+template <int BN_, int BM_, int GN_, int GM_, bool EXACT_, bool GATED_ = false>
 struct GemmShape {
   static constexpr int BN = BN_, BM = BM_;          // tile: rows of w, rows of q
   static constexpr int GN = GN_, GM = GM_;          // waves along each
   static constexpr int WAVES = GN * GM, THREADS = 64 * WAVES;
   static constexpr int TN = BN / GN / 16, TM = BM / GM / 16;
   static constexpr bool EXACT = EXACT_;             // fp16 operands
+  // A tile of w is BN / 2 gate rows and the BN / 2 up rows of the same channels, and the tile's
+  // result is quantised silu(gate) * up. Each wave holds both rows of its channels.
+  static constexpr bool GATED = GATED_;
+  static constexpr int NF = GATED ? 2 : 1;          // blocks of 128 rows of w that a wave reads
+  static_assert(!GATED || BN == 256, "a gated tile is one block of 128 channels");
   static constexpr int CA = BN / 8 / WAVES, CB = BM / 8 / WAVES;   // copies per wave and block
 };
 
@@ -55,7 +60,7 @@ __device__ __forceinline__ f32x4 block_dot(const i32x8& a, const i32x8& b) {
 }
 
 template <class S>
-__global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int tiles_n, int tiles_m) {
+__global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int tiles_n, int tiles_m_arg) {
   // one array per operand and stage: the compiler can then tell that the copies into one
   // stage do not touch what is being read
   __shared__ uint8_t bufA0[S::BN * 128], bufA1[S::BN * 128], bufB0[S::BM * 128], bufB1[S::BM * 128];
@@ -64,13 +69,14 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   const int g = lane >> 4, u = lane & 15;
   const int wn = (wave % S::GN) * (S::BN / S::GN), wm = (wave / S::GN) * (S::BM / S::GM);
 
+  const int tiles_m = p.map.tiles ? *p.map.n_tiles : tiles_m_arg;
   int id = blockIdx.x;
-  const int total = tiles_n * tiles_m;
-  // XCD x takes a contiguous run of tiles
   {
-    const int per = (total + 7) / 8, rest = total % 8 ? total % 8 : 8;   // first `rest` XCDs have `per`
+    // XCD x (workgroups are dealt to the eight XCDs in turn) takes a contiguous run of tiles
+    const int total = tiles_n * tiles_m, per = total / 8, more = total % 8;
     const int xcd = id & 7, i = id >> 3;
-    id = xcd < rest ? xcd * per + i : rest * per + (xcd - rest) * (per - 1) + i;
+    if (i >= per + (xcd < more)) return;
+    id = xcd * per + min(xcd, more) + i;
   }
   // bands of 8 tiles of q, within a band q runs first
   const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n;
@@ -81,7 +87,6 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   int64_t first = static_cast<int64_t>(tm) * S::BM;
   int rows = 0, expert = 0;
   if (p.map.tiles) {
-    if (tm >= *p.map.n_tiles) return;
     expert = p.map.tiles[4 * tm];
     first = p.map.tiles[4 * tm + 1];
     rows = p.map.tiles[4 * tm + 2];
@@ -94,11 +99,20 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   // lane % 8 of a row holds the 16 codes of piece (lane % 8) ^ (row % 8)
   const int piece = (lane & 7) ^ (lane >> 3);
   uint32_t oa[S::CA], ob[S::CB];
-  const auto ba = make_buffer(a.w + expert * p.w_stride + n0 * K);
+  const auto ba = make_buffer(a.w + expert * p.w_stride + (S::GATED ? 0 : n0 * K));
   const auto bb = make_buffer(p.map.gather_div > 0 ? a.q : a.q + first * K);
+  const int c0 = tn * (S::BN / 2);                  // GATED: the tile's first channel
 #pragma unroll
   for (int i = 0; i < S::CA; ++i) {
-    const int n = min(8 * (i * S::WAVES + wave) + (lane >> 3), static_cast<int>(min<int64_t>(a.N - 1 - n0, S::BN)));
+    int n = 8 * (i * S::WAVES + wave) + (lane >> 3);
+    if constexpr (S::GATED) {
+      // row n of the tile: wave column n / (BN / GN), gate rows first, then up rows
+      constexpr int W = S::BN / S::GN, half = W / 2;
+      const int c = min(c0 + n / W * half + n % half, static_cast<int>(a.N) - 1);
+      n = n % W < half ? c : static_cast<int>(a.N) + c;
+    } else {
+      n = min(n, static_cast<int>(min<int64_t>(a.N - 1 - n0, S::BN)));
+    }
     oa[i] = static_cast<uint32_t>(n) * static_cast<uint32_t>(K) + 16 * piece;
   }
 #pragma unroll
@@ -127,22 +141,26 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     if (p.map.gather_div > 0) at = p.map.pair[at] / p.map.gather_div;
     ox[j] = 4 * static_cast<uint32_t>(at);
   }
-  // the wave's weight rows lie in one block of 128 (BN / GN divides 128)
-  const float* sw = a.sw + expert * p.sw_stride + min<int64_t>((n0 + wn) / kFp8Block, (a.N - 1) / kFp8Block) * KB;
+  // the wave's weight rows (GATED: of either half) lie in one block of 128 (BN / GN divides 128)
+  const float* sw = a.sw + expert * p.sw_stride;
+  const int64_t up_scales = (a.N + kFp8Block - 1) / kFp8Block * KB;
+  sw += (S::GATED ? static_cast<int64_t>(tn) : min<int64_t>((n0 + wn) / kFp8Block, (a.N - 1) / kFp8Block)) * KB;
 
   const uint32_t in_row = u * 128 + 16 * (g ^ (u & 7));
   const uint32_t wa = wn * 128 + in_row, wa2 = wn * 128 + (in_row ^ 64);
   const uint32_t qa = wm * 128 + in_row, qa2 = wm * 128 + (in_row ^ 64);
   struct Scales {
-    float x[S::TM], w;
+    float x[S::TM], w[S::NF];
   };
   f32x4 acc[S::TN][S::TM] = {};
   // One block of inputs. While the matrix cores multiply weight fragment i by the TM fragments
   // of q, the products of fragment i - 1 are scaled and added (VALU) and fragment i + 1 is read.
   auto compute = [&](const uint8_t* ta, const uint8_t* tb, const Scales& sc) __attribute__((always_inline)) {
-    float f[S::TM];
+    float f[S::NF][S::TM];
 #pragma unroll
-    for (int j = 0; j < S::TM; ++j) f[j] = sc.x[j] * sc.w;
+    for (int h = 0; h < S::NF; ++h)
+#pragma unroll
+      for (int j = 0; j < S::TM; ++j) f[h][j] = sc.x[j] * sc.w[h];
     typename OperandT<S::EXACT>::type b[S::TM], w[2];
     f32x4 part[2][S::TM];
     w[0] = read_operand<S::EXACT>(ta, wa, wa2);
@@ -157,7 +175,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
         if (i > 0) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            acc[i - 1][j][e] = fmaf(part[(i - 1) & 1][j][e], f[j], acc[i - 1][j][e]);
+            acc[i - 1][j][e] = fmaf(part[(i - 1) & 1][j][e], f[(i - 1) * S::NF / S::TN][j], acc[i - 1][j][e]);
           asm volatile("" : "+v"(acc[i - 1][j]));   // the sum is formed here, not sunk to its next use
         }
       }
@@ -172,7 +190,8 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     }
   };
   auto scales = [&](int kb, Scales& sc) __attribute__((always_inline)) {
-    sc.w = sw[kb];
+    sc.w[0] = sw[kb];
+    if constexpr (S::GATED) sc.w[1] = sw[up_scales + kb];
     const auto sx = make_buffer(a.sx + kb * a.M);
 #pragma unroll
     for (int j = 0; j < S::TM; ++j)
@@ -202,6 +221,49 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   arrive();                                       // no copy outlives the workgroup
   if (blocks & 1) compute(bufA0, bufB0, f0);
 
+  if constexpr (S::GATED) {
+    // h = silu(gate) * up stays in fp32 up to its quantisation: the maximum of a row over the
+    // tile's 128 channels meets over the lanes that share the row, then over the waves in LDS
+    auto* top = reinterpret_cast<uint32_t*>(bufA0);   // [GN][BM], every wave is past the tiles
+    uint32_t mine[S::TM];
+#pragma unroll
+    for (int j = 0; j < S::TM; ++j) {
+      mine[j] = kFp8FloorBits;
+#pragma unroll
+      for (int i = 0; i < S::TN / 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = c0 + wn / 2 + 16 * i + 4 * g + e;
+          const float h = silu_mul(acc[i][j][e], acc[i + S::TN / 2][j][e]);
+          acc[i][j][e] = c < a.N ? h : 0.0f;
+          mine[j] = max(mine[j], abs_bits(acc[i][j][e]));
+        }
+      mine[j] = max(mine[j], static_cast<uint32_t>(__shfl_xor(static_cast<int>(mine[j]), 16)));
+      mine[j] = max(mine[j], static_cast<uint32_t>(__shfl_xor(static_cast<int>(mine[j]), 32)));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < S::TM; ++j)
+      if (g == 0) top[wave % S::GN * S::BM + wm + 16 * j + u] = mine[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < S::TM; ++j) {
+      const int r = wm + 16 * j + u;
+      uint32_t m = top[r];
+#pragma unroll
+      for (int v = 1; v < S::GN; ++v) m = max(m, top[v * S::BM + r]);
+      const float am = __uint_as_float(m), rcp = code_factor(am);
+      if (r >= rows) continue;
+      if (wn == 0 && g == 0) p.hs[tn * p.h_rows + first + r] = am / kFp8Max;
+#pragma unroll
+      for (int i = 0; i < S::TN / 2; ++i) {
+        const int c = c0 + wn / 2 + 16 * i + 4 * g;
+        if (c < a.N)                                  // N % 16 == 0: all four or none
+          *reinterpret_cast<uint32_t*>(p.hq + (first + r) * a.N + c) = pack4(acc[i][j], rcp);
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < S::TM; ++j) {
     const int r = wm + 16 * j + u;
@@ -220,7 +282,8 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
 
 template <class S>
 hipError_t start_gemm(const ProductArgs& p, int64_t tiles_m, hipStream_t s) {
-  const int64_t tiles_n = (p.a.N + S::BN - 1) / S::BN;
+  constexpr int64_t cols = S::GATED ? S::BN / 2 : S::BN;
+  const int64_t tiles_n = (p.a.N + cols - 1) / cols;
   fp8_gemm_kernel<S><<<dim3(static_cast<uint32_t>(tiles_n * tiles_m)), S::THREADS, 0, s>>>(
       p, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
   return hipGetLastError();

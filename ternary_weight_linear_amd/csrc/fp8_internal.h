@@ -111,6 +111,12 @@ __device__ __forceinline__ void store_as(void* y, int dtype, int64_t at, float v
   else static_cast<uint16_t*>(y)[at] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
 }
 
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// What a block's values are multiplied by before they are rounded to codes, from its maximum.
+// IEEE steps: they decide codes.
+__device__ __forceinline__ float code_factor(float a) { return kFp8Max * (1.0f / a); }
+
 // silu(g) * u in fp32
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 

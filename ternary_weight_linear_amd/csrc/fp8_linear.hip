@@ -8,7 +8,7 @@ hipError_t launch_fp8_linear(const Fp8LinearArgs& a, hipStream_t s) {
   const uint32_t nt = static_cast<uint32_t>((a.N + 15) / 16);
   if (a.M <= 16) {
     fp8_stream_kernel<1><<<dim3(nt, 1), 512, 0, s>>>(p);
-  } else if (a.M <= 64) {
+  } else if (a.M <= 64 || 256 * a.K >= (int64_t(1) << 31)) {   // the tiled kernel's offsets are 32 bits
     fp8_stream_kernel<4><<<dim3(nt, static_cast<uint32_t>((a.M + 63) / 64)), 512, 0, s>>>(p);
   } else if (a.ydtype == BL_F32) {
     const int64_t tiles = ((a.N + 127) / 128) * ((a.M + 127) / 128);

@@ -57,6 +57,13 @@ __device__ __forceinline__ FragH to_half(const Frag& f) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t pack4(const f32x4& v, float r) {
+  int c = 0;
+  c = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * r, v[1] * r, c, false);
+  c = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * r, v[3] * r, c, true);
+  return static_cast<uint32_t>(c);
+}
+
 // Sum over a block: D[row of a][row of b]; lane 16 g + u holds rows 4 g + i of a, row u of b.
 // The codes go to the fp16 matrix cores, whose sums keep fp32's precision; the e4m3 form of
 // the instruction keeps about 16 bits below the largest product (measured: relative error
@@ -81,6 +88,10 @@ struct ProductArgs {
   Fp8LinearArgs a;
   RowMap map;
   int64_t w_stride, sw_stride;   // elements between experts
+  // gated products: codes [h_rows, N] and scales [ceil(N / 128), h_rows] of silu(gate) * up
+  uint8_t* hq;
+  float* hs;
+  int64_t h_rows;
 };
 
 // One workgroup of eight waves: 16 rows of w by 16 MT rows of q; wave v takes blocks v, v + 8,

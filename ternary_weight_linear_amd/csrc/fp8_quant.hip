@@ -13,11 +13,6 @@
 namespace bl {
 namespace {
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-// What values are multiplied by before they are rounded to codes. IEEE steps: they decide codes.
-__device__ __forceinline__ float code_factor(float a) { return kFp8Max * (1.0f / a); }
-
 // Eight consecutive values at p (16-byte aligned).
 template <int DT>
 __device__ __forceinline__ void load8(const typename Elem<DT>::type* p, float (&v)[8]) {

@@ -378,7 +378,7 @@ def choose(M, E, k, seed, away=0.0):
 
 
 EXPERTS = [(1, 4, 2, 16, 16), (1, 8, 8, 272, 144), (2, 3, 2, 512, 128), (7, 5, 3, 400, 272), (40, 6, 4, 256, 400),
-           (150, 2, 1, 272, 144), (90, 3, 3, 144, 272)]
+           (150, 2, 1, 272, 144), (90, 3, 3, 144, 272), (500, 2, 1, 144, 272), (420, 1, 1, 400, 144)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
