@@ -736,8 +736,8 @@ int bl_fp8_linear(const uint8_t* q, const float* scales_x, int64_t M, int64_t K,
                       {w, static_cast<size_t>(N) * K},
                       {scales_w, static_cast<size_t>(fp8_blocks(N)) * fp8_blocks(K) * 4}};
   if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
-  return check_launch(launch_fp8_linear(Fp8LinearArgs{q, scales_x, w, scales_w, M, N, K, y, ldy, ydtype},
-                                        static_cast<hipStream_t>(stream)),
+  return check_launch(launch_fp8_linear(Fp8LinearArgs{q, scales_x, w, scales_w, M, N, K, y, ldy, ydtype}, nullptr,
+                                        0, 0, static_cast<hipStream_t>(stream)),
                       "bl_fp8_linear");
 }
 
@@ -762,10 +762,8 @@ int bl_fp8_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, 
   if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
   auto* q = static_cast<uint8_t*>(ws);
   auto* sx = reinterpret_cast<float*>(static_cast<char*>(ws) + L.sx_off);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = launch_fp8_quant_act(x, dtype, M, K, ldx, 0, nullptr, q, sx, s);
-  if (e != hipSuccess) return hip_fail(e, "bl_fp8_forward (quantise)");
-  return check_launch(launch_fp8_linear(Fp8LinearArgs{q, sx, w, scales_w, M, N, K, y, ldy, ydtype}, s),
+  return check_launch(launch_fp8_linear(Fp8LinearArgs{q, sx, w, scales_w, M, N, K, y, ldy, ydtype}, x, dtype, ldx,
+                                        static_cast<hipStream_t>(stream)),
                       "bl_fp8_forward");
 }
 

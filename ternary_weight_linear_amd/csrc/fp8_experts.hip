@@ -82,11 +82,6 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a,
   }
 }
 
-template <int MT>
-void start_product(const ProductArgs& p, int64_t tiles, hipStream_t s) {
-  fp8_stream_kernel<MT><<<dim3(static_cast<uint32_t>((p.a.N + 15) / 16), static_cast<uint32_t>(tiles)), 512, 0, s>>>(p);
-}
-
 }  // namespace
 
 int64_t experts_max_tiles(int64_t P, int64_t E, int tile) { return P / tile + (P < E ? P : E); }
@@ -105,7 +100,7 @@ ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
   w.head_off = take(16);
   w.pair_off = take(P * 4);
   w.tile_off = take(experts_max_tiles(P, E, 16) * 16);
-  w.gu_off = take(P * 2 * I * 4);
+  w.h_off = take(P * I * 4);
   w.hq_off = take(P * I);
   w.hs_off = take(P * IB * 4);
   w.part_off = take(P * H * 4);
@@ -121,7 +116,7 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   auto* head = reinterpret_cast<int32_t*>(ws + L.head_off);
   auto* pair = reinterpret_cast<int32_t*>(ws + L.pair_off);
   auto* tiles = reinterpret_cast<int32_t*>(ws + L.tile_off);
-  auto* gu = reinterpret_cast<float*>(ws + L.gu_off);
+  auto* h = reinterpret_cast<float*>(ws + L.h_off);
   auto* hq = reinterpret_cast<uint8_t*>(ws + L.hq_off);
   auto* hs = reinterpret_cast<float*>(ws + L.hs_off);
   auto* part = reinterpret_cast<float*>(ws + L.part_off);
@@ -134,50 +129,71 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
                      256 * a.I < (int64_t(1) << 31);
   const int tile = !tiled ? (P <= 16 * a.E ? 16 : 64) : P <= 192 * a.E || exact || exact_down ? 128 : 256;
   const int64_t nt = experts_max_tiles(P, a.E, tile);
+  // few slots: a tile each, nothing to sort, and the rows are quantised where they are used
+  constexpr int kStagedMost = 48 * 1024;
+  const bool direct = (4 * P <= a.E || P <= 16) && a.H <= kStagedMost && a.k * a.I <= kStagedMost &&
+                      staged_bytes(1, static_cast<int>(HB)) <= kStagedMost &&
+                      staged_bytes(static_cast<int>(a.k), static_cast<int>(IB)) <= kStagedMost;
 
-  hipError_t e = launch_fp8_quant_act(a.x, a.xdtype, a.M, a.H, a.ldx, 0, nullptr, q, sx, s);
-  if (e != hipSuccess) return e;
+  // gate and up: silu(gate) * up of every sorted row, in fp32 (streamed) or as codes (tiled)
+  StreamArgs up{};
+  up.p.a = Fp8LinearArgs{q, sx, a.wgu, a.sgu, a.M, a.I, a.H, h, a.I, BL_F32, 1};
+  up.p.map = RowMap{tiles, head + 1, direct ? nullptr : pair, static_cast<int>(a.k), 0};
+  up.p.w_stride = 2 * a.I * a.H;
+  up.p.sw_stride = 2 * IB * HB;
+  up.p.hq = hq;
+  up.p.hs = hs;
+  up.p.h_rows = P;
+  up.x = a.x;
+  up.ldx = a.ldx;
+  up.E = static_cast<int>(a.E);
+  up.k = static_cast<int>(a.k);
+  StreamArgs down{};
+  down.p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, BL_F32, 1};
+  down.p.map = RowMap{tiles, head + 1, pair, 0, 1};
+  down.p.w_stride = a.H * a.I;
+  down.p.sw_stride = HB * IB;
+  down.x = h;
+  down.ldx = a.I;
+  down.E = up.E;
+  down.k = up.k;
+  hipError_t e;
+
+  if (direct) {
+    up.index = down.index = a.index;
+    down.weight = a.weight;
+    down.p.a.y = a.y;
+    down.p.a.ydtype = a.ydtype;
+    down.p.a.ldy = a.ldy;
+    down.p.a.vec = vec_rows(a.y, a.ldy, a.ydtype);
+    e = start_stream_x<2, 8, kStreamGated>(up, a.xdtype, P, 1, s);
+    if (e != hipSuccess) return e;
+    return start_stream<1, 1, 8, BL_F32, kStreamSlots>(down, a.M, static_cast<int>(a.k), s);
+  }
+
   experts_sort_kernel<<<1, kSortThreads, static_cast<size_t>(a.E) * 8, s>>>(
       a.index, static_cast<int>(P), static_cast<int>(a.E), tile, head, pair, tiles);
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  e = launch_fp8_quant_act(a.x, a.xdtype, a.M, a.H, a.ldx, 0, nullptr, q, sx, s);
+  if (e != hipSuccess) return e;
   if (tile <= 64) {
-    for (int half = 0; half < 2; ++half) {
-      ProductArgs p{};
-      p.a = Fp8LinearArgs{q, sx, a.wgu + half * a.I * a.H, a.sgu + half * IB * HB, a.M, a.I, a.H, gu + half * a.I, 2 * a.I, BL_F32};
-      p.map = RowMap{tiles, head + 1, pair, static_cast<int>(a.k), 0};
-      p.w_stride = 2 * a.I * a.H;
-      p.sw_stride = 2 * IB * HB;
-      if (tile == 16) start_product<1>(p, nt, s);
-      else start_product<4>(p, nt, s);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    e = launch_fp8_quant_act(gu, BL_F32, P, a.I, 2 * a.I, 1, head, hq, hs, s);
+    e = tile == 16 ? start_stream<1, 4, 8, kSrcCodes, kStreamGated>(up, nt, 0, s)
+                   : start_stream<4, 2, 8, kSrcCodes, kStreamGated>(up, nt, 0, s);
+    if (e != hipSuccess) return e;
+    e = launch_fp8_quant_act(h, BL_F32, P, a.I, a.I, 0, head, hq, hs, s);
+    if (e != hipSuccess) return e;
+    e = tile == 16 ? start_stream<1, 4, 8, kSrcCodes, kStreamLinear>(down, nt, 0, s)
+                   : start_stream<4, 2, 8, kSrcCodes, kStreamLinear>(down, nt, 0, s);
   } else {
-    ProductArgs p{};
-    p.a = Fp8LinearArgs{q, sx, a.wgu, a.sgu, a.M, a.I, a.H, nullptr, 0, BL_F32};
-    p.map = RowMap{tiles, head + 1, pair, static_cast<int>(a.k), 0};
-    p.w_stride = 2 * a.I * a.H;
-    p.sw_stride = 2 * IB * HB;
-    p.hq = hq;
-    p.hs = hs;
-    p.h_rows = P;
-    e = exact         ? start_gemm<GemmShape<256, 128, 2, 4, true, true>>(p, nt, s)
-        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, false, true>>(p, nt, s)
-                      : start_gemm<GemmShape<256, 256, 2, 4, false, true>>(p, nt, s);
+    e = exact         ? start_gemm<GemmShape<256, 128, 2, 4, true, true>>(up.p, nt, s)
+        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, false, true>>(up.p, nt, s)
+                      : start_gemm<GemmShape<256, 256, 2, 4, false, true>>(up.p, nt, s);
+    if (e != hipSuccess) return e;
+    e = exact_down    ? start_gemm<GemmShape<256, 128, 2, 4, true>>(down.p, nt, s)
+        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, false>>(down.p, nt, s)
+                      : start_gemm<GemmShape<256, 256, 2, 4, false>>(down.p, nt, s);
   }
   if (e != hipSuccess) return e;
-  ProductArgs p{};
-  p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, BL_F32};
-  p.map = RowMap{tiles, head + 1, pair, 0, 1};
-  p.w_stride = a.H * a.I;
-  p.sw_stride = HB * IB;
-  if (tile == 16) start_product<1>(p, nt, s);
-  else if (tile == 64) start_product<4>(p, nt, s);
-  else
-    e = exact_down    ? start_gemm<GemmShape<256, 128, 2, 4, true>>(p, nt, s)
-        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, false>>(p, nt, s)
-                      : start_gemm<GemmShape<256, 256, 2, 4, false>>(p, nt, s);
-  if (e != hipSuccess || (e = hipGetLastError()) != hipSuccess) return e;
   const uint32_t cols = static_cast<uint32_t>((a.H + 255) / 256);
   experts_combine_kernel<<<dim3(static_cast<uint32_t>(a.M), cols < 16 ? cols : 16), 256, 0, s>>>(a, part);
   return hipGetLastError();

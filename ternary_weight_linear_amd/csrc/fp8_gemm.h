@@ -271,12 +271,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     int64_t at = first + r;
     if (p.map.scatter) at = p.map.pair[at];
 #pragma unroll
-    for (int i = 0; i < S::TN; ++i) {
-      const int64_t n = n0 + wn + 16 * i + 4 * g;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < a.N) store_as(a.y, a.ydtype, at * a.ldy + n + e, acc[i][j][e]);
-    }
+    for (int i = 0; i < S::TN; ++i) store4(a, at, n0 + wn + 16 * i + 4 * g, acc[i][j]);
   }
 }
 

@@ -27,7 +27,12 @@ struct Fp8LinearArgs {
   void* y;               // [M, N], rows ldy elements apart
   int64_t ldy;
   int ydtype;
+  int vec = 0;           // four consecutive values of y can be written at once
 };
+// Whether rows ldy apart at y take aligned stores of four values.
+inline int vec_rows(const void* y, int64_t ldy, int dtype) {
+  return ldy % 4 == 0 && reinterpret_cast<uintptr_t>(y) % (4 * dtype_bytes(dtype)) == 0;
+}
 
 struct Fp8ExpertsArgs {
   const void* x;         // [M, H], rows ldx elements apart
@@ -65,7 +70,7 @@ struct ExpertsWs {
   size_t head_off;             // int32 [4]: rows used, tiles
   size_t pair_off;             // int32 [P] slot m * k + j of each sorted row
   size_t tile_off;             // int32 [tiles, 4]: expert, first row, rows
-  size_t gu_off;               // fp32 [P, 2 I] gate and up products
+  size_t h_off;                // fp32 [P, I] silu(gate) * up, where it is not quantised at once
   size_t hq_off, hs_off;       // quantised silu(gate) * up: codes [P, I], scales [IB, P]
   size_t part_off;             // fp32 [P, H] the experts' outputs before the weighted sum
   size_t total;
@@ -78,7 +83,8 @@ hipError_t launch_fp8_quant_act(const void* x, int dtype, int64_t M, int64_t K, 
                                 hipStream_t s);
 hipError_t launch_fp8_quant_weight(const float* W, int64_t N, int64_t K, uint8_t* codes,
                                    float* scale, hipStream_t s);
-hipError_t launch_fp8_linear(const Fp8LinearArgs& a, hipStream_t s);
+// a.q and a.sx are scratch when x is given: they are filled from it where the product takes codes.
+hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const void* x, int xdtype, int64_t ldx, hipStream_t s);
 hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s);
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 
@@ -105,10 +111,14 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
+__device__ __forceinline__ uint16_t half_bits(float v) {
+  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+}
+
 __device__ __forceinline__ void store_as(void* y, int dtype, int64_t at, float v) {
   if (dtype == BL_F32) static_cast<float*>(y)[at] = v;
   else if (dtype == BL_BF16) static_cast<uint16_t*>(y)[at] = bf16_bits(v);
-  else static_cast<uint16_t*>(y)[at] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+  else static_cast<uint16_t*>(y)[at] = half_bits(v);
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }

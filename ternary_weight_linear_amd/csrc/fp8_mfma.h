@@ -94,18 +94,122 @@ struct ProductArgs {
   int64_t h_rows;
 };
 
-// One workgroup of eight waves: 16 rows of w by 16 MT rows of q; wave v takes blocks v, v + 8,
-// ..., and the eight sums meet in LDS in the order of the waves.
-template <int MT>
-__global__ __launch_bounds__(512) void fp8_stream_kernel(ProductArgs p) {
-  __shared__ f32x4 red[7][MT][64];
+// Four consecutive outputs of a row, in one store where y's rows allow it (a.vec).
+__device__ __forceinline__ void store4(const Fp8LinearArgs& a, int64_t row, int64_t n, const f32x4& v) {
+  const int64_t at = row * a.ldy + n;
+  if (a.vec && n + 3 < a.N) {
+    if (a.ydtype == BL_F32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = v;
+    } else {
+      u32x2 b;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = a.ydtype == BL_BF16 ? bf16_bits(v[2 * i]) : half_bits(v[2 * i]);
+        const uint32_t hi = a.ydtype == BL_BF16 ? bf16_bits(v[2 * i + 1]) : half_bits(v[2 * i + 1]);
+        b[i] = lo | hi << 16;
+      }
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = b;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.N) store_as(a.y, a.ydtype, at + e, v[e]);
+  }
+}
+
+// Source of a streaming product's activations: e4m3 codes with their scales in memory, or
+// values of a bl_dtype that each workgroup quantises into LDS first.
+constexpr int kSrcCodes = -1;
+// What the streaming kernel computes.
+constexpr int kStreamLinear = 0;   // rows of q times w
+constexpr int kStreamGated = 1;    // NT / 2 gate and NT / 2 up fragments: silu(gate) * up
+constexpr int kStreamSlots = 2;    // one token's weighted sum over its slots (x is [M k, K])
+
+struct StreamArgs {
+  ProductArgs p;
+  const void* x;           // SRC >= 0: values, rows ldx apart
+  int64_t ldx;
+  const int32_t* index;    // direct tiles: tile t is slot t, its expert index[t]; null: as p.map says
+  const float* weight;     // kStreamSlots
+  int E, k;
+};
+
+constexpr int kStreamWaves = 8;
+constexpr int kStreamThreads = 64 * kStreamWaves;
+
+// LDS bytes of `rows` quantised rows: codes (rows 64 bytes past a multiple of 128, so that
+// they start in different banks), then scales.
+__host__ __device__ inline int staged_row(int KB) { return KB * kFp8Block + 64; }
+__host__ __device__ inline int staged_bytes(int rows, int KB) { return rows * (staged_row(KB) + 4 * KB); }
+
+// Eight consecutive values of a bl_dtype at p (16-byte aligned).
+template <int DT>
+__device__ __forceinline__ void load8(const typename Elem<DT>::type* p, float (&v)[8]) {
+  if constexpr (DT == BL_F32) {
+    const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = a[j];
+      v[4 + j] = b[j];
+    }
+  } else {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = to_float<DT>(static_cast<uint16_t>(a[j] & 0xFFFFu));
+      v[2 * j + 1] = to_float<DT>(static_cast<uint16_t>(a[j] >> 16));
+    }
+  }
+}
+
+// The maximum of |v| over the 16 lanes of a block, as bits, at least the floor.
+__device__ __forceinline__ uint32_t block_top(const float (&v)[8]) {
+  uint32_t a = kFp8FloorBits;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[i]));
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), off)));
+  return a;
+}
+
+__device__ __forceinline__ u32x2 pack8(const float (&v)[8], float r) {
+  return u32x2{pack4(f32x4{v[0], v[1], v[2], v[3]}, r), pack4(f32x4{v[4], v[5], v[6], v[7]}, r)};
+}
+
+// Streaming product for few rows: the weights are read once, straight into registers, and
+// decide the time. A workgroup of eight waves is S ranges of K by 8 / S groups of 16 NT weight
+// rows; range r takes blocks r, r + S, ..., so the workgroup reads the next 128 S codes of each
+// row together, and the ranges meet in LDS in order. The loads of several waves per SIMD hide
+// each other's latency: keeping a second block's loads in flight per wave measured slower in
+// every shape (more registers, a block too many read at the end). Workgroups start at different
+// blocks (rot): weight rows are usually a power of two apart, and all workgroups at the same
+// input would meet in a few of the memory's channels.
+// Measured, us (weight bytes / time): 1 x 8192 x 8192 12.3 (5.4 TB/s), 16 x 8192 x 8192 14.2,
+// 16 x 28672 x 8192 43.8 (5.4 TB/s), 1 x 28672 x 8192 39.6 (5.9 TB/s).
+template <int MT, int NT, int S, int SRC, int MODE>
+__global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s) {
+  constexpr bool GATED = MODE == kStreamGated;
+  constexpr int G = kStreamWaves / S;               // groups of weight rows
+  constexpr int NC = GATED ? NT / 2 : NT;           // fragments of output columns of a group
+  __shared__ f32x4 red[S][G * NT * MT][64];
+  extern __shared__ __attribute__((aligned(16))) uint8_t staged[];
+  const ProductArgs& p = s.p;
   const Fp8LinearArgs& a = p.a;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, u = lane & 15;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int range = wave % S, group = wave / S;
+  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * G + group) * (16 * NC);
   int64_t first = static_cast<int64_t>(blockIdx.y) * (16 * MT);
   int rows = 0, expert = 0;
-  if (p.map.tiles) {
+  if constexpr (MODE == kStreamSlots) {
+    first = static_cast<int64_t>(blockIdx.y) * s.k;
+    rows = 1;
+  } else if (s.index) {
+    first = blockIdx.y;
+    rows = 1;
+    expert = s.index[first];
+    if (expert < 0 || expert >= s.E) return;
+  } else if (p.map.tiles) {
     if (static_cast<int>(blockIdx.y) >= *p.map.n_tiles) return;
     expert = p.map.tiles[4 * blockIdx.y];
     first = p.map.tiles[4 * blockIdx.y + 1];
@@ -113,47 +217,184 @@ __global__ __launch_bounds__(512) void fp8_stream_kernel(ProductArgs p) {
   } else {
     rows = static_cast<int>(a.M - first < 16 * MT ? a.M - first : 16 * MT);
   }
-  const int64_t KB = (a.K + kFp8Block - 1) / kFp8Block;
-  const int64_t n = n0 + u < a.N ? n0 + u : a.N - 1;
-  const uint8_t* wrow = a.w + expert * p.w_stride + n * a.K;
-  const float* sw = a.sw + expert * p.sw_stride + (n0 / kFp8Block) * KB;
-  const uint8_t* qrow[MT];
-  int64_t srow[MT];
+  const int KB = static_cast<int>((a.K + kFp8Block - 1) / kFp8Block);
+  const int64_t scale_rows = (a.N + kFp8Block - 1) / kFp8Block * KB;
+  const uint8_t* wrow[NT];
+  const float* sw[NT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int r = 16 * t + u < rows ? 16 * t + u : rows - 1;
-    int64_t at = first + r;
-    if (p.map.gather_div > 0) at = p.map.pair[at] / p.map.gather_div;
-    srow[t] = at;
-    qrow[t] = a.q + at * a.K;
+  for (int i = 0; i < NT; ++i) {
+    const int64_t c = n0 + 16 * (i % NC);
+    const int64_t n = (c + u < a.N ? c + u : a.N - 1) + (i >= NC ? a.N : 0);
+    wrow[i] = a.w + expert * p.w_stride + n * a.K;
+    sw[i] = a.sw + expert * p.sw_stride + (i >= NC ? scale_rows : 0) +
+            (c < a.N ? c : a.N - 1) / kFp8Block * KB;
   }
-  f32x4 acc[MT] = {};
-  for (int64_t kb = wave; kb < KB; kb += 8) {
-    const FragH w = to_half(load_frag(wrow, kb * kFp8Block, a.K, g));
-    const float s = sw[kb];
+  const uint8_t* qrow[MT];
+  const float* srow[MT];
+  if constexpr (SRC == kSrcCodes) {
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const FragH q = to_half(load_frag(qrow[t], kb * kFp8Block, a.K, g));
-      const float f = a.sx[kb * a.M + srow[t]] * s;
-      acc[t] += block_dot(w, q) * f;
+      int64_t at = first + (16 * t + u < rows ? 16 * t + u : rows - 1);
+      if (p.map.gather_div > 0) at = p.map.pair[at] / p.map.gather_div;
+      qrow[t] = a.q + at * a.K;
+      srow[t] = a.sx + at;
     }
   }
-  if (wave > 0) {
+
+  struct Stage {
+    Frag w[NT], q[MT];
+    float sw[NT], sx[MT];
+    int kb, row;           // staged rows: which block of which
+    bool some;
+  };
+  // kStreamSlots: item it is block it % KB of slot it / KB; a slot that names no expert is read
+  // at expert 0 (in bounds) and left out of the sum
+  const int items = MODE == kStreamSlots ? s.k * KB : KB;
+  const int rot = MODE == kStreamSlots ? 0 : static_cast<int>(blockIdx.x % KB);
+  auto load = [&](Stage& st, int it) __attribute__((always_inline)) {
+    int kb = it + rot < KB || MODE == kStreamSlots ? it + rot : it + rot - KB;
+    int64_t wo = 0, so = 0;
+    float weigh = 1.0f;
+    st.row = 0;
+    if constexpr (MODE == kStreamSlots) {
+      st.row = it / KB;
+      kb = it - st.row * KB;
+      int e = s.index[first + st.row];
+      st.some = e >= 0 && e < s.E;
+      weigh = s.weight[first + st.row];
+      e = st.some ? e : 0;
+      wo = e * p.w_stride;
+      so = e * p.sw_stride;
+    }
+    st.kb = kb;
+    const int64_t k0 = static_cast<int64_t>(kb) * kFp8Block;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) red[wave - 1][t][lane] = acc[t];
+    for (int i = 0; i < NT; ++i) {
+      st.w[i] = load_frag(wrow[i] + wo, k0, a.K, g);
+      st.sw[i] = sw[i][so + kb] * weigh;
+    }
+    if constexpr (SRC == kSrcCodes) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        st.q[t] = load_frag(qrow[t], k0, a.K, g);
+        st.sx[t] = srow[t][kb * a.M];
+      }
+    }
+  };
+  f32x4 acc[NT][MT] = {};
+  const int staged_rows = MODE == kStreamSlots ? s.k : rows;
+  const auto* staged_scale = reinterpret_cast<const float*>(staged + staged_rows * staged_row(KB));
+  auto multiply = [&](const Stage& st) __attribute__((always_inline)) {
+    if constexpr (MODE == kStreamSlots) {
+      if (!st.some) return;
+    }
+    FragH q[MT];
+    float sx[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      if constexpr (SRC == kSrcCodes) {
+        q[t] = to_half(st.q[t]);
+        sx[t] = st.sx[t];
+      } else {
+        const int r = MODE == kStreamSlots ? st.row : min(u, rows - 1);
+        const uint8_t* at = staged + r * staged_row(KB) + st.kb * kFp8Block + 16 * g;
+        q[t] = to_half(Frag{*reinterpret_cast<const u32x4*>(at), *reinterpret_cast<const u32x4*>(at + 64)});
+        sx[t] = staged_scale[r * KB + st.kb];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const FragH w = to_half(st.w[i]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[i][t] += block_dot(w, q[t]) * (sx[t] * st.sw[i]);
+    }
+  };
+
+  Stage st;
+  if constexpr (SRC != kSrcCodes) {
+    // 16 lanes per block of 128 values, as in fp8_quant_act_kernel; the first pass's loads go
+    // out before the first weights', so that waiting for them does not wait for those
+    const int blocks = staged_rows * KB;
+    using T = typename Elem<SRC == kSrcCodes ? 0 : SRC>::type;
+    float v[8];
+    auto fetch = [&](int b) __attribute__((always_inline)) {
+      const int r = b / KB, k = (b - r * KB) * kFp8Block + (threadIdx.x & 15) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      int64_t at = first + r;
+      if (MODE != kStreamSlots && p.map.gather_div > 0) at /= p.map.gather_div;
+      if (b < blocks && k < a.K) load8<SRC == kSrcCodes ? 0 : SRC>(static_cast<const T*>(s.x) + at * s.ldx + k, v);
+    };
+    auto put = [&](int b) __attribute__((always_inline)) {
+      const float am = __uint_as_float(block_top(v));
+      if (b >= blocks) return;
+      const int r = b / KB, kb = b - r * KB;
+      *reinterpret_cast<u32x2*>(staged + r * staged_row(KB) + kb * kFp8Block + (threadIdx.x & 15) * 8) =
+          pack8(v, code_factor(am));
+      if ((threadIdx.x & 15) == 0) const_cast<float*>(staged_scale)[b] = am / kFp8Max;
+    };
+    constexpr int step = kStreamThreads / 16;
+    const int b0 = threadIdx.x >> 4;
+    fetch(b0);
+    load(st, min(range, items - 1));
+    put(b0);
+    for (int b = b0 + step; b - b0 < blocks; b += step) {
+      fetch(b);
+      put(b);
+    }
+    __syncthreads();
+  } else {
+    load(st, min(range, items - 1));
   }
-  __syncthreads();
-  if (wave > 0) return;
+  for (int it = range; it < items; it += S) {
+    if (it > range) load(st, it);
+    multiply(st);
+  }
+
+  auto finish = [&](int64_t n, int t, f32x4 r, const f32x4& up) __attribute__((always_inline)) {
+    if constexpr (GATED) {
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    for (int v = 0; v < 7; ++v) acc[t] += red[v][t][lane];
-    if (16 * t + u >= rows) continue;
+      for (int e = 0; e < 4; ++e) r[e] = silu_mul(r[e], up[e]);
+    }
+    if (16 * t + u >= rows) return;
     int64_t at = first + 16 * t + u;
-    if (p.map.scatter) at = p.map.pair[at];
+    if constexpr (MODE == kStreamSlots) at = blockIdx.y;
+    else if (p.map.scatter) at = p.map.pair[at];
+    store4(a, at, n + 4 * g, r);
+  };
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n0 + 4 * g + i < a.N) store_as(a.y, a.ydtype, at * a.ldy + n0 + 4 * g + i, acc[t][i]);
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) red[range][(group * NT + i) * MT + t][lane] = acc[i][t];
+  __syncthreads();
+  // wave v finishes the workgroup's output fragments v, v + 8, ...
+  for (int f = wave; f < G * NC * MT; f += kStreamWaves) {
+    const int t = f % MT, i = f / MT % NC, gr = f / (MT * NC);
+    auto total = [&](int n) __attribute__((always_inline)) {
+      f32x4 sum = red[0][(gr * NT + n) * MT + t][lane];
+#pragma unroll
+      for (int v = 1; v < S; ++v) sum += red[v][(gr * NT + n) * MT + t][lane];
+      return sum;
+    };
+    const f32x4 r = total(i);
+    finish((static_cast<int64_t>(blockIdx.x) * G + gr) * (16 * NC) + 16 * i, t, r, GATED ? total(i + NC) : r);
   }
+}
+
+// Starts the kernel over the columns of w and `tiles` tiles of rows; staged: rows to quantise.
+template <int MT, int NT, int S, int SRC, int MODE>
+hipError_t start_stream(const StreamArgs& st, int64_t tiles, int staged, hipStream_t s) {
+  constexpr int cols = 16 * NT * (kStreamWaves / S) / (MODE == kStreamGated ? 2 : 1);
+  const int lds = SRC == kSrcCodes ? 0 : staged_bytes(staged, static_cast<int>(fp8_blocks(st.p.a.K)));
+  const dim3 grid(static_cast<uint32_t>((st.p.a.N + cols - 1) / cols), static_cast<uint32_t>(tiles));
+  fp8_stream_kernel<MT, NT, S, SRC, MODE><<<grid, kStreamThreads, lds, s>>>(st);
+  return hipGetLastError();
+}
+template <int NT, int S, int MODE>
+hipError_t start_stream_x(const StreamArgs& st, int xdtype, int64_t tiles, int staged, hipStream_t s) {
+  return xdtype == BL_F16    ? start_stream<1, NT, S, BL_F16, MODE>(st, tiles, staged, s)
+         : xdtype == BL_BF16 ? start_stream<1, NT, S, BL_BF16, MODE>(st, tiles, staged, s)
+                             : start_stream<1, NT, S, BL_F32, MODE>(st, tiles, staged, s);
 }
 
 }  // namespace

@@ -8,37 +8,10 @@
 // a > 2^126, and still right to 21 bits). The
 // maximum is taken over the bit patterns of |v| as unsigned integers: there NaN > inf > every
 // finite value, so a block that holds NaN gets scale NaN and NaN codes.
-#include "fp8_internal.h"
+#include "fp8_mfma.h"
 
 namespace bl {
 namespace {
-
-// Eight consecutive values at p (16-byte aligned).
-template <int DT>
-__device__ __forceinline__ void load8(const typename Elem<DT>::type* p, float (&v)[8]) {
-  if constexpr (DT == BL_F32) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = to_float<DT>(static_cast<uint16_t>(w[j] & 0xFFFFu));
-      v[2 * j + 1] = to_float<DT>(static_cast<uint16_t>(w[j] >> 16));
-    }
-  }
-}
-
-__device__ __forceinline__ uint2 pack8(const float (&v)[8], float r) {
-  int lo = 0, hi = 0;
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * r, v[1] * r, lo, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * r, v[3] * r, lo, true);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * r, v[5] * r, hi, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * r, v[7] * r, hi, true);
-  return make_uint2(static_cast<uint32_t>(lo), static_cast<uint32_t>(hi));
-}
 
 // Sixteen lanes per block of 128, eight values each: one 16-byte load per lane, a maximum over
 // the sixteen lanes, one 8-byte store. The block index runs over inputs first.
@@ -61,13 +34,8 @@ __global__ __launch_bounds__(256) void fp8_quant_act_kernel(
       for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], u[i]);
     }
   }
-  uint32_t a = kFp8FloorBits;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[i]));
-#pragma unroll
-  for (int off = 8; off > 0; off >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), off)));
-  const float am = __uint_as_float(a);
-  if (k < K) *reinterpret_cast<uint2*>(q + m * K + k) = pack8(v, code_factor(am));
+  const float am = __uint_as_float(block_top(v));
+  if (k < K) *reinterpret_cast<u32x2*>(q + m * K + k) = pack8(v, code_factor(am));
   if (j == 0) scale[kb * M + m] = am / kFp8Max;
 }
 
@@ -100,7 +68,7 @@ __global__ __launch_bounds__(256) void fp8_quant_weight_kernel(const float* __re
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t n = nb * kFp8Block + r + 16 * i;
-    if (n < N && k < K) *reinterpret_cast<uint2*>(codes + n * K + k) = pack8(v[i], rcp);
+    if (n < N && k < K) *reinterpret_cast<u32x2*>(codes + n * K + k) = pack8(v[i], rcp);
   }
   if (threadIdx.x == 0) scale[nb * KB + kb] = am / kFp8Max;
 }
