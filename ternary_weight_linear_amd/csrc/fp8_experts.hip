@@ -6,79 +6,174 @@
 namespace bl {
 namespace {
 
-constexpr int kSortThreads = 1024;
+constexpr int kSortThreads = 256;
 
-// One workgroup: counts per expert, their running sum, the sorted rows and the tiles of at
-// most `tile` rows. Slots whose index is outside [0, E) get no row. The order of the rows
-// within an expert may differ from run to run; no output depends on it, since each row is
-// multiplied by itself.
-__global__ __launch_bounds__(kSortThreads) void experts_sort_kernel(
-    const int32_t* __restrict__ index, int P, int E, int tile, int32_t* __restrict__ head,
-    int32_t* __restrict__ pair, int32_t* __restrict__ tiles) {
-  extern __shared__ int cnt[];              // [E] counts, then [E] next positions
-  __shared__ int scan[2][kSortThreads];
-  int* next = cnt + E;
-  for (int e = threadIdx.x; e < E; e += kSortThreads) cnt[e] = 0;
+// The sort of the slots by expert. A chunk of slots per workgroup: each counts its chunk's
+// slots per expert, and where there is more than one chunk, a second launch (which needs all
+// counts) places them. Slots whose index is outside [0, E) get no row. The order of the rows of
+// one expert within a chunk may differ from run to run; no output depends on it, since each
+// row is multiplied by itself.
+struct SortArgs {
+  const int32_t* index;
+  int P, E, chunk, chunks, tile;
+  int32_t* head;      // [2] rows used, tiles
+  int32_t* pair;      // [P] slot of each sorted row
+  int32_t* tiles;     // [tiles, 4] expert, first row, rows
+  int32_t* counts;    // [chunks, E], more than one chunk
+};
+inline int sort_chunk(int64_t P) { return static_cast<int>(P <= 2048 * 64 ? 2048 : (P + 63) / 64); }
+inline int sort_lds(int64_t E) { return static_cast<int>(E) * 8; }
+
+__device__ __forceinline__ void count_slots(const SortArgs& a, int chunk, int* cnt) {
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) cnt[e] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < P; i += kSortThreads) {
-    const int e = index[i];
-    if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+  const int end = min((chunk + 1) * a.chunk, a.P);
+  for (int i = chunk * a.chunk + threadIdx.x; i < end; i += kSortThreads) {
+    const int e = a.index[i];
+    if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
-  // each thread sums its run of experts, then a scan over the threads
-  const int per = (E + kSortThreads - 1) / kSortThreads;
-  const int e0 = threadIdx.x * per;
+}
+
+// From all slots per expert (cnt) and those of earlier chunks (next): the rows of this chunk's
+// slots, and from chunk 0 the tiles. Each thread has a run of experts; runs are summed by a
+// scan over the workgroup.
+__device__ __forceinline__ void place_slots(const SortArgs& a, int chunk, const int* cnt, int* next) {
+  __shared__ int sums[2][kSortThreads / 64];
+  const int per = (a.E + kSortThreads - 1) / kSortThreads;
+  const int e0 = threadIdx.x * per, e1 = min(e0 + per, a.E);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int rows = 0, nt = 0;
-  for (int e = e0; e < min(e0 + per, E); ++e) {
+  for (int e = e0; e < e1; ++e) {
     rows += cnt[e];
-    nt += (cnt[e] + tile - 1) / tile;
+    nt += (cnt[e] + a.tile - 1) / a.tile;
   }
-  scan[0][threadIdx.x] = rows;
-  scan[1][threadIdx.x] = nt;
+  int row = rows, at = nt;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int r = __shfl_up(row, off), t = __shfl_up(at, off);
+    if (lane >= off) {
+      row += r;
+      at += t;
+    }
+  }
+  if (lane == 63) {
+    sums[0][wave] = row;
+    sums[1][wave] = at;
+  }
   __syncthreads();
-  for (int off = 1; off < kSortThreads; off <<= 1) {
-    int r = 0, t = 0;
-    if (static_cast<int>(threadIdx.x) >= off) {
-      r = scan[0][threadIdx.x - off];
-      t = scan[1][threadIdx.x - off];
-    }
-    __syncthreads();
-    scan[0][threadIdx.x] += r;
-    scan[1][threadIdx.x] += t;
-    __syncthreads();
+  for (int v = 0; v < wave; ++v) {
+    row += sums[0][v];
+    at += sums[1][v];
   }
-  int row = scan[0][threadIdx.x] - rows, at = scan[1][threadIdx.x] - nt;
-  for (int e = e0; e < min(e0 + per, E); ++e) {
-    next[e] = row;
-    for (int r = 0; r < cnt[e]; r += tile, ++at) {
-      tiles[4 * at] = e;
-      tiles[4 * at + 1] = row + r;
-      tiles[4 * at + 2] = min(tile, cnt[e] - r);
-    }
+  if (chunk == 0 && threadIdx.x == kSortThreads - 1) {
+    a.head[0] = row;
+    a.head[1] = at;
+  }
+  row -= rows;
+  at -= nt;
+  for (int e = e0; e < e1; ++e) {
+    next[e] += row;
+    if (chunk == 0)
+      for (int r = 0; r < cnt[e]; r += a.tile, ++at) {
+        a.tiles[4 * at] = e;
+        a.tiles[4 * at + 1] = row + r;
+        a.tiles[4 * at + 2] = min(a.tile, cnt[e] - r);
+      }
     row += cnt[e];
   }
-  if (threadIdx.x == kSortThreads - 1) {
-    head[0] = scan[0][threadIdx.x];
-    head[1] = scan[1][threadIdx.x];
-  }
   __syncthreads();
-  for (int i = threadIdx.x; i < P; i += kSortThreads) {
-    const int e = index[i];
-    if (e >= 0 && e < E) pair[atomicAdd(&next[e], 1)] = i;
+  const int end = min((chunk + 1) * a.chunk, a.P);
+  for (int i = chunk * a.chunk + threadIdx.x; i < end; i += kSortThreads) {
+    const int e = a.index[i];
+    if (e >= 0 && e < a.E) a.pair[atomicAdd(&next[e], 1)] = i;
   }
 }
 
-// y[m, n] = sum_j weight[m, j] part[m k + j, n], slots in their order.
-__global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a,
-                                                              const float* __restrict__ part) {
-  const int64_t m = blockIdx.x;
-  for (int64_t n = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x; n < a.H; n += 256 * gridDim.y) {
-    float sum = 0.0f;
-    for (int64_t j = 0; j < a.k; ++j) {
-      const int e = a.index[m * a.k + j];
-      if (e >= 0 && e < a.E) sum += a.weight[m * a.k + j] * part[(m * a.k + j) * a.H + n];
+// One launch for what needs only the inputs: the first workgroups sort (or count) the slots,
+// the others quantise x.
+template <int DT>
+__global__ __launch_bounds__(kSortThreads) void experts_prepare_kernel(SortArgs a, QuantArgs q) {
+  extern __shared__ int lds[];                     // [2, E]
+  const int chunk = blockIdx.x;
+  if (chunk >= a.chunks) {
+    quant_blocks<DT, false>(q, static_cast<int64_t>(chunk - a.chunks) * (kSortThreads / 16));
+    return;
+  }
+  int *cnt = lds, *next = lds + a.E;
+  count_slots(a, chunk, cnt);
+  if (a.chunks == 1) {
+    for (int e = threadIdx.x; e < a.E; e += kSortThreads) next[e] = 0;
+    __syncthreads();
+    place_slots(a, 0, cnt, next);
+  } else {
+    for (int e = threadIdx.x; e < a.E; e += kSortThreads) a.counts[chunk * a.E + e] = cnt[e];
+  }
+}
+
+__global__ __launch_bounds__(kSortThreads) void experts_place_kernel(SortArgs a) {
+  extern __shared__ int lds[];                     // [2, E]
+  const int chunk = blockIdx.x;
+  int *cnt = lds, *next = lds + a.E;
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+    int all = 0, before = 0;
+    for (int c = 0; c < a.chunks; ++c) {
+      const int n = a.counts[c * a.E + e];
+      all += n;
+      before += c < chunk ? n : 0;
     }
-    store_as(a.y, a.ydtype, m * a.ldy + n, sum);
+    cnt[e] = all;
+    next[e] = before;
+  }
+  __syncthreads();
+  place_slots(a, chunk, cnt, next);
+}
+
+// y[m, n] = sum_j weight[m, j] part[m k + j, n], slots in their order. A thread has V columns
+// (16 bytes) and up to eight slots' loads in flight: reading the parts bounds it (32768 x 4096
+// fp16: 65 us).
+template <bool HALF>
+__global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, const void* __restrict__ part,
+                                                              const float* __restrict__ scale, int vec) {
+  constexpr int V = HALF ? 8 : 4;
+  const int64_t m = blockIdx.x, P = a.M * a.k;
+  const int64_t n = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * V;
+  if (n >= a.H) return;                             // H % 16 == 0: all V or none
+  float sum[V] = {};
+  for (int64_t j0 = 0; j0 < a.k; j0 += 8) {
+    u32x4 v[8];
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t slot = m * a.k + j0 + j;
+      const int e = j0 + j < a.k ? a.index[slot] : -1;
+      w[j] = 0.0f;
+      v[j] = u32x4{0, 0, 0, 0};
+      if (e >= 0 && e < a.E) {
+        w[j] = a.weight[slot];
+        if constexpr (HALF) w[j] *= scale[(n / kFp8Block) * P + slot];
+        v[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(part) + (slot * a.H + n) * (HALF ? 2 : 4));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float x;
+        if constexpr (HALF) x = to_float<BL_F16>(static_cast<uint16_t>(v[j][i / 2] >> (16 * (i & 1))));
+        else x = __uint_as_float(v[j][i]);
+        sum[i] += w[j] * x;
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    Fp8LinearArgs o{};
+    o.N = a.H;
+    o.y = a.y;
+    o.ldy = a.ldy;
+    o.ydtype = a.ydtype;
+    o.vec = vec;
+    store4(o, m, n + i, f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]});
   }
 }
 
@@ -100,10 +195,12 @@ ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
   w.head_off = take(16);
   w.pair_off = take(P * 4);
   w.tile_off = take(experts_max_tiles(P, E, 16) * 16);
+  w.count_off = take((P + sort_chunk(P) - 1) / sort_chunk(P) * E * 4);
   w.h_off = take(P * I * 4);
   w.hq_off = take(P * I);
   w.hs_off = take(P * IB * 4);
   w.part_off = take(P * H * 4);
+  w.ps_off = take(P * HB * 4);
   w.total = off;
   return w;
 }
@@ -149,7 +246,13 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   up.E = static_cast<int>(a.E);
   up.k = static_cast<int>(a.k);
   StreamArgs down{};
-  down.p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, BL_F32, 1};
+  // The experts' outputs wait for their sum in fp32, or, for results in bf16, as fp16 with a
+  // power-of-two scale per row and 128 columns (its rounding is 1/8 of the result's own): half
+  // the bytes to write and read back.
+  const bool half_parts = tile >= 128 && a.ydtype == BL_BF16;
+  auto* part_scale = reinterpret_cast<float*>(ws + L.ps_off);
+  down.p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, half_parts ? kPartType : BL_F32, 1, 1};
+  down.p.part_scale = part_scale;
   down.p.map = RowMap{tiles, head + 1, pair, 0, 1};
   down.p.w_stride = a.H * a.I;
   down.p.sw_stride = HB * IB;
@@ -171,11 +274,19 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
     return start_stream<1, 1, 8, BL_F32, kStreamSlots>(down, a.M, static_cast<int>(a.k), s);
   }
 
-  experts_sort_kernel<<<1, kSortThreads, static_cast<size_t>(a.E) * 8, s>>>(
-      a.index, static_cast<int>(P), static_cast<int>(a.E), tile, head, pair, tiles);
+  SortArgs sort{a.index, static_cast<int>(P), static_cast<int>(a.E), sort_chunk(P), 0, tile, head, pair, tiles,
+                reinterpret_cast<int32_t*>(ws + L.count_off)};
+  sort.chunks = static_cast<int>((P + sort.chunk - 1) / sort.chunk);
+  const QuantArgs quant{a.x, a.M, a.H, HB, a.ldx, nullptr, q, sx};
+  const dim3 prepare(static_cast<uint32_t>(sort.chunks + (a.M * HB + 15) / 16));
+  if (a.xdtype == BL_F16) experts_prepare_kernel<BL_F16><<<prepare, kSortThreads, sort_lds(a.E), s>>>(sort, quant);
+  else if (a.xdtype == BL_BF16) experts_prepare_kernel<BL_BF16><<<prepare, kSortThreads, sort_lds(a.E), s>>>(sort, quant);
+  else experts_prepare_kernel<BL_F32><<<prepare, kSortThreads, sort_lds(a.E), s>>>(sort, quant);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  e = launch_fp8_quant_act(a.x, a.xdtype, a.M, a.H, a.ldx, 0, nullptr, q, sx, s);
-  if (e != hipSuccess) return e;
+  if (sort.chunks > 1) {
+    experts_place_kernel<<<sort.chunks, kSortThreads, sort_lds(a.E), s>>>(sort);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   if (tile <= 64) {
     e = tile == 16 ? start_stream<1, 4, 8, kSrcCodes, kStreamGated>(up, nt, 0, s)
                    : start_stream<4, 2, 8, kSrcCodes, kStreamGated>(up, nt, 0, s);
@@ -194,8 +305,11 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
                       : start_gemm<GemmShape<256, 256, 2, 4, false>>(down.p, nt, s);
   }
   if (e != hipSuccess) return e;
-  const uint32_t cols = static_cast<uint32_t>((a.H + 255) / 256);
-  experts_combine_kernel<<<dim3(static_cast<uint32_t>(a.M), cols < 16 ? cols : 16), 256, 0, s>>>(a, part);
+  const int vec = vec_rows(a.y, a.ldy, a.ydtype);
+  const uint32_t per = half_parts ? 2048 : 1024;
+  const dim3 grid(static_cast<uint32_t>(a.M), static_cast<uint32_t>((a.H + per - 1) / per));
+  if (half_parts) experts_combine_kernel<true><<<grid, 256, 0, s>>>(a, part, part_scale, vec);
+  else experts_combine_kernel<false><<<grid, 256, 0, s>>>(a, part, nullptr, vec);
   return hipGetLastError();
 }
 

@@ -33,6 +33,7 @@ struct GemmShape {
   // A tile of w is BN / 2 gate rows and the BN / 2 up rows of the same channels, and the tile's
   // result is quantised silu(gate) * up. Each wave holds both rows of its channels.
   static constexpr bool GATED = GATED_;
+  static constexpr bool WIDE = !GATED && WAVES == 8 && TN == 8 && TM % 2 == 0;   // store_wide
   static constexpr int NF = GATED ? 2 : 1;          // blocks of 128 rows of w that a wave reads
   static_assert(!GATED || BN == 256, "a gated tile is one block of 128 channels");
   static constexpr int CA = BN / 8 / WAVES, CB = BM / 8 / WAVES;   // copies per wave and block
@@ -57,6 +58,68 @@ __device__ __forceinline__ typename OperandT<EXACT>::type read_operand(const uin
 __device__ __forceinline__ f32x4 block_dot(const i32x8& a, const i32x8& b) {
   const f32x4 c = {0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// Stores a wave's 16-bit results through 8 KB of LDS of its own, 32 rows of 128 columns at a
+// time, so that each row goes out as 256 consecutive bytes (from registers a row gets 32 bytes
+// per store: four lanes of four columns). 16-byte pieces are in XOR order as in the tiles.
+// kPartType: fp16 of value / scale, scale a power of two per row and 128 columns that brings
+// their largest magnitude to [2^14, 2^15); values that are not finite stay so.
+template <class S>
+__device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&acc)[S::TN][S::TM], uint8_t* room,
+                                           int64_t first, int rows, int wm, int64_t n, int lane) {
+  const Fp8LinearArgs& a = p.a;
+  const int g = lane >> 4, u = lane & 15;
+  __syncthreads();                                  // the last tile has been read
+#pragma unroll
+  for (int jj = 0; jj < S::TM; jj += 2) {
+#pragma unroll
+    for (int j = jj; j < jj + 2; ++j) {
+      float f = 1.0f;
+      if (a.ydtype == kPartType) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < S::TN; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t b = n + 16 * i + 4 * g + e < a.N ? abs_bits(acc[i][j][e]) : 0;
+            m = max(m, b < 0x7F800000u ? b : 0);
+          }
+        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
+        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
+        // exponent of the scale, kept where the scale and its reciprocal are normal numbers
+        const int e = min(max(static_cast<int>(m >> 23) - 14, 1), 253);
+        f = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        const int r = wm + 16 * j + u;
+        if (g == 0 && r < rows && n < a.N)
+          p.part_scale[(n / kFp8Block) * a.M + p.map.pair[first + r]] = __uint_as_float(static_cast<uint32_t>(e) << 23);
+      }
+      const int row = 16 * (j - jj) + u;
+#pragma unroll
+      for (int i = 0; i < S::TN; ++i) {
+        u32x2 b;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float v0 = acc[i][j][2 * h] * f, v1 = acc[i][j][2 * h + 1] * f;
+          const uint32_t lo = a.ydtype == BL_BF16 ? bf16_bits(v0) : half_bits(v0);
+          const uint32_t hi = a.ydtype == BL_BF16 ? bf16_bits(v1) : half_bits(v1);
+          b[h] = lo | hi << 16;
+        }
+        *reinterpret_cast<u32x2*>(room + row * 256 + 16 * ((2 * i + (g >> 1)) ^ u) + 8 * (g & 1)) = b;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const int row = 4 * t + g, r = wm + 16 * jj + row;
+      const u32x4 b = *reinterpret_cast<const u32x4*>(room + row * 256 + 16 * (u ^ (row & 15)));
+      if (r >= rows || n + 8 * u >= a.N) continue;   // N % 8 == 0: all eight or none
+      int64_t at = first + r;
+      if (p.map.scatter) at = p.map.pair[at];
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.y) + at * a.ldy + n + 8 * u) = b;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
 }
 
 template <class S>
@@ -204,6 +267,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   };
 
   const int blocks = static_cast<int>(KB);
+  const bool busy = wm < rows;                      // a wave past the tile's rows only helps to copy
   Scales f0, f1;
   stage(0, bufA0, bufB0);
   scales(0, f0);
@@ -211,15 +275,15 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     arrive();
     stage(kb + 1, bufA1, bufB1);
     scales(kb + 1, f1);
-    compute(bufA0, bufB0, f0);
+    if (busy) compute(bufA0, bufB0, f0);
     arrive();
     const int next = min(kb + 2, blocks - 1);     // past the end the last block again, never read
     stage(next, bufA0, bufB0);
     scales(next, f0);
-    compute(bufA1, bufB1, f1);
+    if (busy) compute(bufA1, bufB1, f1);
   }
   arrive();                                       // no copy outlives the workgroup
-  if (blocks & 1) compute(bufA0, bufB0, f0);
+  if (busy && (blocks & 1)) compute(bufA0, bufB0, f0);
 
   if constexpr (S::GATED) {
     // h = silu(gate) * up stays in fp32 up to its quantisation: the maximum of a row over the
@@ -263,6 +327,12 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
       }
     }
     return;
+  }
+  if constexpr (S::WIDE) {
+    if (a.ydtype != BL_F32 && a.vec8) {
+      store_wide<S>(p, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * 8192, first, rows, wm, n0 + wn, lane);
+      return;
+    }
   }
 #pragma unroll
   for (int j = 0; j < S::TM; ++j) {

@@ -28,11 +28,17 @@ struct Fp8LinearArgs {
   int64_t ldy;
   int ydtype;
   int vec = 0;           // four consecutive values of y can be written at once
+  int vec8 = 0;          // eight of 16 bits, in every row to its end
 };
 // Whether rows ldy apart at y take aligned stores of four values.
 inline int vec_rows(const void* y, int64_t ldy, int dtype) {
   return ldy % 4 == 0 && reinterpret_cast<uintptr_t>(y) % (4 * dtype_bytes(dtype)) == 0;
 }
+inline int vec8_rows(const void* y, int64_t n, int64_t ldy) {
+  return n % 8 == 0 && ldy % 8 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+}
+// Besides bl_dtype: the experts' outputs before their weighted sum, as scaled fp16.
+constexpr int kPartType = 3;
 
 struct Fp8ExpertsArgs {
   const void* x;         // [M, H], rows ldx elements apart
@@ -70,9 +76,11 @@ struct ExpertsWs {
   size_t head_off;             // int32 [4]: rows used, tiles
   size_t pair_off;             // int32 [P] slot m * k + j of each sorted row
   size_t tile_off;             // int32 [tiles, 4]: expert, first row, rows
+  size_t count_off;            // int32 [chunks, E]: slots per expert of each chunk of the sort
   size_t h_off;                // fp32 [P, I] silu(gate) * up, where it is not quantised at once
   size_t hq_off, hs_off;       // quantised silu(gate) * up: codes [P, I], scales [IB, P]
-  size_t part_off;             // fp32 [P, H] the experts' outputs before the weighted sum
+  size_t part_off;             // fp32 or scaled fp16 [P, H]: outputs before the weighted sum
+  size_t ps_off;               // fp32 [HB, P] scales of fp16 outputs
   size_t total;
 };
 ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I);

@@ -43,6 +43,7 @@ hipError_t start_values(const StreamArgs& st, int xdtype, hipStream_t s) {
 hipError_t launch_fp8_linear(const Fp8LinearArgs& args, const void* x, int xdtype, int64_t ldx, hipStream_t s) {
   Fp8LinearArgs a = args;
   a.vec = vec_rows(a.y, a.ldy, a.ydtype);
+  a.vec8 = vec8_rows(a.y, a.N, a.ldy);
   StreamArgs st{};
   st.p.a = a;
   st.x = x;

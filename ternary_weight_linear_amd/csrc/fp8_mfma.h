@@ -92,6 +92,7 @@ struct ProductArgs {
   uint8_t* hq;
   float* hs;
   int64_t h_rows;
+  float* part_scale;             // y of kPartType: [ceil(N / 128), rows of y]
 };
 
 // Four consecutive outputs of a row, in one store where y's rows allow it (a.vec).
@@ -174,6 +175,39 @@ __device__ __forceinline__ uint32_t block_top(const float (&v)[8]) {
 
 __device__ __forceinline__ u32x2 pack8(const float (&v)[8], float r) {
   return u32x2{pack4(f32x4{v[0], v[1], v[2], v[3]}, r), pack4(f32x4{v[4], v[5], v[6], v[7]}, r)};
+}
+
+struct QuantArgs {
+  const void* x;              // rows of K values (GATED: 2 K), ldx apart
+  int64_t M, K, KB, ldx;
+  const int32_t* rows_used;   // device count of rows, or null: M
+  uint8_t* q;                 // [M, K]
+  float* scale;               // [KB, M]
+};
+
+// Quantises 16 blocks of 128 values from block `first` on (inputs run first), one per 16 lanes:
+// a 16-byte load per lane (two of fp32), a maximum over the lanes, an 8-byte store.
+template <int DT, bool GATED>
+__device__ __forceinline__ void quant_blocks(const QuantArgs& a, int64_t first) {
+  using T = typename Elem<DT>::type;
+  const int64_t blk = first + (threadIdx.x >> 4);
+  const int64_t m = blk / a.KB, kb = blk - m * a.KB;
+  const int64_t k = kb * kFp8Block + (threadIdx.x & 15) * 8;
+  if (m >= (a.rows_used ? *a.rows_used : a.M)) return;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (k < a.K) {
+    const T* x = static_cast<const T*>(a.x) + m * a.ldx + k;
+    load8<DT>(x, v);
+    if constexpr (GATED) {
+      float u[8];
+      load8<DT>(x + a.K, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], u[i]);
+    }
+  }
+  const float am = __uint_as_float(block_top(v));
+  if (k < a.K) *reinterpret_cast<u32x2*>(a.q + m * a.K + k) = pack8(v, code_factor(am));
+  if ((threadIdx.x & 15) == 0) a.scale[kb * a.M + m] = am / kFp8Max;
 }
 
 // Streaming product for few rows: the weights are read once, straight into registers, and

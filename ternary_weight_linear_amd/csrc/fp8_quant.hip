@@ -13,30 +13,9 @@
 namespace bl {
 namespace {
 
-// Sixteen lanes per block of 128, eight values each: one 16-byte load per lane, a maximum over
-// the sixteen lanes, one 8-byte store. The block index runs over inputs first.
 template <int DT, bool GATED>
-__global__ __launch_bounds__(256) void fp8_quant_act_kernel(
-    const typename Elem<DT>::type* __restrict__ x, int64_t M, int64_t K, int64_t KB, int64_t ldx,
-    const int32_t* __restrict__ rows_used, uint8_t* __restrict__ q, float* __restrict__ scale) {
-  const int64_t blk = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-  const int j = threadIdx.x & 15;
-  const int64_t m = blk / KB, kb = blk % KB;
-  if (m >= (rows_used ? *rows_used : M)) return;
-  const int64_t k = kb * kFp8Block + j * 8;
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (k < K) {
-    load8<DT>(x + m * ldx + k, v);
-    if constexpr (GATED) {
-      float u[8];
-      load8<DT>(x + m * ldx + K + k, u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], u[i]);
-    }
-  }
-  const float am = __uint_as_float(block_top(v));
-  if (k < K) *reinterpret_cast<u32x2*>(q + m * K + k) = pack8(v, code_factor(am));
-  if (j == 0) scale[kb * M + m] = am / kFp8Max;
+__global__ __launch_bounds__(256) void fp8_quant_act_kernel(QuantArgs q) {
+  quant_blocks<DT, GATED>(q, static_cast<int64_t>(blockIdx.x) * 16);
 }
 
 // One workgroup per 128 x 128 block: thread t holds rows t / 16 + 16 i, inputs 8 (t % 16) ...
@@ -76,13 +55,10 @@ __global__ __launch_bounds__(256) void fp8_quant_weight_kernel(const float* __re
 template <int DT>
 void start_quant(const void* x, int64_t M, int64_t K, int64_t ldx, int gated,
                  const int32_t* rows_used, uint8_t* q, float* scale, hipStream_t s) {
-  using T = typename Elem<DT>::type;
-  const int64_t KB = fp8_blocks(K);
-  const dim3 grid(static_cast<uint32_t>((M * KB + 15) / 16));
-  if (gated)
-    fp8_quant_act_kernel<DT, true><<<grid, 256, 0, s>>>(static_cast<const T*>(x), M, K, KB, ldx, rows_used, q, scale);
-  else
-    fp8_quant_act_kernel<DT, false><<<grid, 256, 0, s>>>(static_cast<const T*>(x), M, K, KB, ldx, rows_used, q, scale);
+  const QuantArgs a{x, M, K, fp8_blocks(K), ldx, rows_used, q, scale};
+  const dim3 grid(static_cast<uint32_t>((M * a.KB + 15) / 16));
+  if (gated) fp8_quant_act_kernel<DT, true><<<grid, 256, 0, s>>>(a);
+  else fp8_quant_act_kernel<DT, false><<<grid, 256, 0, s>>>(a);
 }
 
 }  // namespace

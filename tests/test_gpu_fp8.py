@@ -397,6 +397,21 @@ def test_experts(M, E, k, H, I, dtype):
     close(y, ref, bound + 2.0 ** -20 * np.abs(ref).max(), dtype, (M, E, k, H, I))
 
 
+@pytest.mark.parametrize("M,E,k,times", [(700, 300, 4, 1), (100, 5, 8, 200), (60, 700, 2, 30)])
+def test_experts_many_slots(M, E, k, times):
+    """Enough slots that several workgroups sort them; repeated tokens get the same bits."""
+    say("experts many slots", M * times, E, k)
+    H = I = 16
+    x, v = act((M, H), "fp32", M, spread=0.5)
+    W = expert_weights(E, H, I, 200)
+    index, wt = choose(M, E, k, 9, 0.1)
+    many = [torch.cat([t] * times).contiguous() for t in (x, gpu(index), gpu(wt))]
+    y = tw.bl_fp8_experts(*many, f8(W[0]), gpu(W[1]), f8(W[2]), gpu(W[3])).view(times, M, H)
+    assert torch.equal(y, y[:1].expand(times, M, H))
+    ref, bound = of.experts(v, index, wt, *W, H ** 0.5 * 2.0 ** -21)
+    close(y[0], ref, bound + 2.0 ** -20 * np.abs(ref).max(), "fp32", (M, E, k))
+
+
 def test_experts_slots_that_name_no_expert():
     """-1, out-of-range and repeated indices; a row without any expert gives zeros."""
     say("experts slots")
