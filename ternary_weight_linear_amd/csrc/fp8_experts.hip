@@ -21,7 +21,11 @@ struct SortArgs {
   int32_t* tiles;     // [tiles, 4] expert, first row, rows
   int32_t* counts;    // [chunks, E], more than one chunk
 };
-inline int sort_chunk(int64_t P) { return static_cast<int>(P <= 2048 * 64 ? 2048 : (P + 63) / 64); }
+// Up to 2048 slots one workgroup, which needs no second launch; else chunks of 512 (two slots
+// per thread: the passes over a chunk wait on memory), at most 64.
+inline int sort_chunk(int64_t P) {
+  return static_cast<int>(P <= 2048 ? 2048 : P <= 512 * 64 ? 512 : (P + 63) / 64);
+}
 inline int sort_lds(int64_t E) { return static_cast<int>(E) * 8; }
 
 __device__ __forceinline__ void count_slots(const SortArgs& a, int chunk, int* cnt) {
