@@ -71,8 +71,8 @@ _SIGS = {
     "bl_bitlinear_forward_gemv_noalloc": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I64, _I64, _P, _P]),
     "bl_fp8_quant_weight": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
     "bl_quant_act_fp8": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P]),
-    "bl_fp8_linear": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _I64, _P]),
-    "bl_fp8_workspace_bytes": (_SZ, [_I64, _I64]),
+    "bl_fp8_linear": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _I64, _P, _SZ, _P]),
+    "bl_fp8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "bl_fp8_forward": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _P, _I64, _P, _INT, _I64, _P,
                                       _SZ, _P]),
     "bl_route_experts": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _INT, _INT, _INT, _I64,
@@ -631,9 +631,10 @@ def bl_fp8_linear(q, scales_x, w, scales_w, out_dtype=torch.float32, out=None):
     _shape(w, (N, K), "w")
     _shape(scales_x, (_blocks(K), M), "scales_x")
     y = _out(out, (M, N), out_dtype, d)
+    ws = _scratch(_lib.bl_fp8_workspace_bytes(M, N, K), d, f"M={M} N={N} K={K}")
     _check(_lib.bl_fp8_linear(_ptr(q), _ptr(scales_x), M, K, _ptr(w), _ptr(scales_w), N, _ptr(y),
-                              _dtype(y.dtype, "out"), _row_stride(y, "out"), _stream(d)),
-           "bl_fp8_linear")
+                              _dtype(y.dtype, "out"), _row_stride(y, "out"), _ptr(ws), ws.numel(),
+                              _stream(d)), "bl_fp8_linear")
     return y
 
 
@@ -647,7 +648,7 @@ def bl_fp8_forward(x, w, scales_w, out_dtype=torch.float32, out=None):
     N = w.shape[0]
     _shape(w, (N, K), "w")
     y = _out(out, (M, N), out_dtype, d)
-    ws = _scratch(_lib.bl_fp8_workspace_bytes(M, K), d, f"M={M} K={K}")
+    ws = _scratch(_lib.bl_fp8_workspace_bytes(M, N, K), d, f"M={M} N={N} K={K}")
     _check(_lib.bl_fp8_forward(_ptr(x), dt, M, K, ld, _ptr(w), _ptr(scales_w), N, _ptr(y),
                                _dtype(y.dtype, "out"), _row_stride(y, "out"), _ptr(ws), ws.numel(),
                                _stream(d)), "bl_fp8_forward")

@@ -86,12 +86,14 @@ int check_rows_out(const void* y, int dtype, int64_t n, int64_t ld) {
   return aligned_to(y, dtype_bytes(dtype)) ? BL_OK : BL_ERR_ALIGN;
 }
 struct Fp8Ws {
-  size_t sx_off, total;       // codes [M, K] at 0, scales [KB, M]
+  size_t sx_off, part_off, total;   // codes [M, K] at 0, scales [KB, M], partial sums [parts, M, N]
 };
-Fp8Ws fp8_ws(int64_t M, int64_t K) {
+Fp8Ws fp8_ws(int64_t M, int64_t N, int64_t K) {
   Fp8Ws w{};
   w.sx_off = round256(static_cast<size_t>(M) * K);
-  w.total = w.sx_off + round256(static_cast<size_t>(M) * fp8_blocks(K) * 4);
+  w.part_off = w.sx_off + round256(static_cast<size_t>(M) * fp8_blocks(K) * 4);
+  const int parts = fp8_split_parts(M, N, K);
+  w.total = w.part_off + (parts > 1 ? round256(static_cast<size_t>(parts) * M * N * 4) : 0);
   return w;
 }
 bool experts_dims_ok(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
@@ -723,26 +725,29 @@ int bl_quant_act_fp8(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx
 }
 
 int bl_fp8_linear(const uint8_t* q, const float* scales_x, int64_t M, int64_t K, const uint8_t* w,
-                  const float* scales_w, int64_t N, void* y, int ydtype, int64_t ldy,
-                  void* stream) {
+                  const float* scales_w, int64_t N, void* y, int ydtype, int64_t ldy, void* ws,
+                  size_t ws_bytes, void* stream) {
   if (!q || !scales_x || !w || !scales_w || !y) return BL_ERR_NULL;
   if (!fp8_dims_ok(M, N, K)) return BL_ERR_SHAPE;
   if (int st = check_rows_out(y, ydtype, N, ldy)) return st;
-  if (!aligned16(q) || !aligned16(w) || !aligned_to(scales_x, 4) || !aligned_to(scales_w, 4))
+  const Fp8Ws L = fp8_ws(M, N, K);
+  if (!ws || ws_bytes < L.total) return BL_ERR_WORKSPACE;
+  if (!aligned16(q) || !aligned16(w) || !aligned16(ws) || !aligned_to(scales_x, 4) || !aligned_to(scales_w, 4))
     return BL_ERR_ALIGN;
-  const Span outs[] = {{y, rows_bytes(M, N, ldy, ydtype)}};
+  const Span outs[] = {{y, rows_bytes(M, N, ldy, ydtype)}, {ws, L.total}};
   const Span ins[] = {{q, static_cast<size_t>(M) * K},
                       {scales_x, static_cast<size_t>(M) * fp8_blocks(K) * 4},
                       {w, static_cast<size_t>(N) * K},
                       {scales_w, static_cast<size_t>(fp8_blocks(N)) * fp8_blocks(K) * 4}};
   if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  auto* part = reinterpret_cast<float*>(static_cast<char*>(ws) + L.part_off);
   return check_launch(launch_fp8_linear(Fp8LinearArgs{q, scales_x, w, scales_w, M, N, K, y, ldy, ydtype}, nullptr,
-                                        0, 0, static_cast<hipStream_t>(stream)),
+                                        0, 0, part, static_cast<hipStream_t>(stream)),
                       "bl_fp8_linear");
 }
 
-size_t bl_fp8_workspace_bytes(int64_t M, int64_t K) {
-  return fp8_dims_ok(M, 1, K) ? fp8_ws(M, K).total : 0;
+size_t bl_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return fp8_dims_ok(M, N, K) ? fp8_ws(M, N, K).total : 0;
 }
 
 int bl_fp8_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* w,
@@ -752,7 +757,7 @@ int bl_fp8_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, 
   if (!fp8_dims_ok(M, N, K) || M * fp8_blocks(K) >= (int64_t(1) << 34)) return BL_ERR_SHAPE;
   if (int st = check_rows_in(x, dtype, K, ldx)) return st;
   if (int st = check_rows_out(y, ydtype, N, ldy)) return st;
-  const Fp8Ws L = fp8_ws(M, K);
+  const Fp8Ws L = fp8_ws(M, N, K);
   if (!ws || ws_bytes < L.total) return BL_ERR_WORKSPACE;
   if (!aligned16(w) || !aligned_to(scales_w, 4) || !aligned16(ws)) return BL_ERR_ALIGN;
   const Span outs[] = {{y, rows_bytes(M, N, ldy, ydtype)}, {ws, L.total}};
@@ -762,8 +767,9 @@ int bl_fp8_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, 
   if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
   auto* q = static_cast<uint8_t*>(ws);
   auto* sx = reinterpret_cast<float*>(static_cast<char*>(ws) + L.sx_off);
+  auto* part = reinterpret_cast<float*>(static_cast<char*>(ws) + L.part_off);
   return check_launch(launch_fp8_linear(Fp8LinearArgs{q, sx, w, scales_w, M, N, K, y, ldy, ydtype}, x, dtype, ldx,
-                                        static_cast<hipStream_t>(stream)),
+                                        part, static_cast<hipStream_t>(stream)),
                       "bl_fp8_forward");
 }
 

@@ -300,13 +300,13 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
     e = tile == 16 ? start_stream<1, 4, 8, kSrcCodes, kStreamLinear>(down, nt, 0, s)
                    : start_stream<4, 2, 8, kSrcCodes, kStreamLinear>(down, nt, 0, s);
   } else {
-    e = exact         ? start_gemm<GemmShape<256, 128, 2, 4, true, true>>(up.p, nt, s)
-        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, false, true>>(up.p, nt, s)
-                      : start_gemm<GemmShape<256, 256, 2, 4, false, true>>(up.p, nt, s);
+    e = exact         ? start_gemm<GemmShape<256, 128, 2, 4, 2, true, true>>(up.p, nt, s)
+        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, 2, false, true>>(up.p, nt, s)
+                      : start_gemm<GemmShape<256, 256, 2, 4, 2, false, true>>(up.p, nt, s);
     if (e != hipSuccess) return e;
-    e = exact_down    ? start_gemm<GemmShape<256, 128, 2, 4, true>>(down.p, nt, s)
-        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, false>>(down.p, nt, s)
-                      : start_gemm<GemmShape<256, 256, 2, 4, false>>(down.p, nt, s);
+    e = exact_down    ? start_gemm<GemmShape<256, 128, 2, 4, 2, true>>(down.p, nt, s)
+        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, 2, false>>(down.p, nt, s)
+                      : start_gemm<GemmShape<256, 256, 2, 4, 2, false>>(down.p, nt, s);
   }
   if (e != hipSuccess) return e;
   const int vec = vec_rows(a.y, a.ldy, a.ydtype);

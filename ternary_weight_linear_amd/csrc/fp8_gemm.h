@@ -6,8 +6,6 @@
 namespace bl {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
 // Offsets from here on are outside every buffer below: a load there gives zeros.
 constexpr uint32_t kOutside = 0x80000000u;
 
@@ -17,13 +15,31 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_buffer(const void* base) 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(kOutside), 0x00020000);
 }
 
-// 16 bytes per lane from base + offset + k0 into LDS at `to` + 16 lane.
-__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, uint32_t k0, uint8_t* to) {
+// 16 (4) bytes per lane from base + offset + k0 into LDS at `to` + 16 (4) lane.
+__device__ __forceinline__ void copy16_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, uint32_t k0, void* to) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16,
                                            static_cast<int>(offset), static_cast<int>(k0), 0, 0);
 }
+__device__ __forceinline__ void copy4_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, void* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 4,
+                                           static_cast<int>(offset), 0, 0, 0);
+}
+// Waits until at most N of this wave's loads and copies are in flight.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
 
-template <int BN_, int BM_, int GN_, int GM_, bool EXACT_, bool GATED_ = false>
+// The workgroup's waves meet. Unlike __syncthreads this does not wait for the copies in flight:
+// wait_copies does, for those that are needed, and what a wave has read from LDS it has used in
+// a matrix instruction by now. The fences only keep the compiler from moving accesses across.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+template <int BN_, int BM_, int GN_, int GM_, int NS_, bool EXACT_, bool GATED_ = false>
 struct GemmShape {
   static constexpr int BN = BN_, BM = BM_;          // tile: rows of w, rows of q
   static constexpr int GN = GN_, GM = GM_;          // waves along each
@@ -36,28 +52,21 @@ struct GemmShape {
   static constexpr bool WIDE = !GATED && WAVES == 8 && TN == 8 && TM % 2 == 0;   // store_wide
   static constexpr int NF = GATED ? 2 : 1;          // blocks of 128 rows of w that a wave reads
   static_assert(!GATED || BN == 256, "a gated tile is one block of 128 channels");
+  static constexpr int NS = NS_;                    // stages: NS - 1 blocks' copies in flight
   static constexpr int CA = BN / 8 / WAVES, CB = BM / 8 / WAVES;   // copies per wave and block
+  static constexpr int COPIES = CA + CB + 1;        // and one of its rows' scales
+  static_assert(NS >= 2 && NS <= 4 && COPIES * (NS - 2) < 64, "what s_waitcnt can count");
+  static_assert(BM / GM <= 64, "one copy holds a wave's scales");
 };
-
-template <bool EXACT>
-struct OperandT { using type = i32x8; };
-template <>
-struct OperandT<true> { using type = FragH; };
 
 // The fragment of 16 rows whose first byte for this lane is at `at` of a staged tile; the
 // second 16 codes are in the piece four further on, which the XOR order puts 64 bytes away.
 template <bool EXACT>
-__device__ __forceinline__ typename OperandT<EXACT>::type read_operand(const uint8_t* tile, uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ Operand<EXACT> read_operand(const uint8_t* tile, uint32_t lo, uint32_t hi) {
   Frag f;
   f.lo = *reinterpret_cast<const u32x4*>(tile + lo);
   f.hi = *reinterpret_cast<const u32x4*>(tile + hi);
-  if constexpr (EXACT) return to_half(f);
-  else return i32x8{(int)f.lo.x, (int)f.lo.y, (int)f.lo.z, (int)f.lo.w, (int)f.hi.x, (int)f.hi.y, (int)f.hi.z, (int)f.hi.w};
-}
-
-__device__ __forceinline__ f32x4 block_dot(const i32x8& a, const i32x8& b) {
-  const f32x4 c = {0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+  return operand<EXACT>(f);
 }
 
 // Stores a wave's 16-bit results through 8 KB of LDS of its own, 32 rows of 128 columns at a
@@ -70,7 +79,6 @@ __device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&a
                                            int64_t first, int rows, int wm, int64_t n, int lane) {
   const Fp8LinearArgs& a = p.a;
   const int g = lane >> 4, u = lane & 15;
-  __syncthreads();                                  // the last tile has been read
 #pragma unroll
   for (int jj = 0; jj < S::TM; jj += 2) {
 #pragma unroll
@@ -126,7 +134,10 @@ template <class S>
 __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int tiles_n, int tiles_m_arg) {
   // one array per operand and stage: the compiler can then tell that the copies into one
   // stage do not touch what is being read
-  __shared__ uint8_t bufA0[S::BN * 128], bufA1[S::BN * 128], bufB0[S::BM * 128], bufB1[S::BM * 128];
+  constexpr int N3 = S::NS > 2 ? 1 : 0, N4 = S::NS > 3 ? 1 : 0;
+  __shared__ uint8_t bufA0[S::BN * 128], bufA1[S::BN * 128], bufA2[N3 ? S::BN * 128 : 1], bufA3[N4 ? S::BN * 128 : 1];
+  __shared__ uint8_t bufB0[S::BM * 128], bufB1[S::BM * 128], bufB2[N3 ? S::BM * 128 : 1], bufB3[N4 ? S::BM * 128 : 1];
+  __shared__ float bufS0[S::WAVES][64], bufS1[S::WAVES][64], bufS2[N3 ? S::WAVES : 1][64], bufS3[N4 ? S::WAVES : 1][64];
   const Fp8LinearArgs& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, u = lane & 15;
@@ -150,9 +161,9 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   int64_t first = static_cast<int64_t>(tm) * S::BM;
   int rows = 0, expert = 0;
   if (p.map.tiles) {
-    expert = p.map.tiles[4 * tm];
-    first = p.map.tiles[4 * tm + 1];
-    rows = p.map.tiles[4 * tm + 2];
+    expert = __builtin_amdgcn_readfirstlane(p.map.tiles[4 * tm]);
+    first = __builtin_amdgcn_readfirstlane(p.map.tiles[4 * tm + 1]);
+    rows = __builtin_amdgcn_readfirstlane(p.map.tiles[4 * tm + 2]);
   } else {
     rows = static_cast<int>(a.M - first < S::BM ? a.M - first : S::BM);
   }
@@ -184,47 +195,57 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     if (p.map.gather_div > 0) r = p.map.pair[first + r] / p.map.gather_div;
     ob[i] = static_cast<uint32_t>(r) * static_cast<uint32_t>(K) + 16 * piece;
   }
-  const int kb_cut = K % kFp8Block ? static_cast<int>(KB) - 1 : -1;   // the block that K ends in
-  const bool out = (KB - 1) * kFp8Block + 16 * piece >= K;
-  auto stage = [&](int kb, uint8_t* ta, uint8_t* tb) __attribute__((always_inline)) {
-    const bool skip = out && kb == kb_cut;
-    const uint32_t k0 = static_cast<uint32_t>(kb) * kFp8Block;
-#pragma unroll
-    for (int i = 0; i < S::CA; ++i)
-      copy_to_lds(ba, skip ? kOutside : oa[i], k0, ta + 1024 * (i * S::WAVES + wave));
-#pragma unroll
-    for (int i = 0; i < S::CB; ++i)
-      copy_to_lds(bb, skip ? kOutside : ob[i], k0, tb + 1024 * (i * S::WAVES + wave));
-  };
-
-  uint32_t ox[S::TM];
-#pragma unroll
-  for (int j = 0; j < S::TM; ++j) {
-    int64_t at = first + min(wm + 16 * j + u, rows - 1);
+  // scales: one copy brings those of the wave's up to 64 rows
+  uint32_t os;
+  {
+    int64_t at = first + min(wm + min(lane, S::BM / S::GM - 1), rows - 1);
     if (p.map.gather_div > 0) at = p.map.pair[at] / p.map.gather_div;
-    ox[j] = 4 * static_cast<uint32_t>(at);
+    os = 4 * static_cast<uint32_t>(at);
   }
   // the wave's weight rows (GATED: of either half) lie in one block of 128 (BN / GN divides 128)
   const float* sw = a.sw + expert * p.sw_stride;
   const int64_t up_scales = (a.N + kFp8Block - 1) / kFp8Block * KB;
   sw += (S::GATED ? static_cast<int64_t>(tn) : min<int64_t>((n0 + wn) / kFp8Block, (a.N - 1) / kFp8Block)) * KB;
 
+  // blocks [kb, blocks): all of them, or the workgroup's range of a split K
+  const int per = static_cast<int>((KB + gridDim.y - 1) / gridDim.y);
+  int kb = blockIdx.y * per;
+  const int blocks = min(kb + per, static_cast<int>(KB));
+  const bool cut = (KB - 1) * kFp8Block + 16 * piece >= K;   // this lane's piece of the last block is past K
+  struct Weigh {
+    float w[S::NF];
+  };
+  // Block kb into a stage; past the last block, zeros (no memory is read)
+  auto stage = [&](int kb, uint8_t* ta, uint8_t* tb, float (*ts)[64], Weigh& sc) __attribute__((always_inline)) {
+    const bool skip = kb >= blocks || (cut && kb == KB - 1);
+    const uint32_t k0 = static_cast<uint32_t>(kb) * kFp8Block;
+#pragma unroll
+    for (int i = 0; i < S::CA; ++i)
+      copy16_to_lds(ba, skip ? kOutside : oa[i], k0, ta + 1024 * (i * S::WAVES + wave));
+#pragma unroll
+    for (int i = 0; i < S::CB; ++i)
+      copy16_to_lds(bb, skip ? kOutside : ob[i], k0, tb + 1024 * (i * S::WAVES + wave));
+    const int ks = min(kb, blocks - 1);
+    copy4_to_lds(make_buffer(a.sx + ks * a.M), os, ts[wave]);
+    sc.w[0] = sw[ks];
+    if constexpr (S::GATED) sc.w[1] = sw[up_scales + ks];
+  };
+
   const uint32_t in_row = u * 128 + 16 * (g ^ (u & 7));
   const uint32_t wa = wn * 128 + in_row, wa2 = wn * 128 + (in_row ^ 64);
   const uint32_t qa = wm * 128 + in_row, qa2 = wm * 128 + (in_row ^ 64);
-  struct Scales {
-    float x[S::TM], w[S::NF];
-  };
   f32x4 acc[S::TN][S::TM] = {};
   // One block of inputs. While the matrix cores multiply weight fragment i by the TM fragments
   // of q, the products of fragment i - 1 are scaled and added (VALU) and fragment i + 1 is read.
-  auto compute = [&](const uint8_t* ta, const uint8_t* tb, const Scales& sc) __attribute__((always_inline)) {
+  auto compute = [&](const uint8_t* ta, const uint8_t* tb, const float (*ts)[64], const Weigh& sc) __attribute__((always_inline)) {
     float f[S::NF][S::TM];
 #pragma unroll
-    for (int h = 0; h < S::NF; ++h)
+    for (int j = 0; j < S::TM; ++j) {
+      const float x = ts[wave][16 * j + u];
 #pragma unroll
-      for (int j = 0; j < S::TM; ++j) f[h][j] = sc.x[j] * sc.w[h];
-    typename OperandT<S::EXACT>::type b[S::TM], w[2];
+      for (int h = 0; h < S::NF; ++h) f[h][j] = x * sc.w[h];
+    }
+    Operand<S::EXACT> b[S::TM], w[2];
     f32x4 part[2][S::TM];
     w[0] = read_operand<S::EXACT>(ta, wa, wa2);
 #pragma unroll
@@ -232,63 +253,88 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
 #pragma unroll
     for (int i = 0; i <= S::TN; ++i) {
       if (i + 1 < S::TN) w[(i + 1) & 1] = read_operand<S::EXACT>(ta + 2048 * (i + 1), wa, wa2);
+      if (i < S::TN) {
+        if constexpr (S::EXACT) {
+          // the four instructions of a sum depend on each other: those of the TM sums take turns
 #pragma unroll
-      for (int j = 0; j < S::TM; ++j) {
-        if (i < S::TN) part[i & 1][j] = block_dot(w[i & 1], b[j]);
-        if (i > 0) {
+          for (int j = 0; j < S::TM; ++j) part[i & 1][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < S::TM; ++j)
+              part[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i & 1].h[k], b[j].h[k], part[i & 1][j], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < S::TM; ++j) part[i & 1][j] = block_dot(w[i & 1], b[j]);
+        }
+      }
+      if (i > 0) {
+#pragma unroll
+        for (int j = 0; j < S::TM; ++j) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             acc[i - 1][j][e] = fmaf(part[(i - 1) & 1][j][e], f[(i - 1) * S::NF / S::TN][j], acc[i - 1][j][e]);
           asm volatile("" : "+v"(acc[i - 1][j]));   // the sum is formed here, not sunk to its next use
         }
       }
-      // both LDS reads first, then each matrix instruction beside four FMAs of the one before
+      // both LDS reads first, then the matrix instructions with the FMAs of the fragment before
+      // (and the conversions of the next) between them
       if (i + 1 < S::TN) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
-      for (int j = 0; j < S::TM; ++j) {
-        if (i < S::TN) __builtin_amdgcn_sched_group_barrier(0x008, S::EXACT ? 4 : 1, 0);
-        if (i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      for (int j = 0; j < (S::EXACT ? 4 : 1) * S::TM; ++j) {
+        if (i < S::TN) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, S::EXACT ? 1 + 4 / S::TM : 4, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto scales = [&](int kb, Scales& sc) __attribute__((always_inline)) {
-    sc.w[0] = sw[kb];
-    if constexpr (S::GATED) sc.w[1] = sw[up_scales + kb];
-    const auto sx = make_buffer(a.sx + kb * a.M);
-#pragma unroll
-    for (int j = 0; j < S::TM; ++j)
-      sc.x[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sx, static_cast<int>(ox[j]), 0, 0));
-  };
-  // every copy of this wave has landed, then every wave's
-  auto arrive = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);             // vmcnt(0)
-    __syncthreads();
-  };
-
-  const int blocks = static_cast<int>(KB);
   const bool busy = wm < rows;                      // a wave past the tile's rows only helps to copy
-  Scales f0, f1;
-  stage(0, bufA0, bufB0);
-  scales(0, f0);
-  for (int kb = 0; kb + 1 < blocks; kb += 2) {
-    arrive();
-    stage(kb + 1, bufA1, bufB1);
-    scales(kb + 1, f1);
-    if (busy) compute(bufA0, bufB0, f0);
-    arrive();
-    const int next = min(kb + 2, blocks - 1);     // past the end the last block again, never read
-    stage(next, bufA0, bufB0);
-    scales(next, f0);
-    if (busy) compute(bufA1, bufB1, f1);
+  Weigh w0, w1, w2, w3;
+  stage(kb, bufA0, bufB0, bufS0, w0);
+  if constexpr (S::NS > 2) stage(kb + 1, bufA1, bufB1, bufS1, w1);
+  if constexpr (S::NS > 3) stage(kb + 2, bufA2, bufB2, bufS2, w2);
+  // Step kb: its copies have landed (this wave's, then every wave's, who are also done with the
+  // stage of block kb - 1), block kb + NS - 1 goes there, block kb is multiplied.
+#define BL_STEP(KB_, A, B, SC, W, NA, NB, NSC, NW)           \
+  {                                                          \
+    wait_copies<S::COPIES * (S::NS - 2)>();                  \
+    meet();                                                  \
+    stage((KB_) + S::NS - 1, NA, NB, NSC, NW);               \
+    if (busy) compute(A, B, SC, W);                          \
   }
-  arrive();                                       // no copy outlives the workgroup
-  if (busy && (blocks & 1)) compute(bufA0, bufB0, f0);
+  if constexpr (S::NS == 2) {
+    for (; kb + 2 <= blocks; kb += 2) {
+      BL_STEP(kb, bufA0, bufB0, bufS0, w0, bufA1, bufB1, bufS1, w1)
+      BL_STEP(kb + 1, bufA1, bufB1, bufS1, w1, bufA0, bufB0, bufS0, w0)
+    }
+    if (kb < blocks) BL_STEP(kb, bufA0, bufB0, bufS0, w0, bufA1, bufB1, bufS1, w1)
+  } else if constexpr (S::NS == 3) {
+    for (; kb + 3 <= blocks; kb += 3) {
+      BL_STEP(kb, bufA0, bufB0, bufS0, w0, bufA2, bufB2, bufS2, w2)
+      BL_STEP(kb + 1, bufA1, bufB1, bufS1, w1, bufA0, bufB0, bufS0, w0)
+      BL_STEP(kb + 2, bufA2, bufB2, bufS2, w2, bufA1, bufB1, bufS1, w1)
+    }
+    if (kb < blocks) BL_STEP(kb, bufA0, bufB0, bufS0, w0, bufA2, bufB2, bufS2, w2)
+    if (kb + 1 < blocks) BL_STEP(kb + 1, bufA1, bufB1, bufS1, w1, bufA0, bufB0, bufS0, w0)
+  } else {
+    for (; kb + 4 <= blocks; kb += 4) {
+      BL_STEP(kb, bufA0, bufB0, bufS0, w0, bufA3, bufB3, bufS3, w3)
+      BL_STEP(kb + 1, bufA1, bufB1, bufS1, w1, bufA0, bufB0, bufS0, w0)
+      BL_STEP(kb + 2, bufA2, bufB2, bufS2, w2, bufA1, bufB1, bufS1, w1)
+      BL_STEP(kb + 3, bufA3, bufB3, bufS3, w3, bufA2, bufB2, bufS2, w2)
+    }
+    if (kb < blocks) BL_STEP(kb, bufA0, bufB0, bufS0, w0, bufA3, bufB3, bufS3, w3)
+    if (kb + 1 < blocks) BL_STEP(kb + 1, bufA1, bufB1, bufS1, w1, bufA0, bufB0, bufS0, w0)
+    if (kb + 2 < blocks) BL_STEP(kb + 2, bufA2, bufB2, bufS2, w2, bufA1, bufB1, bufS1, w1)
+  }
+#undef BL_STEP
+  wait_copies<0>();                                 // no copy outlives the workgroup
+  __syncthreads();                                  // and every wave is past the tiles
 
   if constexpr (S::GATED) {
     // h = silu(gate) * up stays in fp32 up to its quantisation: the maximum of a row over the
     // tile's 128 channels meets over the lanes that share the row, then over the waves in LDS
-    auto* top = reinterpret_cast<uint32_t*>(bufA0);   // [GN][BM], every wave is past the tiles
+    auto* top = reinterpret_cast<uint32_t*>(bufA0);   // [GN][BM]
     uint32_t mine[S::TM];
 #pragma unroll
     for (int j = 0; j < S::TM; ++j) {
@@ -305,7 +351,6 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
       mine[j] = max(mine[j], static_cast<uint32_t>(__shfl_xor(static_cast<int>(mine[j]), 16)));
       mine[j] = max(mine[j], static_cast<uint32_t>(__shfl_xor(static_cast<int>(mine[j]), 32)));
     }
-    __syncthreads();
 #pragma unroll
     for (int j = 0; j < S::TM; ++j)
       if (g == 0) top[wave % S::GN * S::BM + wm + 16 * j + u] = mine[j];
@@ -341,8 +386,23 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     int64_t at = first + r;
     if (p.map.scatter) at = p.map.pair[at];
 #pragma unroll
-    for (int i = 0; i < S::TN; ++i) store4(a, at, n0 + wn + 16 * i + 4 * g, acc[i][j]);
+    for (int i = 0; i < S::TN; ++i) store4(a, blockIdx.y * a.M + at, n0 + wn + 16 * i + 4 * g, acc[i][j]);
   }
+}
+
+// y = the sum of `parts` partial results [parts, M, N] in their order.
+__global__ __launch_bounds__(256) void sum_parts_kernel(Fp8LinearArgs a, const float* __restrict__ part, int parts,
+                                                        int64_t row4) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t m = id / row4, n = (id - m * row4) * 4;
+  if (m >= a.M) return;
+  f32x4 sum = {0, 0, 0, 0};
+  for (int z = 0; z < parts; ++z) {
+    const float* p = part + (static_cast<int64_t>(z) * a.M + m) * a.N + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += n + e < a.N ? p[e] : 0.0f;
+  }
+  store4(a, m, n, sum);
 }
 
 template <class S>
@@ -351,6 +411,24 @@ hipError_t start_gemm(const ProductArgs& p, int64_t tiles_m, hipStream_t s) {
   const int64_t tiles_n = (p.a.N + cols - 1) / cols;
   fp8_gemm_kernel<S><<<dim3(static_cast<uint32_t>(tiles_n * tiles_m)), S::THREADS, 0, s>>>(
       p, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
+  return hipGetLastError();
+}
+
+// The product with K split over `parts` workgroups per tile; part: fp32 [parts, M, N].
+template <class S>
+hipError_t start_split_gemm(const ProductArgs& p, int parts, float* part, hipStream_t s) {
+  const int64_t tiles_n = (p.a.N + S::BN - 1) / S::BN, tiles_m = (p.a.M + S::BM - 1) / S::BM;
+  ProductArgs q = p;
+  q.a.y = part;
+  q.a.ldy = p.a.N;
+  q.a.ydtype = BL_F32;
+  q.a.vec = p.a.N % 4 == 0;
+  fp8_gemm_kernel<S><<<dim3(static_cast<uint32_t>(tiles_n * tiles_m), static_cast<uint32_t>(parts)), S::THREADS, 0, s>>>(
+      q, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t row4 = (p.a.N + 3) / 4;
+  sum_parts_kernel<<<dim3(static_cast<uint32_t>((p.a.M * row4 + 255) / 256)), 256, 0, s>>>(p.a, part, parts, row4);
   return hipGetLastError();
 }
 

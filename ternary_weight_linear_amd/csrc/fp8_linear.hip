@@ -38,9 +38,62 @@ hipError_t start_values(const StreamArgs& st, int xdtype, hipStream_t s) {
   }
 }
 
+int64_t tiles(int64_t M, int64_t N, int bn, int bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); }
+
+template <class S>
+hipError_t start_whole(const ProductArgs& p, hipStream_t s) {
+  return start_gemm<S>(p, (p.a.M + S::BM - 1) / S::BM, s);
+}
+
+// Tile of the tiled kernel. Large tiles read less from L2 (64 x 64 tiles are bound by it, at
+// 11 to 15 TB/s), small ones fill the 256 CUs. Measured on MI355X, us, e4m3 instruction
+// (256 x 256 / 128 x 128, four waves / 128 x 128, eight waves, four stages / 128 x 64 / 64 x 64):
+//   4096 x 28672 x 8192  785 / 926 / - / - / -      2048 x 8192 x 8192  117 / 143 / 168 / 191 / -
+//   512 x 8640 x 3200    - / 26.3 / 36 / 27.4 / 30  512 x 8192 x 8192   - / 57 / 43.0 / 52.8 / -
+//   1024 x 4096 x 4096   - / 28.1 / 23.9 / 24.4 / 30   512 x 3200 x 8640 - / 57 / 38 / 30.7 / 32.6
+//   96 x 28672 x 8192    - / 58.9 / 57.2 / 68.5 / 73.5
+// and with K in parts where 64 x 64 tiles alone leave CUs idle (1 / 2 / 4 parts):
+//   512 x 1024 x 8192 20.9 / 15.8 / 16.3   64 x 8192 x 8192 23.4 / 18.7 / 20.4
+//   200 x 1024 x 8192 20.1 / 15.2 / 12.7   24 x 4096 x 11008 24.3 / 16.8 / 14.1
+// fp16 operands: 4096 x 28672 x 8192 1545 (128 x 128); 512 x 3200 x 8640 45.5 (64 x 64), as with
+// every other tile: converting the codes (a quarter-rate instruction per two of them, for each
+// fragment that a wave reads) bounds it; staging q as fp16 halved that and lost as much to L2.
+template <bool EXACT>
+hipError_t start_tiled(const ProductArgs& p, float* part, hipStream_t s) {
+  const int64_t M = p.a.M, N = p.a.N, t128 = tiles(M, N, 128, 128);
+  const int parts = fp8_split_parts(M, N, p.a.K);
+  if (parts > 1) return start_split_gemm<GemmShape<64, 64, 2, 2, EXACT ? 3 : 4, EXACT>>(p, parts, part, s);
+  if constexpr (EXACT) {
+    if (t128 >= 256) return start_whole<GemmShape<128, 128, 2, 2, 2, true>>(p, s);
+    return start_whole<GemmShape<64, 64, 2, 2, 3, true>>(p, s);
+  } else {
+    if (t128 > 256) {
+      // rounds over the chip: 256 large tiles take 1, 512 small ones 0.6 of it
+      const double large = static_cast<double>((tiles(M, N, 256, 256) + 255) / 256), small = 0.6 * ((t128 + 511) / 512);
+      if (large <= small) return start_whole<GemmShape<256, 256, 2, 4, 2, false>>(p, s);
+      return start_whole<GemmShape<128, 128, 2, 2, 2, false>>(p, s);
+    }
+    if (t128 >= 200) return start_whole<GemmShape<128, 128, 2, 4, 4, false>>(p, s);
+    if (tiles(M, N, 128, 64) >= 200 && tiles(M, N, 128, 64) <= 256)
+      return start_whole<GemmShape<128, 64, 2, 2, 4, false>>(p, s);
+    return start_whole<GemmShape<64, 64, 2, 2, 4, false>>(p, s);
+  }
+}
+
 }  // namespace
 
-hipError_t launch_fp8_linear(const Fp8LinearArgs& args, const void* x, int xdtype, int64_t ldx, hipStream_t s) {
+int fp8_split_parts(int64_t M, int64_t N, int64_t K) {
+  const int64_t t = tiles(M, N, 64, 64), KB = fp8_blocks(K);
+  if (t > 128) return 1;
+  int64_t parts = 256 / t < 8 ? 256 / t : 8;
+  if (parts > KB / 8) parts = KB / 8;               // at least eight blocks each
+  if (parts <= 1) return 1;
+  const int64_t per = (KB + parts - 1) / parts;
+  return static_cast<int>((KB + per - 1) / per);    // none empty
+}
+
+hipError_t launch_fp8_linear(const Fp8LinearArgs& args, const void* x, int xdtype, int64_t ldx, float* part,
+                             hipStream_t s) {
   Fp8LinearArgs a = args;
   a.vec = vec_rows(a.y, a.ldy, a.ydtype);
   a.vec8 = vec8_rows(a.y, a.N, a.ldy);
@@ -56,22 +109,10 @@ hipError_t launch_fp8_linear(const Fp8LinearArgs& args, const void* x, int xdtyp
     if (e != hipSuccess) return e;
   }
   if (a.M <= 16) return start_codes<1>(st, s);
-  if (a.M <= 32) return start_codes<2>(st, s);
-  // Up to 64 rows the streaming kernel reads 8 KB of codes of q per block and workgroup; the
-  // tiled one shares them in LDS and wins once its 64 x 64 tiles fill the CUs (M = 64, K = 8192:
-  // N = 8192 26.7 us streamed, 39.4 tiled; N = 28672 95.9 and 59.9). Its offsets are 32 bits.
-  if ((a.M <= 64 && a.N < 64 * 256) || 256 * a.K >= (int64_t(1) << 31)) return start_codes<4>(st, s);
-  const ProductArgs& p = st.p;
-  if (a.ydtype == BL_F32) {
-    const int64_t tiles = ((a.N + 127) / 128) * ((a.M + 127) / 128);
-    if (tiles >= 256) return start_gemm<GemmShape<128, 128, 2, 2, true>>(p, (a.M + 127) / 128, s);
-    return start_gemm<GemmShape<64, 64, 2, 2, true>>(p, (a.M + 63) / 64, s);
-  }
-  const int64_t tiles = ((a.N + 255) / 256) * ((a.M + 255) / 256);
-  if (tiles >= 256) return start_gemm<GemmShape<256, 256, 2, 4, false>>(p, (a.M + 255) / 256, s);
-  const int64_t tiles2 = ((a.N + 127) / 128) * ((a.M + 127) / 128);
-  if (tiles2 >= 256) return start_gemm<GemmShape<128, 128, 2, 2, false>>(p, (a.M + 127) / 128, s);
-  return start_gemm<GemmShape<64, 64, 2, 2, false>>(p, (a.M + 63) / 64, s);
+  // fp32 results stream up to 32 rows (32 x 8192 x 8192: 20.5 us, tiled 23)
+  if ((a.M <= 32 && a.ydtype == BL_F32) || 256 * a.K >= (int64_t(1) << 31))   // tiled: 32-bit offsets
+    return start_codes<2>(st, s);
+  return a.ydtype == BL_F32 ? start_tiled<true>(st.p, part, s) : start_tiled<false>(st.p, part, s);
 }
 
 }  // namespace bl

@@ -65,14 +65,35 @@ __device__ __forceinline__ uint32_t pack4(const f32x4& v, float r) {
 }
 
 // Sum over a block: D[row of a][row of b]; lane 16 g + u holds rows 4 g + i of a, row u of b.
-// The codes go to the fp16 matrix cores, whose sums keep fp32's precision; the e4m3 form of
-// the instruction keeps about 16 bits below the largest product (measured: relative error
-// 1.4e-5 of a 128-term sum, against 9e-9 in fp16).
+//
+// EXACT: the codes go to the fp16 matrix instruction, whose sums keep fp32's precision. The
+// e4m3 instruction takes the codes as they are at twice the rate, but keeps about 16 bits below
+// the largest product of a sum (measured on sums of 128 products: relative error 1.4e-5, fp16
+// 9e-9). It serves results of 16 bits: 1/100 of bf16's rounding, 1/14 of fp16's.
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+template <bool EXACT>
+struct OperandT { using type = i32x8; };
+template <>
+struct OperandT<true> { using type = FragH; };
+template <bool EXACT>
+using Operand = typename OperandT<EXACT>::type;
+
+template <bool EXACT>
+__device__ __forceinline__ Operand<EXACT> operand(const Frag& f) {
+  if constexpr (EXACT) return to_half(f);
+  else return i32x8{(int)f.lo.x, (int)f.lo.y, (int)f.lo.z, (int)f.lo.w, (int)f.hi.x, (int)f.hi.y, (int)f.hi.z, (int)f.hi.w};
+}
+
 __device__ __forceinline__ f32x4 block_dot(const FragH& a, const FragH& b) {
   f32x4 c = {0, 0, 0, 0};
 #pragma unroll
   for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.h[s], b.h[s], c, 0, 0, 0);
   return c;
+}
+__device__ __forceinline__ f32x4 block_dot(const i32x8& a, const i32x8& b) {
+  const f32x4 c = {0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);   // no scales
 }
 
 // Where the rows of a product come from and go to.
@@ -220,7 +241,7 @@ __device__ __forceinline__ void quant_blocks(const QuantArgs& a, int64_t first) 
 // input would meet in a few of the memory's channels.
 // Measured, us (weight bytes / time): 1 x 8192 x 8192 12.3 (5.4 TB/s), 16 x 8192 x 8192 14.2,
 // 16 x 28672 x 8192 43.8 (5.4 TB/s), 1 x 28672 x 8192 39.6 (5.9 TB/s).
-template <int MT, int NT, int S, int SRC, int MODE>
+template <int MT, int NT, int S, int SRC, int MODE, bool EXACT>
 __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s) {
   constexpr bool GATED = MODE == kStreamGated;
   constexpr int G = kStreamWaves / S;               // groups of weight rows
@@ -322,23 +343,23 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
     if constexpr (MODE == kStreamSlots) {
       if (!st.some) return;
     }
-    FragH q[MT];
+    Operand<EXACT> q[MT];
     float sx[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       if constexpr (SRC == kSrcCodes) {
-        q[t] = to_half(st.q[t]);
+        q[t] = operand<EXACT>(st.q[t]);
         sx[t] = st.sx[t];
       } else {
         const int r = MODE == kStreamSlots ? st.row : min(u, rows - 1);
         const uint8_t* at = staged + r * staged_row(KB) + st.kb * kFp8Block + 16 * g;
-        q[t] = to_half(Frag{*reinterpret_cast<const u32x4*>(at), *reinterpret_cast<const u32x4*>(at + 64)});
+        q[t] = operand<EXACT>(Frag{*reinterpret_cast<const u32x4*>(at), *reinterpret_cast<const u32x4*>(at + 64)});
         sx[t] = staged_scale[r * KB + st.kb];
       }
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const FragH w = to_half(st.w[i]);
+      const Operand<EXACT> w = operand<EXACT>(st.w[i]);
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[i][t] += block_dot(w, q[t]) * (sx[t] * st.sw[i]);
     }
@@ -416,12 +437,12 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
 }
 
 // Starts the kernel over the columns of w and `tiles` tiles of rows; staged: rows to quantise.
-template <int MT, int NT, int S, int SRC, int MODE>
+template <int MT, int NT, int S, int SRC, int MODE, bool EXACT = true>
 hipError_t start_stream(const StreamArgs& st, int64_t tiles, int staged, hipStream_t s) {
   constexpr int cols = 16 * NT * (kStreamWaves / S) / (MODE == kStreamGated ? 2 : 1);
   const int lds = SRC == kSrcCodes ? 0 : staged_bytes(staged, static_cast<int>(fp8_blocks(st.p.a.K)));
   const dim3 grid(static_cast<uint32_t>((st.p.a.N + cols - 1) / cols), static_cast<uint32_t>(tiles));
-  fp8_stream_kernel<MT, NT, S, SRC, MODE><<<grid, kStreamThreads, lds, s>>>(st);
+  fp8_stream_kernel<MT, NT, S, SRC, MODE, EXACT><<<grid, kStreamThreads, lds, s>>>(st);
   return hipGetLastError();
 }
 template <int NT, int S, int MODE>

@@ -27,7 +27,7 @@ def call(name, defaults, **kw):
 
 
 QUANT = dict(x=A, dtype=F16, M=4, K=256, ldx=256, gated=0, q=B, scales=C, stream=None)
-LINEAR = dict(q=A, sx=B, M=4, K=256, w=C, sw=D, N=100, y=Y, ydtype=F32, ldy=100, stream=None)
+LINEAR = dict(q=A, sx=B, M=4, K=256, w=C, sw=D, N=100, y=Y, ydtype=F32, ldy=100, ws=W_, wsb=1 << 20, stream=None)
 FORWARD = dict(x=A, dtype=F16, M=4, K=256, ldx=256, w=C, sw=D, N=100, y=Y, ydtype=F32, ldy=100, ws=W_, wsb=1 << 20,
                stream=None)
 ROUTE = dict(logits=A, dtype=F32, M=4, E=64, ld=64, bias=None, score=1, groups=8, kept=4, k=8, renorm=1, factor=1.0,
@@ -50,7 +50,8 @@ def test_quant_refusals(kw, want):
     (dict(q=None), NULL), (dict(sx=None), NULL), (dict(w=None), NULL), (dict(sw=None), NULL), (dict(y=None), NULL),
     (dict(M=0), SHAPE), (dict(N=0), SHAPE), (dict(K=-16), SHAPE), (dict(K=120), SHAPE), (dict(ldy=99), SHAPE),
     (dict(ydtype=7), ARG), (dict(q=A + 4), ALIGN), (dict(w=C + 8), ALIGN), (dict(sx=B + 1), ALIGN), (dict(y=Y + 2), ALIGN),
-    (dict(y=C + 16), ALIAS), (dict(y=A), ALIAS), (dict(y=D), ALIAS)])
+    (dict(y=C + 16), ALIAS), (dict(y=A), ALIAS), (dict(y=D), ALIAS), (dict(ws=None), WS), (dict(wsb=64), WS),
+    (dict(ws=W_ + 4), ALIGN), (dict(ws=B), ALIAS)])
 def test_linear_refusals(kw, want):
     assert call("bl_fp8_linear", LINEAR, **kw) == want
 
@@ -93,8 +94,10 @@ def test_quant_weight_refusals():
 
 
 def test_size_queries():
-    assert lib.bl_fp8_workspace_bytes(0, 128) == 0 and lib.bl_fp8_workspace_bytes(1, 100) == 0
-    assert lib.bl_fp8_workspace_bytes(5, 272) >= 5 * 272 + 5 * 3 * 4
+    assert lib.bl_fp8_workspace_bytes(0, 1, 128) == 0 and lib.bl_fp8_workspace_bytes(1, 1, 100) == 0
+    assert lib.bl_fp8_workspace_bytes(1, 0, 128) == 0
+    assert lib.bl_fp8_workspace_bytes(5, 64, 272) >= 5 * 272 + 5 * 3 * 4
+    assert lib.bl_fp8_workspace_bytes(64, 1024, 8192) >= 64 * 8192 + 64 * 64 * 4 + 2 * 64 * 1024 * 4   # K in parts
     assert lib.bl_fp8_experts_workspace_bytes(1, 256, 0, 4, 128) == 0
     assert lib.bl_fp8_experts_workspace_bytes(1, 256, 2, 4, 120) == 0
     small, large = (lib.bl_fp8_experts_workspace_bytes(m, 256, 2, 4, 128) for m in (1, 64))

@@ -171,6 +171,20 @@ def test_linear(M, N, K, out):
     assert torch.equal(y, two)
 
 
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(1100, 8200, 272), (520, 8200, 400), (500, 6600, 656), (500, 3300, 1040), (300, 2500, 912),
+                                   (40, 1000, 8208), (24, 28680, 400)])
+def test_linear_wide(M, N, K, out):
+    """Shapes of every tile that the product takes, odd rows, columns and blocks at their ends."""
+    say("fp8 linear wide", M, N, K, out)
+    x, v = act((M, K), "bf16", M)
+    wc, ws = weight(N, K, K)
+    y = tw.bl_fp8_forward(x, f8(wc), gpu(ws), out_dtype=TYPES[out])
+    c, s, _ = of.quant_act(v)
+    ref, mag = of.linear(c, s, wc, ws)
+    close(y, ref, (SUM[out] + (K // 128 + 4) * 2.0 ** -23) * mag, out, (M, N, K))
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 384, 1040), (16, 1000, 2064), (80, 640, 1152), (300, 513, 784)])
 def test_linear_results_keep_the_precision_of_their_type(M, N, K):
     """Far below the worst-case bounds: fp32 results within fp32 roundings of the magnitudes of
