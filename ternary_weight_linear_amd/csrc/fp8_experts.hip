@@ -181,6 +181,21 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, 
   }
 }
 
+template <bool EXACT>
+hipError_t start_up(const ProductArgs& p, int tile, int64_t nt, hipStream_t s) {
+  if (tile == 64) return start_gemm<GemmShape<256, 64, 4, 2, 3, EXACT, true>>(p, nt, s);
+  if constexpr (!EXACT)
+    if (tile == 256) return start_gemm<GemmShape<256, 256, 2, 4, 2, false, true>>(p, nt, s);
+  return start_gemm<GemmShape<256, 128, 2, 4, 2, EXACT, true>>(p, nt, s);
+}
+template <bool EXACT>
+hipError_t start_down(const ProductArgs& p, int tile, int64_t nt, hipStream_t s) {
+  if (tile == 64) return start_gemm<GemmShape<256, 64, 4, 2, 3, EXACT>>(p, nt, s);
+  if constexpr (!EXACT)
+    if (tile == 256) return start_gemm<GemmShape<256, 256, 2, 4, 2, false>>(p, nt, s);
+  return start_gemm<GemmShape<256, 128, 2, 4, 2, EXACT>>(p, nt, s);
+}
+
 }  // namespace
 
 int64_t experts_max_tiles(int64_t P, int64_t E, int tile) { return P / tile + (P < E ? P : E); }
@@ -225,10 +240,14 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   // instruction's sums (its error, 1.4e-5 of a block's, moves a few hidden codes: 1/2 of
   // bf16's rounding of the result, 4 times fp16's)
   const bool exact = a.xdtype != BL_BF16, exact_down = a.ydtype == BL_F32;
-  // rows per tile, by the average rows of an expert; the tiled kernel's offsets are 32 bits
-  const bool tiled = P > 48 * a.E && a.M * a.H < (int64_t(1) << 31) && 2 * a.I * a.H < (int64_t(1) << 31) &&
+  // Rows per tile, by the average rows of an expert. Measured, us for tiles of 16 / 64 / 128 / 256
+  // rows, 64 experts of 4096 x 1024, top 8, bf16: 16 rows an expert 209 / 207 / 229 / 257, 32 312 /
+  // 257 / 240 / 264, 64 526 / 266 / 299 / 277, 128 - / 383 / 352 / 374, 256 - / 618 / 540 / 461;
+  // 16 experts of 2048 x 1024, top 2: 32 56 / 37 / 45 / 52, 128 144 / 67 / 55 / 75. The tiled
+  // kernel's offsets are 32 bits.
+  const bool tiled = P > 16 * a.E && a.M * a.H < (int64_t(1) << 31) && 2 * a.I * a.H < (int64_t(1) << 31) &&
                      256 * a.I < (int64_t(1) << 31);
-  const int tile = !tiled ? (P <= 16 * a.E ? 16 : 64) : P <= 192 * a.E || exact || exact_down ? 128 : 256;
+  const int tile = !tiled ? 16 : P <= 96 * a.E ? 64 : P <= 192 * a.E || exact || exact_down ? 128 : 256;
   const int64_t nt = experts_max_tiles(P, a.E, tile);
   // few slots: a tile each, nothing to sort, and the rows are quantised where they are used
   constexpr int kStagedMost = 48 * 1024;
@@ -291,22 +310,16 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
     experts_place_kernel<<<sort.chunks, kSortThreads, sort_lds(a.E), s>>>(sort);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (tile <= 64) {
-    e = tile == 16 ? start_stream<1, 4, 8, kSrcCodes, kStreamGated>(up, nt, 0, s)
-                   : start_stream<4, 2, 8, kSrcCodes, kStreamGated>(up, nt, 0, s);
+  if (tile == 16) {
+    e = start_stream<1, 4, 8, kSrcCodes, kStreamGated>(up, nt, 0, s);
     if (e != hipSuccess) return e;
     e = launch_fp8_quant_act(h, BL_F32, P, a.I, a.I, 0, head, hq, hs, s);
     if (e != hipSuccess) return e;
-    e = tile == 16 ? start_stream<1, 4, 8, kSrcCodes, kStreamLinear>(down, nt, 0, s)
-                   : start_stream<4, 2, 8, kSrcCodes, kStreamLinear>(down, nt, 0, s);
+    e = start_stream<1, 4, 8, kSrcCodes, kStreamLinear>(down, nt, 0, s);
   } else {
-    e = exact         ? start_gemm<GemmShape<256, 128, 2, 4, 2, true, true>>(up.p, nt, s)
-        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, 2, false, true>>(up.p, nt, s)
-                      : start_gemm<GemmShape<256, 256, 2, 4, 2, false, true>>(up.p, nt, s);
+    e = exact ? start_up<true>(up.p, tile, nt, s) : start_up<false>(up.p, tile, nt, s);
     if (e != hipSuccess) return e;
-    e = exact_down    ? start_gemm<GemmShape<256, 128, 2, 4, 2, true>>(down.p, nt, s)
-        : tile == 128 ? start_gemm<GemmShape<256, 128, 2, 4, 2, false>>(down.p, nt, s)
-                      : start_gemm<GemmShape<256, 256, 2, 4, 2, false>>(down.p, nt, s);
+    e = exact_down ? start_down<true>(down.p, tile, nt, s) : start_down<false>(down.p, tile, nt, s);
   }
   if (e != hipSuccess) return e;
   const int vec = vec_rows(a.y, a.ldy, a.ydtype);

@@ -314,9 +314,13 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
     if constexpr (MODE == kStreamSlots) {
       st.row = it / KB;
       kb = it - st.row * KB;
-      int e = s.index[first + st.row];
+      // uniform loads through the scalar cache: a vector load here would put its latency before
+      // that of the weights it leads to
+      using ConstInt = const __attribute__((address_space(4))) int32_t;
+      using ConstFloat = const __attribute__((address_space(4))) float;
+      int e = ((ConstInt*)s.index)[first + st.row];
       st.some = e >= 0 && e < s.E;
-      weigh = s.weight[first + st.row];
+      weigh = ((ConstFloat*)s.weight)[first + st.row];
       e = st.some ? e : 0;
       wo = e * p.w_stride;
       so = e * p.sw_stride;
@@ -365,7 +369,13 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
     }
   };
 
-  Stage st;
+  // kStreamSlots runs one workgroup per CU: two blocks per wave are read at a time
+  constexpr int D = MODE == kStreamSlots ? 2 : 1;
+  Stage st[D];
+  auto load_all = [&](int it) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(st[d], min(it + d * S, items - 1));
+  };
   if constexpr (SRC != kSrcCodes) {
     // 16 lanes per block of 128 values, as in fp8_quant_act_kernel; the first pass's loads go
     // out before the first weights', so that waiting for them does not wait for those
@@ -391,7 +401,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
     constexpr int step = kStreamThreads / 16;
     const int b0 = threadIdx.x >> 4;
     fetch(b0);
-    load(st, min(range, items - 1));
+    load_all(range);
     put(b0);
     for (int b = b0 + step; b - b0 < blocks; b += step) {
       fetch(b);
@@ -399,11 +409,13 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
     }
     __syncthreads();
   } else {
-    load(st, min(range, items - 1));
+    load_all(range);
   }
-  for (int it = range; it < items; it += S) {
-    if (it > range) load(st, it);
-    multiply(st);
+  for (int it = range; it < items; it += D * S) {
+    if (it > range) load_all(it);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (it + d * S < items) multiply(st[d]);
   }
 
   auto finish = [&](int64_t n, int t, f32x4 r, const f32x4& up) __attribute__((always_inline)) {
