@@ -369,8 +369,8 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
     }
   };
 
-  // kStreamSlots runs one workgroup per CU: two blocks per wave are read at a time
-  constexpr int D = MODE == kStreamSlots ? 2 : 1;
+  // kStreamSlots runs one workgroup per CU: four blocks per wave are read at a time
+  constexpr int D = MODE == kStreamSlots ? 4 : 1;
   Stage st[D];
   auto load_all = [&](int it) __attribute__((always_inline)) {
 #pragma unroll
@@ -381,31 +381,33 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
     // out before the first weights', so that waiting for them does not wait for those
     const int blocks = staged_rows * KB;
     using T = typename Elem<SRC == kSrcCodes ? 0 : SRC>::type;
-    float v[8];
-    auto fetch = [&](int b) __attribute__((always_inline)) {
+    constexpr int step = kStreamThreads / 16, P = 2;   // blocks per pass, passes loaded ahead
+    float v[P][8];
+    auto fetch = [&](int b, float (&x)[8]) __attribute__((always_inline)) {
       const int r = b / KB, k = (b - r * KB) * kFp8Block + (threadIdx.x & 15) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
       int64_t at = first + r;
       if (MODE != kStreamSlots && p.map.gather_div > 0) at /= p.map.gather_div;
-      if (b < blocks && k < a.K) load8<SRC == kSrcCodes ? 0 : SRC>(static_cast<const T*>(s.x) + at * s.ldx + k, v);
+      if (b < blocks && k < a.K) load8<SRC == kSrcCodes ? 0 : SRC>(static_cast<const T*>(s.x) + at * s.ldx + k, x);
     };
-    auto put = [&](int b) __attribute__((always_inline)) {
-      const float am = __uint_as_float(block_top(v));
+    auto put = [&](int b, const float (&x)[8]) __attribute__((always_inline)) {
+      const float am = __uint_as_float(block_top(x));
       if (b >= blocks) return;
       const int r = b / KB, kb = b - r * KB;
       *reinterpret_cast<u32x2*>(staged + r * staged_row(KB) + kb * kFp8Block + (threadIdx.x & 15) * 8) =
-          pack8(v, code_factor(am));
+          pack8(x, code_factor(am));
       if ((threadIdx.x & 15) == 0) const_cast<float*>(staged_scale)[b] = am / kFp8Max;
     };
-    constexpr int step = kStreamThreads / 16;
     const int b0 = threadIdx.x >> 4;
-    fetch(b0);
+#pragma unroll
+    for (int i = 0; i < P; ++i) fetch(b0 + i * step, v[i]);
     load_all(range);
-    put(b0);
-    for (int b = b0 + step; b - b0 < blocks; b += step) {
-      fetch(b);
-      put(b);
+#pragma unroll
+    for (int i = 0; i < P; ++i) put(b0 + i * step, v[i]);
+    for (int b = b0 + P * step; b - b0 < blocks; b += step) {
+      fetch(b, v[0]);
+      put(b, v[0]);
     }
     __syncthreads();
   } else {
