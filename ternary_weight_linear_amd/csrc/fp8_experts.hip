@@ -119,15 +119,15 @@ __global__ __launch_bounds__(kSortThreads) void experts_place_kernel(SortArgs a)
   extern __shared__ int lds[];                     // [2, E]
   const int chunk = blockIdx.x;
   int *cnt = lds, *next = lds + a.E;
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
-    int all = 0, before = 0;
-    for (int c = 0; c < a.chunks; ++c) {
-      const int n = a.counts[c * a.E + e];
-      all += n;
-      before += c < chunk ? n : 0;
-    }
-    cnt[e] = all;
-    next[e] = before;
+  for (int i = threadIdx.x; i < 2 * a.E; i += kSortThreads) lds[i] = 0;
+  __syncthreads();
+  // the table is read as it lies, several words of it in flight per thread
+  const int before = chunk * a.E;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < a.chunks * a.E; i += kSortThreads) {
+    const int n = a.counts[i], e = i % a.E;
+    atomicAdd(&cnt[e], n);
+    if (i < before) atomicAdd(&next[e], n);
   }
   __syncthreads();
   place_slots(a, chunk, cnt, next);

@@ -217,20 +217,23 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   struct Weigh {
     float w[S::NF];
   };
-  // Block kb into a stage; past the last block, zeros (no memory is read)
-  auto stage = [&](int kb, uint8_t* ta, uint8_t* tb, float (*ts)[64], Weigh& sc) __attribute__((always_inline)) {
+  // Copy n (of COPIES) of block kb into a stage; past the last block, zeros (no memory is read)
+  auto copy = [&](int n, int kb, uint8_t* ta, uint8_t* tb, float (*ts)[64]) __attribute__((always_inline)) {
     const bool skip = kb >= blocks || (cut && kb == KB - 1);
     const uint32_t k0 = static_cast<uint32_t>(kb) * kFp8Block;
+    if (n < S::CA) copy16_to_lds(ba, skip ? kOutside : oa[n], k0, ta + 1024 * (n * S::WAVES + wave));
+    else if (n < S::CA + S::CB) copy16_to_lds(bb, skip ? kOutside : ob[n - S::CA], k0, tb + 1024 * ((n - S::CA) * S::WAVES + wave));
+    else copy4_to_lds(make_buffer(a.sx + min(kb, blocks - 1) * a.M), os, ts[wave]);
+  };
+  auto weigh = [&](int kb, Weigh& sc) __attribute__((always_inline)) {
+    kb = min(kb, blocks - 1);
+    sc.w[0] = sw[kb];
+    if constexpr (S::GATED) sc.w[1] = sw[up_scales + kb];
+  };
+  auto stage = [&](int kb, uint8_t* ta, uint8_t* tb, float (*ts)[64], Weigh& sc) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < S::CA; ++i)
-      copy16_to_lds(ba, skip ? kOutside : oa[i], k0, ta + 1024 * (i * S::WAVES + wave));
-#pragma unroll
-    for (int i = 0; i < S::CB; ++i)
-      copy16_to_lds(bb, skip ? kOutside : ob[i], k0, tb + 1024 * (i * S::WAVES + wave));
-    const int ks = min(kb, blocks - 1);
-    copy4_to_lds(make_buffer(a.sx + ks * a.M), os, ts[wave]);
-    sc.w[0] = sw[ks];
-    if constexpr (S::GATED) sc.w[1] = sw[up_scales + ks];
+    for (int n = 0; n < S::COPIES; ++n) copy(n, kb, ta, tb, ts);
+    weigh(kb, sc);
   };
 
   const uint32_t in_row = u * 128 + 16 * (g ^ (u & 7));
@@ -239,7 +242,13 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   f32x4 acc[S::TN][S::TM] = {};
   // One block of inputs. While the matrix cores multiply weight fragment i by the TM fragments
   // of q, the products of fragment i - 1 are scaled and added (VALU) and fragment i + 1 is read.
-  auto compute = [&](const uint8_t* ta, const uint8_t* tb, const float (*ts)[64], const Weigh& sc) __attribute__((always_inline)) {
+  // With two stages the next block's copies go out between the first half of the products, not
+  // ahead of the reads of LDS (2048 x 8192 x 8192: 115 -> 112 us, fp16 operands 1550 -> 1519);
+  // with more stages they go out first (spread over the products 128 x 8192 x 8192 took 37 us
+  // instead of 26).
+  auto compute = [&](const uint8_t* ta, const uint8_t* tb, const float (*ts)[64], const Weigh& sc, int next,
+                     uint8_t* na, uint8_t* nb, float (*ns)[64]) __attribute__((always_inline)) {
+    constexpr int PER = (S::COPIES + (S::TN + 1) / 2 - 1) / ((S::TN + 1) / 2);
     float f[S::NF][S::TM];
 #pragma unroll
     for (int j = 0; j < S::TM; ++j) {
@@ -255,6 +264,10 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
 #pragma unroll
     for (int i = 0; i <= S::TN; ++i) {
       if (i + 1 < S::TN) w[(i + 1) & 1] = read_operand<S::EXACT>(ta + 2048 * (i + 1), wa, wa2);
+      if constexpr (S::NS == 2) {
+#pragma unroll
+        for (int n = i * PER; n < (i + 1) * PER && n < S::COPIES; ++n) copy(n, next, na, nb, ns);
+      }
       if (i < S::TN) {
         if constexpr (S::EXACT) {
           // the four instructions of a sum depend on each other: those of the TM sums take turns
@@ -301,8 +314,9 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   {                                                          \
     wait_copies<S::COPIES * (S::NS - 2)>();                  \
     meet();                                                  \
-    stage((KB_) + S::NS - 1, NA, NB, NSC, NW);               \
-    if (busy) compute(A, B, SC, W);                          \
+    if (S::NS > 2 || !busy) stage((KB_) + S::NS - 1, NA, NB, NSC, NW); \
+    else weigh((KB_) + S::NS - 1, NW);                       \
+    if (busy) compute(A, B, SC, W, (KB_) + S::NS - 1, NA, NB, NSC); \
   }
   if constexpr (S::NS == 2) {
     for (; kb + 2 <= blocks; kb += 2) {
