@@ -249,9 +249,13 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
                      256 * a.I < (int64_t(1) << 31);
   const int tile = !tiled ? 16 : P <= 96 * a.E ? 64 : P <= 192 * a.E || exact || exact_down ? 128 : 256;
   const int64_t nt = experts_max_tiles(P, a.E, tile);
-  // few slots: a tile each, nothing to sort, and the rows are quantised where they are used
+  // Few slots, most of them of different experts: a tile each, nothing to sort, and the rows are
+  // quantised where they are used: two launches for five. A matrix that several slots share is
+  // read once for each, so this ends where slots meet (us, this way / sorted, matrices of
+  // 4096 x 1024: 24 slots of 64 experts 54 / 63, 32 of 64 75 / 67, 16 of 16 55 / 39, 8 of 16
+  // 28 / 31, 8 of 4 31 / 30).
   constexpr int kStagedMost = 48 * 1024;
-  const bool direct = (4 * P <= a.E || P <= 16) && a.H <= kStagedMost && a.k * a.I <= kStagedMost &&
+  const bool direct = (8 * P <= 3 * a.E || P <= 8) && a.H <= kStagedMost && a.k * a.I <= kStagedMost &&
                       staged_bytes(1, static_cast<int>(HB)) <= kStagedMost &&
                       staged_bytes(static_cast<int>(a.k), static_cast<int>(IB)) <= kStagedMost;
 

@@ -154,6 +154,7 @@ struct StreamArgs {
   const int32_t* index;    // direct tiles: tile t is slot t, its expert index[t]; null: as p.map says
   const float* weight;     // kStreamSlots
   int E, k;
+  int blocks_n;            // workgroups along the columns; the grid runs over these first
 };
 
 constexpr int kStreamWaves = 8;
@@ -238,10 +239,11 @@ __device__ __forceinline__ void quant_blocks(const QuantArgs& a, int64_t first) 
 // each other's latency: keeping a second block's loads in flight per wave measured slower in
 // every shape (more registers, a block too many read at the end). Workgroups start at different
 // blocks (rot): weight rows are usually a power of two apart, and all workgroups at the same
-// input would meet in a few of the memory's channels.
+// input would meet in a few of the memory's channels. The fp16 instruction costs nothing here:
+// with the e4m3 one the times are the same.
 // Measured, us (weight bytes / time): 1 x 8192 x 8192 12.3 (5.4 TB/s), 16 x 8192 x 8192 14.2,
 // 16 x 28672 x 8192 43.8 (5.4 TB/s), 1 x 28672 x 8192 39.6 (5.9 TB/s).
-template <int MT, int NT, int S, int SRC, int MODE, bool EXACT>
+template <int MT, int NT, int S, int SRC, int MODE>
 __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s) {
   constexpr bool GATED = MODE == kStreamGated;
   constexpr int G = kStreamWaves / S;               // groups of weight rows
@@ -253,22 +255,23 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, u = lane & 15;
   const int range = wave % S, group = wave / S;
-  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * G + group) * (16 * NC);
-  int64_t first = static_cast<int64_t>(blockIdx.y) * (16 * MT);
+  const int by = blockIdx.x / s.blocks_n, bx = blockIdx.x - by * s.blocks_n;
+  const int64_t n0 = (static_cast<int64_t>(bx) * G + group) * (16 * NC);
+  int64_t first = static_cast<int64_t>(by) * (16 * MT);
   int rows = 0, expert = 0;
   if constexpr (MODE == kStreamSlots) {
-    first = static_cast<int64_t>(blockIdx.y) * s.k;
+    first = static_cast<int64_t>(by) * s.k;
     rows = 1;
   } else if (s.index) {
-    first = blockIdx.y;
+    first = by;
     rows = 1;
     expert = s.index[first];
     if (expert < 0 || expert >= s.E) return;
   } else if (p.map.tiles) {
-    if (static_cast<int>(blockIdx.y) >= *p.map.n_tiles) return;
-    expert = p.map.tiles[4 * blockIdx.y];
-    first = p.map.tiles[4 * blockIdx.y + 1];
-    rows = p.map.tiles[4 * blockIdx.y + 2];
+    if (by >= *p.map.n_tiles) return;
+    expert = p.map.tiles[4 * by];
+    first = p.map.tiles[4 * by + 1];
+    rows = p.map.tiles[4 * by + 2];
   } else {
     rows = static_cast<int>(a.M - first < 16 * MT ? a.M - first : 16 * MT);
   }
@@ -305,7 +308,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
   // kStreamSlots: item it is block it % KB of slot it / KB; a slot that names no expert is read
   // at expert 0 (in bounds) and left out of the sum
   const int items = MODE == kStreamSlots ? s.k * KB : KB;
-  const int rot = MODE == kStreamSlots ? 0 : static_cast<int>(blockIdx.x % KB);
+  const int rot = MODE == kStreamSlots ? 0 : bx % KB;
   auto load = [&](Stage& st, int it) __attribute__((always_inline)) {
     int kb = it + rot < KB || MODE == kStreamSlots ? it + rot : it + rot - KB;
     int64_t wo = 0, so = 0;
@@ -347,23 +350,23 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
     if constexpr (MODE == kStreamSlots) {
       if (!st.some) return;
     }
-    Operand<EXACT> q[MT];
+    FragH q[MT];
     float sx[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       if constexpr (SRC == kSrcCodes) {
-        q[t] = operand<EXACT>(st.q[t]);
+        q[t] = to_half(st.q[t]);
         sx[t] = st.sx[t];
       } else {
         const int r = MODE == kStreamSlots ? st.row : min(u, rows - 1);
         const uint8_t* at = staged + r * staged_row(KB) + st.kb * kFp8Block + 16 * g;
-        q[t] = operand<EXACT>(Frag{*reinterpret_cast<const u32x4*>(at), *reinterpret_cast<const u32x4*>(at + 64)});
+        q[t] = to_half(Frag{*reinterpret_cast<const u32x4*>(at), *reinterpret_cast<const u32x4*>(at + 64)});
         sx[t] = staged_scale[r * KB + st.kb];
       }
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const Operand<EXACT> w = operand<EXACT>(st.w[i]);
+      const FragH w = to_half(st.w[i]);
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[i][t] += block_dot(w, q[t]) * (sx[t] * st.sw[i]);
     }
@@ -427,7 +430,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
     }
     if (16 * t + u >= rows) return;
     int64_t at = first + 16 * t + u;
-    if constexpr (MODE == kStreamSlots) at = blockIdx.y;
+    if constexpr (MODE == kStreamSlots) at = by;
     else if (p.map.scatter) at = p.map.pair[at];
     store4(a, at, n + 4 * g, r);
   };
@@ -446,17 +449,19 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
       return sum;
     };
     const f32x4 r = total(i);
-    finish((static_cast<int64_t>(blockIdx.x) * G + gr) * (16 * NC) + 16 * i, t, r, GATED ? total(i + NC) : r);
+    finish((static_cast<int64_t>(bx) * G + gr) * (16 * NC) + 16 * i, t, r, GATED ? total(i + NC) : r);
   }
 }
 
 // Starts the kernel over the columns of w and `tiles` tiles of rows; staged: rows to quantise.
-template <int MT, int NT, int S, int SRC, int MODE, bool EXACT = true>
+template <int MT, int NT, int S, int SRC, int MODE>
 hipError_t start_stream(const StreamArgs& st, int64_t tiles, int staged, hipStream_t s) {
   constexpr int cols = 16 * NT * (kStreamWaves / S) / (MODE == kStreamGated ? 2 : 1);
   const int lds = SRC == kSrcCodes ? 0 : staged_bytes(staged, static_cast<int>(fp8_blocks(st.p.a.K)));
-  const dim3 grid(static_cast<uint32_t>((st.p.a.N + cols - 1) / cols), static_cast<uint32_t>(tiles));
-  fp8_stream_kernel<MT, NT, S, SRC, MODE, EXACT><<<grid, kStreamThreads, lds, s>>>(st);
+  StreamArgs a = st;
+  a.blocks_n = static_cast<int>((st.p.a.N + cols - 1) / cols);
+  const dim3 grid(static_cast<uint32_t>(a.blocks_n * tiles));
+  fp8_stream_kernel<MT, NT, S, SRC, MODE><<<grid, kStreamThreads, lds, s>>>(a);
   return hipGetLastError();
 }
 template <int NT, int S, int MODE>

@@ -512,3 +512,14 @@ def test_route_and_experts_together():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, step())
+
+
+def test_example_runs_the_operators_together(capsys):
+    """The example's layer, prompt and decode; quantising activations to 3 bits of mantissa twice
+    leaves about 2 x 2^-4 / sqrt(3) x sqrt(2) = 0.1 of each product's size at most."""
+    say("example")
+    import examples.experts_decode as ex
+    error = ex.main(["--hidden", "512", "--inner", "272", "--experts", "16", "--top", "4", "--groups", "4",
+                     "--kept-groups", "2", "--prompt", "40", "--tokens", "3"])
+    assert 0 < error < 0.1
+    assert "us per token" in capsys.readouterr().out
