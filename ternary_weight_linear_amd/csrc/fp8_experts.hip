@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kSortThreads) void experts_place_kernel(SortArgs a)
 // fp16: 65 us).
 template <bool HALF>
 __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, const void* __restrict__ part,
-                                                              const float* __restrict__ scale, int vec) {
+                                                              const float* __restrict__ scale) {
   constexpr int V = HALF ? 8 : 4;
   const int64_t m = blockIdx.x, P = a.M * a.k;
   const int64_t n = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * V;
@@ -176,7 +176,6 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, 
     o.y = a.y;
     o.ldy = a.ldy;
     o.ydtype = a.ydtype;
-    o.vec = vec;
     store4(o, m, n + i, f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]});
   }
 }
@@ -261,7 +260,7 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
 
   // gate and up: silu(gate) * up of every sorted row, in fp32 (streamed) or as codes (tiled)
   StreamArgs up{};
-  up.p.a = Fp8LinearArgs{q, sx, a.wgu, a.sgu, a.M, a.I, a.H, h, a.I, BL_F32, 1};
+  up.p.a = Fp8LinearArgs{q, sx, a.wgu, a.sgu, a.M, a.I, a.H, h, a.I, BL_F32};
   up.p.map = RowMap{tiles, head + 1, direct ? nullptr : pair, static_cast<int>(a.k), 0};
   up.p.w_stride = 2 * a.I * a.H;
   up.p.sw_stride = 2 * IB * HB;
@@ -278,7 +277,7 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   // the bytes to write and read back.
   const bool half_parts = tile >= 128 && a.ydtype == BL_BF16;
   auto* part_scale = reinterpret_cast<float*>(ws + L.ps_off);
-  down.p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, half_parts ? kPartType : BL_F32, 1, 1};
+  down.p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, half_parts ? kPartType : BL_F32};
   down.p.part_scale = part_scale;
   down.p.map = RowMap{tiles, head + 1, pair, 0, 1};
   down.p.w_stride = a.H * a.I;
@@ -295,7 +294,6 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
     down.p.a.y = a.y;
     down.p.a.ydtype = a.ydtype;
     down.p.a.ldy = a.ldy;
-    down.p.a.vec = vec_rows(a.y, a.ldy, a.ydtype);
     e = start_stream_x<2, 8, kStreamGated>(up, a.xdtype, P, 1, s);
     if (e != hipSuccess) return e;
     return start_stream<1, 1, 8, BL_F32, kStreamSlots>(down, a.M, static_cast<int>(a.k), s);
@@ -326,11 +324,10 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
     e = exact_down ? start_down<true>(down.p, tile, nt, s) : start_down<false>(down.p, tile, nt, s);
   }
   if (e != hipSuccess) return e;
-  const int vec = vec_rows(a.y, a.ldy, a.ydtype);
   const uint32_t per = half_parts ? 2048 : 1024;
   const dim3 grid(static_cast<uint32_t>(a.M), static_cast<uint32_t>((a.H + per - 1) / per));
-  if (half_parts) experts_combine_kernel<true><<<grid, 256, 0, s>>>(a, part, part_scale, vec);
-  else experts_combine_kernel<false><<<grid, 256, 0, s>>>(a, part, nullptr, vec);
+  if (half_parts) experts_combine_kernel<true><<<grid, 256, 0, s>>>(a, part, part_scale);
+  else experts_combine_kernel<false><<<grid, 256, 0, s>>>(a, part, nullptr);
   return hipGetLastError();
 }
 

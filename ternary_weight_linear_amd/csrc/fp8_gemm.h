@@ -105,14 +105,8 @@ __device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&a
       const int row = 16 * (j - jj) + u;
 #pragma unroll
       for (int i = 0; i < S::TN; ++i) {
-        u32x2 b;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float v0 = acc[i][j][2 * h] * f, v1 = acc[i][j][2 * h + 1] * f;
-          const uint32_t lo = a.ydtype == BL_BF16 ? bf16_bits(v0) : half_bits(v0);
-          const uint32_t hi = a.ydtype == BL_BF16 ? bf16_bits(v1) : half_bits(v1);
-          b[h] = lo | hi << 16;
-        }
+        const u32x2 b = {pack16(a.ydtype, acc[i][j][0] * f, acc[i][j][1] * f),
+                         pack16(a.ydtype, acc[i][j][2] * f, acc[i][j][3] * f)};
         *reinterpret_cast<u32x2*>(room + row * 256 + 16 * ((2 * i + (g >> 1)) ^ u) + 8 * (g & 1)) = b;
       }
     }
@@ -121,12 +115,19 @@ __device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&a
     for (int t = 0; t < 8; ++t) {
       const int row = 4 * t + g, r = wm + 16 * jj + row;
       const u32x4 b = *reinterpret_cast<const u32x4*>(room + row * 256 + 16 * (u ^ (row & 15)));
-      if (r >= rows || n + 8 * u >= a.N) continue;   // N % 8 == 0: all eight or none
+      if (r >= rows || n + 8 * u >= a.N) continue;
       int64_t at = first + r;
       if (p.map.scatter) at = p.map.pair[at];
+      uint16_t* to = static_cast<uint16_t*>(a.y) + at * a.ldy + n + 8 * u;
       // non-temporal: all CUs store at once, and 128 KB each would turn over the L2 (8192 x 8192 x
       // 1024: 98 us with ordinary stores, 94)
-      __builtin_nontemporal_store(b, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.y) + at * a.ldy + n + 8 * u));
+      if (n + 8 * u + 7 < a.N) {
+        __builtin_nontemporal_store(b, reinterpret_cast<u32x4_at2*>(to));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + 8 * u + e < a.N) to[e] = static_cast<uint16_t>(b[e / 2] >> (16 * (e & 1)));
+      }
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     return;
   }
   if constexpr (S::WIDE) {
-    if (a.ydtype != BL_F32 && a.vec8) {
+    if (a.ydtype != BL_F32) {
       store_wide<S>(p, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * 8192, first, rows, wm, n0 + wn, lane);
       return;
     }
@@ -415,8 +416,11 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(Fp8LinearArgs a, const f
   f32x4 sum = {0, 0, 0, 0};
   for (int z = 0; z < parts; ++z) {
     const float* p = part + (static_cast<int64_t>(z) * a.M + m) * a.N + n;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] += n + e < a.N ? p[e] : 0.0f;
+    if (n + 3 < a.N) {
+      sum += *reinterpret_cast<const f32x4_at4*>(p);
+    } else {
+      for (int e = 0; n + e < a.N; ++e) sum[e] += p[e];
+    }
   }
   store4(a, m, n, sum);
 }
@@ -438,7 +442,6 @@ hipError_t start_split_gemm(const ProductArgs& p, int parts, float* part, hipStr
   q.a.y = part;
   q.a.ldy = p.a.N;
   q.a.ydtype = BL_F32;
-  q.a.vec = p.a.N % 4 == 0;
   fp8_gemm_kernel<S><<<dim3(static_cast<uint32_t>(tiles_n * tiles_m), static_cast<uint32_t>(parts)), S::THREADS, 0, s>>>(
       q, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
   const hipError_t e = hipGetLastError();

@@ -27,16 +27,7 @@ struct Fp8LinearArgs {
   void* y;               // [M, N], rows ldy elements apart
   int64_t ldy;
   int ydtype;
-  int vec = 0;           // four consecutive values of y can be written at once
-  int vec8 = 0;          // eight of 16 bits, in every row to its end
 };
-// Whether rows ldy apart at y take aligned stores of four values.
-inline int vec_rows(const void* y, int64_t ldy, int dtype) {
-  return ldy % 4 == 0 && reinterpret_cast<uintptr_t>(y) % (4 * dtype_bytes(dtype)) == 0;
-}
-inline int vec8_rows(const void* y, int64_t n, int64_t ldy) {
-  return n % 8 == 0 && ldy % 8 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
-}
 // Besides bl_dtype: the experts' outputs before their weighted sum, as scaled fp16.
 constexpr int kPartType = 3;
 

@@ -92,11 +92,8 @@ int fp8_split_parts(int64_t M, int64_t N, int64_t K) {
   return static_cast<int>((KB + per - 1) / per);    // none empty
 }
 
-hipError_t launch_fp8_linear(const Fp8LinearArgs& args, const void* x, int xdtype, int64_t ldx, float* part,
+hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const void* x, int xdtype, int64_t ldx, float* part,
                              hipStream_t s) {
-  Fp8LinearArgs a = args;
-  a.vec = vec_rows(a.y, a.ldy, a.ydtype);
-  a.vec8 = vec8_rows(a.y, a.N, a.ldy);
   StreamArgs st{};
   st.p.a = a;
   st.x = x;

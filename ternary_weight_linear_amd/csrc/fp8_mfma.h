@@ -116,22 +116,24 @@ struct ProductArgs {
   float* part_scale;             // y of kPartType: [ceil(N / 128), rows of y]
 };
 
-// Four consecutive outputs of a row, in one store where y's rows allow it (a.vec).
+// Vectors at any multiple of their element's size: global memory takes unaligned accesses.
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+
+__device__ __forceinline__ uint32_t pack16(int dtype, float lo, float hi) {
+  return dtype == BL_BF16 ? bf16_bits(lo) | static_cast<uint32_t>(bf16_bits(hi)) << 16
+                          : half_bits(lo) | static_cast<uint32_t>(half_bits(hi)) << 16;
+}
+
+// Four consecutive outputs of a row, in one store where the row has them all.
 __device__ __forceinline__ void store4(const Fp8LinearArgs& a, int64_t row, int64_t n, const f32x4& v) {
   const int64_t at = row * a.ldy + n;
-  if (a.vec && n + 3 < a.N) {
-    if (a.ydtype == BL_F32) {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = v;
-    } else {
-      u32x2 b;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = a.ydtype == BL_BF16 ? bf16_bits(v[2 * i]) : half_bits(v[2 * i]);
-        const uint32_t hi = a.ydtype == BL_BF16 ? bf16_bits(v[2 * i + 1]) : half_bits(v[2 * i + 1]);
-        b[i] = lo | hi << 16;
-      }
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = b;
-    }
+  if (n + 3 < a.N) {
+    if (a.ydtype == BL_F32) *reinterpret_cast<f32x4_at4*>(static_cast<float*>(a.y) + at) = v;
+    else
+      *reinterpret_cast<u32x2_at2*>(static_cast<uint16_t*>(a.y) + at) =
+          u32x2{pack16(a.ydtype, v[0], v[1]), pack16(a.ydtype, v[2], v[3])};
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)

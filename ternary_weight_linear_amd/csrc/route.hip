@@ -2,8 +2,8 @@
 // their weights. The contract is bl_route_experts in include/libbitlinear.h.
 //
 // Two kernels. route_row16_kernel gives a row 16 lanes (a DPP row) and keeps its experts in
-// registers, a contiguous run per lane: what a row needs of all its experts is four DPP steps.
-// It takes E <= 512, k <= 16 and groups that are whole lanes, a power of two of them;
+// registers, a contiguous run per lane and no lane in two groups: what a row needs of all its
+// experts is four DPP steps. It takes up to 32 experts per lane, k <= 16 and 16 groups;
 // route_kernel, one wave per row with the choices in LDS, takes the rest.
 #include "fp8_internal.h"
 
@@ -91,23 +91,27 @@ __device__ __forceinline__ float from_ordered(uint32_t b) {
   return __uint_as_float(b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
 }
 
-// Lane j of a row holds experts j C .. j C + C - 1, C = ceil(E / 16) <= NE; groups are 2^shift
-// lanes. Choice values are kept as unsigned keys in their order, 0 for what cannot be chosen.
+// A group has 2^shift lanes of C <= NE experts each (without groups all 16 lanes): lane j holds
+// experts e0 = (j >> shift) size + (j % 2^shift) C .. of its group, as far as that goes. Choice
+// values are kept as unsigned keys in their order, 0 for what cannot be chosen.
 // VALU work bounds it: the scores (an exponential and a division each) and, per round, two
 // passes over the lane's NE keys.
 template <int DT, int NE>
 __global__ __launch_bounds__(256) void route_row16_kernel(RouteArgs a, int C, int shift, int vec) {
-  __shared__ float scores[16][16 * NE + 16];        // expert C j + i of a row at 16 i + j
+  __shared__ float scores[16][16 * NE + 16];        // expert e0 + i of lane j at 16 i + j
   __shared__ uint32_t chosen[16][16];               // place in scores, expert
   const uint32_t lane = threadIdx.x & 15, in = threadIdx.x >> 4;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + in;
   const int64_t mc = m < a.M ? m : a.M - 1;         // rows past the end work on the last one
-  const int E = static_cast<int>(a.E), e0 = static_cast<int>(lane) * C;
+  const int E = static_cast<int>(a.E), size = E / a.groups;
+  const int group = static_cast<int>(lane) >> shift, within = (static_cast<int>(lane) & ((1 << shift) - 1)) * C;
+  const int e0 = group * size + within;
+  const int mine_n = group < a.groups ? min(C, size - within) : 0;   // may be negative
   const float none = -INFINITY;
   using T = typename Elem<DT>::type;
   const T* row = static_cast<const T*>(a.logits) + mc * a.ld;
   float c[NE], bias[NE] = {};                       // no bias adds 0, which changes nothing
-  if (vec) {                                        // C == NE, whole and aligned pieces
+  if (vec) {                                        // every lane has NE, whole and aligned pieces
     constexpr int V = 16 / sizeof(T);
 #pragma unroll
     for (int i = 0; i < NE / V; ++i) {
@@ -137,7 +141,7 @@ __global__ __launch_bounds__(256) void route_row16_kernel(RouteArgs a, int C, in
       for (int i = 0; i < NE; ++i) bias[i] = a.bias[min(e0 + i, E - 1)];
     }
 #pragma unroll
-    for (int i = 0; i < NE; ++i) c[i] = i < C && e0 + i < E ? c[i] : none;
+    for (int i = 0; i < NE; ++i) c[i] = i < mine_n ? c[i] : none;
   }
 #pragma unroll
   for (int i = 0; i < NE; ++i) c[i] = c[i] > none ? fminf(c[i], 3.402823466e38f) : none;   // NaN compares false
@@ -362,15 +366,15 @@ hipError_t start_row16(const RouteArgs& a, int C, int shift, hipStream_t s) {
 
 template <int DT>
 hipError_t start_route(const RouteArgs& a, hipStream_t s) {
-  const int C = static_cast<int>((a.E + 15) / 16);
-  const int64_t size = a.E / a.groups;
-  int shift = 0;
-  while (shift < 3 && (size >> shift) > C) ++shift;
-  if (a.E <= 512 && a.k <= 16 && (a.groups == 1 || size == int64_t(C) << shift)) {
+  int shift = 4;                                    // lanes per group: the most that 16 lanes have
+  while (shift >= 0 && (a.groups << shift) > 16) --shift;
+  if (shift >= 0 && a.k <= 16) {
+    const int64_t size = a.E / a.groups;
+    const int C = static_cast<int>((size + (1 << shift) - 1) >> shift);
     if (C <= 4) return start_row16<DT, 4>(a, C, shift, s);
     if (C <= 8) return start_row16<DT, 8>(a, C, shift, s);
     if (C <= 16) return start_row16<DT, 16>(a, C, shift, s);
-    return start_row16<DT, 32>(a, C, shift, s);
+    if (C <= 32) return start_row16<DT, 32>(a, C, shift, s);
   }
   const dim3 grid(static_cast<uint32_t>((a.M + kRouteWaves - 1) / kRouteWaves));
   route_kernel<DT><<<grid, 64 * kRouteWaves, static_cast<size_t>(kRouteWaves) * 2 * a.E * 4, s>>>(a);

@@ -313,7 +313,9 @@ def grid_logits(M, E, seed):
 
 
 ROUTES = [(1, 1, 1, 1, 1), (1, 256, 8, 8, 4), (7, 60, 4, 1, 1), (33, 64, 6, 8, 3), (5, 100, 64, 1, 1), (130, 512, 8, 16, 4),
-          (3, 2048, 10, 64, 9), (9, 24, 3, 12, 5), (4, 65, 65 - 2, 1, 1), (6, 8, 2, 8, 2)]
+          (3, 2048, 10, 64, 9), (9, 24, 3, 12, 5), (4, 65, 65 - 2, 1, 1), (6, 8, 2, 8, 2),
+          (18, 120, 5, 8, 6), (5, 428, 4, 4, 2), (9, 264, 2, 8, 6), (3, 300, 16, 12, 4), (20, 406, 4, 2, 1), (2, 640, 9, 1, 1),
+          (5, 51, 7, 3, 2), (4, 544, 3, 17, 6)]
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
