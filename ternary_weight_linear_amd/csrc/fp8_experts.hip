@@ -242,11 +242,20 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   // Rows per tile, by the average rows of an expert. Measured, us for tiles of 16 / 64 / 128 / 256
   // rows, 64 experts of 4096 x 1024, top 8, bf16: 16 rows an expert 209 / 207 / 229 / 257, 32 312 /
   // 257 / 240 / 264, 64 526 / 266 / 299 / 277, 128 - / 383 / 352 / 374, 256 - / 618 / 540 / 461;
-  // 16 experts of 2048 x 1024, top 2: 32 56 / 37 / 45 / 52, 128 144 / 67 / 55 / 75. The tiled
+  // 16 experts of 2048 x 1024, top 2: 32 56 / 37 / 45 / 52, 128 144 / 67 / 55 / 75. Too few
+  // workgroups of a tile call for the next smaller one: 8 experts of 1024 x 256, top 2: 128 42 / 31
+  // / 39 / 48, 512 96 / 43 / 43 / 58; 9 of 2784 x 336, top 8: 32 35 / 42 / 49 / 59. The tiled
   // kernel's offsets are 32 bits.
   const bool tiled = P > 16 * a.E && a.M * a.H < (int64_t(1) << 31) && 2 * a.I * a.H < (int64_t(1) << 31) &&
                      256 * a.I < (int64_t(1) << 31);
-  const int tile = !tiled ? 16 : P <= 96 * a.E ? 64 : P <= 192 * a.E || exact || exact_down ? 128 : 256;
+  const auto groups = [&](int64_t rows) {
+    const int64_t most = (P + a.E - 1) / a.E;         // of one expert, were all alike
+    return a.E * ((most + rows - 1) / rows) * ((a.I + 127) / 128);
+  };
+  int tile = !tiled ? 16 : P <= 96 * a.E ? 64 : P <= 192 * a.E || exact || exact_down ? 128 : 256;
+  if (tile == 256 && groups(256) < 128) tile = 128;
+  if (tile == 128 && groups(128) < 64) tile = 64;
+  if (tile == 64 && P <= 40 * a.E && groups(64) <= 64) tile = 16;
   const int64_t nt = experts_max_tiles(P, a.E, tile);
   // Few slots, most of them of different experts: a tile each, nothing to sort, and the rows are
   // quantised where they are used: two launches for five. A matrix that several slots share is

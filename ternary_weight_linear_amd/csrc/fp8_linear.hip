@@ -19,11 +19,9 @@ template <int MT>
 hipError_t start_codes(const StreamArgs& st, hipStream_t s) {
   const int64_t tiles = (st.p.a.M + 16 * MT - 1) / (16 * MT);
   const int rows = stream_rows(st.p.a.N, tiles);
-  if constexpr (MT <= 2) {
-    if (rows == 128) return start_stream<MT, 4, 4, kSrcCodes, kStreamLinear>(st, tiles, 0, s);
-    if (rows == 64) return start_stream<MT, 4, 8, kSrcCodes, kStreamLinear>(st, tiles, 0, s);
-  }
-  if (rows >= 32) return start_stream<MT, 2, 8, kSrcCodes, kStreamLinear>(st, tiles, 0, s);
+  if (rows == 128) return start_stream<MT, 4, 4, kSrcCodes, kStreamLinear>(st, tiles, 0, s);
+  if (rows == 64) return start_stream<MT, 4, 8, kSrcCodes, kStreamLinear>(st, tiles, 0, s);
+  if (rows == 32) return start_stream<MT, 2, 8, kSrcCodes, kStreamLinear>(st, tiles, 0, s);
   return start_stream<MT, 1, 8, kSrcCodes, kStreamLinear>(st, tiles, 0, s);
 }
 
@@ -39,6 +37,33 @@ hipError_t start_values(const StreamArgs& st, int xdtype, hipStream_t s) {
 }
 
 int64_t tiles(int64_t M, int64_t N, int bn, int bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); }
+
+// Parts of K for 64 x 64 tiles that do not fill the CUs by themselves: up to eight, of at least
+// eight blocks, by the share of the CUs' rounds that their workgroups fill less 4 % per part more
+// (partial sums are written and read again), if that is a fifth better than without.
+// Measured, us by parts: 168 tiles, K = 16384 1 38.7, 2 35.3, 3 29.3, 4 35.1 (fp16 operands 63,
+// 51, 40, 42); 81 tiles, K = 19664 1 49.6, 2 32.5, 3 26.3, 6 29.8; 252 tiles 1 16.7, 2 20.2.
+int split_parts(int64_t M, int64_t N, int64_t K) {
+  const int64_t t = tiles(M, N, 64, 64), KB = fp8_blocks(K);
+  if (t > 200) return 1;
+  const auto fill = [t](int64_t parts) {
+    const int64_t n = t * parts;
+    return static_cast<double>(n) / static_cast<double>((n + 255) / 256 * 256) * (1.04 - 0.04 * static_cast<double>(parts));
+  };
+  int64_t best = 1;
+  for (int64_t parts = 2; parts <= 8 && parts * 8 <= KB; ++parts)
+    if (fill(parts) > fill(best) && fill(parts) > 1.2 * fill(1)) best = parts;
+  const int64_t per = (KB + best - 1) / best;
+  return static_cast<int>((KB + per - 1) / per);    // none empty
+}
+
+// The same for 128 x 128 tiles: the parts that make one round of the CUs, if they fill three
+// quarters of it and have 32 blocks each (a part's first loads and its sums take about ten).
+int large_parts(int64_t M, int64_t N, int64_t K) {
+  const int64_t t = tiles(M, N, 128, 128);
+  const int64_t parts = 256 / t < 8 ? 256 / t : 8;
+  return parts > 1 && t * parts >= 192 && fp8_blocks(K) / parts >= 32 ? static_cast<int>(parts) : 1;
+}
 
 template <class S>
 hipError_t start_whole(const ProductArgs& p, hipStream_t s) {
@@ -58,10 +83,13 @@ hipError_t start_whole(const ProductArgs& p, hipStream_t s) {
 // fp16 operands: 4096 x 28672 x 8192 1545 (128 x 128); 512 x 3200 x 8640 45.5 (64 x 64), as with
 // every other tile: converting the codes (a quarter-rate instruction per two of them, for each
 // fragment that a wave reads) bounds it; staging q as fp16 halved that and lost as much to L2.
+// 128 x 128 tiles, eight waves, K in parts (whole 64 x 64 / in parts): 1692 x 927 x 22848 103 / 73,
+// 600 x 2000 x 12288 41 / 31, 300 x 4000 x 16384 62 / 46, 1000 x 1500 x 16384 50 / 46.5, with 16
+// blocks a part only 128 x 8192 x 8192 26 / 28.5. fp16 operands gain nothing from it.
 template <bool EXACT>
 hipError_t start_tiled(const ProductArgs& p, float* part, hipStream_t s) {
   const int64_t M = p.a.M, N = p.a.N, t128 = tiles(M, N, 128, 128);
-  const int parts = fp8_split_parts(M, N, p.a.K);
+  const int parts = split_parts(M, N, p.a.K);
   if (parts > 1) return start_split_gemm<GemmShape<64, 64, 2, 2, EXACT ? 3 : 4, EXACT>>(p, parts, part, s);
   if constexpr (EXACT) {
     if (t128 >= 256) return start_whole<GemmShape<128, 128, 2, 2, 2, true>>(p, s);
@@ -73,7 +101,11 @@ hipError_t start_tiled(const ProductArgs& p, float* part, hipStream_t s) {
       if (large <= small) return start_whole<GemmShape<256, 256, 2, 4, 2, false>>(p, s);
       return start_whole<GemmShape<128, 128, 2, 2, 2, false>>(p, s);
     }
-    if (t128 >= 200) return start_whole<GemmShape<128, 128, 2, 4, 4, false>>(p, s);
+    const int large = large_parts(M, N, p.a.K);
+    if (large > 1) return start_split_gemm<GemmShape<128, 128, 2, 4, 4, false>>(p, large, part, s);
+    // (more than 512 small tiles are a third workgroup on some CUs: 1500 x 1500 x 8192, 144 large
+    // or 576 small tiles, 37 / 45)
+    if (t128 >= 200 || tiles(M, N, 64, 64) > 512) return start_whole<GemmShape<128, 128, 2, 4, 4, false>>(p, s);
     if (tiles(M, N, 128, 64) >= 200 && tiles(M, N, 128, 64) <= 256)
       return start_whole<GemmShape<128, 64, 2, 2, 4, false>>(p, s);
     return start_whole<GemmShape<64, 64, 2, 2, 4, false>>(p, s);
@@ -83,13 +115,8 @@ hipError_t start_tiled(const ProductArgs& p, float* part, hipStream_t s) {
 }  // namespace
 
 int fp8_split_parts(int64_t M, int64_t N, int64_t K) {
-  const int64_t t = tiles(M, N, 64, 64), KB = fp8_blocks(K);
-  if (t > 128) return 1;
-  int64_t parts = 256 / t < 8 ? 256 / t : 8;
-  if (parts > KB / 8) parts = KB / 8;               // at least eight blocks each
-  if (parts <= 1) return 1;
-  const int64_t per = (KB + parts - 1) / parts;
-  return static_cast<int>((KB + per - 1) / per);    // none empty
+  const int small = split_parts(M, N, K), large = large_parts(M, N, K);
+  return small > large ? small : large;
 }
 
 hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const void* x, int xdtype, int64_t ldx, float* part,
@@ -106,9 +133,12 @@ hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const void* x, int xdtype, 
     if (e != hipSuccess) return e;
   }
   if (a.M <= 16) return start_codes<1>(st, s);
-  // fp32 results stream up to 32 rows (32 x 8192 x 8192: 20.5 us, tiled 23)
-  if ((a.M <= 32 && a.ydtype == BL_F32) || 256 * a.K >= (int64_t(1) << 31))   // tiled: 32-bit offsets
-    return start_codes<2>(st, s);
+  // Up to 32 rows of short K still stream; over a long K the tiled kernel in parts has more loads
+  // in flight (us, streamed / tiled, 16-bit results: 25 x 1750 x 3232 5.6 / 10.2, 32 x 4096 x 4096
+  // 9.4 / 10.4, 32 x 8192 x 8192 20.6 / 17.4, 24 x 4096 x 11008 19.6 / 14.0; fp32: 32 x 8192 x 8192
+  // 20.5 / 22, 25 x 910 x 20864 32.7 / 18.9). The tiled kernel's offsets are 32 bits.
+  const int64_t stream_k = a.ydtype == BL_F32 ? 8192 : 4096;
+  if ((a.M <= 32 && a.K <= stream_k) || 256 * a.K >= (int64_t(1) << 31)) return start_codes<2>(st, s);
   return a.ydtype == BL_F32 ? start_tiled<true>(st.p, part, s) : start_tiled<false>(st.p, part, s);
 }
 

@@ -185,6 +185,20 @@ def test_linear_wide(M, N, K, out):
     close(y, ref, (SUM[out] + (K // 128 + 4) * 2.0 ** -23) * mag, out, (M, N, K))
 
 
+@pytest.mark.parametrize("out", ["fp16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(300, 2100, 3104), (25, 300, 8208), (270, 4100, 8208), (1500, 1500, 272), (1601, 777, 8336)])
+def test_linear_long_sums(M, N, K, out):
+    """Sums over K in parts, with parts of unequal lengths, of small and of large tiles."""
+    say("fp8 linear long sums", M, N, K, out)
+    x, v = act((M, K), "fp16", M)
+    wc, ws = weight(N, K, K)
+    y = tw.bl_fp8_forward(x, f8(wc), gpu(ws), out_dtype=TYPES[out])
+    c, s, _ = of.quant_act(v)
+    ref, mag = of.linear(c, s, wc, ws)
+    close(y, ref, (SUM[out] + (K // 128 + 4) * 2.0 ** -23) * mag, out, (M, N, K))
+    assert torch.equal(y, tw.bl_fp8_linear(*tw.bl_quant_act_fp8(x), f8(wc), gpu(ws), out_dtype=TYPES[out]))
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 384, 1040), (16, 1000, 2064), (80, 640, 1152), (300, 513, 784)])
 def test_linear_results_keep_the_precision_of_their_type(M, N, K):
     """Far below the worst-case bounds: fp32 results within fp32 roundings of the magnitudes of
@@ -411,6 +425,13 @@ def test_experts(M, E, k, H, I, dtype):
     ref, bound = of.experts(v, index, wt, *W, rel)
     assert y.dtype == TYPES[dtype]
     close(y, ref, bound + 2.0 ** -20 * np.abs(ref).max(), dtype, (M, E, k, H, I))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M,E,k,H,I", [(3201, 32, 2, 144, 528), (1601, 16, 1, 272, 528), (36, 9, 8, 400, 336)])
+def test_experts_many_workgroups(M, E, k, H, I, dtype):
+    """Enough workgroups for the large tiles of each type; many rows and few workgroups."""
+    test_experts(M, E, k, H, I, dtype)
 
 
 @pytest.mark.parametrize("M,E,k,times", [(700, 300, 4, 1), (100, 5, 8, 200), (60, 700, 2, 30)])
