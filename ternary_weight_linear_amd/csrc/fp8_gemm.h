@@ -72,10 +72,11 @@ __device__ __forceinline__ Operand<EXACT> read_operand(const uint8_t* tile, uint
 // Stores a wave's 16-bit results through 8 KB of LDS of its own, 32 rows of 128 columns at a
 // time, so that each row goes out as 256 consecutive bytes (from registers a row gets 32 bytes
 // per store: four lanes of four columns). 16-byte pieces are in XOR order as in the tiles.
+// to_row: the wave's 64 output rows if they are scattered.
 // kPartType: fp16 of value / scale, scale a power of two per row and 128 columns that brings
 // their largest magnitude to [2^14, 2^15); values that are not finite stay so.
 template <class S>
-__device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&acc)[S::TN][S::TM], uint8_t* room,
+__device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&acc)[S::TN][S::TM], uint8_t* room, const int* to_row,
                                            int64_t first, int rows, int wm, int64_t n, int lane) {
   const Fp8LinearArgs& a = p.a;
   const int g = lane >> 4, u = lane & 15;
@@ -100,7 +101,7 @@ __device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&a
         f = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
         const int r = wm + 16 * j + u;
         if (g == 0 && r < rows && n < a.N)
-          p.part_scale[(n / kFp8Block) * a.M + p.map.pair[first + r]] = __uint_as_float(static_cast<uint32_t>(e) << 23);
+          p.part_scale[(n / kFp8Block) * a.M + to_row[16 * j + u]] = __uint_as_float(static_cast<uint32_t>(e) << 23);
       }
       const int row = 16 * (j - jj) + u;
 #pragma unroll
@@ -116,8 +117,7 @@ __device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&a
       const int row = 4 * t + g, r = wm + 16 * jj + row;
       const u32x4 b = *reinterpret_cast<const u32x4*>(room + row * 256 + 16 * (u ^ (row & 15)));
       if (r >= rows || n + 8 * u >= a.N) continue;
-      int64_t at = first + r;
-      if (p.map.scatter) at = p.map.pair[at];
+      const int64_t at = p.map.scatter ? to_row[16 * jj + row] : first + r;
       uint16_t* to = static_cast<uint16_t*>(a.y) + at * a.ldy + n + 8 * u;
       // non-temporal: all CUs store at once, and 128 KB each would turn over the L2 (8192 x 8192 x
       // 1024: 98 us with ordinary stores, 94)
@@ -141,6 +141,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   __shared__ uint8_t bufA0[S::BN * 128], bufA1[S::BN * 128], bufA2[N3 ? S::BN * 128 : 1], bufA3[N4 ? S::BN * 128 : 1];
   __shared__ uint8_t bufB0[S::BM * 128], bufB1[S::BM * 128], bufB2[N3 ? S::BM * 128 : 1], bufB3[N4 ? S::BM * 128 : 1];
   __shared__ float bufS0[S::WAVES][64], bufS1[S::WAVES][64], bufS2[N3 ? S::WAVES : 1][64], bufS3[N4 ? S::WAVES : 1][64];
+  __shared__ int to_rows[S::WAVES][64];             // output rows, where they are scattered
   const Fp8LinearArgs& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, u = lane & 15;
@@ -306,6 +307,10 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   };
   const bool busy = wm < rows;                      // a wave past the tile's rows only helps to copy
   Weigh w0, w1, w2, w3;
+  // (a load of them between the stores of the results would wait for the stores)
+  if (p.map.scatter)
+    copy4_to_lds(make_buffer(p.map.pair + first), 4 * static_cast<uint32_t>(min(wm + min(lane, S::BM / S::GM - 1), rows - 1)),
+                 to_rows[wave]);
   stage(kb, bufA0, bufB0, bufS0, w0);
   if constexpr (S::NS > 2) stage(kb + 1, bufA1, bufB1, bufS1, w1);
   if constexpr (S::NS > 3) stage(kb + 2, bufA2, bufB2, bufS2, w2);
@@ -392,7 +397,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   }
   if constexpr (S::WIDE) {
     if (a.ydtype != BL_F32) {
-      store_wide<S>(p, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * 8192, first, rows, wm, n0 + wn, lane);
+      store_wide<S>(p, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * 8192, to_rows[wave], first, rows, wm, n0 + wn, lane);
       return;
     }
   }
@@ -400,8 +405,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   for (int j = 0; j < S::TM; ++j) {
     const int r = wm + 16 * j + u;
     if (r >= rows) continue;
-    int64_t at = first + r;
-    if (p.map.scatter) at = p.map.pair[at];
+    const int64_t at = p.map.scatter ? to_rows[wave][16 * j + u] : first + r;
 #pragma unroll
     for (int i = 0; i < S::TN; ++i) store4(a, blockIdx.y * a.M + at, n0 + wn + 16 * i + 4 * g, acc[i][j]);
   }
