@@ -95,7 +95,8 @@ __device__ __forceinline__ void place_slots(const SortArgs& a, int chunk, const 
 }
 
 // One launch for what needs only the inputs: the first workgroups sort (or count) the slots,
-// the others quantise x.
+// the others quantise x. 48 tokens of 4096, top 8 of 64: 4.7 us; 4096 tokens: 13 (and 7.7 for
+// the placing), most of it waits of the passes over a chunk's slots.
 template <int DT>
 __global__ __launch_bounds__(kSortThreads) void experts_prepare_kernel(SortArgs a, QuantArgs q) {
   extern __shared__ int lds[];                     // [2, E]
@@ -135,7 +136,7 @@ __global__ __launch_bounds__(kSortThreads) void experts_place_kernel(SortArgs a)
 
 // y[m, n] = sum_j weight[m, j] part[m k + j, n], slots in their order. A thread has V columns
 // (16 bytes) and up to eight slots' loads in flight: reading the parts bounds it (32768 x 4096
-// fp16: 65 us).
+// fp16: 62 us, 4.9 TB/s).
 template <bool HALF>
 __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, const void* __restrict__ part,
                                                               const float* __restrict__ scale) {
