@@ -38,85 +38,97 @@ hipError_t start_values(const StreamArgs& st, int xdtype, hipStream_t s) {
 
 int64_t tiles(int64_t M, int64_t N, int bn, int bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); }
 
-// Parts of K for 64 x 64 tiles that do not fill the CUs by themselves: up to eight, of at least
-// eight blocks, by the share of the CUs' rounds that their workgroups fill less 4 % per part more
-// (partial sums are written and read again), if that is a fifth better than without.
-// Measured, us by parts: 168 tiles, K = 16384 1 38.7, 2 35.3, 3 29.3, 4 35.1 (fp16 operands 63,
-// 51, 40, 42); 81 tiles, K = 19664 1 49.6, 2 32.5, 3 26.3, 6 29.8; 252 tiles 1 16.7, 2 20.2.
-int split_parts(int64_t M, int64_t N, int64_t K) {
-  const int64_t t = tiles(M, N, 64, 64), KB = fp8_blocks(K);
-  if (t > 200) return 1;
-  const auto fill = [t](int64_t parts) {
-    const int64_t n = t * parts;
-    return static_cast<double>(n) / static_cast<double>((n + 255) / 256 * 256) * (1.04 - 0.04 * static_cast<double>(parts));
-  };
-  int64_t best = 1;
-  for (int64_t parts = 2; parts <= 8 && parts * 8 <= KB; ++parts)
-    if (fill(parts) > fill(best) && fill(parts) > 1.2 * fill(1)) best = parts;
-  const int64_t per = (KB + best - 1) / best;
-  return static_cast<int>((KB + per - 1) / per);    // none empty
-}
+// The tiled kernel's tiles and, in us, what one takes: `alone` per block of K with one workgroup
+// on every CU, `shared` with `per_cu` of them (their LDS), a part `idle` of it however few CUs are
+// busy, and `ends` for the start and the stores. Large tiles read less from L2 (64 x 64 tiles are
+// bound by it, at 11 to 15 TB/s), small ones fill the CUs. Fitted to 1900 products measured on
+// MI355X (17 to 4096 rows, 64 to 28672 columns, K of 256 to 28672, in one to eight parts of K), to
+// 17 %; the tile and parts of the least estimate are on average 2 % (fp16 operands 3 %) from the
+// best that was measured, at most 21 %. Some of them (256 x 256 / 256 x 128 / 128 x 128, four
+// waves / 128 x 128, eight waves / 128 x 64 / 64 x 64):
+//   4096 x 28672 x 8192  785 / - / 926 / - / - / -     2048 x 8192 x 8192  117 / - / 143 / 168 / 191 / -
+//   192 x 28672 x 8192   103 / 72 / 80 / 84 / 101 / 112   1500 x 1500 x 8192  - / - / - / 37 / - / 45
+//   512 x 8640 x 3200    - / - / 26 / 36 / 27 / 30     512 x 3200 x 8640   - / - / 57 / 38 / 31 / 33
+// in parts, best (unsplit): 512 x 8192 x 28672 128 x 128 155, 256 x 256 128 with 4 (334);
+//   300 x 4000 x 16384 64 x 64 62 (62), 128 x 128 46 with 2; 877 x 761 x 16384 64 x 64 29 with 3 (39)
+// fp16 operands, 128 x 128 / 64 x 64: 4096 x 28672 x 8192 1545 / -, 128 x 28672 x 8192 79 / 97,
+//   512 x 3200 x 8640 57 / 46; 96 x 8192 x 28672 78 with 4 parts (242) / 87 with 2 (133). With them
+// converting the codes bounds it (a quarter-rate instruction per two of them, for each fragment
+// that a wave reads); staging q as fp16 halved that and lost as much to L2.
+struct Tile {
+  int bn, bm, per_cu;
+  float alone, shared, idle, ends;
+};
+constexpr Tile kTiles[] = {
+    {64, 64, 2, 0.34f, 0.57f, 0.6f, 5.7f},     {128, 64, 1, 0.46f, 0.46f, 0.8f, 5.3f},
+    {128, 128, 1, 0.70f, 0.70f, 0.7f, 6.1f},   {128, 128, 2, 1.00f, 1.30f, 0.5f, 7.4f},
+    {256, 128, 1, 1.20f, 1.20f, 0.6f, 7.6f},   {256, 256, 1, 1.86f, 1.86f, 0.7f, 11.2f},
+};
+constexpr Tile kExactTiles[] = {{64, 64, 3, 0.54f, 0.95f, 0.6f, 5.0f}, {128, 128, 2, 1.40f, 1.90f, 0.5f, 12.0f}};
 
-// The same for 128 x 128 tiles: the parts that make one round of the CUs, if they fill three
-// quarters of it and have 32 blocks each (a part's first loads and its sums take about ten).
-int large_parts(int64_t M, int64_t N, int64_t K) {
-  const int64_t t = tiles(M, N, 128, 128);
-  const int64_t parts = 256 / t < 8 ? 256 / t : 8;
-  return parts > 1 && t * parts >= 192 && fp8_blocks(K) / parts >= 32 ? static_cast<int>(parts) : 1;
+struct Plan {
+  int tile, parts;
+};
+// Parts: up to eight of at least six blocks, if their workgroups make one round of the CUs at
+// most. Their sums cost a launch and the partial sums' way to memory and back.
+template <size_t N_TILES>
+Plan make_plan(const Tile (&list)[N_TILES], int64_t M, int64_t N, int64_t K) {
+  const int KB = static_cast<int>(fp8_blocks(K));
+  Plan best{0, 1};
+  float least = 0;
+  for (int i = 0; i < static_cast<int>(N_TILES); ++i) {
+    const Tile& t = list[i];
+    const int64_t n = tiles(M, N, t.bn, t.bm), round = 256 * t.per_cu;
+    for (int parts = 1; parts <= 8; ++parts) {
+      if (parts > 1 && (n * parts > round || KB < 6 * parts)) break;
+      const int steps = (KB + parts - 1) / parts;
+      if ((KB + steps - 1) / steps != parts) continue;   // the last part would be empty
+      const int64_t full = n * parts / round;
+      const float load = static_cast<float>(n * parts - full * round) / 256;   // of the last round, per CU
+      const float step = load <= 1 ? t.alone * (t.idle + (1 - t.idle) * load)
+                                   : t.alone + (t.shared - t.alone) * (load - 1) / static_cast<float>(t.per_cu - 1);
+      float us = static_cast<float>(full) * (static_cast<float>(steps) * t.shared + t.ends);
+      if (load > 0) us += static_cast<float>(steps) * step + t.ends;
+      if (parts > 1) us += 3.7f + static_cast<float>(parts) * static_cast<float>(M) * static_cast<float>(N) * 8e-7f;
+      if ((i == 0 && parts == 1) || us < least) {
+        least = us;
+        best = Plan{i, parts};
+      }
+    }
+  }
+  return best;
 }
 
 template <class S>
-hipError_t start_whole(const ProductArgs& p, hipStream_t s) {
-  return start_gemm<S>(p, (p.a.M + S::BM - 1) / S::BM, s);
+hipError_t start_plan(const ProductArgs& p, int parts, float* part, hipStream_t s) {
+  return parts > 1 ? start_split_gemm<S>(p, parts, part, s) : start_gemm<S>(p, (p.a.M + S::BM - 1) / S::BM, s);
 }
 
-// Tile of the tiled kernel. Large tiles read less from L2 (64 x 64 tiles are bound by it, at
-// 11 to 15 TB/s), small ones fill the 256 CUs. Measured on MI355X, us, e4m3 instruction
-// (256 x 256 / 128 x 128, four waves / 128 x 128, eight waves, four stages / 128 x 64 / 64 x 64):
-//   4096 x 28672 x 8192  785 / 926 / - / - / -      2048 x 8192 x 8192  117 / 143 / 168 / 191 / -
-//   512 x 8640 x 3200    - / 26.3 / 36 / 27.4 / 30  512 x 8192 x 8192   - / 57 / 43.0 / 52.8 / -
-//   1024 x 4096 x 4096   - / 28.1 / 23.9 / 24.4 / 30   512 x 3200 x 8640 - / 57 / 38 / 30.7 / 32.6
-//   96 x 28672 x 8192    - / 58.9 / 57.2 / 68.5 / 73.5
-// and with K in parts where 64 x 64 tiles alone leave CUs idle (1 / 2 / 4 parts):
-//   512 x 1024 x 8192 20.9 / 15.8 / 16.3   64 x 8192 x 8192 23.4 / 18.7 / 20.4
-//   200 x 1024 x 8192 20.1 / 15.2 / 12.7   24 x 4096 x 11008 24.3 / 16.8 / 14.1
-// fp16 operands: 4096 x 28672 x 8192 1545 (128 x 128); 512 x 3200 x 8640 45.5 (64 x 64), as with
-// every other tile: converting the codes (a quarter-rate instruction per two of them, for each
-// fragment that a wave reads) bounds it; staging q as fp16 halved that and lost as much to L2.
-// 128 x 128 tiles, eight waves, K in parts (whole 64 x 64 / in parts): 1692 x 927 x 22848 103 / 73,
-// 600 x 2000 x 12288 41 / 31, 300 x 4000 x 16384 62 / 46, 1000 x 1500 x 16384 50 / 46.5, with 16
-// blocks a part only 128 x 8192 x 8192 26 / 28.5. fp16 operands gain nothing from it.
 template <bool EXACT>
 hipError_t start_tiled(const ProductArgs& p, float* part, hipStream_t s) {
-  const int64_t M = p.a.M, N = p.a.N, t128 = tiles(M, N, 128, 128);
-  const int parts = split_parts(M, N, p.a.K);
-  if (parts > 1) return start_split_gemm<GemmShape<64, 64, 2, 2, EXACT ? 3 : 4, EXACT>>(p, parts, part, s);
   if constexpr (EXACT) {
-    if (t128 >= 256) return start_whole<GemmShape<128, 128, 2, 2, 2, true>>(p, s);
-    return start_whole<GemmShape<64, 64, 2, 2, 3, true>>(p, s);
+    const Plan q = make_plan(kExactTiles, p.a.M, p.a.N, p.a.K);
+    if (q.tile == 1) return start_plan<GemmShape<128, 128, 2, 2, 2, true>>(p, q.parts, part, s);
+    return start_plan<GemmShape<64, 64, 2, 2, 3, true>>(p, q.parts, part, s);
   } else {
-    if (t128 > 256) {
-      // rounds over the chip: 256 large tiles take 1, 512 small ones 0.6 of it
-      const double large = static_cast<double>((tiles(M, N, 256, 256) + 255) / 256), small = 0.6 * ((t128 + 511) / 512);
-      if (large <= small) return start_whole<GemmShape<256, 256, 2, 4, 2, false>>(p, s);
-      return start_whole<GemmShape<128, 128, 2, 2, 2, false>>(p, s);
+    const Plan q = make_plan(kTiles, p.a.M, p.a.N, p.a.K);
+    switch (q.tile) {
+      case 0: return start_plan<GemmShape<64, 64, 2, 2, 4, false>>(p, q.parts, part, s);
+      case 1: return start_plan<GemmShape<128, 64, 2, 2, 4, false>>(p, q.parts, part, s);
+      case 2: return start_plan<GemmShape<128, 128, 2, 4, 4, false>>(p, q.parts, part, s);
+      case 3: return start_plan<GemmShape<128, 128, 2, 2, 2, false>>(p, q.parts, part, s);
+      case 4: return start_plan<GemmShape<256, 128, 2, 4, 3, false>>(p, q.parts, part, s);
+      default: return start_plan<GemmShape<256, 256, 2, 4, 2, false>>(p, q.parts, part, s);
     }
-    const int large = large_parts(M, N, p.a.K);
-    if (large > 1) return start_split_gemm<GemmShape<128, 128, 2, 4, 4, false>>(p, large, part, s);
-    // (more than 512 small tiles are a third workgroup on some CUs: 1500 x 1500 x 8192, 144 large
-    // or 576 small tiles, 37 / 45)
-    if (t128 >= 200 || tiles(M, N, 64, 64) > 512) return start_whole<GemmShape<128, 128, 2, 4, 4, false>>(p, s);
-    if (tiles(M, N, 128, 64) >= 200 && tiles(M, N, 128, 64) <= 256)
-      return start_whole<GemmShape<128, 64, 2, 2, 4, false>>(p, s);
-    return start_whole<GemmShape<64, 64, 2, 2, 4, false>>(p, s);
   }
 }
 
 }  // namespace
 
 int fp8_split_parts(int64_t M, int64_t N, int64_t K) {
-  const int small = split_parts(M, N, K), large = large_parts(M, N, K);
-  return small > large ? small : large;
+  if (M <= 16) return 1;                            // streamed
+  const int a = make_plan(kTiles, M, N, K).parts, b = make_plan(kExactTiles, M, N, K).parts;
+  return a > b ? a : b;
 }
 
 hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const void* x, int xdtype, int64_t ldx, float* part,
