@@ -430,7 +430,8 @@ def test_experts(M, E, k, H, I, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
-@pytest.mark.parametrize("M,E,k,H,I", [(3201, 32, 2, 144, 528), (1601, 16, 1, 272, 528), (36, 9, 8, 400, 336)])
+@pytest.mark.parametrize("M,E,k,H,I", [(3201, 32, 2, 144, 528), (1601, 16, 1, 272, 528), (36, 9, 8, 400, 336),
+                                       (3500, 32, 1, 272, 528)])
 def test_experts_many_workgroups(M, E, k, H, I, dtype):
     """Enough workgroups for the large tiles of each type; many rows and few workgroups."""
     test_experts(M, E, k, H, I, dtype)
