@@ -86,14 +86,13 @@ int check_rows_out(const void* y, int dtype, int64_t n, int64_t ld) {
   return aligned_to(y, dtype_bytes(dtype)) ? BL_OK : BL_ERR_ALIGN;
 }
 struct Fp8Ws {
-  size_t sx_off, part_off, total;   // codes [M, K] at 0, scales [KB, M], partial sums [parts, M, N]
+  size_t sx_off, part_off, total;   // codes [M, K] at 0, scales [KB, M], partial sums
 };
 Fp8Ws fp8_ws(int64_t M, int64_t N, int64_t K) {
   Fp8Ws w{};
   w.sx_off = round256(static_cast<size_t>(M) * K);
   w.part_off = w.sx_off + round256(static_cast<size_t>(M) * fp8_blocks(K) * 4);
-  const int parts = fp8_split_parts(M, N, K);
-  w.total = w.part_off + (parts > 1 ? round256(static_cast<size_t>(parts) * M * N * 4) : 0);
+  w.total = w.part_off + round256(static_cast<size_t>(fp8_part_bytes(M, N, K)));
   return w;
 }
 bool experts_dims_ok(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {

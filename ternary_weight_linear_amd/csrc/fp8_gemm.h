@@ -39,6 +39,21 @@ __device__ __forceinline__ void meet() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
+// XCD x (workgroups are dealt to the eight XCDs in turn) takes a contiguous run of n tiles.
+__device__ __forceinline__ int in_xcd_order(int i, int n) {
+  const int xcd = i & 7, per = n / 8, more = n % 8;
+  return xcd * per + min(xcd, more) + (i >> 3);
+}
+// Tiles lie in bands of 8 tiles of q; within a band q runs first.
+struct TileAt {
+  int m, n;
+};
+__device__ __forceinline__ TileAt tile_at(int id, int tiles_n, int tiles_m) {
+  const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n;
+  const int bm = min(8, tiles_m - band * 8);
+  return {band * 8 + in % bm, in / bm};
+}
+
 template <int BN_, int BM_, int GN_, int GM_, int NS_, bool EXACT_, bool GATED_ = false>
 struct GemmShape {
   static constexpr int BN = BN_, BM = BM_;          // tile: rows of w, rows of q
@@ -156,18 +171,20 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   const int wn = (wave % S::GN) * (S::BN / S::GN), wm = (wave / S::GN) * (S::BM / S::GM);
 
   const int tiles_m = p.map.tiles ? *p.map.n_tiles : tiles_m_arg;
-  int id = blockIdx.x;
-  {
-    // XCD x (workgroups are dealt to the eight XCDs in turn) takes a contiguous run of tiles
-    const int total = tiles_n * tiles_m, per = total / 8, more = total % 8;
-    const int xcd = id & 7, i = id >> 3;
-    if (i >= per + (xcd < more)) return;
-    id = xcd * per + min(xcd, more) + i;
+  const int total = tiles_n * tiles_m, whole = p.parts > 1 ? p.whole : total;
+  const bool split = static_cast<int>(blockIdx.x) >= whole;   // K in parts: this is part z of tile whole + i
+  int id = blockIdx.x, z = 0, i_of_rest = 0;
+  if (split) {
+    const int j = id - whole, rest = total - whole;
+    if (p.parts <= 1) return;                       // (the grid is made for the most tiles there may be)
+    z = j / rest;
+    i_of_rest = in_xcd_order(j - z * rest, rest);
+    id = whole + i_of_rest;
+  } else {
+    id = in_xcd_order(id, whole);
   }
-  // bands of 8 tiles of q, within a band q runs first
-  const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n;
-  const int bm = min(8, tiles_m - band * 8);
-  const int tm = band * 8 + in % bm, tn = in / bm;
+  const TileAt tile = tile_at(id, tiles_n, tiles_m);
+  const int tm = tile.m, tn = tile.n;
 
   const int64_t n0 = static_cast<int64_t>(tn) * S::BN;
   int64_t first = static_cast<int64_t>(tm) * S::BM;
@@ -220,8 +237,8 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   sw += (S::GATED ? static_cast<int64_t>(tn) : min<int64_t>((n0 + wn) / kFp8Block, (a.N - 1) / kFp8Block)) * KB;
 
   // blocks [kb, blocks): all of them, or the workgroup's range of a split K
-  const int per = static_cast<int>((KB + gridDim.y - 1) / gridDim.y);
-  int kb = blockIdx.y * per;
+  const int per = split ? (static_cast<int>(KB) + p.parts - 1) / p.parts : static_cast<int>(KB);
+  int kb = z * per;
   const int blocks = min(kb + per, static_cast<int>(KB));
   const bool cut = (KB - 1) * kFp8Block + 16 * piece >= K;   // this lane's piece of the last block is past K
   struct Weigh {
@@ -403,6 +420,17 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     }
     return;
   }
+  if (!S::GATED && split) {
+    float* to = p.part + (static_cast<int64_t>(z) * (total - whole) + i_of_rest) * (S::BM * S::BN);
+#pragma unroll
+    for (int j = 0; j < S::TM; ++j) {
+      const int r = wm + 16 * j + u;
+      if (r >= rows) continue;
+#pragma unroll
+      for (int i = 0; i < S::TN; ++i) *reinterpret_cast<f32x4*>(to + r * S::BN + wn + 16 * i + 4 * g) = acc[i][j];
+    }
+    return;
+  }
   if constexpr (S::WIDE) {
     if (a.ydtype != BL_F32) {
       store_wide<S>(p, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * 8192, to_rows[wave], first, rows, wm, n0 + wn, lane);
@@ -415,27 +443,24 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     if (r >= rows) continue;
     const int64_t at = p.map.scatter ? to_rows[wave][16 * j + u] : first + r;
 #pragma unroll
-    for (int i = 0; i < S::TN; ++i) store4(a, blockIdx.y * a.M + at, n0 + wn + 16 * i + 4 * g, acc[i][j]);
+    for (int i = 0; i < S::TN; ++i) store4(a, at, n0 + wn + 16 * i + 4 * g, acc[i][j]);
   }
 }
 
-// y = the sum of `parts` partial results [parts, M, N] in their order; the parts come from L2, and
-// a launch is most of its time.
-__global__ __launch_bounds__(256) void sum_parts_kernel(Fp8LinearArgs a, const float* __restrict__ part, int parts,
-                                                        int64_t row4) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t m = id / row4, n = (id - m * row4) * 4;
-  if (m >= a.M) return;
+// y = the sum of the `parts` partial sums of each tile from `whole` on, in their order, four
+// columns per thread; they come from L2, and a launch is most of its time.
+template <class S>
+__global__ __launch_bounds__(256) void sum_parts_kernel(ProductArgs p, int tiles_n, int tiles_m) {
+  constexpr int PER = S::BM * S::BN / 1024;         // workgroups per tile
+  const int i = blockIdx.x / PER, at = (blockIdx.x % PER * 256 + threadIdx.x) * 4;
+  const int rest = tiles_n * tiles_m - p.whole;
+  const TileAt t = tile_at(p.whole + i, tiles_n, tiles_m);
+  const int64_t m = static_cast<int64_t>(t.m) * S::BM + at / S::BN, n = static_cast<int64_t>(t.n) * S::BN + at % S::BN;
+  if (m >= p.a.M || n >= p.a.N) return;
   f32x4 sum = {0, 0, 0, 0};
-  for (int z = 0; z < parts; ++z) {
-    const float* p = part + (static_cast<int64_t>(z) * a.M + m) * a.N + n;
-    if (n + 3 < a.N) {
-      sum += *reinterpret_cast<const f32x4_at4*>(p);
-    } else {
-      for (int e = 0; n + e < a.N; ++e) sum[e] += p[e];
-    }
-  }
-  store4(a, m, n, sum);
+  for (int z = 0; z < p.parts; ++z)
+    sum += *reinterpret_cast<const f32x4*>(p.part + (static_cast<int64_t>(z) * rest + i) * (S::BM * S::BN) + at);
+  store4(p.a, m, n, sum);
 }
 
 template <class S>
@@ -447,20 +472,17 @@ hipError_t start_gemm(const ProductArgs& p, int64_t tiles_m, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The product with K split over `parts` workgroups per tile; part: fp32 [parts, M, N].
+// The product with K split over p.parts workgroups for each tile from p.whole on.
 template <class S>
-hipError_t start_split_gemm(const ProductArgs& p, int parts, float* part, hipStream_t s) {
+hipError_t start_split_gemm(const ProductArgs& p, hipStream_t s) {
   const int64_t tiles_n = (p.a.N + S::BN - 1) / S::BN, tiles_m = (p.a.M + S::BM - 1) / S::BM;
-  ProductArgs q = p;
-  q.a.y = part;
-  q.a.ldy = p.a.N;
-  q.a.ydtype = BL_F32;
-  fp8_gemm_kernel<S><<<dim3(static_cast<uint32_t>(tiles_n * tiles_m), static_cast<uint32_t>(parts)), S::THREADS, 0, s>>>(
-      q, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
+  const int64_t rest = tiles_n * tiles_m - p.whole;
+  fp8_gemm_kernel<S><<<dim3(static_cast<uint32_t>(p.whole + rest * p.parts)), S::THREADS, 0, s>>>(
+      p, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t row4 = (p.a.N + 3) / 4;
-  sum_parts_kernel<<<dim3(static_cast<uint32_t>((p.a.M * row4 + 255) / 256)), 256, 0, s>>>(p.a, part, parts, row4);
+  sum_parts_kernel<S><<<dim3(static_cast<uint32_t>(rest * (S::BM * S::BN / 1024))), 256, 0, s>>>(
+      p, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
   return hipGetLastError();
 }
 

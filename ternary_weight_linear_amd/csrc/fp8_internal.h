@@ -83,10 +83,10 @@ hipError_t launch_fp8_quant_act(const void* x, int dtype, int64_t M, int64_t K, 
 hipError_t launch_fp8_quant_weight(const float* W, int64_t N, int64_t K, uint8_t* codes,
                                    float* scale, hipStream_t s);
 // a.q and a.sx are scratch when x is given: they are filled from it where the product takes codes.
-// part: fp32 [fp8_split_parts(M, N, K), M, N] where that is more than 1 (the most it uses).
+// part: fp8_part_bytes(M, N, K) of scratch for partial sums.
 hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const void* x, int xdtype, int64_t ldx, float* part,
                              hipStream_t s);
-int fp8_split_parts(int64_t M, int64_t N, int64_t K);
+int64_t fp8_part_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s);
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 

@@ -66,33 +66,37 @@ constexpr Tile kTiles[] = {
 };
 constexpr Tile kExactTiles[] = {{64, 64, 3, 0.54f, 0.95f, 0.6f, 5.0f}, {128, 128, 2, 1.40f, 1.90f, 0.5f, 12.0f}};
 
+// Tiles run in rounds of 256 per_cu. Those of the last round, from `whole` on, may have K in parts:
+// up to eight of at least six blocks, if they are then still one round. Their sums cost a launch
+// and the partial sums' way to memory and back. Without / with the last round in parts:
+// 1477 x 11045 x 15264 (264 tiles of 256 x 256) 438 / 311, 768 x 28672 x 8192 225 / 194.
 struct Plan {
-  int tile, parts;
+  int tile, parts, whole;
+  int64_t part_bytes;
 };
-// Parts: up to eight of at least six blocks, if their workgroups make one round of the CUs at
-// most. Their sums cost a launch and the partial sums' way to memory and back.
 template <size_t N_TILES>
 Plan make_plan(const Tile (&list)[N_TILES], int64_t M, int64_t N, int64_t K) {
   const int KB = static_cast<int>(fp8_blocks(K));
-  Plan best{0, 1};
+  Plan best{0, 1, 0, 0};
   float least = 0;
   for (int i = 0; i < static_cast<int>(N_TILES); ++i) {
     const Tile& t = list[i];
-    const int64_t n = tiles(M, N, t.bn, t.bm), round = 256 * t.per_cu;
+    const int64_t n = tiles(M, N, t.bn, t.bm), round = 256 * t.per_cu, full = n / round, rest = n - full * round;
+    const float used = static_cast<float>(M) / static_cast<float>((M + t.bm - 1) / t.bm * t.bm);   // of its rows
     for (int parts = 1; parts <= 8; ++parts) {
-      if (parts > 1 && (n * parts > round || KB < 6 * parts)) break;
+      if (parts > 1 && (rest == 0 || rest * parts > round || KB < 6 * parts)) break;
       const int steps = (KB + parts - 1) / parts;
       if ((KB + steps - 1) / steps != parts) continue;   // the last part would be empty
-      const int64_t full = n * parts / round;
-      const float load = static_cast<float>(n * parts - full * round) / 256;   // of the last round, per CU
+      const float load = static_cast<float>(rest * parts) / 256;   // of the last round, per CU
       const float step = load <= 1 ? t.alone * (t.idle + (1 - t.idle) * load)
                                    : t.alone + (t.shared - t.alone) * (load - 1) / static_cast<float>(t.per_cu - 1);
-      float us = static_cast<float>(full) * (static_cast<float>(steps) * t.shared + t.ends);
+      const int64_t bytes = parts > 1 ? rest * parts * t.bn * t.bm * 4 : 0;
+      float us = static_cast<float>(full) * (static_cast<float>(KB) * t.shared + t.ends);
       if (load > 0) us += static_cast<float>(steps) * step + t.ends;
-      if (parts > 1) us += 3.7f + static_cast<float>(parts) * static_cast<float>(M) * static_cast<float>(N) * 8e-7f;
+      if (parts > 1) us += 3.7f + static_cast<float>(bytes) * used * 2e-7f;
       if ((i == 0 && parts == 1) || us < least) {
         least = us;
-        best = Plan{i, parts};
+        best = Plan{i, parts, static_cast<int>(full * round), bytes};
       }
     }
   }
@@ -100,34 +104,38 @@ Plan make_plan(const Tile (&list)[N_TILES], int64_t M, int64_t N, int64_t K) {
 }
 
 template <class S>
-hipError_t start_plan(const ProductArgs& p, int parts, float* part, hipStream_t s) {
-  return parts > 1 ? start_split_gemm<S>(p, parts, part, s) : start_gemm<S>(p, (p.a.M + S::BM - 1) / S::BM, s);
+hipError_t start_plan(const ProductArgs& p, const Plan& plan, float* part, hipStream_t s) {
+  ProductArgs q = p;
+  q.whole = plan.whole;
+  q.parts = plan.parts;
+  q.part = part;
+  return plan.parts > 1 ? start_split_gemm<S>(q, s) : start_gemm<S>(q, (p.a.M + S::BM - 1) / S::BM, s);
 }
 
 template <bool EXACT>
 hipError_t start_tiled(const ProductArgs& p, float* part, hipStream_t s) {
   if constexpr (EXACT) {
     const Plan q = make_plan(kExactTiles, p.a.M, p.a.N, p.a.K);
-    if (q.tile == 1) return start_plan<GemmShape<128, 128, 2, 2, 2, true>>(p, q.parts, part, s);
-    return start_plan<GemmShape<64, 64, 2, 2, 3, true>>(p, q.parts, part, s);
+    if (q.tile == 1) return start_plan<GemmShape<128, 128, 2, 2, 2, true>>(p, q, part, s);
+    return start_plan<GemmShape<64, 64, 2, 2, 3, true>>(p, q, part, s);
   } else {
     const Plan q = make_plan(kTiles, p.a.M, p.a.N, p.a.K);
     switch (q.tile) {
-      case 0: return start_plan<GemmShape<64, 64, 2, 2, 4, false>>(p, q.parts, part, s);
-      case 1: return start_plan<GemmShape<128, 64, 2, 2, 4, false>>(p, q.parts, part, s);
-      case 2: return start_plan<GemmShape<128, 128, 2, 4, 4, false>>(p, q.parts, part, s);
-      case 3: return start_plan<GemmShape<128, 128, 2, 2, 2, false>>(p, q.parts, part, s);
-      case 4: return start_plan<GemmShape<256, 128, 2, 4, 3, false>>(p, q.parts, part, s);
-      default: return start_plan<GemmShape<256, 256, 2, 4, 2, false>>(p, q.parts, part, s);
+      case 0: return start_plan<GemmShape<64, 64, 2, 2, 4, false>>(p, q, part, s);
+      case 1: return start_plan<GemmShape<128, 64, 2, 2, 4, false>>(p, q, part, s);
+      case 2: return start_plan<GemmShape<128, 128, 2, 4, 4, false>>(p, q, part, s);
+      case 3: return start_plan<GemmShape<128, 128, 2, 2, 2, false>>(p, q, part, s);
+      case 4: return start_plan<GemmShape<256, 128, 2, 4, 3, false>>(p, q, part, s);
+      default: return start_plan<GemmShape<256, 256, 2, 4, 2, false>>(p, q, part, s);
     }
   }
 }
 
 }  // namespace
 
-int fp8_split_parts(int64_t M, int64_t N, int64_t K) {
-  if (M <= 16) return 1;                            // streamed
-  const int a = make_plan(kTiles, M, N, K).parts, b = make_plan(kExactTiles, M, N, K).parts;
+int64_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 16) return 0;                            // streamed
+  const int64_t a = make_plan(kTiles, M, N, K).part_bytes, b = make_plan(kExactTiles, M, N, K).part_bytes;
   return a > b ? a : b;
 }
 

@@ -113,6 +113,10 @@ struct ProductArgs {
   uint8_t* hq;
   float* hs;
   int64_t h_rows;
+  // tiled linear product: tiles from `whole` on have K in `parts` (2 or more; else none has), and
+  // leave fp32 sums [parts, tiles, BM, BN] in part
+  int whole, parts;
+  float* part;
   float* part_scale;             // y of kPartType: [ceil(N / 128), rows of y]
 };
 
