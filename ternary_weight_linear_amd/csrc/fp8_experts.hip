@@ -181,19 +181,22 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, 
   }
 }
 
+// Stages: three where the matrix instructions are fast, two where converting the codes is what
+// takes long (tiles of 128 rows, us for two / three: 1024 tokens, top 8 of 64, 4096 x 1024, bf16
+// 344 / 326, fp16 operands 3055 tokens, top 3 of 29, 1872 x 720 163 / 181).
 template <bool EXACT>
 hipError_t start_up(const ProductArgs& p, int tile, int64_t nt, hipStream_t s) {
   if (tile == 64) return start_gemm<GemmShape<256, 64, 4, 2, 3, EXACT, true>>(p, nt, s);
   if constexpr (!EXACT)
     if (tile == 256) return start_gemm<GemmShape<256, 256, 2, 4, 2, false, true>>(p, nt, s);
-  return start_gemm<GemmShape<256, 128, 2, 4, 2, EXACT, true>>(p, nt, s);
+  return start_gemm<GemmShape<256, 128, 2, 4, EXACT ? 2 : 3, EXACT, true>>(p, nt, s);
 }
 template <bool EXACT>
 hipError_t start_down(const ProductArgs& p, int tile, int64_t nt, hipStream_t s) {
   if (tile == 64) return start_gemm<GemmShape<256, 64, 4, 2, 3, EXACT>>(p, nt, s);
   if constexpr (!EXACT)
     if (tile == 256) return start_gemm<GemmShape<256, 256, 2, 4, 2, false>>(p, nt, s);
-  return start_gemm<GemmShape<256, 128, 2, 4, 2, EXACT>>(p, nt, s);
+  return start_gemm<GemmShape<256, 128, 2, 4, EXACT ? 2 : 3, EXACT>>(p, nt, s);
 }
 
 }  // namespace
