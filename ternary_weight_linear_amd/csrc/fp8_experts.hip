@@ -245,7 +245,7 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   const bool exact = a.xdtype != BL_BF16, exact_down = a.ydtype == BL_F32;
   // Rows per tile, by the average rows of an expert. Measured, us for tiles of 16 / 64 / 128 / 256
   // rows, 64 experts of 4096 x 1024, top 8, bf16: 16 rows an expert 209 / 207 / 229 / 257, 32 312 /
-  // 257 / 240 / 264, 64 526 / 266 / 299 / 277, 128 - / 383 / 352 / 374, 256 - / 618 / 540 / 461;
+  // 257 / 240 / 264, 64 526 / 266 / 299 / 277, 128 - / 378 / 330 / 378, 256 - / 596 / 492 / 449;
   // 16 experts of 2048 x 1024, top 2: 32 56 / 37 / 45 / 52, 128 144 / 67 / 55 / 75. Too few
   // workgroups of a tile call for the next smaller one: 8 experts of 1024 x 256, top 2: 128 42 / 31
   // / 39 / 48, 512 96 / 43 / 43 / 58; 9 of 2784 x 336, top 8: 32 35 / 42 / 49 / 59; 49 of 2384 x
