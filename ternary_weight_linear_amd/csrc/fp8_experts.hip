@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kSortThreads) void experts_place_kernel(SortArgs a)
 // fp16: 62 us, 4.9 TB/s).
 template <bool HALF>
 __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, const void* __restrict__ part,
-                                                              const float* __restrict__ scale) {
+                                                              const float* __restrict__ scale, int scale_cols) {
   constexpr int V = HALF ? 8 : 4;
   const int64_t m = blockIdx.x, P = a.M * a.k;
   const int64_t n = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * V;
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, 
       v[j] = u32x4{0, 0, 0, 0};
       if (e >= 0 && e < a.E) {
         w[j] = a.weight[slot];
-        if constexpr (HALF) w[j] *= scale[(n / kFp8Block) * P + slot];
+        if constexpr (HALF) w[j] *= scale[n / scale_cols * P + slot];
         v[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(part) + (slot * a.H + n) * (HALF ? 2 : 4));
       }
     }
@@ -222,7 +222,7 @@ ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
   w.hq_off = take(P * I);
   w.hs_off = take(P * IB * 4);
   w.part_off = take(P * H * 4);
-  w.ps_off = take(P * HB * 4);
+  w.ps_off = take(P * ((H + 63) / 64) * 4);
   w.total = off;
   return w;
 }
@@ -287,9 +287,10 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   up.k = static_cast<int>(a.k);
   StreamArgs down{};
   // The experts' outputs wait for their sum in fp32, or, for results in bf16, as fp16 with a
-  // power-of-two scale per row and 128 columns (its rounding is 1/8 of the result's own): half
-  // the bytes to write and read back.
-  const bool half_parts = tile >= 128 && a.ydtype == BL_BF16;
+  // power-of-two scale per row and 64 or 128 columns (its rounding is 1/8 of the result's own):
+  // half the bytes to write and read back (1315 tokens, top 7 of 59, 2992 x 128, tiles of 64 rows:
+  // 116 / 103 us).
+  const bool half_parts = tile >= 64 && a.ydtype == BL_BF16;
   auto* part_scale = reinterpret_cast<float*>(ws + L.ps_off);
   down.p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, half_parts ? kPartType : BL_F32};
   down.p.part_scale = part_scale;
@@ -340,8 +341,8 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   if (e != hipSuccess) return e;
   const uint32_t per = half_parts ? 2048 : 1024;
   const dim3 grid(static_cast<uint32_t>(a.M), static_cast<uint32_t>((a.H + per - 1) / per));
-  if (half_parts) experts_combine_kernel<true><<<grid, 256, 0, s>>>(a, part, part_scale);
-  else experts_combine_kernel<false><<<grid, 256, 0, s>>>(a, part, nullptr);
+  if (half_parts) experts_combine_kernel<true><<<grid, 256, 0, s>>>(a, part, part_scale, tile == 64 ? 64 : 128);
+  else experts_combine_kernel<false><<<grid, 256, 0, s>>>(a, part, nullptr, 1);
   return hipGetLastError();
 }
 

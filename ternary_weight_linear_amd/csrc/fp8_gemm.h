@@ -64,7 +64,8 @@ struct GemmShape {
   // A tile of w is BN / 2 gate rows and the BN / 2 up rows of the same channels, and the tile's
   // result is quantised silu(gate) * up. Each wave holds both rows of its channels.
   static constexpr bool GATED = GATED_;
-  static constexpr bool WIDE = !GATED && WAVES == 8 && TN == 8 && TM % 2 == 0;   // store_wide
+  // 16-bit results go out as rows of a wave's 64 or 128 columns (store_wide)
+  static constexpr bool WIDE = !EXACT && !GATED && BN == 256 && WAVES == 8 && (TN == 4 || TN == 8) && TM % 2 == 0;
   static constexpr int NF = GATED ? 2 : 1;          // blocks of 128 rows of w that a wave reads
   static_assert(!GATED || BN == 256, "a gated tile is one block of 128 channels");
   static constexpr int NS = NS_;                    // stages: NS - 1 blocks' copies in flight
@@ -84,15 +85,16 @@ __device__ __forceinline__ Operand<EXACT> read_operand(const uint8_t* tile, uint
   return operand<EXACT>(f);
 }
 
-// Stores a wave's 16-bit results through 8 KB of LDS of its own, 32 rows of 128 columns at a
-// time, so that each row goes out as 256 consecutive bytes (from registers a row gets 32 bytes
-// per store: four lanes of four columns). 16-byte pieces are in XOR order as in the tiles.
+// Stores a wave's 16-bit results through LDS of its own, 32 rows at a time, so that each row's 64
+// or 128 columns go out as 128 or 256 consecutive bytes (from registers a row gets 32 bytes per
+// store: four lanes of four columns). 16-byte pieces are in XOR order as in the tiles.
 // to_row: the wave's 64 output rows if they are scattered.
-// kPartType: fp16 of value / scale, scale a power of two per row and 128 columns that brings
+// kPartType: fp16 of value / scale, scale a power of two per row and a wave's columns that brings
 // their largest magnitude to [2^14, 2^15); values that are not finite stay so.
 template <class S>
 __device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&acc)[S::TN][S::TM], uint8_t* room, const int* to_row,
                                            int64_t first, int rows, int wm, int64_t n, int lane) {
+  constexpr int PIECES = 2 * S::TN, ROWS = 64 / PIECES;   // 16-byte pieces of a row, rows per store
   const Fp8LinearArgs& a = p.a;
   const int g = lane >> 4, u = lane & 15;
 #pragma unroll
@@ -116,32 +118,32 @@ __device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&a
         f = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
         const int r = wm + 16 * j + u;
         if (g == 0 && r < rows && n < a.N)
-          p.part_scale[(n / kFp8Block) * a.M + to_row[16 * j + u]] = __uint_as_float(static_cast<uint32_t>(e) << 23);
+          p.part_scale[n / (8 * PIECES) * a.M + to_row[16 * j + u]] = __uint_as_float(static_cast<uint32_t>(e) << 23);
       }
       const int row = 16 * (j - jj) + u;
 #pragma unroll
       for (int i = 0; i < S::TN; ++i) {
         const u32x2 b = {pack16(a.ydtype, acc[i][j][0] * f, acc[i][j][1] * f),
                          pack16(a.ydtype, acc[i][j][2] * f, acc[i][j][3] * f)};
-        *reinterpret_cast<u32x2*>(room + row * 256 + 16 * ((2 * i + (g >> 1)) ^ u) + 8 * (g & 1)) = b;
+        *reinterpret_cast<u32x2*>(room + row * 16 * PIECES + 16 * ((2 * i + (g >> 1)) ^ (u % PIECES)) + 8 * (g & 1)) = b;
       }
     }
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int row = 4 * t + g, r = wm + 16 * jj + row;
-      const u32x4 b = *reinterpret_cast<const u32x4*>(room + row * 256 + 16 * (u ^ (row & 15)));
-      if (r >= rows || n + 8 * u >= a.N) continue;
+    for (int t = 0; t < 32 / ROWS; ++t) {
+      const int row = ROWS * t + lane / PIECES, c = lane % PIECES, r = wm + 16 * jj + row;
+      const u32x4 b = *reinterpret_cast<const u32x4*>(room + row * 16 * PIECES + 16 * (c ^ (row % PIECES)));
+      if (r >= rows || n + 8 * c >= a.N) continue;
       const int64_t at = p.map.scatter ? to_row[16 * jj + row] : first + r;
-      uint16_t* to = static_cast<uint16_t*>(a.y) + at * a.ldy + n + 8 * u;
+      uint16_t* to = static_cast<uint16_t*>(a.y) + at * a.ldy + n + 8 * c;
       // non-temporal: all CUs store at once, and 128 KB each would turn over the L2 (8192 x 8192 x
       // 1024: 98 us with ordinary stores, 94)
-      if (n + 8 * u + 7 < a.N) {
+      if (n + 8 * c + 7 < a.N) {
         __builtin_nontemporal_store(b, reinterpret_cast<u32x4_at2*>(to));
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (n + 8 * u + e < a.N) to[e] = static_cast<uint16_t>(b[e / 2] >> (16 * (e & 1)));
+          if (n + 8 * c + e < a.N) to[e] = static_cast<uint16_t>(b[e / 2] >> (16 * (e & 1)));
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -433,7 +435,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   }
   if constexpr (S::WIDE) {
     if (a.ydtype != BL_F32) {
-      store_wide<S>(p, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * 8192, to_rows[wave], first, rows, wm, n0 + wn, lane);
+      store_wide<S>(p, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * (1024 * S::TN), to_rows[wave], first, rows, wm, n0 + wn, lane);
       return;
     }
   }
