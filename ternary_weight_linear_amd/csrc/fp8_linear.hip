@@ -25,7 +25,7 @@ hipError_t start_codes(const StreamArgs& st, hipStream_t s) {
   return start_stream<MT, 1, 8, kSrcCodes, kStreamLinear>(st, tiles, 0, s);
 }
 
-// One to four rows: each workgroup quantises them into LDS itself.
+// Each workgroup quantises the rows into LDS itself.
 hipError_t start_values(const StreamArgs& st, int xdtype, hipStream_t s) {
   const int rows = static_cast<int>(st.p.a.M);
   switch (stream_rows(st.p.a.N, 1)) {
@@ -145,8 +145,13 @@ hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const void* x, int xdtype, 
   st.p.a = a;
   st.x = x;
   st.ldx = ldx;
-  // (their codes and the reduction's 32 KB stay within 64 KB of LDS)
-  if (x && a.M <= 4 && a.M * a.K <= 28672) return start_values(st, xdtype, s);
+  // Few short rows: every workgroup quantises them itself, in one launch for two (us, this way /
+  // with the quantiser's launch: 16 x 8192 x 1792 11.5 / 14.1, 8 x 8192 x 3584 12.1 / 14.1), up to
+  // where more than four rows hold up long streams (16 x 28672 x 1792 15.6 / 14.2, 8 x 28672 x 3584
+  // 21.9 / 20.7). Their codes and the reduction's 32 KB stay within 64 KB of LDS.
+  if (x && a.M <= 16 && (a.M <= 4 || a.N * a.K <= (int64_t(1) << 25)) &&
+      a.K <= 32768 && staged_bytes(static_cast<int>(a.M), static_cast<int>(fp8_blocks(a.K))) <= 32768)
+    return start_values(st, xdtype, s);
   if (x) {
     const hipError_t e = launch_fp8_quant_act(x, xdtype, a.M, a.K, ldx, 0, nullptr, const_cast<uint8_t*>(a.q),
                                               const_cast<float*>(a.sx), s);

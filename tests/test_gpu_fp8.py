@@ -189,7 +189,7 @@ def test_linear_wide(M, N, K, out):
 @pytest.mark.parametrize("M,N,K", [(300, 2100, 3104), (25, 300, 8208), (270, 4100, 8208), (1500, 1500, 272), (1601, 777, 8336),
                                    (412, 8645, 144), (728, 8239, 144), (69, 1702, 3760), (67, 5774, 4448), (130, 6406, 10016),
                                    (70, 8272, 11136), (421, 8246, 5584), (265, 11054, 6960), (2377, 7091, 1424), (195, 12384, 2704),
-                                   (635, 14773, 2016)])
+                                   (635, 14773, 2016), (13, 100, 2192), (9, 300, 4112), (16, 5000, 8208), (8, 16500, 2064)])
 def test_linear_long_sums(M, N, K, out):
     """Every tile, whole, with K in parts, some of unequal lengths, and with the last tiles' in parts."""
     say("fp8 linear long sums", M, N, K, out)
