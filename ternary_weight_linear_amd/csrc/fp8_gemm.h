@@ -155,7 +155,7 @@ __device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&a
 // BN x BM outputs; a block of both operands is copied straight into LDS while the one before it is
 // multiplied. What bounds it: large tiles the matrix cores and the card's power (256 x 256,
 // 4096 x 28672 x 8192: 797 to 840 us, 2.3 to 2.4 PFLOP/s), small ones L2, fp16 operands the conversion of
-// the codes (512 x 3200 x 8640: 46 to 53 us). Of a 256 x 256 tile about 10 us are its start and its
+// the codes (512 x 3200 x 8640, K in five parts: 34 us). Of a 256 x 256 tile about 10 us are its start and its
 // stores; one workgroup per CU that takes tile after tile and copies the next one's first block
 // while it stores measured 1 to 3 % slower at every shape.
 template <class S>
@@ -450,7 +450,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
 }
 
 // y = the sum of the `parts` partial sums of each tile from `whole` on, in their order, four
-// columns per thread; they come from L2, and a launch is most of its time.
+// columns per thread. Reading them bounds it (five of 512 x 3200, 33 MB: 7 us).
 template <class S>
 __global__ __launch_bounds__(256) void sum_parts_kernel(ProductArgs p, int tiles_n, int tiles_m) {
   constexpr int PER = S::BM * S::BN / 1024;         // workgroups per tile

@@ -52,7 +52,7 @@ int64_t tiles(int64_t M, int64_t N, int bn, int bm) { return ((N + bn - 1) / bn)
 // in parts, best (unsplit): 512 x 8192 x 28672 128 x 128 155, 256 x 256 128 with 4 (334);
 //   300 x 4000 x 16384 64 x 64 62 (62), 128 x 128 46 with 2; 877 x 761 x 16384 64 x 64 29 with 3 (39)
 // fp16 operands, 128 x 128 / 64 x 64: 4096 x 28672 x 8192 1545 / -, 128 x 28672 x 8192 79 / 97,
-//   512 x 3200 x 8640 57 / 46; 96 x 8192 x 28672 78 with 4 parts (242) / 87 with 2 (133). With them
+//   512 x 3200 x 8640 57 (41 with 5 parts) / 46; 96 x 8192 x 28672 78 with 4 parts (242) / 87 with 2 (133). With them
 // converting the codes bounds it (a quarter-rate instruction per two of them, for each fragment
 // that a wave reads); staging q as fp16 halved that and lost as much to L2.
 struct Tile {
