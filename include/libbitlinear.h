@@ -422,8 +422,8 @@ int bl_route_experts(const void* logits, int dtype, int64_t M, int64_t E, int64_
  * outside [0, E) adds nothing (a row without any gives zeros). wgu codes [E, 2, I, H] (gate,
  * up) with scales [E, 2, ceil(I/128), ceil(H/128)]; wd codes [E, H, I] with scales
  * [E, ceil(H/128), ceil(I/128)]. H and I are multiples of 16; 1 <= E <= 4096,
- * 1 <= k <= 64, M k <= 2^20. Sums are fp32 sums in a fixed order for a given shape. Uses ws
- * (bl_fp8_experts_workspace_bytes). */
+ * 1 <= k <= 64, M k <= 2^20. G's and U's sums are those of fp32 results of bl_fp8_linear, D's
+ * those of ydtype; orders are fixed for a given shape. Uses ws (bl_fp8_experts_workspace_bytes). */
 size_t bl_fp8_experts_workspace_bytes(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I);
 int bl_fp8_experts(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
                    const int32_t* index, const float* weight, int64_t k, const uint8_t* wgu,

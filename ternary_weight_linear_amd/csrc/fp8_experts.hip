@@ -181,21 +181,18 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, 
   }
 }
 
-// Stages: three where the matrix instructions are fast, two where converting the codes is what
-// takes long (tiles of 128 rows, us for two / three: 1024 tokens, top 8 of 64, 4096 x 1024, bf16
-// 344 / 326, fp16 operands 3055 tokens, top 3 of 29, 1872 x 720 163 / 181).
-template <bool EXACT>
+// The gate and up products take fp16 operands whatever the types: a sum that errs by more than
+// fp32 does moves codes of silu(gate) * up (with the e4m3 instruction 1 of 3000, which put 1.2e-3
+// of the result beside the 1.7e-3 of its rounding to bf16).
 hipError_t start_up(const ProductArgs& p, int tile, int64_t nt, hipStream_t s) {
-  if (tile == 64) return start_gemm<GemmShape<256, 64, 4, 2, 3, EXACT, true>>(p, nt, s);
-  if constexpr (!EXACT)
-    if (tile == 256) return start_gemm<GemmShape<256, 256, 2, 4, 2, false, true>>(p, nt, s);
-  return start_gemm<GemmShape<256, 128, 2, 4, EXACT ? 2 : 3, EXACT, true>>(p, nt, s);
+  if (tile == 64) return start_gemm<GemmShape<256, 64, 4, 2, 3, true, true>>(p, nt, s);
+  return start_gemm<GemmShape<256, 128, 2, 4, 2, true, true>>(p, nt, s);
 }
+// Stages: three where the matrix instructions are fast, two where converting the codes is what
+// takes long.
 template <bool EXACT>
 hipError_t start_down(const ProductArgs& p, int tile, int64_t nt, hipStream_t s) {
   if (tile == 64) return start_gemm<GemmShape<256, 64, 4, 2, 3, EXACT>>(p, nt, s);
-  if constexpr (!EXACT)
-    if (tile == 256) return start_gemm<GemmShape<256, 256, 2, 4, 2, false>>(p, nt, s);
   return start_gemm<GemmShape<256, 128, 2, 4, EXACT ? 2 : 3, EXACT>>(p, nt, s);
 }
 
@@ -239,26 +236,21 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   auto* hq = reinterpret_cast<uint8_t*>(ws + L.hq_off);
   auto* hs = reinterpret_cast<float*>(ws + L.hs_off);
   auto* part = reinterpret_cast<float*>(ws + L.part_off);
-  // fp16 operands where the hidden layer's or the result's type would show the e4m3
-  // instruction's sums (its error, 1.4e-5 of a block's, moves a few hidden codes: 1/2 of
-  // bf16's rounding of the result, 4 times fp16's)
-  const bool exact = a.xdtype != BL_BF16, exact_down = a.ydtype == BL_F32;
-  // Rows per tile, by the average rows of an expert. Measured, us for tiles of 16 / 64 / 128 / 256
-  // rows, 64 experts of 4096 x 1024, top 8, bf16: 16 rows an expert 209 / 207 / 229 / 257, 32 312 /
-  // 257 / 240 / 264, 64 526 / 266 / 299 / 277, 128 - / 378 / 330 / 378, 256 - / 596 / 492 / 449;
-  // 16 experts of 2048 x 1024, top 2: 32 56 / 37 / 45 / 52, 128 144 / 67 / 55 / 75. Too few
-  // workgroups of a tile call for the next smaller one: 8 experts of 1024 x 256, top 2: 128 42 / 31
-  // / 39 / 48, 512 96 / 43 / 43 / 58; 9 of 2784 x 336, top 8: 32 35 / 42 / 49 / 59; 49 of 2384 x
-  // 128: 151 254 / 75 / 83 / 100 (over 60 shapes 1.3 % from the best tile on average). The tiled
-  // kernel's offsets are 32 bits.
+  const bool exact_down = a.ydtype == BL_F32;
+  // Rows per tile, by the average rows of an expert. Measured, us for tiles of 16 / 64 / 128 rows, 64
+  // experts of 4096 x 1024, top 8, bf16: 16 rows an expert 208 / 215 / 227, 32 319 / 257 / 241, 64
+  // 551 / 262 / 303, 96 782 / 343 / 313, 128 1019 / 389 / 333, 512 3849 / 1240 / 978; 16 experts of
+  // 2048 x 1024, top 2: 32 56 / 45 / 47, 128 149 / 84 / 66. Too few workgroups of a tile call for the
+  // next smaller one: 8 experts of 1024 x 256, top 2: 32 25 / 29 / 32, 128 41 / 32 / 41; 9 of 2784 x
+  // 336, top 8: 32 32 / 52 / 54; 49 of 2384 x 128: 151 251 / 82 / 91. The tiled kernel's offsets are
+  // 32 bits.
   const bool tiled = P > 16 * a.E && a.M * a.H < (int64_t(1) << 31) && 2 * a.I * a.H < (int64_t(1) << 31) &&
                      256 * a.I < (int64_t(1) << 31);
   const auto groups = [&](int64_t rows) {
     const int64_t most = (P + a.E - 1) / a.E;         // of one expert, were all alike
     return a.E * ((most + rows - 1) / rows) * ((a.I + 127) / 128);
   };
-  int tile = !tiled ? 16 : P <= 96 * a.E ? 64 : P <= 192 * a.E || exact || exact_down ? 128 : 256;
-  if (tile == 256 && groups(256) < 128) tile = 128;
+  int tile = !tiled ? 16 : P <= 96 * a.E ? 64 : 128;
   if (tile == 128 && groups(128) < 128) tile = 64;
   if (tile == 64 && P <= 40 * a.E && groups(64) <= 64) tile = 16;
   const int64_t nt = experts_max_tiles(P, a.E, tile);
@@ -334,7 +326,7 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
     if (e != hipSuccess) return e;
     e = start_stream<1, 4, 8, kSrcCodes, kStreamLinear>(down, nt, 0, s);
   } else {
-    e = exact ? start_up<true>(up.p, tile, nt, s) : start_up<false>(up.p, tile, nt, s);
+    e = start_up(up.p, tile, nt, s);
     if (e != hipSuccess) return e;
     e = exact_down ? start_down<true>(down.p, tile, nt, s) : start_down<false>(down.p, tile, nt, s);
   }
