@@ -134,51 +134,39 @@ __global__ __launch_bounds__(kSortThreads) void experts_place_kernel(SortArgs a)
   place_slots(a, chunk, cnt, next);
 }
 
-// y[m, n] = sum_j weight[m, j] part[m k + j, n], slots in their order. A thread has V columns
-// (16 bytes) and up to eight slots' loads in flight: reading the parts bounds it (32768 x 4096
-// fp16: 62 us, 4.9 TB/s).
-template <bool HALF>
-__global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, const void* __restrict__ part,
-                                                              const float* __restrict__ scale, int scale_cols) {
-  constexpr int V = HALF ? 8 : 4;
-  const int64_t m = blockIdx.x, P = a.M * a.k;
-  const int64_t n = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * V;
-  if (n >= a.H) return;                             // H % 16 == 0: all V or none
-  float sum[V] = {};
+// y[m, n] = sum_j weight[m, j] part[m k + j, n], slots in their order. A thread has four columns
+// (16 bytes) and up to eight slots' loads in flight: reading the parts bounds it (32768 x
+// 4096: 124 us, 4.6 TB/s).
+__global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, const float* __restrict__ part) {
+  const int64_t m = blockIdx.x;
+  const int64_t n = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * 4;
+  if (n >= a.H) return;                             // H % 16 == 0: all four or none
+  f32x4 sum = {0, 0, 0, 0};
   for (int64_t j0 = 0; j0 < a.k; j0 += 8) {
-    u32x4 v[8];
+    f32x4 v[8];
     float w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int64_t slot = m * a.k + j0 + j;
       const int e = j0 + j < a.k ? a.index[slot] : -1;
       w[j] = 0.0f;
-      v[j] = u32x4{0, 0, 0, 0};
+      v[j] = f32x4{0, 0, 0, 0};
       if (e >= 0 && e < a.E) {
         w[j] = a.weight[slot];
-        if constexpr (HALF) w[j] *= scale[n / scale_cols * P + slot];
-        v[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(part) + (slot * a.H + n) * (HALF ? 2 : 4));
+        v[j] = *reinterpret_cast<const f32x4*>(part + slot * a.H + n);
       }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float x;
-        if constexpr (HALF) x = to_float<BL_F16>(static_cast<uint16_t>(v[j][i / 2] >> (16 * (i & 1))));
-        else x = __uint_as_float(v[j][i]);
-        sum[i] += w[j] * x;
-      }
+      for (int i = 0; i < 4; ++i) sum[i] += w[j] * v[j][i];
   }
-#pragma unroll
-  for (int i = 0; i < V; i += 4) {
-    Fp8LinearArgs o{};
-    o.N = a.H;
-    o.y = a.y;
-    o.ldy = a.ldy;
-    o.ydtype = a.ydtype;
-    store4(o, m, n + i, f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]});
-  }
+  Fp8LinearArgs o{};
+  o.N = a.H;
+  o.y = a.y;
+  o.ldy = a.ldy;
+  o.ydtype = a.ydtype;
+  store4(o, m, n, sum);
 }
 
 // The gate and up products take fp16 operands whatever the types: a sum that errs by more than
@@ -219,7 +207,6 @@ ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
   w.hq_off = take(P * I);
   w.hs_off = take(P * IB * 4);
   w.part_off = take(P * H * 4);
-  w.ps_off = take(P * ((H + 63) / 64) * 4);
   w.total = off;
   return w;
 }
@@ -238,11 +225,11 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   auto* part = reinterpret_cast<float*>(ws + L.part_off);
   const bool exact_down = a.ydtype == BL_F32;
   // Rows per tile, by the average rows of an expert. Measured, us for tiles of 16 / 64 / 128 rows, 64
-  // experts of 4096 x 1024, top 8, bf16: 16 rows an expert 208 / 215 / 227, 32 319 / 257 / 241, 64
-  // 551 / 262 / 303, 96 782 / 343 / 313, 128 1019 / 389 / 333, 512 3849 / 1240 / 978; 16 experts of
-  // 2048 x 1024, top 2: 32 56 / 45 / 47, 128 149 / 84 / 66. Too few workgroups of a tile call for the
-  // next smaller one: 8 experts of 1024 x 256, top 2: 32 25 / 29 / 32, 128 41 / 32 / 41; 9 of 2784 x
-  // 336, top 8: 32 32 / 52 / 54; 49 of 2384 x 128: 151 251 / 82 / 91. The tiled kernel's offsets are
+  // experts of 4096 x 1024, top 8, bf16: 16 rows an expert 208 / 210 / 221, 32 319 / 262 / 242, 64
+  // 548 / 271 / 311, 96 782 / 351 / 322, 128 1015 / 396 / 347, 512 3833 / 1292 / 1076; 16 experts of
+  // 2048 x 1024, top 2: 32 57 / 44 / 45, 128 148 / 86 / 67. Too few workgroups of a tile call for the
+  // next smaller one: 8 experts of 1024 x 256, top 2: 32 28 / 29 / 30, 128 42 / 33 / 42; 9 of 2784 x
+  // 336, top 8: 32 33 / 50 / 49; 49 of 2384 x 128: 151 251 / 80 / 89. The tiled kernel's offsets are
   // 32 bits.
   const bool tiled = P > 16 * a.E && a.M * a.H < (int64_t(1) << 31) && 2 * a.I * a.H < (int64_t(1) << 31) &&
                      256 * a.I < (int64_t(1) << 31);
@@ -278,14 +265,7 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   up.E = static_cast<int>(a.E);
   up.k = static_cast<int>(a.k);
   StreamArgs down{};
-  // The experts' outputs wait for their sum in fp32, or, for results in bf16, as fp16 with a
-  // power-of-two scale per row and 64 or 128 columns (its rounding is 1/8 of the result's own):
-  // half the bytes to write and read back (1315 tokens, top 7 of 59, 2992 x 128, tiles of 64 rows:
-  // 116 / 103 us).
-  const bool half_parts = tile >= 64 && a.ydtype == BL_BF16;
-  auto* part_scale = reinterpret_cast<float*>(ws + L.ps_off);
-  down.p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, half_parts ? kPartType : BL_F32};
-  down.p.part_scale = part_scale;
+  down.p.a = Fp8LinearArgs{hq, hs, a.wd, a.sd, P, a.H, a.I, part, a.H, BL_F32};
   down.p.map = RowMap{tiles, head + 1, pair, 0, 1};
   down.p.w_stride = a.H * a.I;
   down.p.sw_stride = HB * IB;
@@ -331,10 +311,8 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
     e = exact_down ? start_down<true>(down.p, tile, nt, s) : start_down<false>(down.p, tile, nt, s);
   }
   if (e != hipSuccess) return e;
-  const uint32_t per = half_parts ? 2048 : 1024;
-  const dim3 grid(static_cast<uint32_t>(a.M), static_cast<uint32_t>((a.H + per - 1) / per));
-  if (half_parts) experts_combine_kernel<true><<<grid, 256, 0, s>>>(a, part, part_scale, tile == 64 ? 64 : 128);
-  else experts_combine_kernel<false><<<grid, 256, 0, s>>>(a, part, nullptr, 1);
+  const dim3 grid(static_cast<uint32_t>(a.M), static_cast<uint32_t>((a.H + 1023) / 1024));
+  experts_combine_kernel<<<grid, 256, 0, s>>>(a, part);
   return hipGetLastError();
 }
 

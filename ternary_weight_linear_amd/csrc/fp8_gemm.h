@@ -64,8 +64,8 @@ struct GemmShape {
   // A tile of w is BN / 2 gate rows and the BN / 2 up rows of the same channels, and the tile's
   // result is quantised silu(gate) * up. Each wave holds both rows of its channels.
   static constexpr bool GATED = GATED_;
-  // 16-bit results go out as rows of a wave's 64 or 128 columns (store_wide)
-  static constexpr bool WIDE = !EXACT && !GATED && BN == 256 && WAVES == 8 && (TN == 4 || TN == 8) && TM % 2 == 0;
+  // 16-bit results go out as rows of a wave's 128 columns (store_wide)
+  static constexpr bool WIDE = !EXACT && !GATED && BN == 256 && WAVES == 8 && TN == 8 && TM % 2 == 0;
   static constexpr int NF = GATED ? 2 : 1;          // blocks of 128 rows of w that a wave reads
   static_assert(!GATED || BN == 256, "a gated tile is one block of 128 channels");
   static constexpr int NS = NS_;                    // stages: NS - 1 blocks' copies in flight
@@ -85,46 +85,22 @@ __device__ __forceinline__ Operand<EXACT> read_operand(const uint8_t* tile, uint
   return operand<EXACT>(f);
 }
 
-// Stores a wave's 16-bit results through LDS of its own, 32 rows at a time, so that each row's 64
-// or 128 columns go out as 128 or 256 consecutive bytes (from registers a row gets 32 bytes per
-// store: four lanes of four columns). 16-byte pieces are in XOR order as in the tiles.
-// to_row: the wave's 64 output rows if they are scattered.
-// kPartType: fp16 of value / scale, scale a power of two per row and a wave's columns that brings
-// their largest magnitude to [2^14, 2^15); values that are not finite stay so.
+// Stores a wave's 16-bit results through LDS of its own, 32 rows at a time, so that each row's 128
+// columns go out as 256 consecutive bytes (from registers a row gets 32 bytes per store: four
+// lanes of four columns). 16-byte pieces are in XOR order as in the tiles.
 template <class S>
-__device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&acc)[S::TN][S::TM], uint8_t* room, const int* to_row,
-                                           int64_t first, int rows, int wm, int64_t n, int lane) {
+__device__ __forceinline__ void store_wide(const Fp8LinearArgs& a, const f32x4 (&acc)[S::TN][S::TM], uint8_t* room, int64_t first,
+                                           int rows, int wm, int64_t n, int lane) {
   constexpr int PIECES = 2 * S::TN, ROWS = 64 / PIECES;   // 16-byte pieces of a row, rows per store
-  const Fp8LinearArgs& a = p.a;
   const int g = lane >> 4, u = lane & 15;
 #pragma unroll
   for (int jj = 0; jj < S::TM; jj += 2) {
 #pragma unroll
     for (int j = jj; j < jj + 2; ++j) {
-      float f = 1.0f;
-      if (a.ydtype == kPartType) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < S::TN; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t b = n + 16 * i + 4 * g + e < a.N ? abs_bits(acc[i][j][e]) : 0;
-            m = max(m, b < 0x7F800000u ? b : 0);
-          }
-        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
-        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
-        // exponent of the scale, kept where the scale and its reciprocal are normal numbers
-        const int e = min(max(static_cast<int>(m >> 23) - 14, 1), 253);
-        f = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        const int r = wm + 16 * j + u;
-        if (g == 0 && r < rows && n < a.N)
-          p.part_scale[n / (8 * PIECES) * a.M + to_row[16 * j + u]] = __uint_as_float(static_cast<uint32_t>(e) << 23);
-      }
       const int row = 16 * (j - jj) + u;
 #pragma unroll
       for (int i = 0; i < S::TN; ++i) {
-        const u32x2 b = {pack16(a.ydtype, acc[i][j][0] * f, acc[i][j][1] * f),
-                         pack16(a.ydtype, acc[i][j][2] * f, acc[i][j][3] * f)};
+        const u32x2 b = {pack16(a.ydtype, acc[i][j][0], acc[i][j][1]), pack16(a.ydtype, acc[i][j][2], acc[i][j][3])};
         *reinterpret_cast<u32x2*>(room + row * 16 * PIECES + 16 * ((2 * i + (g >> 1)) ^ (u % PIECES)) + 8 * (g & 1)) = b;
       }
     }
@@ -134,8 +110,7 @@ __device__ __forceinline__ void store_wide(const ProductArgs& p, const f32x4 (&a
       const int row = ROWS * t + lane / PIECES, c = lane % PIECES, r = wm + 16 * jj + row;
       const u32x4 b = *reinterpret_cast<const u32x4*>(room + row * 16 * PIECES + 16 * (c ^ (row % PIECES)));
       if (r >= rows || n + 8 * c >= a.N) continue;
-      const int64_t at = p.map.scatter ? to_row[16 * jj + row] : first + r;
-      uint16_t* to = static_cast<uint16_t*>(a.y) + at * a.ldy + n + 8 * c;
+      uint16_t* to = static_cast<uint16_t*>(a.y) + (first + r) * a.ldy + n + 8 * c;
       // non-temporal: all CUs store at once, and 128 KB each would turn over the L2 (8192 x 8192 x
       // 1024: 98 us with ordinary stores, 94)
       if (n + 8 * c + 7 < a.N) {
@@ -435,7 +410,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
   }
   if constexpr (S::WIDE) {
     if (a.ydtype != BL_F32) {
-      store_wide<S>(p, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * (1024 * S::TN), to_rows[wave], first, rows, wm, n0 + wn, lane);
+      store_wide<S>(a, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * (1024 * S::TN), first, rows, wm, n0 + wn, lane);
       return;
     }
   }

@@ -28,8 +28,6 @@ struct Fp8LinearArgs {
   int64_t ldy;
   int ydtype;
 };
-// Besides bl_dtype: the experts' outputs before their weighted sum, as scaled fp16.
-constexpr int kPartType = 3;
 
 struct Fp8ExpertsArgs {
   const void* x;         // [M, H], rows ldx elements apart
@@ -70,8 +68,7 @@ struct ExpertsWs {
   size_t count_off;            // int32 [chunks, E]: slots per expert of each chunk of the sort
   size_t h_off;                // fp32 [P, I] silu(gate) * up, where it is not quantised at once
   size_t hq_off, hs_off;       // quantised silu(gate) * up: codes [P, I], scales [IB, P]
-  size_t part_off;             // fp32 or scaled fp16 [P, H]: outputs before the weighted sum
-  size_t ps_off;               // fp32 [HB, P] scales of fp16 outputs
+  size_t part_off;             // fp32 [P, H]: outputs before the weighted sum
   size_t total;
 };
 ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I);

@@ -117,7 +117,6 @@ struct ProductArgs {
   // leave fp32 sums [parts, tiles, BM, BN] in part
   int whole, parts;
   float* part;
-  float* part_scale;             // y of kPartType: [a wave's columns, rows of y]
 };
 
 // Vectors at any multiple of their element's size: global memory takes unaligned accesses.

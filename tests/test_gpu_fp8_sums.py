@@ -105,3 +105,23 @@ def test_experts_sums_have_32_bits(M, E, k, H, I, dtype, out):
     y = values(tw.bl_fp8_experts(x, gpu(index), gpu(wt), *operands(W), out_dtype=TYPES[out]))
     some = np.random.default_rng(1).permutation(M)[:128]
     most_rows_err_by_rounding(y[some], experts_exact(v[some], index[some], wt[some], *W), out, 2.0 ** -14)
+
+
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("M,E,H,I", [(300, 4, 272, 528), (1200, 4, 528, 1040), (2000, 16, 1040, 272)])
+def test_experts_outputs_that_nearly_cancel(M, E, H, I, out):
+    """Two experts alike but for 2^-9 of the down matrix's scales, with weights 1 and -1: the
+    result is 2^-9 of either output, so that those have to be summed as fp32."""
+    say("experts cancel", M, E, H, I, out)
+    x, v = act((M, H), "bf16", M)
+    wgu, sgu, wd, sd = expert_weights(E, H, I, 50)
+    wgu, sgu, wd = (np.repeat(a[: E // 2], 2, 0) for a in (wgu, sgu, wd))
+    sd = np.repeat(sd[: E // 2], 2, 0)
+    sd[1::2] *= np.float32(1 + 2.0 ** -9)
+    first = 2 * np.random.default_rng(3).integers(0, E // 2, M)
+    index = np.stack([first, first + 1], 1).astype(np.int32)
+    wt = np.tile(np.array([1, -1], np.float32), (M, 1))
+    y = values(tw.bl_fp8_experts(x, gpu(index), gpu(wt), f8(wgu), gpu(sgu), f8(wd), gpu(sd), out_dtype=TYPES[out]))
+    some = np.random.default_rng(4).permutation(M)[:128]
+    # the outputs' fp32 sums, within 2^-22, are 2^-13 of the result each
+    most_rows_err_by_rounding(y[some], experts_exact(v[some], index[some], wt[some], wgu, sgu, wd, sd), out, 2.0 ** -11)
