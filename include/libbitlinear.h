@@ -381,9 +381,10 @@ int bl_quant_act_fp8(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx
 
 /* Block-scaled product of codes:
  *   y[m, n] = sum_b scales_x[b, m] scales_w[n / 128, b] sum_{k in block b} q[m, k] w[n, k],
- * rounded once to ydtype. Sums run in a fixed order for a given shape and ydtype: for fp32
- * results in fp32; for 16-bit results and more than 16 rows the sum within a block may keep
- * only 16 bits below its largest product (relative error 1.4e-5), the sum over blocks is fp32.
+ * rounded once to ydtype. Sums run in a fixed order for a given shape and ydtype. For fp32 and
+ * fp16 results they are fp32 sums. For bf16 results and more than 16 rows a block's sum of
+ * products may err by 7 2^-13 of the sum of their magnitudes (2e-5 of it on normal values, 3e-4
+ * where one input is far larger than the others); the sum over blocks is fp32.
  * Uses ws (bl_fp8_workspace_bytes(M, N, K)). */
 size_t bl_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int bl_fp8_linear(const uint8_t* q, const float* scales_x, int64_t M, int64_t K, const uint8_t* w,

@@ -64,7 +64,7 @@ struct GemmShape {
   // A tile of w is BN / 2 gate rows and the BN / 2 up rows of the same channels, and the tile's
   // result is quantised silu(gate) * up. Each wave holds both rows of its channels.
   static constexpr bool GATED = GATED_;
-  // 16-bit results go out as rows of a wave's 128 columns (store_wide)
+  // bf16 results go out as rows of a wave's 128 columns (store_wide)
   static constexpr bool WIDE = !EXACT && !GATED && BN == 256 && WAVES == 8 && TN == 8 && TM % 2 == 0;
   static constexpr int NF = GATED ? 2 : 1;          // blocks of 128 rows of w that a wave reads
   static_assert(!GATED || BN == 256, "a gated tile is one block of 128 channels");
@@ -85,7 +85,7 @@ __device__ __forceinline__ Operand<EXACT> read_operand(const uint8_t* tile, uint
   return operand<EXACT>(f);
 }
 
-// Stores a wave's 16-bit results through LDS of its own, 32 rows at a time, so that each row's 128
+// Stores a wave's bf16 results through LDS of its own, 32 rows at a time, so that each row's 128
 // columns go out as 256 consecutive bytes (from registers a row gets 32 bytes per store: four
 // lanes of four columns). 16-byte pieces are in XOR order as in the tiles.
 template <class S>
@@ -409,7 +409,7 @@ __global__ __launch_bounds__(S::THREADS) void fp8_gemm_kernel(ProductArgs p, int
     return;
   }
   if constexpr (S::WIDE) {
-    if (a.ydtype != BL_F32) {
+    if (a.ydtype == BL_BF16) {
       store_wide<S>(a, acc, (wave < 4 ? bufA0 : bufA1) + (wave & 3) * (1024 * S::TN), first, rows, wm, n0 + wn, lane);
       return;
     }

@@ -159,12 +159,13 @@ hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const void* x, int xdtype, 
   }
   if (a.M <= 16) return start_codes<1>(st, s);
   // Up to 32 rows of short K still stream; over a long K the tiled kernel in parts has more loads
-  // in flight (us, streamed / tiled, 16-bit results: 25 x 1750 x 3232 5.6 / 10.2, 32 x 4096 x 4096
-  // 9.4 / 10.4, 32 x 8192 x 8192 20.6 / 17.4, 24 x 4096 x 11008 19.6 / 14.0; fp32: 32 x 8192 x 8192
+  // in flight (us, streamed / tiled, bf16 results: 25 x 1750 x 3232 5.6 / 10.2, 32 x 4096 x 4096
+  // 9.4 / 10.4, 32 x 8192 x 8192 20.6 / 17.4, 24 x 4096 x 11008 19.6 / 14.0; fp16 operands: 32 x 8192 x 8192
   // 20.5 / 22, 25 x 910 x 20864 32.7 / 18.9). The tiled kernel's offsets are 32 bits.
-  const int64_t stream_k = a.ydtype == BL_F32 ? 8192 : 4096;
+  const bool exact = a.ydtype != BL_BF16;
+  const int64_t stream_k = exact ? 8192 : 4096;
   if ((a.M <= 32 && a.K <= stream_k) || 256 * a.K >= (int64_t(1) << 31)) return start_codes<2>(st, s);
-  return a.ydtype == BL_F32 ? start_tiled<true>(st.p, part, s) : start_tiled<false>(st.p, part, s);
+  return exact ? start_tiled<true>(st.p, part, s) : start_tiled<false>(st.p, part, s);
 }
 
 }  // namespace bl

@@ -125,3 +125,68 @@ def test_experts_outputs_that_nearly_cancel(M, E, H, I, out):
     some = np.random.default_rng(4).permutation(M)[:128]
     # the outputs' fp32 sums, within 2^-22, are 2^-13 of the result each
     most_rows_err_by_rounding(y[some], experts_exact(v[some], index[some], wt[some], wgu, sgu, wd, sd), out, 2.0 ** -11)
+
+
+# ------------------------------------------------------------------------------------------
+# one loud channel in every block
+# ------------------------------------------------------------------------------------------
+def half_unit(ref, dtype):
+    """Half a unit in the last place of the type at ref."""
+    bits, least = {"fp16": (10, -14), "bf16": (7, -126), "fp32": (23, -126)}[dtype]
+    return np.exp2(np.maximum(np.frexp(ref)[1] - 1, least) - bits - 1)
+
+
+# Streamed, and each tile of each instruction, whole and with K in parts.
+WIDTHS = [(1, 300, 1040), (16, 1000, 2064), (24, 900, 4112), (40, 1000, 8208), (64, 128, 128), (129, 384, 528),
+          (300, 2100, 3104), (270, 4100, 8208), (500, 3300, 1040), (500, 6600, 656), (520, 8200, 400), (1601, 777, 2192),
+          (421, 8246, 1584)]
+
+
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("M,N,K", WIDTHS)
+def test_linear_with_a_loud_channel(M, N, K, out):
+    """Positive values, in each block one channel 448 times the others: the small products add up
+    to a tenth of the large one, and sums that dropped their low bits would all err the same way.
+    Every result within its own rounding and that of an fp32 sum: 128 roundings of a block's
+    magnitudes and one for each block; bf16 results within 7 2^-13 of the magnitudes beside it."""
+    say("fp8 linear loud", M, N, K, out)
+    g = np.random.default_rng(M + N)
+    v = np.abs(g.standard_normal((M, K))).astype(np.float32) + np.float32(0.1)
+    v[:, 77::128] = 448 * (1 + np.arange(v[:, 77::128].shape[1]) % 3)
+    x = gpu(v).to(torch.bfloat16)
+    w, s = of.quant_weight(np.abs(g.standard_normal((N, K))).astype(np.float32) * np.float32(K ** -0.5))
+    c, sx, _ = of.quant_act(values(x).astype(np.float32))
+    ref, mag = of.linear(c, sx, w, s)
+    y = values(tw.bl_fp8_forward(x, f8(w), gpu(s), out_dtype=TYPES[out]))
+    tol = half_unit(ref, out) * (1 + 2.0 ** -10) + (2.0 ** -17 + (K // 128 + 4) * 2.0 ** -23) * mag
+    if out == "bf16":
+        tol += 7 * 2.0 ** -13 * mag
+    worst = float((np.abs(y - ref) / tol).max())
+    assert worst <= 1, f"{worst} times the allowed error"
+
+
+@pytest.mark.parametrize("M,E,k,H,I", [(300, 6, 4, 272, 528), (1300, 4, 2, 400, 1040)])
+def test_experts_fp16_results_with_a_loud_channel(M, E, k, H, I):
+    """As above in the down product: everything positive, every eighth channel of silu(gate) * up a
+    few hundred times the others."""
+    say("experts loud", M, E, k, H, I)
+    g = np.random.default_rng(M)
+    x = gpu(np.abs(g.standard_normal((M, H))).astype(np.float32)).half()
+    pos = lambda n, m: np.abs(g.standard_normal((n, m))).astype(np.float32) / np.float32(m)
+    gu, d = [], []
+    for e in range(E):
+        up = pos(I, H)
+        up[3::8] *= 300
+        gu.append([of.quant_weight(pos(I, H)), of.quant_weight(up)])
+        d.append(of.quant_weight(pos(H, I)))
+    W = (np.stack([np.stack([c for c, _ in p]) for p in gu]), np.stack([np.stack([s for _, s in p]) for p in gu]),
+         np.stack([c for c, _ in d]), np.stack([s for _, s in d]))
+    index, wt = choose(M, E, k, 6)
+    y = values(tw.bl_fp8_experts(x, gpu(index), gpu(wt), *operands(W)))
+    some = g.permutation(M)[:128]
+    ref = experts_exact(values(x)[some].astype(np.float32), index[some], wt[some], *W)
+    most_rows_err_by_rounding(y[some], ref, "fp16", 2.0 ** -14)
+    # roundings to fp16, up to 2^-11 either way, leave 2^-15 or less in the mean over a row's
+    # columns (and codes that are others touch few rows); low bits dropped of positive sums stay
+    shift = abs(float(np.median(np.mean(y[some] / ref - 1, 1))))
+    assert shift <= 2.0 ** -15, f"results are off by {shift:.3g} on average"
