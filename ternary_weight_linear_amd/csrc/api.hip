@@ -698,7 +698,7 @@ int bl_residual_linear(const uint16_t* x, const void* planes_o, const float* alp
 int bl_fp8_quant_weight(const float* W, int64_t N, int64_t K, uint8_t* codes, float* scales,
                         void* stream) {
   if (!W || !codes || !scales) return BL_ERR_NULL;
-  if (!fp8_dims_ok(1, N, K) || fp8_blocks(N) * fp8_blocks(K) >= (int64_t(1) << 31)) return BL_ERR_SHAPE;
+  if (!fp8_dims_ok(1, N, K)) return BL_ERR_SHAPE;
   if (!aligned16(W) || !aligned16(codes) || !aligned_to(scales, 4)) return BL_ERR_ALIGN;
   const size_t n = static_cast<size_t>(N) * K;
   const Span outs[] = {{codes, n}, {scales, static_cast<size_t>(fp8_blocks(N)) * fp8_blocks(K) * 4}};
@@ -711,7 +711,7 @@ int bl_fp8_quant_weight(const float* W, int64_t N, int64_t K, uint8_t* codes, fl
 int bl_quant_act_fp8(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, int gated,
                      uint8_t* q, float* scales, void* stream) {
   if (!x || !q || !scales) return BL_ERR_NULL;
-  if (!fp8_dims_ok(M, 1, K) || M * fp8_blocks(K) >= (int64_t(1) << 34)) return BL_ERR_SHAPE;
+  if (!fp8_dims_ok(M, 1, K)) return BL_ERR_SHAPE;
   const int64_t width = gated ? 2 * K : K;
   if (int st = check_rows_in(x, dtype, width, ldx)) return st;
   if (!aligned16(q) || !aligned_to(scales, 4)) return BL_ERR_ALIGN;
@@ -753,7 +753,7 @@ int bl_fp8_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, 
                    const float* scales_w, int64_t N, void* y, int ydtype, int64_t ldy, void* ws,
                    size_t ws_bytes, void* stream) {
   if (!x || !w || !scales_w || !y) return BL_ERR_NULL;
-  if (!fp8_dims_ok(M, N, K) || M * fp8_blocks(K) >= (int64_t(1) << 34)) return BL_ERR_SHAPE;
+  if (!fp8_dims_ok(M, N, K)) return BL_ERR_SHAPE;
   if (int st = check_rows_in(x, dtype, K, ldx)) return st;
   if (int st = check_rows_out(y, ydtype, N, ldy)) return st;
   const Fp8Ws L = fp8_ws(M, N, K);

@@ -17,6 +17,13 @@ constexpr uint32_t kFp8FloorBits = 0x0D800000u;     // 2^-100, the least block m
 inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 inline size_t dtype_bytes(int dtype) { return dtype == BL_F32 ? 4 : 2; }
 
+// A launch whose work-items along one dimension pass 2^32 runs modulo that, without an error. So
+// workgroups that may be many go over two dimensions (the last few of them may be too many).
+inline dim3 grid_of(int64_t groups) {
+  const int64_t x = groups < (int64_t(1) << 20) ? groups : int64_t(1) << 20;
+  return dim3(static_cast<uint32_t>(x), static_cast<uint32_t>((groups + x - 1) / x));
+}
+
 // y = linear(q, w) on rows that are all multiplied by one weight matrix.
 struct Fp8LinearArgs {
   const uint8_t* q;      // e4m3 codes [M, K]
@@ -88,6 +95,9 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s);
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 
 // ---- device helpers ------------------------------------------------------------------------
+
+// Which workgroup of grid_of's this is.
+__device__ __forceinline__ int64_t group_id() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
 
 template <int DT>
 struct Elem;  // storage type of a bl_dtype

@@ -17,7 +17,7 @@ namespace {
 // 2048 x 8640 20.6 (4.3 TB/s), fp16 16 x 8192 2.8.
 template <int DT, bool GATED>
 __global__ __launch_bounds__(256) void fp8_quant_act_kernel(QuantArgs q) {
-  quant_blocks<DT, GATED>(q, static_cast<int64_t>(blockIdx.x) * 16);
+  quant_blocks<DT, GATED>(q, group_id() * 16);
 }
 
 // One workgroup per 128 x 128 block: thread t holds rows t / 16 + 16 i, inputs 8 (t % 16) ...,
@@ -27,7 +27,8 @@ __global__ __launch_bounds__(256) void fp8_quant_weight_kernel(const float* __re
                                                                uint8_t* __restrict__ codes,
                                                                float* __restrict__ scale) {
   __shared__ uint32_t red[4];
-  const int64_t nb = blockIdx.x / KB, kb = blockIdx.x % KB;
+  const int64_t nb = group_id() / KB, kb = group_id() - nb * KB;
+  if (nb * kFp8Block >= N) return;
   const int r = threadIdx.x >> 4;
   const int64_t k = kb * kFp8Block + (threadIdx.x & 15) * 8;
   float v[8][8];
@@ -59,7 +60,7 @@ template <int DT>
 void start_quant(const void* x, int64_t M, int64_t K, int64_t ldx, int gated,
                  const int32_t* rows_used, uint8_t* q, float* scale, hipStream_t s) {
   const QuantArgs a{x, M, K, fp8_blocks(K), ldx, rows_used, q, scale};
-  const dim3 grid(static_cast<uint32_t>((M * a.KB + 15) / 16));
+  const dim3 grid = grid_of((M * a.KB + 15) / 16);
   if (gated) fp8_quant_act_kernel<DT, true><<<grid, 256, 0, s>>>(a);
   else fp8_quant_act_kernel<DT, false><<<grid, 256, 0, s>>>(a);
 }
@@ -78,7 +79,7 @@ hipError_t launch_fp8_quant_act(const void* x, int dtype, int64_t M, int64_t K, 
 hipError_t launch_fp8_quant_weight(const float* W, int64_t N, int64_t K, uint8_t* codes,
                                    float* scale, hipStream_t s) {
   const int64_t NB = fp8_blocks(N), KB = fp8_blocks(K);
-  fp8_quant_weight_kernel<<<static_cast<uint32_t>(NB * KB), 256, 0, s>>>(W, N, K, KB, codes, scale);
+  fp8_quant_weight_kernel<<<grid_of(NB * KB), 256, 0, s>>>(W, N, K, KB, codes, scale);
   return hipGetLastError();
 }
 

@@ -1,0 +1,39 @@
+"""Calls of the 8-bit floating point operators that need more than 2^32 work-items or offsets past
+32 bits: accepted sizes are computed, from the first row to the last."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.fp8 as of
+import ternary_weight_linear_amd as tw
+from tests.gpu_util import DEV, host, say
+
+pytestmark = pytest.mark.gpu
+
+
+def needs(gib):
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0]
+    if free < gib * 2 ** 30:
+        pytest.skip(f"needs {gib} GiB of free GPU memory, has {free / 2 ** 30:.0f}")
+
+
+@pytest.fixture(autouse=True)
+def give_back():
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_quant_act_of_more_than_2_28_blocks():
+    M, K = 1 << 20, 33008                          # 258 blocks a row
+    needs(110)
+    say("quant_act large", M, K)
+    x = torch.zeros((M, K), dtype=torch.float16, device=DEV)
+    rows = [0, 1, (1 << 19) + 3, M - 2, M - 1]
+    v = np.random.default_rng(0).standard_normal((len(rows), K)).astype(np.float16)
+    x[rows] = torch.from_numpy(v).to(DEV)
+    q, s = tw.bl_quant_act_fp8(x)
+    c, sr, _ = of.quant_act(v.astype(np.float32))
+    assert np.array_equal(host(q[rows].view(torch.uint8)), c) and np.array_equal(host(s[:, rows]), sr)
+    zero, floor = [2, (1 << 19) + 4, M - 3], of.quant_act(np.zeros((1, K), np.float32))[1]
+    assert not host(q[zero].view(torch.uint8)).any() and np.array_equal(host(s[:, zero]), np.repeat(floor, 3, 1))
