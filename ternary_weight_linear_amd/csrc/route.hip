@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256) void route_row16_kernel(RouteArgs a, int C, in
   __shared__ float scores[16][16 * NE + 16];        // expert e0 + i of lane j at 16 i + j
   __shared__ uint32_t chosen[16][16];               // place in scores, expert
   const uint32_t lane = threadIdx.x & 15, in = threadIdx.x >> 4;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + in;
+  const int64_t m = group_id() * 16 + in;
   const int64_t mc = m < a.M ? m : a.M - 1;         // rows past the end work on the last one
   const int E = static_cast<int>(a.E), size = E / a.groups;
   const int group = static_cast<int>(lane) >> shift, within = (static_cast<int>(lane) & ((1 << shift) - 1)) * C;
@@ -250,7 +250,7 @@ template <int DT>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wave;
+  const int64_t m = group_id() * kRouteWaves + wave;
   if (m >= a.M) return;                     // waves never meet: no barrier below
   const int E = static_cast<int>(a.E);
   float* score = lds + wave * 2 * E;
@@ -364,7 +364,7 @@ hipError_t start_row16(const RouteArgs& a, int C, int shift, hipStream_t s) {
   const int vec = C == NE && 16 * C == a.E && C * size % 16 == 0 && a.ld * size % 16 == 0 &&
                   reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
                   reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-  route_row16_kernel<DT, NE><<<dim3(static_cast<uint32_t>((a.M + 15) / 16)), 256, 0, s>>>(a, C, shift, vec);
+  route_row16_kernel<DT, NE><<<grid_of((a.M + 15) / 16), 256, 0, s>>>(a, C, shift, vec);
   return hipGetLastError();
 }
 
@@ -380,7 +380,7 @@ hipError_t start_route(const RouteArgs& a, hipStream_t s) {
     if (C <= 16) return start_row16<DT, 16>(a, C, shift, s);
     if (C <= 32) return start_row16<DT, 32>(a, C, shift, s);
   }
-  const dim3 grid(static_cast<uint32_t>((a.M + kRouteWaves - 1) / kRouteWaves));
+  const dim3 grid = grid_of((a.M + kRouteWaves - 1) / kRouteWaves);
   route_kernel<DT><<<grid, 64 * kRouteWaves, static_cast<size_t>(kRouteWaves) * 2 * a.E * 4, s>>>(a);
   return hipGetLastError();
 }

@@ -37,3 +37,18 @@ def test_quant_act_of_more_than_2_28_blocks():
     assert np.array_equal(host(q[rows].view(torch.uint8)), c) and np.array_equal(host(s[:, rows]), sr)
     zero, floor = [2, (1 << 19) + 4, M - 3], of.quant_act(np.zeros((1, K), np.float32))[1]
     assert not host(q[zero].view(torch.uint8)).any() and np.array_equal(host(s[:, zero]), np.repeat(floor, 3, 1))
+
+
+@pytest.mark.parametrize("M,E,k", [((1 << 26) + 5, 18, 17), ((1 << 28) + 5, 2, 1)])
+def test_route_of_many_rows(M, E, k):
+    """Rows repeat every 1000: each repetition gives what the first does."""
+    needs(24)
+    say("route large", M, E, k)
+    some = torch.from_numpy(np.random.default_rng(1).standard_normal((1000, E)).astype(np.float16)).to(DEV)
+    times = -(-M // 1000)
+    logits = some.repeat(times, 1)[:M]
+    w, i = tw.bl_route_experts(logits, k)
+    w0, i0 = tw.bl_route_experts(some, k)
+    for got, want in ((w, w0), (i, i0)):
+        whole = got[: (times - 1) * 1000].view(times - 1, 1000, k)
+        assert bool((whole == want).all()) and torch.equal(got[(times - 1) * 1000:], want[: M - (times - 1) * 1000])
