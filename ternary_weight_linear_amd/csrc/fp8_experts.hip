@@ -1,6 +1,8 @@
 // The experts' gated products (bl_fp8_experts): sort the (token, slot) pairs by expert,
 // quantise x, multiply by the gate and up matrices, quantise silu(gate) * up, multiply by the
 // down matrix, and add each token's slots with their weights.
+#include <algorithm>
+
 #include "fp8_gemm.h"
 
 namespace bl {
@@ -184,12 +186,29 @@ hipError_t start_down(const ProductArgs& p, int tile, int64_t nt, hipStream_t s)
   return start_gemm<GemmShape<256, 128, 2, 4, EXACT ? 2 : 3, EXACT>>(p, nt, s);
 }
 
+int64_t max_tiles(int64_t P, int64_t E, int tile) { return P / tile + (P < E ? P : E); }
+
+// The tiled kernel's offsets within a matrix are 32 bits.
+bool matrices_fit(int64_t H, int64_t I) {
+  return 2 * I * H < (int64_t(1) << 31) && 256 * I < (int64_t(1) << 31);
+}
+
+// Tokens of one pass: a call of more runs pass after pass. The tiled kernel gathers rows of x's
+// codes by 32-bit offsets, and the grids of the products stay in their limits (the streamed tiles
+// of 16 rows lie along a dimension of 65535).
+int64_t pass_tokens(int64_t M, int64_t H, int64_t k, int64_t I) {
+  int64_t most = ((int64_t(1) << 31) - 1) / H;
+  const int64_t slots = (int64_t(1) << 35) / I;
+  most = std::min(most, std::max<int64_t>((matrices_fit(H, I) ? slots : std::min<int64_t>(slots, 1 << 19)) / k, 1));
+  const int64_t passes = (M + most - 1) / most;
+  return (M + passes - 1) / passes;
+}
+
 }  // namespace
 
-int64_t experts_max_tiles(int64_t P, int64_t E, int tile) { return P / tile + (P < E ? P : E); }
-
-ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
+ExpertsWs experts_ws(int64_t M_all, int64_t H, int64_t k, int64_t E, int64_t I) {
   ExpertsWs w{};
+  const int64_t M = pass_tokens(M_all, H, k, I);
   const int64_t P = M * k, HB = fp8_blocks(H), IB = fp8_blocks(I);
   size_t off = 0;
   auto take = [&](int64_t bytes) {
@@ -201,7 +220,7 @@ ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
   w.sx_off = take(M * HB * 4);
   w.head_off = take(16);
   w.pair_off = take(P * 4);
-  w.tile_off = take(experts_max_tiles(P, E, 16) * 16);
+  w.tile_off = take(max_tiles(P, E, 16) * 16);
   w.count_off = take((P + sort_chunk(P) - 1) / sort_chunk(P) * E * 4);
   w.h_off = take(P * I * 4);
   w.hq_off = take(P * I);
@@ -211,7 +230,9 @@ ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
   return w;
 }
 
-hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) {
+namespace {
+
+hipError_t start_pass(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) {
   const ExpertsWs L = experts_ws(a.M, a.H, a.k, a.E, a.I);
   const int64_t P = a.M * a.k, HB = fp8_blocks(a.H), IB = fp8_blocks(a.I);
   auto* q = reinterpret_cast<uint8_t*>(ws + L.q_off);
@@ -229,10 +250,8 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   // 548 / 271 / 311, 96 782 / 351 / 322, 128 1015 / 396 / 347, 512 3833 / 1292 / 1076; 16 experts of
   // 2048 x 1024, top 2: 32 57 / 44 / 45, 128 148 / 86 / 67. Too few workgroups of a tile call for the
   // next smaller one: 8 experts of 1024 x 256, top 2: 32 28 / 29 / 30, 128 42 / 33 / 42; 9 of 2784 x
-  // 336, top 8: 32 33 / 50 / 49; 49 of 2384 x 128: 151 251 / 80 / 89. The tiled kernel's offsets are
-  // 32 bits.
-  const bool tiled = P > 16 * a.E && a.M * a.H < (int64_t(1) << 31) && 2 * a.I * a.H < (int64_t(1) << 31) &&
-                     256 * a.I < (int64_t(1) << 31);
+  // 336, top 8: 32 33 / 50 / 49; 49 of 2384 x 128: 151 251 / 80 / 89.
+  const bool tiled = P > 16 * a.E && matrices_fit(a.H, a.I);
   const auto groups = [&](int64_t rows) {
     const int64_t most = (P + a.E - 1) / a.E;         // of one expert, were all alike
     return a.E * ((most + rows - 1) / rows) * ((a.I + 127) / 128);
@@ -240,7 +259,7 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   int tile = !tiled ? 16 : P <= 96 * a.E ? 64 : 128;
   if (tile == 128 && groups(128) < 128) tile = 64;
   if (tile == 64 && P <= 40 * a.E && groups(64) <= 64) tile = 16;
-  const int64_t nt = experts_max_tiles(P, a.E, tile);
+  const int64_t nt = max_tiles(P, a.E, tile);
   // Few slots, most of them of different experts: a tile each, nothing to sort, and the rows are
   // quantised where they are used: two launches for five. A matrix that several slots share is
   // read once for each, so this ends where slots meet (us, this way / sorted, matrices of
@@ -314,6 +333,23 @@ hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) 
   const dim3 grid(static_cast<uint32_t>(a.M), static_cast<uint32_t>((a.H + 1023) / 1024));
   experts_combine_kernel<<<grid, 256, 0, s>>>(a, part);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_experts(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) {
+  const int64_t tokens = pass_tokens(a.M, a.H, a.k, a.I);
+  for (int64_t m = 0; m < a.M; m += tokens) {
+    Fp8ExpertsArgs p = a;
+    p.M = std::min(tokens, a.M - m);
+    p.x = static_cast<const char*>(a.x) + m * a.ldx * dtype_bytes(a.xdtype);
+    p.y = static_cast<char*>(a.y) + m * a.ldy * dtype_bytes(a.ydtype);
+    p.index = a.index + m * a.k;
+    p.weight = a.weight + m * a.k;
+    const hipError_t e = start_pass(p, ws, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace bl

@@ -444,6 +444,7 @@ template <class S>
 hipError_t start_gemm(const ProductArgs& p, int64_t tiles_m, hipStream_t s) {
   constexpr int64_t cols = S::GATED ? S::BN / 2 : S::BN;
   const int64_t tiles_n = (p.a.N + cols - 1) / cols;
+  if (!grid_fits(tiles_n * tiles_m, S::THREADS)) return hipErrorInvalidConfiguration;
   fp8_gemm_kernel<S><<<dim3(static_cast<uint32_t>(tiles_n * tiles_m)), S::THREADS, 0, s>>>(
       p, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
   return hipGetLastError();
@@ -454,6 +455,7 @@ template <class S>
 hipError_t start_split_gemm(const ProductArgs& p, hipStream_t s) {
   const int64_t tiles_n = (p.a.N + S::BN - 1) / S::BN, tiles_m = (p.a.M + S::BM - 1) / S::BM;
   const int64_t rest = tiles_n * tiles_m - p.whole;
+  if (!grid_fits(p.whole + rest * p.parts, S::THREADS)) return hipErrorInvalidConfiguration;
   fp8_gemm_kernel<S><<<dim3(static_cast<uint32_t>(p.whole + rest * p.parts)), S::THREADS, 0, s>>>(
       p, static_cast<int>(tiles_n), static_cast<int>(tiles_m));
   const hipError_t e = hipGetLastError();

@@ -17,8 +17,9 @@ constexpr uint32_t kFp8FloorBits = 0x0D800000u;     // 2^-100, the least block m
 inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 inline size_t dtype_bytes(int dtype) { return dtype == BL_F32 ? 4 : 2; }
 
-// A launch whose work-items along one dimension pass 2^32 runs modulo that, without an error. So
-// workgroups that may be many go over two dimensions (the last few of them may be too many).
+// A launch whose work-items along one dimension pass 2^32 runs modulo that, without an error.
+inline bool grid_fits(int64_t groups, int threads) { return groups * threads < (int64_t(1) << 32); }
+// So workgroups that may be many go over two dimensions (the last few of them may be too many).
 inline dim3 grid_of(int64_t groups) {
   const int64_t x = groups < (int64_t(1) << 20) ? groups : int64_t(1) << 20;
   return dim3(static_cast<uint32_t>(x), static_cast<uint32_t>((groups + x - 1) / x));
@@ -79,7 +80,6 @@ struct ExpertsWs {
   size_t total;
 };
 ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I);
-int64_t experts_max_tiles(int64_t P, int64_t E, int tile);
 
 hipError_t launch_fp8_quant_act(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx,
                                 int gated, const int32_t* rows_used, uint8_t* q, float* scale,

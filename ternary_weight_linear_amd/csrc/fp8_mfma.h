@@ -162,7 +162,6 @@ struct StreamArgs {
   const int32_t* index;    // direct tiles: tile t is slot t, its expert index[t]; null: as p.map says
   const float* weight;     // kStreamSlots
   int E, k;
-  int blocks_n;            // workgroups along the columns; the grid runs over these first
 };
 
 constexpr int kStreamWaves = 8;
@@ -263,7 +262,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, u = lane & 15;
   const int range = wave % S, group = wave / S;
-  const int by = blockIdx.x / s.blocks_n, bx = blockIdx.x - by * s.blocks_n;
+  const int by = blockIdx.y, bx = blockIdx.x;       // tile of rows; workgroups along the columns run first
   const int64_t n0 = (static_cast<int64_t>(bx) * G + group) * (16 * NC);
   int64_t first = static_cast<int64_t>(by) * (16 * MT);
   int rows = 0, expert = 0;
@@ -466,10 +465,10 @@ template <int MT, int NT, int S, int SRC, int MODE>
 hipError_t start_stream(const StreamArgs& st, int64_t tiles, int staged, hipStream_t s) {
   constexpr int cols = 16 * NT * (kStreamWaves / S) / (MODE == kStreamGated ? 2 : 1);
   const int lds = SRC == kSrcCodes ? 0 : staged_bytes(staged, static_cast<int>(fp8_blocks(st.p.a.K)));
-  StreamArgs a = st;
-  a.blocks_n = static_cast<int>((st.p.a.N + cols - 1) / cols);
-  const dim3 grid(static_cast<uint32_t>(a.blocks_n * tiles));
-  fp8_stream_kernel<MT, NT, S, SRC, MODE><<<grid, kStreamThreads, lds, s>>>(a);
+  const int64_t along = (st.p.a.N + cols - 1) / cols;
+  if (tiles > 65535 || !grid_fits(along, kStreamThreads)) return hipErrorInvalidConfiguration;
+  const dim3 grid(static_cast<uint32_t>(along), static_cast<uint32_t>(tiles));
+  fp8_stream_kernel<MT, NT, S, SRC, MODE><<<grid, kStreamThreads, lds, s>>>(st);
   return hipGetLastError();
 }
 template <int NT, int S, int MODE>

@@ -1,0 +1,20 @@
+"""Size queries of the 8-bit floating point operators at the limits of one pass (no GPU)."""
+import ternary_weight_linear_amd as tw
+
+ws = tw._lib.bl_fp8_experts_workspace_bytes
+
+
+def test_experts_run_in_passes_of_less_than_2_gib_of_codes():
+    """The workspace is one pass's: 2^31 / H tokens and more run in equal passes."""
+    one = ws((1 << 18), 4096, 2, 8, 4096)
+    assert ws((1 << 18) + 1, 4096, 2, 8, 4096) > one
+    assert ws(1 << 19, 4096, 2, 8, 4096) == one
+    assert ws((1 << 19) - 1, 4096, 2, 8, 4096) > one
+    assert ws(1 << 20, 4096, 1, 8, 4096) == ws(-(-(1 << 20) // 3), 4096, 1, 8, 4096)
+
+
+def test_passes_of_wide_experts_keep_the_grids_in_their_limits():
+    # matrices of 2 GiB and more are streamed, 2^19 slots at a time
+    assert ws(1 << 15, 1 << 15, 32, 1, 1 << 15) == ws(1 << 14, 1 << 15, 32, 1, 1 << 15)
+    # 2^35 hidden values at most
+    assert ws(1 << 18, 128, 4, 1, 1 << 17) == ws(1 << 16, 128, 4, 1, 1 << 17)

@@ -52,3 +52,26 @@ def test_route_of_many_rows(M, E, k):
     for got, want in ((w, w0), (i, i0)):
         whole = got[: (times - 1) * 1000].view(times - 1, 1000, k)
         assert bool((whole == want).all()) and torch.equal(got[(times - 1) * 1000:], want[: M - (times - 1) * 1000])
+
+
+def test_experts_of_activations_past_2_gib():
+    """2^19 tokens of 4096: any 4096 of them by themselves give the same bits."""
+    M, E, k, H, I = 1 << 19, 8, 2, 4096, 4096
+    needs(70)
+    say("experts large", M, E, k, H, I)
+    g = torch.Generator(device=DEV).manual_seed(2)
+
+    def matrices(count, rows, cols):
+        both = [tw.bl_fp8_quant_weight(torch.randn(rows, cols, generator=g, device=DEV) * cols ** -0.5) for _ in range(count)]
+        return torch.stack([c.view(torch.uint8) for c, _ in both]).view(torch.float8_e4m3fn), torch.stack([s for _, s in both])
+
+    wgu, sgu = (t.view(E, 2, *t.shape[1:]) for t in matrices(2 * E, I, H))
+    wd, sd = matrices(E, H, I)
+    x = torch.randn(M, H, generator=g, device=DEV, dtype=torch.bfloat16)
+    first = torch.randint(0, E, (M,), generator=g, device=DEV)
+    index = torch.stack([first, (first + torch.randint(1, E, (M,), generator=g, device=DEV)) % E], 1).to(torch.int32)
+    weight = torch.rand(M, k, generator=g, device=DEV)
+    y = tw.bl_fp8_experts(x, index, weight, wgu, sgu, wd, sd)
+    for at in (0, M // 2 - 2048, M - 4096):
+        s = slice(at, at + 4096)
+        assert torch.equal(y[s], tw.bl_fp8_experts(x[s], index[s].contiguous(), weight[s].contiguous(), wgu, sgu, wd, sd))
