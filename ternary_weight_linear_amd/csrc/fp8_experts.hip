@@ -222,10 +222,9 @@ ExpertsWs experts_ws(int64_t M_all, int64_t H, int64_t k, int64_t E, int64_t I) 
   w.pair_off = take(P * 4);
   w.tile_off = take(max_tiles(P, E, 16) * 16);
   w.count_off = take((P + sort_chunk(P) - 1) / sort_chunk(P) * E * 4);
-  w.h_off = take(P * I * 4);
   w.hq_off = take(P * I);
   w.hs_off = take(P * IB * 4);
-  w.part_off = take(P * H * 4);
+  w.sum_off = take(P * std::max(H, I) * 4);
   w.total = off;
   return w;
 }
@@ -240,10 +239,10 @@ hipError_t start_pass(const Fp8ExpertsArgs& a, char* ws, hipStream_t s) {
   auto* head = reinterpret_cast<int32_t*>(ws + L.head_off);
   auto* pair = reinterpret_cast<int32_t*>(ws + L.pair_off);
   auto* tiles = reinterpret_cast<int32_t*>(ws + L.tile_off);
-  auto* h = reinterpret_cast<float*>(ws + L.h_off);
+  auto* h = reinterpret_cast<float*>(ws + L.sum_off);
   auto* hq = reinterpret_cast<uint8_t*>(ws + L.hq_off);
   auto* hs = reinterpret_cast<float*>(ws + L.hs_off);
-  auto* part = reinterpret_cast<float*>(ws + L.part_off);
+  float* part = h;                                  // h is done with before the down product starts
   const bool exact_down = a.ydtype != BL_BF16;
   // Rows per tile, by the average rows of an expert. Measured, us for tiles of 16 / 64 / 128 rows, 64
   // experts of 4096 x 1024, top 8, bf16: 16 rows an expert 208 / 210 / 221, 32 319 / 262 / 242, 64

@@ -74,9 +74,9 @@ struct ExpertsWs {
   size_t pair_off;             // int32 [P] slot m * k + j of each sorted row
   size_t tile_off;             // int32 [tiles, 4]: expert, first row, rows
   size_t count_off;            // int32 [chunks, E]: slots per expert of each chunk of the sort
-  size_t h_off;                // fp32 [P, I] silu(gate) * up, where it is not quantised at once
   size_t hq_off, hs_off;       // quantised silu(gate) * up: codes [P, I], scales [IB, P]
-  size_t part_off;             // fp32 [P, H]: outputs before the weighted sum
+  size_t sum_off;              // fp32 [P, I] silu(gate) * up, where it is not quantised at once, and
+                               // after that [P, H]: outputs before the weighted sum
   size_t total;
 };
 ExpertsWs experts_ws(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I);

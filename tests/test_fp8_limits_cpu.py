@@ -18,3 +18,12 @@ def test_passes_of_wide_experts_keep_the_grids_in_their_limits():
     assert ws(1 << 15, 1 << 15, 32, 1, 1 << 15) == ws(1 << 14, 1 << 15, 32, 1, 1 << 15)
     # 2^35 hidden values at most
     assert ws(1 << 18, 128, 4, 1, 1 << 17) == ws(1 << 16, 128, 4, 1, 1 << 17)
+
+
+def test_experts_workspace_holds_one_fp32_buffer():
+    """Codes of x and of the hidden values, fp32 values before or after the down product (never
+    both at a time), and what goes by slot or block."""
+    M, H, k, E, I = 4096, 4096, 8, 64, 1024
+    slots = M * k
+    most = M * H + slots * I + 4 * slots * max(H, I) + M * H // 32 + slots * I // 32 + 64 * slots + (1 << 20)
+    assert M * H + slots * I + 4 * slots * max(H, I) <= ws(M, H, k, E, I) <= most
