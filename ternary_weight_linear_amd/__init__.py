@@ -567,6 +567,15 @@ def _blocks(n):
     return (n + 127) // 128
 
 
+def _out_dtype(out, dtype, default):
+    """The results' type: out's where there is one, which has to be the type asked for, if any."""
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out must be {dtype}, got {out.dtype}")
+    dtype = out.dtype if out is not None else dtype if dtype is not None else default
+    _dtype(dtype, "out")
+    return dtype
+
+
 def _out(out, shape, dtype, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
@@ -619,9 +628,11 @@ def _check_weight(w, scales, lead, name):
     _shape(scales, (*w.shape[:lead], _blocks(w.shape[-2]), _blocks(w.shape[-1])), f"the scales of {name}")
 
 
-def bl_fp8_linear(q, scales_x, w, scales_w, out_dtype=torch.float32, out=None):
+def bl_fp8_linear(q, scales_x, w, scales_w, out_dtype=None, out=None):
     """e4m3 q [M, K] and scales from bl_quant_act_fp8, w [N, K] and scales as from
-    bl_fp8_quant_weight -> y [M, N] in out_dtype. out: y, its rows may be strided."""
+    bl_fp8_quant_weight -> y [M, N] in out_dtype (out's type, else fp32, by default). out: y, its
+    rows may be strided."""
+    out_dtype = _out_dtype(out, out_dtype, torch.float32)
     _need(q, _F8, "q")
     _need(scales_x, torch.float32, "scales_x")
     _check_weight(w, scales_w, 0, "w")
@@ -638,9 +649,10 @@ def bl_fp8_linear(q, scales_x, w, scales_w, out_dtype=torch.float32, out=None):
     return y
 
 
-def bl_fp8_forward(x, w, scales_w, out_dtype=torch.float32, out=None):
-    """x [M, K] in fp16, bf16 or fp32 (rows may be strided) -> y [M, N] in out_dtype: quantise,
-    then the block-scaled product."""
+def bl_fp8_forward(x, w, scales_w, out_dtype=None, out=None):
+    """x [M, K] in fp16, bf16 or fp32 (rows may be strided) -> y [M, N] in out_dtype (out's type,
+    else fp32, by default): quantise, then the block-scaled product."""
+    out_dtype = _out_dtype(out, out_dtype, torch.float32)
     dt, ld = _dtype(x.dtype, "x"), _row_stride(x, "x")
     _check_weight(w, scales_w, 0, "w")
     d = _dev(x, w, scales_w, out)
@@ -678,8 +690,10 @@ def bl_route_experts(logits, k: int, bias=None, score: str = "softmax", groups: 
 def bl_fp8_experts(x, index, weight, wgu, scales_gu, wd, scales_d, out_dtype=None, out=None):
     """x [M, H], index int32 [M, k] and weight fp32 [M, k] as from bl_route_experts, gate and up
     codes wgu [E, 2, I, H], down codes wd [E, H, I], each with its scales per block of 128 x 128
-    -> y [M, H] in out_dtype (x's type by default): the weighted sum of each token's experts."""
+    -> y [M, H] in out_dtype (out's type, else x's, by default): the weighted sum of each token's
+    experts."""
     dt, ld = _dtype(x.dtype, "x"), _row_stride(x, "x")
+    out_dtype = _out_dtype(out, out_dtype, x.dtype)
     _need(index, torch.int32, "index")
     _need(weight, torch.float32, "weight")
     _check_weight(wgu, scales_gu, 2, "wgu")
@@ -693,7 +707,7 @@ def bl_fp8_experts(x, index, weight, wgu, scales_gu, wd, scales_d, out_dtype=Non
         raise ValueError(f"index must be [M, k] with M = {M}")
     k = index.shape[1]
     _shape(weight, (M, k), "weight")
-    y = _out(out, (M, H), out_dtype or x.dtype, d)
+    y = _out(out, (M, H), out_dtype, d)
     ws = _scratch(_lib.bl_fp8_experts_workspace_bytes(M, H, k, E, inner), d,
                   f"M={M} H={H} k={k} E={E} I={inner}")
     _check(_lib.bl_fp8_experts(_ptr(x), dt, M, H, ld, _ptr(index), _ptr(weight), k, _ptr(wgu),
