@@ -360,7 +360,9 @@ int bl_residual_linear(const uint16_t* x, const void* planes_o, const float* alp
  *  - x and y hold `dtype` values (enum bl_dtype) and their rows are ldx / ldy elements apart
  *    (at least the row's length). x, codes and ws are 16-byte aligned, and so is every row of
  *    x; scales are 4-byte aligned, y and its rows by the size of its type.
- *  - The workspace needs no fill and holds nothing between calls. */
+ *  - The workspace needs no fill and holds nothing between calls.
+ *  - Buffers are taken from their first byte to their last, with whatever lies between strided
+ *    rows: columns of one matrix do not serve as input and output of one call. */
 enum bl_dtype { BL_F16 = 0, BL_BF16 = 1, BL_F32 = 2 };
 enum bl_score { BL_SCORE_SOFTMAX = 0, BL_SCORE_SIGMOID = 1 };
 
@@ -384,7 +386,8 @@ int bl_quant_act_fp8(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx
  * rounded once to ydtype. Sums run in a fixed order for a given shape and ydtype. For fp32 and
  * fp16 results they are fp32 sums. For bf16 results and more than 16 rows a block's sum of
  * products may err by 7 2^-13 of the sum of their magnitudes (2e-5 of it on normal values, 3e-4
- * where one input is far larger than the others); the sum over blocks is fp32.
+ * where one input is far larger than the others; bf16 rounds by 2^-9), and the sum over blocks is
+ * fp32: ask for fp32 results where bf16 ones have to come from fp32 sums.
  * Uses ws (bl_fp8_workspace_bytes(M, N, K)). */
 size_t bl_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int bl_fp8_linear(const uint8_t* q, const float* scales_x, int64_t M, int64_t K, const uint8_t* w,

@@ -97,7 +97,7 @@ __device__ __forceinline__ void place_slots(const SortArgs& a, int chunk, const 
 }
 
 // One launch for what needs only the inputs: the first workgroups sort (or count) the slots,
-// the others quantise x. 48 tokens of 4096, top 8 of 64: 4.7 us; 4096 tokens: 13 (and 7.7 for
+// the others quantise x. 48 tokens of 4096, top 8 of 64: 4.7 us; 4096 tokens: 13 (and 7.4 for
 // the placing), most of it waits of the passes over a chunk's slots.
 template <int DT>
 __global__ __launch_bounds__(kSortThreads) void experts_prepare_kernel(SortArgs a, QuantArgs q) {
@@ -173,7 +173,9 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(Fp8ExpertsArgs a, 
 
 // The gate and up products take fp16 operands whatever the types: a sum that errs by more than
 // fp32 does moves codes of silu(gate) * up (with the e4m3 instruction 1 of 3000, which put 1.2e-3
-// of the result beside the 1.7e-3 of its rounding to bf16).
+// of the result beside the 1.7e-3 of its rounding to bf16). 4096 tokens, top 8 of 64 experts of 4096
+// x 1024: 630 us, 0.87 PFLOP/s; converting the codes bounds it, and a ninth of the tiles' rows
+// are empty.
 hipError_t start_up(const ProductArgs& p, int tile, int64_t nt, hipStream_t s) {
   if (tile == 64) return start_gemm<GemmShape<256, 64, 4, 2, 3, true, true>>(p, nt, s);
   return start_gemm<GemmShape<256, 128, 2, 4, 2, true, true>>(p, nt, s);

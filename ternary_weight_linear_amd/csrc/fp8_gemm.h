@@ -129,7 +129,7 @@ __device__ __forceinline__ void store_wide(const Fp8LinearArgs& a, const f32x4 (
 // from zero in the matrix cores and are added, scaled, to fp32 sums in registers. A workgroup has
 // BN x BM outputs; a block of both operands is copied straight into LDS while the one before it is
 // multiplied. What bounds it: large tiles the matrix cores and the card's power (256 x 256,
-// 4096 x 28672 x 8192: 797 to 840 us, 2.3 to 2.4 PFLOP/s), small ones L2, fp16 operands the conversion of
+// 4096 x 28672 x 8192: 820 to 840 us, 2.3 PFLOP/s), small ones L2, fp16 operands the conversion of
 // the codes (512 x 3200 x 8640, K in five parts: 34 us). Of a 256 x 256 tile about 10 us are its start and its
 // stores; one workgroup per CU that takes tile after tile and copies the next one's first block
 // while it stores measured 1 to 3 % slower at every shape.

@@ -248,8 +248,10 @@ __device__ __forceinline__ void quant_blocks(const QuantArgs& a, int64_t first) 
 // blocks (rot): weight rows are usually a power of two apart, and all workgroups at the same
 // input would meet in a few of the memory's channels. The fp16 instruction costs nothing here:
 // with the e4m3 one the times are the same.
-// Measured, us (weight bytes / time): 1 x 8192 x 8192 12.3 (5.4 TB/s), 16 x 8192 x 8192 14.2,
-// 16 x 28672 x 8192 43.8 (5.4 TB/s), 1 x 28672 x 8192 39.6 (5.9 TB/s).
+// Kernel trace, weights that no cache holds, us (weight bytes / time): 1 x 8192 x 8192 17.1 (3.9
+// TB/s; 14.4 where 200 MB of weights take turns), 16 x 8192 x 8192 18.3, 16 x 28672 x 8192 43.7 (5.4
+// TB/s), 1 x 28672 x 8192 40.4 (5.8 TB/s). Reading that much and nothing else in one launch: 67 MB
+// 12.1, 235 MB 36.7.
 template <int MT, int NT, int S, int SRC, int MODE>
 __global__ __launch_bounds__(kStreamThreads) void fp8_stream_kernel(StreamArgs s) {
   constexpr bool GATED = MODE == kStreamGated;

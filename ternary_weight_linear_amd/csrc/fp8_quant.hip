@@ -13,15 +13,15 @@
 namespace bl {
 namespace {
 
-// Memory bounds it, and small calls their launch: bf16 32768 x 8192 148 us (5.5 TB/s), gated
-// 2048 x 8640 20.6 (4.3 TB/s), fp16 16 x 8192 2.8.
+// Memory bounds it, and small calls their launch (kernel trace): bf16 32768 x 8192 145 us (5.6
+// TB/s), gated 2048 x 8640 22.7 (20.7 a call among others, 4.3 TB/s), fp16 16 x 8192 2.8.
 template <int DT, bool GATED>
 __global__ __launch_bounds__(256) void fp8_quant_act_kernel(QuantArgs q) {
   quant_blocks<DT, GATED>(q, group_id() * 16);
 }
 
 // One workgroup per 128 x 128 block: thread t holds rows t / 16 + 16 i, inputs 8 (t % 16) ...,
-// read once and kept in registers for the codes. Memory bounds it: 28672 x 8192 203 us (5.8 TB/s).
+// read once and kept in registers for the codes. Memory bounds it: 28672 x 8192 204 us (5.8 TB/s).
 __global__ __launch_bounds__(256) void fp8_quant_weight_kernel(const float* __restrict__ W,
                                                                int64_t N, int64_t K, int64_t KB,
                                                                uint8_t* __restrict__ codes,

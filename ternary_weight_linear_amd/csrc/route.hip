@@ -95,8 +95,9 @@ __device__ __forceinline__ float from_ordered(uint32_t b) {
 // experts e0 = (j >> shift) size + (j % 2^shift) C .. of its group, as far as that goes. Choice
 // values are kept as unsigned keys in their order, 0 for what cannot be chosen.
 // VALU work bounds it: the scores (an exponential and a division each) and, per round, two
-// passes over the lane's NE keys. 16384 rows of 256 experts, 8 groups, top 8: 13.5 us; 4096 rows
-// of 60, top 4: 4; one row 6.4, a chain of waits.
+// passes over the lane's NE keys. 16384 rows of 256 experts, 8 groups, top 8: 13.5 us a call among
+// others (kernel trace 14.9, at least 14.0); 4096 rows of 60, top 4: 4.1; one row 6.7, a chain of
+// waits.
 template <int DT, int NE>
 __global__ __launch_bounds__(256) void route_row16_kernel(RouteArgs a, int C, int shift, int vec) {
   __shared__ float scores[16][16 * NE + 16];        // expert e0 + i of lane j at 16 i + j
