@@ -413,8 +413,8 @@ int bl_fp8_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, 
  *    expert is left for holds index -1 and weight 0.
  *  - weight = p (without the bias), divided by its row's sum if renorm != 0 (0 where the sum
  *    is 0), times factor.
- * M <= 2^30, 1 <= E <= 2048, 1 <= k <= min(64, E / groups * kept), 1 <= kept <= groups. Outputs: weight
- * fp32 [M, k], index int32 [M, k]. */
+ * M <= 2^30, 1 <= E <= 2048, 1 <= k <= min(64, E / groups * kept), 1 <= kept <= groups.
+ * Outputs: weight fp32 [M, k], index int32 [M, k]. */
 int bl_route_experts(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
                      const float* bias, int score, int groups, int kept, int64_t k, int renorm,
                      float factor, float* weight, int32_t* index, void* stream);
