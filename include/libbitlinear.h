@@ -435,6 +435,72 @@ int bl_fp8_experts(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
                    int64_t I, void* y, int ydtype, int64_t ldy, void* ws, size_t ws_bytes,
                    void* stream);
 
+/* ---- low-rank adapters beside a shared projection, and the router's training ----------------- */
+
+/* What can learn beside frozen weights. The conventions of the 8-bit section hold, but for
+ * these: no size has to be a multiple of anything, and x and the adapters' matrices need the alignment
+ * of their type alone (rows of whole 16-byte pieces at 16-byte addresses are read several times
+ * faster).
+ *
+ * Row m has the adapter e = index[m] (int32 [M]) of the L adapters that a call is given, each of rank
+ * R: a [L, R, K] and b [L, R, N], contiguous, in x's dtype. Both have their rows along the long axis, so b
+ * holds the transpose of an nn.Linear weight [N, R]; an adapter of a lower rank has rows of zeros.
+ * scale fp32 [L], or NULL for 1. A row whose index is outside [0, L) has no adapter. ydtype (dydtype,
+ * dxdtype) is x's dtype or BL_F32. 1 <= M <= 2^20, 1 <= K, N <= 2^24, 1 <= R <= 256, 1 <= L <= 1024.
+ * Sums are fp32 sums of exact products (a 16-bit value times an fp32 one is rounded to fp32 once), in
+ * a fixed order for a given shape and index. Uses ws (bl_adapter_workspace_bytes; the last argument says
+ * which call it is for). */
+size_t bl_adapter_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t R,
+                                  int backward);
+
+/* h[m] = a[e] x[m] (fp32 [M, R], zeros without an adapter; the backward pass takes it) and
+ *   y[m] = base[m] + scale[e] b[e]^T h[m],
+ * rounded once to ydtype. base [M, N] of ydtype, rows ldbase apart: the shared projection's outputs.
+ * It may be y itself (with ldbase = ldy: in place), or NULL for zeros; a row without an adapter is base's. */
+int bl_adapter_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, const void* a,
+                       const void* b, int64_t L, int64_t R, int64_t N, const int32_t* index,
+                       const float* scale, const void* base, int64_t ldbase, void* y, int ydtype,
+                       int64_t ldy, float* h, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients from dy [M, N], with dh[m] = scale[e] b[e] dy[m]:
+ *   dx[m] = base[m] + a[e]^T dh[m]          (base as above: the gradient through the shared
+ *                                           projection; dx may be NULL, base then too),
+ *   da[e] = sum of dh[m] x[m]^T over the rows of e,   db[e] = scale[e] times that of h[m] dy[m]^T,
+ * da fp32 [L, R, K] and db fp32 [L, R, N]: written, zeros for an adapter without rows, or with
+ * add != 0 added onto what they hold. h as bl_adapter_forward gave it. */
+int bl_adapter_backward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, const void* a,
+                        const void* b, int64_t L, int64_t R, int64_t N, const int32_t* index,
+                        const float* scale, const float* h, const void* dy, int dydtype,
+                        int64_t lddy, const void* base, int64_t ldbase, void* dx, int dxdtype,
+                        int64_t lddx, float* da, float* db, int add, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Balance loss of a routing, and how many slots each expert got. Rows are packed sequences: sequence s
+ * holds rows offsets[s] .. offsets[s + 1] - 1 (int32 [S + 1], not falling, on the device; cut at
+ * 0 and M), rows before the first and behind the last count nowhere; NULL: one sequence of
+ * all rows, S = 1. index [M, k] as bl_route_experts gives it; a slot outside [0, E) is no slot, and
+ * only rows with a slot count. With p the scores of bl_route_experts (no bias), t = p / sum of the
+ * row's p, and for each sequence count[e] slots of expert e, C slots in all, T rows that count:
+ *   coef[e] = E count[e] / (C T),   loss = sum over e of coef[e] times the sum of t[m, e] over those rows
+ * (1 for an even load; an empty sequence gives zeros). Outputs: loss fp32 [S], count int32 [S, E],
+ * coef fp32 [S, E], which is the loss's derivative by t. Sums over rows are fp32 within about M / 512
+ * rows and fp64 over those, in a fixed order. E <= 2048, k <= 64, M k < 2^31, S <= 2^20. Uses ws. */
+size_t bl_route_balance_workspace_bytes(int64_t M, int64_t E, int64_t S);
+int bl_route_balance(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
+                     const int32_t* index, int64_t k, int score, const int32_t* offsets, int64_t S,
+                     float* loss, int32_t* count, float* coef, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* Gradient of the logits: of the weights of bl_route_experts, from dweight fp32 [M, k] (NULL: none;
+ * score, renorm and factor as there, the choice itself held fixed), plus that of the balance
+ * loss, from dloss fp32 [S] and bl_route_balance's coef (NULL: none; the counts held fixed). One of
+ * the two is needed. An expert whose logit is -inf or NaN gets 0. dlogits [M, E] of ddtype,
+ * rows ldd apart. The same expert twice in a row gets the sum. */
+int bl_route_backward(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
+                      const int32_t* index, int64_t k, int score, const float* dweight, int renorm,
+                      float factor, const float* coef, const float* dloss, const int32_t* offsets,
+                      int64_t S, void* dlogits, int ddtype, int64_t ldd, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

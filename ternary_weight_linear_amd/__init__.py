@@ -80,6 +80,16 @@ _SIGS = {
     "bl_fp8_experts_workspace_bytes": (_SZ, [_I64] * 5),
     "bl_fp8_experts": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _I64,
                                       _I64, _P, _INT, _I64, _P, _SZ, _P]),
+    "bl_adapter_workspace_bytes": (_SZ, [_I64] * 5 + [_INT]),
+    "bl_adapter_forward": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P, _I64,
+                                          _P, _INT, _I64, _P, _P, _SZ, _P]),
+    "bl_adapter_backward": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P,
+                                           _INT, _I64, _P, _I64, _P, _INT, _I64, _P, _P, _INT, _P, _SZ, _P]),
+    "bl_route_balance_workspace_bytes": (_SZ, [_I64] * 3),
+    "bl_route_balance": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _I64, _INT, _P, _I64, _P, _P, _P, _P,
+                                        _SZ, _P]),
+    "bl_route_backward": (ctypes.c_int, [_P, _INT, _I64, _I64, _I64, _P, _I64, _INT, _P, _INT, ctypes.c_float,
+                                         _P, _P, _P, _I64, _P, _INT, _I64, _P]),
 }
 
 
@@ -715,6 +725,166 @@ def bl_fp8_experts(x, index, weight, wgu, scales_gu, wd, scales_d, out_dtype=Non
                                _dtype(y.dtype, "out"), _row_stride(y, "out"), _ptr(ws), ws.numel(),
                                _stream(d)), "bl_fp8_experts")
     return y
+
+
+# ------------------------------------------------------------------------------------------
+# low-rank adapters, and the router's training
+# ------------------------------------------------------------------------------------------
+def _check_adapters(x, a, b, index, scale):
+    """(dtype, row stride of x, M, K, L, R, N) of an adapters' call."""
+    dt, ld = _dtype(x.dtype, "x"), _row_stride(x, "x")
+    _need(a, x.dtype, "a")
+    _need(b, x.dtype, "b")
+    _need(index, torch.int32, "index")
+    M, K = x.shape
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a and b must have three dimensions: [L, R, K] and [L, R, N]")
+    L, R, N = b.shape
+    _shape(a, (L, R, K), "a")
+    _shape(index, (M,), "index")
+    if scale is not None:
+        _need(scale, torch.float32, "scale")
+        _shape(scale, (L,), "scale")
+    return dt, ld, M, K, L, R, N
+
+
+def _beside(t, dtype, name):
+    """The code of t's type, which is dtype or fp32."""
+    if t.dtype != dtype and t.dtype != torch.float32:
+        raise ValueError(f"{name} must be {dtype} or torch.float32, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _onto(base, out, out_dtype, shape, dtype):
+    """Type of what a product is added onto and written to, and base's row stride."""
+    out_dtype = _out_dtype(out, out_dtype, torch.float32 if base is None else base.dtype)
+    ldbase = 0
+    if base is not None:
+        if base.dtype != out_dtype:
+            raise ValueError(f"base must be {out_dtype}, got {base.dtype}")
+        _shape(base, shape, "base")
+        ldbase = _row_stride(base, "base")
+    if out_dtype != dtype and out_dtype != torch.float32:
+        raise ValueError(f"out must be {dtype} or torch.float32, got {out_dtype}")
+    return out_dtype, ldbase
+
+
+def bl_adapter_forward(x, a, b, index, scale=None, base=None, out_dtype=None, out=None):
+    """x [M, K] in fp16, bf16 or fp32 (rows may be strided), adapters a [L, R, K] and b [L, R, N]
+    of x's type (b transposed: both have rows along the long axis), index int32 [M] (outside [0, L):
+    no adapter), scale fp32 [L] -> (y [M, N], h fp32 [M, R]) with h[m] = a[e] x[m] and
+    y[m] = base[m] + scale[e] b[e]^T h[m], e = index[m]. base [M, N]: the shared projection's outputs
+    (None: zeros), which out may be itself. y's type is out_dtype (out's, else base's, else fp32, by
+    default): x's or fp32."""
+    dt, ld, M, K, L, R, N = _check_adapters(x, a, b, index, scale)
+    out_dtype, ldbase = _onto(base, out, out_dtype, (M, N), x.dtype)
+    d = _dev(x, a, b, index, scale, base, out)
+    y = _out(out, (M, N), out_dtype, d)
+    h = torch.empty((M, R), dtype=torch.float32, device=d)
+    ws = _scratch(_lib.bl_adapter_workspace_bytes(M, K, N, L, R, 0), d, f"M={M} K={K} N={N} L={L} R={R}")
+    _check(_lib.bl_adapter_forward(_ptr(x), dt, M, K, ld, _ptr(a), _ptr(b), L, R, N, _ptr(index), _ptr(scale),
+                                   _ptr(base), ldbase, _ptr(y), _DTYPES[out_dtype], _row_stride(y, "out"), _ptr(h),
+                                   _ptr(ws), ws.numel(), _stream(d)), "bl_adapter_forward")
+    return y, h
+
+
+def bl_adapter_backward(x, a, b, index, h, dy, scale=None, base=None, out_dtype=None, out=None, da=None,
+                        db=None, need_dx=True):
+    """x, a, b, index, scale and h as bl_adapter_forward had and gave them, dy [M, N] (x's type or
+    fp32) -> (dx [M, K], da fp32 [L, R, K], db fp32 [L, R, N]). base [M, K]: the gradient of x through the
+    shared projection, which dx is added onto and out may be itself; dx's type as y's there.
+    da and db given: they are added onto. need_dx=False: dx is None."""
+    dt, ld, M, K, L, R, N = _check_adapters(x, a, b, index, scale)
+    _need(h, torch.float32, "h")
+    _shape(h, (M, R), "h")
+    _shape(dy, (M, N), "dy")
+    dydt, lddy = _beside(dy, x.dtype, "dy"), _row_stride(dy, "dy")
+    if (da is None) != (db is None):
+        raise ValueError("da and db must be given together")
+    for t, n, name in ((da, K, "da"), (db, N, "db")):
+        if t is not None:
+            _need(t, torch.float32, name)
+            _shape(t, (L, R, n), name)
+    if not need_dx and not (base is None and out is None and out_dtype is None):
+        raise ValueError("base, out and out_dtype are those of dx, which is not asked for")
+    out_dtype, ldbase = _onto(base, out, out_dtype, (M, K), x.dtype)
+    d = _dev(x, a, b, index, h, dy, scale, base, out, da, db)
+    dx, lddx = None, 0
+    if need_dx:
+        dx = _out(out, (M, K), out_dtype, d)
+        lddx = _row_stride(dx, "out")
+    add = da is not None
+    if not add:
+        da = torch.empty((L, R, K), dtype=torch.float32, device=d)
+        db = torch.empty((L, R, N), dtype=torch.float32, device=d)
+    ws = _scratch(_lib.bl_adapter_workspace_bytes(M, K, N, L, R, 1), d, f"M={M} K={K} N={N} L={L} R={R}")
+    _check(_lib.bl_adapter_backward(_ptr(x), dt, M, K, ld, _ptr(a), _ptr(b), L, R, N, _ptr(index), _ptr(scale),
+                                    _ptr(h), _ptr(dy), dydt, lddy, _ptr(base), ldbase, _ptr(dx),
+                                    _DTYPES[out_dtype], lddx, _ptr(da), _ptr(db), int(add), _ptr(ws), ws.numel(), _stream(d)),
+           "bl_adapter_backward")
+    return dx, da, db
+
+
+def _check_route(logits, index, score, offsets):
+    """(dtype, row stride, M, E, k, S) of a routing whose choice has been made."""
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    dt, ld = _dtype(logits.dtype, "logits"), _row_stride(logits, "logits")
+    _need(index, torch.int32, "index")
+    M, E = logits.shape
+    if index.dim() != 2 or index.shape[0] != M:
+        raise ValueError(f"index must be [M, k] with M = {M}")
+    S = 1
+    if offsets is not None:
+        _need(offsets, torch.int32, "offsets")
+        if offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError("offsets must be [S + 1] with S at least 1")
+        S = offsets.shape[0] - 1
+    return dt, ld, M, E, index.shape[1], S
+
+
+def bl_route_balance(logits, index, score: str = "softmax", offsets=None):
+    """logits [M, E] (rows may be strided) and index int32 [M, k] as bl_route_experts had and gave
+    them, offsets int32 [S + 1] of packed sequences (None: all rows are one) -> (loss fp32 [S], count
+    int32 [S, E] slots of each expert, coef fp32 [S, E], which bl_route_backward takes)."""
+    dt, ld, M, E, k, S = _check_route(logits, index, score, offsets)
+    d = _dev(logits, index, offsets)
+    loss = torch.empty((S,), dtype=torch.float32, device=d)
+    count = torch.empty((S, E), dtype=torch.int32, device=d)
+    coef = torch.empty((S, E), dtype=torch.float32, device=d)
+    ws = _scratch(_lib.bl_route_balance_workspace_bytes(M, E, S), d, f"M={M} E={E} S={S}")
+    _check(_lib.bl_route_balance(_ptr(logits), dt, M, E, ld, _ptr(index), k, _SCORES[score], _ptr(offsets), S,
+                                 _ptr(loss), _ptr(count), _ptr(coef), _ptr(ws), ws.numel(), _stream(d)),
+           "bl_route_balance")
+    return loss, count, coef
+
+
+def bl_route_backward(logits, index, dweight=None, score: str = "softmax", renorm: bool = True, factor: float = 1.0,
+                      coef=None, dloss=None, offsets=None, out_dtype=None, out=None):
+    """Gradient of the logits [M, E] from dweight fp32 [M, k], the gradient of bl_route_experts's
+    weights (same score, renorm and factor), and from dloss fp32 [S] with coef [S, E], those of
+    bl_route_balance's loss (same offsets) -> dlogits [M, E] in out_dtype (out's type, else logits', by
+    default). Either may be left out."""
+    dt, ld, M, E, k, S = _check_route(logits, index, score, offsets)
+    out_dtype = _out_dtype(out, out_dtype, logits.dtype)
+    if dweight is None and coef is None:
+        raise ValueError("dweight or coef with dloss must be given")
+    if (coef is None) != (dloss is None):
+        raise ValueError("coef and dloss must be given together")
+    if dweight is not None:
+        _need(dweight, torch.float32, "dweight")
+        _shape(dweight, (M, k), "dweight")
+    if coef is not None:
+        _need(coef, torch.float32, "coef")
+        _shape(coef, (S, E), "coef")
+        _need(dloss, torch.float32, "dloss")
+        _shape(dloss, (S,), "dloss")
+    d = _dev(logits, index, dweight, coef, dloss, offsets, out)
+    out = _out(out, (M, E), out_dtype, d)
+    _check(_lib.bl_route_backward(_ptr(logits), dt, M, E, ld, _ptr(index), k, _SCORES[score], _ptr(dweight),
+                                  int(renorm), factor, _ptr(coef), _ptr(dloss), _ptr(offsets), S, _ptr(out),
+                                  _DTYPES[out_dtype], _row_stride(out, "out"), _stream(d)), "bl_route_backward")
+    return out
 
 
 __all__ = [n for n in list(globals()) if n.startswith("bl_")] + [

@@ -40,12 +40,13 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 # scaled by the VALU, which reads no AGPRs.
 EXTRA = {"mf_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "fp8_linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "fp8_experts.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "fp8_experts.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "adapter.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 SOURCES = ["api.hip", "pack.hip", "quant.hip", "gemv.hip", "gemm.hip", "onebit.hip", "svid.hip",
            "stack.hip",
            "residual.hip", "tern_mfma.hip", "mf_decode.hip", "fp8_quant.hip", "fp8_linear.hip",
-           "fp8_experts.hip", "route.hip"]
+           "fp8_experts.hip", "route.hip", "adapter.hip", "route_grad.hip"]
 
 
 def _run(cmd):

@@ -5,6 +5,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "adapter_internal.h"
 #include "bl_internal.h"
 #include "fp8_internal.h"
 
@@ -98,6 +99,29 @@ Fp8Ws fp8_ws(int64_t M, int64_t N, int64_t K) {
 bool experts_dims_ok(int64_t M, int64_t H, int64_t k, int64_t E, int64_t I) {
   return fp8_dims_ok(M, I, H) && I % 16 == 0 && I <= kMaxFp8Dim / 2 && k >= 1 && k <= 64 &&
          E >= 1 && E <= 4096 && M * k <= kMaxFp8Rows;
+}
+
+// ---- adapters, and the router's training ----
+constexpr int64_t kMaxAdapters = 1024, kMaxRank = 256;
+constexpr int64_t kMaxSequences = int64_t(1) << 20;
+
+bool adapter_dims_ok(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N) {
+  return M >= 1 && M <= kMaxFp8Rows && L >= 1 && L <= kMaxAdapters && R >= 1 && R <= kMaxRank && K >= 1 &&
+         K <= kMaxFp8Dim && N >= 1 && N <= kMaxFp8Dim;
+}
+// Values beside a call's own type: that type, or fp32.
+bool beside_ok(int dtype, int other) { return other == dtype || other == BL_F32; }
+// base is y itself, row for row, or apart from it: then it is an input like any other.
+bool same_rows(const void* base, int64_t ldbase, const void* y, int64_t ldy, int64_t M) {
+  return base == y && (ldbase == ldy || M == 1);
+}
+int check_route_rows(const RouteRows& r, int score) {
+  if (r.M < 1 || r.M > kMaxDim || r.E < 1 || r.E > 2048 || r.S < 1 || r.S > kMaxSequences) return BL_ERR_SHAPE;
+  if ((score != BL_SCORE_SOFTMAX && score != BL_SCORE_SIGMOID) || r.k < 1 || r.k > 64) return BL_ERR_ARG;
+  if (r.M * r.k > INT32_MAX) return BL_ERR_SHAPE;
+  if (!r.offsets && r.S != 1) return BL_ERR_ARG;
+  if (int st = check_rows_out(r.logits, r.dtype, r.E, r.ld)) return st;
+  return aligned_to(r.index, 4) && aligned_to(r.offsets, 4) ? BL_OK : BL_ERR_ALIGN;
 }
 
 }  // namespace
@@ -821,6 +845,132 @@ int bl_fp8_experts(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
                                                         wd, scales_d, E, I, y, ydtype, ldy},
                                          static_cast<char*>(ws), static_cast<hipStream_t>(stream)),
                       "bl_fp8_experts");
+}
+
+size_t bl_adapter_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t R, int backward) {
+  return adapter_dims_ok(M, L, R, K, N) ? adapter_ws(M, L, R, K, N, backward != 0).total : 0;
+}
+
+int bl_adapter_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, const void* a,
+                       const void* b, int64_t L, int64_t R, int64_t N, const int32_t* index,
+                       const float* scale, const void* base, int64_t ldbase, void* y, int ydtype,
+                       int64_t ldy, float* h, void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !a || !b || !index || !y || !h) return BL_ERR_NULL;
+  if (!adapter_dims_ok(M, L, R, K, N)) return BL_ERR_SHAPE;
+  if (int st = check_rows_out(x, dtype, K, ldx)) return st;
+  if (!beside_ok(dtype, ydtype)) return BL_ERR_ARG;
+  if (int st = check_rows_out(y, ydtype, N, ldy)) return st;
+  if (base)
+    if (int st = check_rows_out(base, ydtype, N, ldbase)) return st;
+  const size_t need = adapter_ws(M, L, R, K, N, false).total, size = dtype_bytes(dtype);
+  if (!ws || ws_bytes < need) return BL_ERR_WORKSPACE;
+  if (!aligned_to(a, size) || !aligned_to(b, size) || !aligned_to(index, 4) || !aligned_to(scale, 4) ||
+      !aligned_to(h, 4) || !aligned16(ws))
+    return BL_ERR_ALIGN;
+  const bool own = base && !same_rows(base, ldbase, y, ldy, M);
+  const Span outs[] = {{y, rows_bytes(M, N, ldy, ydtype)}, {h, static_cast<size_t>(M) * R * 4}, {ws, need}};
+  const Span ins[] = {{x, rows_bytes(M, K, ldx, dtype)},
+                      {a, static_cast<size_t>(L) * R * K * size},
+                      {b, static_cast<size_t>(L) * R * N * size},
+                      {index, static_cast<size_t>(M) * 4},
+                      {scale, scale ? static_cast<size_t>(L) * 4 : 0},
+                      {base, own ? rows_bytes(M, N, ldbase, ydtype) : 0}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  return check_launch(launch_adapter_forward(AdapterForwardArgs{{index, M, L, R}, x, K, ldx, a, b, dtype, N, scale,
+                                                                base, ldbase, y, ydtype, ldy, h},
+                                             static_cast<char*>(ws), static_cast<hipStream_t>(stream)),
+                      "bl_adapter_forward");
+}
+
+int bl_adapter_backward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, const void* a,
+                        const void* b, int64_t L, int64_t R, int64_t N, const int32_t* index,
+                        const float* scale, const float* h, const void* dy, int dydtype,
+                        int64_t lddy, const void* base, int64_t ldbase, void* dx, int dxdtype,
+                        int64_t lddx, float* da, float* db, int add, void* ws, size_t ws_bytes,
+                        void* stream) {
+  if (!x || !a || !b || !index || !h || !dy || !da || !db) return BL_ERR_NULL;
+  if (!adapter_dims_ok(M, L, R, K, N)) return BL_ERR_SHAPE;
+  if (int st = check_rows_out(x, dtype, K, ldx)) return st;
+  if (!beside_ok(dtype, dydtype)) return BL_ERR_ARG;
+  if (int st = check_rows_out(dy, dydtype, N, lddy)) return st;
+  if (base && !dx) return BL_ERR_ARG;
+  if (dx) {
+    if (!beside_ok(dtype, dxdtype)) return BL_ERR_ARG;
+    if (int st = check_rows_out(dx, dxdtype, K, lddx)) return st;
+    if (base)
+      if (int st = check_rows_out(base, dxdtype, K, ldbase)) return st;
+  }
+  const size_t need = adapter_ws(M, L, R, K, N, true).total, size = dtype_bytes(dtype);
+  if (!ws || ws_bytes < need) return BL_ERR_WORKSPACE;
+  if (!aligned_to(a, size) || !aligned_to(b, size) || !aligned_to(index, 4) || !aligned_to(scale, 4) ||
+      !aligned_to(h, 4) || !aligned_to(da, 4) || !aligned_to(db, 4) || !aligned16(ws))
+    return BL_ERR_ALIGN;
+  const bool own = base && !same_rows(base, ldbase, dx, lddx, M);
+  const size_t na = static_cast<size_t>(L) * R * K, nb = static_cast<size_t>(L) * R * N;
+  const Span outs[] = {{dx, dx ? rows_bytes(M, K, lddx, dxdtype) : 0}, {da, na * 4}, {db, nb * 4}, {ws, need}};
+  const Span ins[] = {{x, rows_bytes(M, K, ldx, dtype)},
+                      {a, na * size},
+                      {b, nb * size},
+                      {index, static_cast<size_t>(M) * 4},
+                      {scale, scale ? static_cast<size_t>(L) * 4 : 0},
+                      {h, static_cast<size_t>(M) * R * 4},
+                      {dy, rows_bytes(M, N, lddy, dydtype)},
+                      {base, own ? rows_bytes(M, K, ldbase, dxdtype) : 0}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  return check_launch(launch_adapter_backward(AdapterBackwardArgs{{index, M, L, R}, x, K, ldx, a, b, dtype, N, scale, h, dy,
+                                                                  dydtype, lddy, base, ldbase, dx, dxdtype, lddx, da, db, add != 0},
+                                              static_cast<char*>(ws), static_cast<hipStream_t>(stream)),
+                      "bl_adapter_backward");
+}
+
+size_t bl_route_balance_workspace_bytes(int64_t M, int64_t E, int64_t S) {
+  return M >= 1 && M <= kMaxDim && E >= 1 && E <= 2048 && S >= 1 && S <= kMaxSequences ? route_balance_ws_bytes(M, E, S) : 0;
+}
+
+int bl_route_balance(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
+                     const int32_t* index, int64_t k, int score, const int32_t* offsets, int64_t S,
+                     float* loss, int32_t* count, float* coef, void* ws, size_t ws_bytes,
+                     void* stream) {
+  if (!logits || !index || !loss || !count || !coef) return BL_ERR_NULL;
+  if (k < 1 || k > 64) return BL_ERR_ARG;
+  const RouteRows r{logits, dtype, M, E, ld, index, static_cast<int>(k), score == BL_SCORE_SIGMOID, offsets, S};
+  if (int st = check_route_rows(r, score)) return st;
+  const size_t need = route_balance_ws_bytes(M, E, S);
+  if (!ws || ws_bytes < need) return BL_ERR_WORKSPACE;
+  if (!aligned_to(loss, 4) || !aligned_to(count, 4) || !aligned_to(coef, 4) || !aligned16(ws)) return BL_ERR_ALIGN;
+  const size_t each = static_cast<size_t>(S) * E * 4;
+  const Span outs[] = {{loss, static_cast<size_t>(S) * 4}, {count, each}, {coef, each}, {ws, need}};
+  const Span ins[] = {{logits, rows_bytes(M, E, ld, dtype)},
+                      {index, static_cast<size_t>(M) * k * 4},
+                      {offsets, offsets ? static_cast<size_t>(S + 1) * 4 : 0}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  return check_launch(launch_route_balance(RouteBalanceArgs{r, loss, count, coef}, static_cast<char*>(ws),
+                                           static_cast<hipStream_t>(stream)),
+                      "bl_route_balance");
+}
+
+int bl_route_backward(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
+                      const int32_t* index, int64_t k, int score, const float* dweight, int renorm,
+                      float factor, const float* coef, const float* dloss, const int32_t* offsets,
+                      int64_t S, void* dlogits, int ddtype, int64_t ldd, void* stream) {
+  if (!logits || !index || !dlogits || (!dweight && !coef) || (coef && !dloss)) return BL_ERR_NULL;
+  if (k < 1 || k > 64) return BL_ERR_ARG;
+  const RouteRows r{logits, dtype, M, E, ld, index, static_cast<int>(k), score == BL_SCORE_SIGMOID, offsets, S};
+  if (int st = check_route_rows(r, score)) return st;
+  if (int st = check_rows_out(dlogits, ddtype, E, ldd)) return st;
+  if (!aligned_to(dweight, 4) || !aligned_to(coef, 4) || !aligned_to(dloss, 4)) return BL_ERR_ALIGN;
+  const size_t slots = static_cast<size_t>(M) * k * 4;
+  const Span outs[] = {{dlogits, rows_bytes(M, E, ldd, ddtype)}};
+  const Span ins[] = {{logits, rows_bytes(M, E, ld, dtype)},
+                      {index, slots},
+                      {dweight, dweight ? slots : 0},
+                      {coef, coef ? static_cast<size_t>(S) * E * 4 : 0},
+                      {dloss, coef ? static_cast<size_t>(S) * 4 : 0},
+                      {offsets, offsets ? static_cast<size_t>(S + 1) * 4 : 0}};
+  if (any_overlap(outs, ins)) return BL_ERR_ALIAS;
+  return check_launch(launch_route_backward(RouteBackwardArgs{r, dweight, renorm, factor, coef, dloss, dlogits, ddtype, ldd},
+                                            static_cast<hipStream_t>(stream)),
+                      "bl_route_backward");
 }
 
 }  // extern "C"
