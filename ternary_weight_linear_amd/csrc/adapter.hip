@@ -9,8 +9,10 @@
 // (expand) and a sum over rows (outer). Rows are sorted by adapter, in tiles of 32 rows of one
 // adapter each.
 #include <algorithm>
+#include <type_traits>
 
 #include "adapter_internal.h"
+#include "bl_internal.h"
 
 namespace bl {
 namespace {
@@ -29,6 +31,11 @@ inline int64_t max_tiles(int64_t M, int64_t L) { return M / kTile + std::min(M, 
 // ------------------------------------------------------------------------------------------
 // eight consecutive values of a row
 // ------------------------------------------------------------------------------------------
+// The hardware reads and writes 16 bytes at any address that its elements' alignment allows, so rows of
+// any length and stride go eight values at a time; a row's last piece may be shorter.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
 template <int DT>
 struct Eight {
   u32x4 w;
@@ -38,22 +45,37 @@ struct Eight<BL_F32> {
   f32x4 w[2];
 };
 
-// Values at .. at + 7 of a row of n; those from n on are 0. VEC: whole pieces, 16-byte aligned.
-template <int DT, bool VEC>
-__device__ __forceinline__ Eight<DT> load8(const typename Elem<DT>::type* row, int64_t at, int64_t n) {
-  Eight<DT> v{};
-  if constexpr (VEC) {
-    if (at < n) v = *reinterpret_cast<const Eight<DT>*>(row + at);
-  } else if constexpr (DT == BL_F32) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (at + j < n) v.w[j / 4][j % 4] = row[at + j];
+template <int DT>
+__device__ __forceinline__ Eight<DT> load_whole(const typename Elem<DT>::type* p) {
+  Eight<DT> v;
+  if constexpr (DT == BL_F32) {
+    v.w[0] = *reinterpret_cast<const f32x4_any*>(p);
+    v.w[1] = *reinterpret_cast<const f32x4_any*>(p + 4);
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (at + j < n) v.w[j / 2] |= static_cast<uint32_t>(row[at + j]) << (16 * (j & 1));
+    v.w = *reinterpret_cast<const u32x4_any*>(p);
   }
   return v;
+}
+// Values at .. at + 7 of a row of n; those from n on are 0. WHOLE: there are none.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ Eight<DT> load8(const typename Elem<DT>::type* row, int64_t at, int64_t n) {
+  if constexpr (WHOLE) return load_whole<DT>(row + at);
+  Eight<DT> v{};
+  if (at + 8 <= n) {
+    v = load_whole<DT>(row + at);
+  } else if (at < n) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (at + j < n) {
+        if constexpr (DT == BL_F32) v.w[j / 4][j % 4] = row[at + j];
+        else v.w[j / 2] |= static_cast<uint32_t>(row[at + j]) << (16 * (j & 1));
+      }
+  }
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ Eight<DT> zero_unless(bool keep, Eight<DT> v) {
+  return keep ? v : Eight<DT>{};
 }
 
 template <int DT>
@@ -62,124 +84,214 @@ __device__ __forceinline__ float value(const Eight<DT>& v, int j) {
   else return to_float<DT>(static_cast<uint16_t>(v.w[j / 2] >> (16 * (j & 1))));
 }
 
-template <int DT, bool VEC>
+template <int DT>
+__device__ __forceinline__ uint16_t bits16(float v) {
+  return DT == BL_BF16 ? bf16_bits(v) : half_bits(v);
+}
+
+template <int DT, bool WHOLE>
 __device__ __forceinline__ void store8(typename Elem<DT>::type* row, int64_t at, int64_t n, const float (&v)[8]) {
   if constexpr (DT == BL_F32) {
-    if constexpr (VEC) {
-      if (at >= n) return;
-      *reinterpret_cast<f32x4*>(row + at) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(row + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (at + j < n) row[at + j] = v[j];
+    if (WHOLE || at + 8 <= n) {
+      *reinterpret_cast<f32x4_any*>(row + at) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_any*>(row + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      return;
     }
+  } else if (WHOLE || at + 8 <= n) {
+    u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = bits16<DT>(v[2 * j]) | static_cast<uint32_t>(bits16<DT>(v[2 * j + 1])) << 16;
+    *reinterpret_cast<u32x4_any*>(row + at) = w;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (at + j < n) {
+      if constexpr (DT == BL_F32) row[at + j] = v[j];
+      else row[at + j] = bits16<DT>(v[j]);
+    }
+}
+
+// Column j of eight rows of eight 16-bit values, as one matrix operand: one byte permutation for
+// each pair of rows.
+__device__ __forceinline__ u32x4 column(const u32x4 (&row)[8], int j) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = __builtin_amdgcn_perm(row[2 * i + 1][j / 2], row[2 * i][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+  return v;
+}
+
+// 16 x 16 products over 32 values of 16 bits each.
+template <int DT>
+__device__ __forceinline__ f32x4 dot32(u32x4 a, u32x4 b, f32x4 acc) {
+  if constexpr (DT == BL_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, a), __builtin_bit_cast(half8v, b), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8v, a), __builtin_bit_cast(bf8v, b), acc, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------------------------------
+// fp32 coefficients as 16-bit parts
+// ------------------------------------------------------------------------------------------
+// h and dh are fp32, and what they are multiplied by has 16 bits. The 16-bit matrix instructions
+// are 16 times as fast as the fp32 one, so a coefficient is split into parts that they take: three bf16
+// parts, cut at 8 bits each, hold all 24 bits; two fp16 parts hold 22 bits or more, after
+// a power of two has brought the largest of the row (or column) to 2^14 .. 2^15.
+template <int DT>
+struct Parts;
+template <>
+struct Parts<BL_BF16> { static constexpr int n = 3; };
+template <>
+struct Parts<BL_F16> { static constexpr int n = 2; };
+template <>
+struct Parts<BL_F32> { static constexpr int n = 1; };
+
+// |v| of what is finite, else 0.
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+  const uint32_t b = abs_bits(v);
+  return b < 0x7F800000u ? b : 0;
+}
+// Exponent e that brings a maximum (its bits) to 2^14 .. 2^15 as v 2^e; 0 for a maximum of 0.
+__device__ __forceinline__ int scale_exponent(uint32_t max_bits) {
+  return max_bits ? min(14 - (static_cast<int>(max_bits >> 23) - 127), 126) : 0;
+}
+// Parts of v (fp16: of v 2^e). Infinities and NaN are in the first part alone.
+template <int DT>
+__device__ __forceinline__ void split(float v, int e, uint16_t (&part)[3]) {
+  if constexpr (DT == BL_BF16) {
+    const bool odd = abs_bits(v) >= 0x7F800000u;
+    const uint32_t hi = odd ? static_cast<uint32_t>(bf16_bits(v)) << 16 : __float_as_uint(v) & 0xFFFF0000u;
+    const float r = odd ? 0.0f : v - __uint_as_float(hi);
+    const uint32_t mid = __float_as_uint(r) & 0xFFFF0000u;
+    const float lo = r - __uint_as_float(mid);
+    part[0] = static_cast<uint16_t>(hi >> 16);
+    part[1] = static_cast<uint16_t>(mid >> 16);
+    part[2] = static_cast<uint16_t>(__float_as_uint(lo) >> 16);
   } else {
-    uint16_t b[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) b[j] = DT == BL_BF16 ? bf16_bits(v[j]) : half_bits(v[j]);
-    if constexpr (VEC) {
-      if (at >= n) return;
-      u32x4 w;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = b[2 * j] | static_cast<uint32_t>(b[2 * j + 1]) << 16;
-      *reinterpret_cast<u32x4*>(row + at) = w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (at + j < n) row[at + j] = b[j];
-    }
+    const bool odd = abs_bits(v) >= 0x7F800000u;
+    const float s = ldexpf(v, e);
+    part[0] = half_bits(s);
+    part[1] = odd ? 0 : half_bits(s - static_cast<float>(__builtin_bit_cast(_Float16, part[0])));
+    part[2] = 0;
   }
 }
+
+// Coefficients of the sorted rows, in what the passes after it need of: fp32 [rows, RP]; parts row by
+// row [n, rows, RK] (RK: R up to 32) with exponents [rows]; parts by columns [n, tiles, RP, 32] with exponents
+// [tiles, RP]. What a row or a rank has not is 0.
+struct Coefs {
+  float* f;
+  uint16_t* by_row;
+  int32_t* row_e;
+  uint16_t* by_rank;
+  int32_t* rank_e;
+};
 
 // ------------------------------------------------------------------------------------------
 // rows sorted by adapter
 // ------------------------------------------------------------------------------------------
-// The sort is stable, so that sums over an adapter's rows have one order. A chunk of 8192 rows per
-// workgroup, 512 per wave; more than one chunk: a first launch counts, the second places. Bucket L
-// holds the rows without an adapter. Each bucket starts a tile of its own.
+// The sort is stable, so that sums over an adapter's rows have one order. A chunk of up to 8192 rows
+// per workgroup; more than one chunk: a first launch counts, the second places. Bucket L holds the
+// rows without an adapter. Each bucket starts a tile of its own. The counters of the call's later
+// launches are cleared on the way.
 constexpr int kSortWaves = 16, kSortSteps = 8;
 constexpr int kSortChunk = kSortWaves * 64 * kSortSteps;
 
 struct SortArgs {
   const int32_t* index;
   int64_t M;
-  int L, chunks;
+  int L, chunks, steps;   // 64 rows per step and wave
   int32_t* order;
   int32_t* tile;
   int32_t* start;
-  int32_t* counts;      // [chunks, L + 1]
+  int32_t* counts;        // [chunks, L + 1]
+  uint32_t* arrived;      // [ncnt]
+  int64_t ncnt;
 };
 
-inline size_t sort_lds(int64_t L) { return static_cast<size_t>(L + 1) * (kSortWaves * 2 + 8); }
+inline size_t sort_lds(int64_t L) { return static_cast<size_t>(L + 1) * (kSortWaves * 2 + 12) + 4; }
+
+// Lanes whose bucket is this lane's, from a ballot of each of its bits.
+__device__ __forceinline__ uint64_t same_bucket(int e, int bits) {
+  uint64_t same = __ballot(e >= 0);
+  for (int i = 0; i < bits; ++i) {
+    const uint64_t set = __ballot((e >> i) & 1);
+    same &= (e >> i) & 1 ? set : ~set;
+  }
+  return same;
+}
 
 // MODE 0: the only chunk. 1: this chunk's counts. 2: its places, from all chunks' counts.
 template <int MODE>
 __global__ __launch_bounds__(64 * kSortWaves) void adapter_sort_kernel(SortArgs a) {
-  extern __shared__ int lds[];
+  extern __shared__ int sort_mem[];
   __shared__ int sums[kSortWaves];
   const int B = a.L + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int* total = lds;                                 // [B] rows of each bucket
-  int* place = lds + B;                             // [B] first place of this chunk's rows
-  uint16_t* cnt = reinterpret_cast<uint16_t*>(lds + 2 * B);   // [waves, B]
-  for (int i = threadIdx.x; i < B * kSortWaves; i += blockDim.x) cnt[i] = 0;
-  __syncthreads();
-
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kSortChunk + wave * 64 * kSortSteps + lane;
+  int* total = sort_mem;                                 // [B] rows of each bucket
+  int* place = sort_mem + B;                             // [B] first place of this chunk's rows
+  int* start = sort_mem + 2 * B;                         // [B + 1] first tile of each bucket, and the end
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(sort_mem + 3 * B + 1);   // [waves, B]
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kSortChunk + wave * 64 * a.steps + lane;
   int e[kSortSteps], rank[kSortSteps];
 #pragma unroll
   for (int i = 0; i < kSortSteps; ++i) {
     const int64_t m = m0 + 64 * i;
     e[i] = -1;
-    if (m < a.M) {
+    if (i < a.steps && m < a.M) {
       const int v = a.index[m];
       e[i] = v >= 0 && v < a.L ? v : a.L;
     }
   }
-  // rank of each row among those of its bucket in its wave; one round per bucket of 64 rows
+  for (int i = threadIdx.x; i < B * kSortWaves; i += blockDim.x) cnt[i] = 0;
+  if constexpr (MODE != 1)
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.ncnt; i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+      a.arrived[i] = 0;
+  __syncthreads();
+  // rank of each row among those of its bucket in its wave: the first lane of each bucket counts
+  const int bits = 32 - __builtin_clz(a.L);
+  uint16_t* mine = cnt + wave * B;
 #pragma unroll
   for (int i = 0; i < kSortSteps; ++i) {
     rank[i] = 0;
-    uint64_t left = __ballot(e[i] >= 0);
-    while (left) {
-      const int b = __builtin_amdgcn_readlane(e[i], __builtin_ctzll(left));
-      const uint64_t same = __ballot(e[i] == b);
-      const int before = cnt[wave * B + b];
-      if (e[i] == b) rank[i] = before + __popcll(same & ((1ull << lane) - 1));
+    if (i >= a.steps) continue;
+    const uint64_t same = same_bucket(e[i], bits);
+    const uint64_t below = same & ((1ull << lane) - 1);
+    if (e[i] >= 0) {
+      const int before = mine[e[i]];
+      rank[i] = before + __popcll(below);
       __builtin_amdgcn_wave_barrier();
-      if (lane == 0) cnt[wave * B + b] = static_cast<uint16_t>(before + __popcll(same));
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      left &= ~same;
+      if (below == 0) mine[e[i]] = static_cast<uint16_t>(before + __popcll(same));
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
   // counts per wave become the rows of earlier waves
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    int sum = 0;
+    int n[kSortWaves], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) n[w] = cnt[w * B + b];
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const int n = cnt[w * B + b];
       cnt[w * B + b] = static_cast<uint16_t>(sum);
-      sum += n;
+      sum += n[w];
     }
     if constexpr (MODE == 1) a.counts[static_cast<int64_t>(blockIdx.x) * B + b] = sum;
+    int before = 0;
+    if constexpr (MODE == 2) {
+      sum = 0;
+#pragma unroll 8
+      for (int c = 0; c < a.chunks; ++c) {
+        const int v = a.counts[static_cast<int64_t>(c) * B + b];
+        before += c < static_cast<int>(blockIdx.x) ? v : 0;
+        sum += v;
+      }
+    }
     total[b] = sum;
-    place[b] = 0;
+    place[b] = before;
   }
   if constexpr (MODE == 1) return;
-  if constexpr (MODE == 2) {
-    for (int b = threadIdx.x; b < B; b += blockDim.x) {
-      int all = 0, before = 0;
-      for (int c = 0; c < a.chunks; ++c) {
-        const int n = a.counts[static_cast<int64_t>(c) * B + b];
-        before += c < static_cast<int>(blockIdx.x) ? n : 0;
-        all += n;
-      }
-      total[b] = all;
-      place[b] = before;
-    }
-  }
   __syncthreads();
   // first tile of each bucket: each thread has a run of buckets
   const int per = (B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
@@ -196,27 +308,35 @@ __global__ __launch_bounds__(64 * kSortWaves) void adapter_sort_kernel(SortArgs 
   __syncthreads();
   for (int w = 0; w < wave; ++w) at += sums[w];
   at -= tiles;
-  const bool first = blockIdx.x == 0;
   for (int b = b0; b < b1; ++b) {
-    const int n = (total[b] + kTile - 1) / kTile;
+    start[b] = at;
     place[b] += at * kTile;
-    if (first) {
-      a.start[b] = at;
-      if (b == a.L) a.start[B] = at + n;
-      for (int t = 0; t < n; ++t) a.tile[at + t] = b;
-      for (int i = total[b]; i < n * kTile; ++i) a.order[static_cast<int64_t>(at) * kTile + i] = -1;
-    }
-    at += n;
+    at += (total[b] + kTile - 1) / kTile;
+    if (b == a.L) start[B] = at;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kSortSteps; ++i)
-    if (e[i] >= 0) a.order[place[e[i]] + cnt[wave * B + e[i]] + rank[i]] = static_cast<int32_t>(m0 + 64 * i);
+    if (e[i] >= 0) a.order[place[e[i]] + mine[e[i]] + rank[i]] = static_cast<int32_t>(m0 + 64 * i);
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b <= B; b += blockDim.x) a.start[b] = start[b];
+    const int all = start[B];
+    for (int t = threadIdx.x; t < all; t += blockDim.x) {
+      int lo = 0, hi = B - 1;                       // the last bucket that starts at t or before; empty ones end where they start
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (start[mid] <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      a.tile[t] = lo;
+    }
+    for (int i = threadIdx.x; i < B * kTile; i += blockDim.x) {
+      const int b = i / kTile, p = total[b] + i % kTile;
+      if (p < (start[b + 1] - start[b]) * kTile) a.order[static_cast<int64_t>(start[b]) * kTile + p] = -1;
+    }
+  }
 }
 
-// ------------------------------------------------------------------------------------------
-// shrink: part[split, row, r] = sum over the split's k of S[row, k] w[e, r, k]
-// ------------------------------------------------------------------------------------------
 struct Sorted {
   const int32_t* order;
   const int32_t* tile;
@@ -225,64 +345,127 @@ struct Sorted {
   int64_t rows;           // places: 32 max_tiles
 };
 
+// ------------------------------------------------------------------------------------------
+// shrink: sums[row, r] = sum over k of S[row, k] w[e, r, k], and the coefficients made of them
+// ------------------------------------------------------------------------------------------
+// A workgroup has a tile of 32 rows, up to 64 ranks and one of the splits of k; its waves take
+// blocks of 64 values in turn, straight from memory in the matrix operands' layout (any order of
+// k serves that both operands share). Where there are several workgroups to a tile, the last one
+// that ends adds their sums, in order, and makes the coefficients.
 struct ShrinkArgs {
   Sorted o;
   const void* s;
   int64_t D, ld;
   const void* w;          // [L, R, D]
   int R, RP, splits;
-  float* part;
+  float* part;            // [splits, rows, RP]
+  uint32_t* arrived;      // [max_tiles]
+  const float* scale;     // [L] or null
+  float* h_out;           // [M, R] or null: the sums
+  const float* h_in;      // [M, R] or null: coefficients of its own, times the scale too
+  Coefs c, hc;            // of the sums times the scale, and of h_in
 };
 
+// Values of a tile in LDS, v [32][RP + 1], as the coefficients that the later passes take.
 template <int DT>
-__device__ __forceinline__ f32x4 dot32(const Eight<DT>& s, const Eight<DT>& w, f32x4 acc) {
-  if constexpr (DT == BL_F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, s.w), __builtin_bit_cast(half8v, w.w), acc, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8v, s.w), __builtin_bit_cast(bf8v, w.w), acc, 0, 0, 0);
+__device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int64_t rows, int64_t tiles, int RP, const float* v) {
+  const int pitch = RP + 1, tid = threadIdx.x;
+  if (c.f)
+    for (int i = tid; i < kTile * RP; i += 256) c.f[t * kTile * RP + i] = v[i / RP * pitch + i % RP];
+  if constexpr (DT != BL_F32) {
+    constexpr int P = Parts<DT>::n;
+    if (c.by_row) {
+      const int RK = (RP + 31) / 32 * 32, m = tid / 8, q = tid % 8;
+      int e = 0;
+      if constexpr (DT == BL_F16) {
+        uint32_t top = 0;
+        for (int r = q; r < RP; r += 8) top = max(top, finite_bits(v[m * pitch + r]));
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off)));
+        e = scale_exponent(top);
+        if (q == 0) c.row_e[t * kTile + m] = -e;
+      }
+      for (int k = q; k < RK / 8; k += 8) {
+        u32x4 w[3] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint16_t part[3];
+          split<DT>(8 * k + j < RP ? v[m * pitch + 8 * k + j] : 0.0f, e, part);
+#pragma unroll
+          for (int p = 0; p < P; ++p) w[p][j / 2] |= static_cast<uint32_t>(part[p]) << (16 * (j & 1));
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(c.by_row + ((p * rows + t * kTile + m) * RK + 8 * k)) = w[p];
+      }
+    }
+    if (c.by_rank) {
+      const int q = tid % 4;
+      for (int r = tid / 4; r < RP; r += 64) {
+        int e = 0;
+        if constexpr (DT == BL_F16) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = max(top, finite_bits(v[(8 * q + j) * pitch + r]));
+#pragma unroll
+          for (int off = 1; off < 4; off <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off)));
+          e = scale_exponent(top);
+          if (q == 0) c.rank_e[t * RP + r] = -e;
+        }
+        u32x4 w[3] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint16_t part[3];
+          split<DT>(v[(8 * q + j) * pitch + r], e, part);
+#pragma unroll
+          for (int p = 0; p < P; ++p) w[p][j / 2] |= static_cast<uint32_t>(part[p]) << (16 * (j & 1));
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(c.by_rank + ((p * tiles + t) * RP + r) * 32 + 8 * q) = w[p];
+      }
+    }
+  }
 }
 
-template <int SD, int WD, int NR, bool VEC>
+// CD: the type of what the coefficients will multiply, HD: of what h_in's will.
+template <int SD, int WD, int NR, int CD, int HD>
 __global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
-  __shared__ float red[4][kTile][16 * NR];
+  extern __shared__ float lds[];                    // [4][32][16 NR], then [32][RP + 1]
+  __shared__ int last;
   const int t = blockIdx.x;
   if (t >= a.o.start[a.o.L]) return;
   const int e = a.o.tile[t];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
   const int r0 = blockIdx.z * 16 * NR;
   using S = typename Elem<SD>::type;
   using W = typename Elem<WD>::type;
+  const int32_t* order = a.o.order + static_cast<int64_t>(t) * kTile;
+  // places without a row and ranks past the last one repeat another: their sums are not used
   const S* row[2];
-  int64_t n[2];                                     // no row: nothing is read
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int m = a.o.order[static_cast<int64_t>(t) * kTile + 16 * i + c];
-    row[i] = static_cast<const S*>(a.s) + static_cast<int64_t>(m < 0 ? 0 : m) * a.ld;
-    n[i] = m < 0 ? 0 : a.D;
+    const int m = order[16 * i + c];
+    row[i] = static_cast<const S*>(a.s) + static_cast<int64_t>(m < 0 ? order[0] : m) * a.ld;
   }
   const W* w[NR];
-  int64_t nw[NR];
 #pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int r = r0 + 16 * i + c;
-    w[i] = static_cast<const W*>(a.w) + (static_cast<int64_t>(e) * a.R + min(r, a.R - 1)) * a.D;
-    nw[i] = r < a.R ? a.D : 0;
-  }
+  for (int i = 0; i < NR; ++i)
+    w[i] = static_cast<const W*>(a.w) + (static_cast<int64_t>(e) * a.R + min(r0 + 16 * i + c, a.R - 1)) * a.D;
   f32x4 acc[2][NR] = {};
-  const int64_t units = (a.D + 63) / 64;
-  const int64_t u0 = units * blockIdx.y / a.splits, u1 = units * (blockIdx.y + 1) / a.splits;
-#pragma unroll 2
-  for (int64_t u = u0 + wave; u < u1; u += 4) {
-    Eight<SD> sv[2][2];
-    Eight<WD> wv[2][NR];
+  struct Unit {
+    Eight<SD> s[2][2];
+    Eight<WD> w[2][NR];
+  };
+  const auto load = [&](Unit& v, int64_t u, auto whole) {
     const int64_t k = u * 64 + g * 16;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) sv[j][i] = load8<SD, VEC>(row[i], k + 8 * j, n[i]);
+      for (int i = 0; i < 2; ++i) v.s[j][i] = load8<SD, decltype(whole)::value>(row[i], k + 8 * j, a.D);
 #pragma unroll
-      for (int i = 0; i < NR; ++i) wv[j][i] = load8<WD, VEC>(w[i], k + 8 * j, nw[i]);
+      for (int i = 0; i < NR; ++i) v.w[j][i] = load8<WD, decltype(whole)::value>(w[i], k + 8 * j, a.D);
     }
+  };
+  const auto multiply = [&](const Unit& v) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -290,25 +473,96 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
 #pragma unroll
         for (int q = 0; q < NR; ++q) {
           if constexpr (SD == WD && SD != BL_F32) {
-            acc[i][q] = dot32<SD>(sv[j][i], wv[j][q], acc[i][q]);
+            acc[i][q] = dot32<SD>(v.s[j][i].w, v.w[j][q].w, acc[i][q]);
           } else {
 #pragma unroll
             for (int l = 0; l < 8; ++l)
-              acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(value<SD>(sv[j][i], l), value<WD>(wv[j][q], l), acc[i][q], 0, 0, 0);
+              acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(value<SD>(v.s[j][i], l), value<WD>(v.w[j][q], l), acc[i][q], 0, 0, 0);
           }
         }
+  };
+  const int64_t units = (a.D + 63) / 64, full = a.D / 64;
+  const int64_t u0 = units * blockIdx.y / a.splits, u1 = units * (blockIdx.y + 1) / a.splits, uf = min(u1, full);
+  int64_t u = u0 + wave;
+  // two blocks in flight
+  Unit v0, v1;
+  if (u < uf) load(v0, u, std::true_type{});
+  for (; u < uf; u += 8) {
+    if (u + 4 < uf) load(v1, u + 4, std::true_type{});
+    multiply(v0);
+    if (u + 4 < uf) {
+      if (u + 8 < uf) load(v0, u + 8, std::true_type{});
+      multiply(v1);
+    }
   }
+  if (u1 > full && (full - u0) % 4 == wave) {       // the block that is not whole
+    load(v0, full, std::false_type{});
+    multiply(v0);
+  }
+
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int q = 0; q < NR; ++q)
 #pragma unroll
-      for (int l = 0; l < 4; ++l) red[wave][16 * i + 4 * g + l][16 * q + c] = acc[i][q][l];
+      for (int l = 0; l < 4; ++l) lds[(wave * kTile + 16 * i + 4 * g + l) * 16 * NR + 16 * q + c] = acc[i][q][l];
   __syncthreads();
-  float* out = a.part + (blockIdx.y * a.o.rows + static_cast<int64_t>(t) * kTile) * a.RP + r0;
-  for (int i = threadIdx.x; i < kTile * 16 * NR; i += 256) {
-    const int m = i / (16 * NR), r = i % (16 * NR);
-    if (r0 + r < a.RP) out[m * a.RP + r] = red[0][m][r] + red[1][m][r] + red[2][m][r] + red[3][m][r];
+  constexpr int kEach = kTile * 16 * NR / 256;
+  float sum[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int at = tid + 256 * i;
+    sum[i] = lds[at] + lds[at + kTile * 16 * NR] + lds[at + 2 * kTile * 16 * NR] + lds[at + 3 * kTile * 16 * NR];
+  }
+  const int groups = a.splits * static_cast<int>(gridDim.z), pitch = a.RP + 1;
+  const float f = a.scale ? a.scale[e] : 1.0f;
+  if (groups > 1) {
+    float* out = a.part + (blockIdx.y * a.o.rows + static_cast<int64_t>(t) * kTile) * a.RP;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int at = tid + 256 * i, m = at / (16 * NR), r = r0 + at % (16 * NR);
+      if (r < a.RP) atomic_store_agent(out + m * a.RP + r, sum[i]);
+    }
+    wait_own_memory_ops();
+    __syncthreads();
+    if (tid == 0) last = arrive_agent(a.arrived + t) + 1 == static_cast<uint32_t>(groups);
+    __syncthreads();
+    if (!last) return;
+    const float* in = a.part + static_cast<int64_t>(t) * kTile * a.RP;
+    const int64_t step = a.o.rows * a.RP;
+    for (int i = tid; i < kTile * a.RP; i += 256) {
+      float v = 0.0f;
+#pragma unroll 8
+      for (int s = 0; s < a.splits; ++s) v += atomic_load_agent(in + s * step + i);
+      lds[i / a.RP * pitch + i % a.RP] = v;
+    }
+  } else {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int at = tid + 256 * i, m = at / (16 * NR), r = at % (16 * NR);
+      if (r < a.RP) lds[m * pitch + r] = sum[i];
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < kTile * a.RP; i += 256) {
+    const int m = i / a.RP, r = i % a.RP, at = order[m];
+    float& v = lds[m * pitch + r];
+    const bool there = at >= 0 && r < a.R;
+    if (there && a.h_out) a.h_out[static_cast<int64_t>(at) * a.R + r] = v;
+    v = there ? v * f : 0.0f;
+  }
+  __syncthreads();
+  const int64_t tiles = a.o.rows / kTile;
+  write_coefs<CD>(a.c, t, a.o.rows, tiles, a.RP, lds);
+  if (a.h_in) {
+    __syncthreads();
+    for (int i = tid; i < kTile * a.RP; i += 256) {
+      const int m = i / a.RP, r = i % a.RP, at = order[m];
+      lds[m * pitch + r] = at >= 0 && r < a.R ? a.h_in[static_cast<int64_t>(at) * a.R + r] * f : 0.0f;
+    }
+    __syncthreads();
+    write_coefs<HD>(a.hc, t, a.o.rows, tiles, a.RP, lds);
   }
 }
 
@@ -317,11 +571,9 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
 // ------------------------------------------------------------------------------------------
 struct ExpandArgs {
   Sorted o;
-  const float* c;         // [splits, rows, RP], summed here
-  int splits;
+  Coefs c;
   int R, RP;
-  const float* scale;     // [L] or null
-  float* h;               // [M, R] or null: the sums without the scale
+  float* h;               // [M, R] or null: rows without an adapter get zeros
   const void* w;          // [L, R, N]
   int64_t N;
   const void* base;
@@ -330,52 +582,72 @@ struct ExpandArgs {
   int64_t ldy;
 };
 
-template <int WD, int YD, bool VEC>
-__global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
-  extern __shared__ float cl[];                     // [32][RP + 4]
-  __shared__ int rows[kTile];
-  const int t = blockIdx.x;
-  if (t >= a.o.start[a.o.L + 1]) return;
-  const int e = a.o.tile[t], lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-  const int pitch = a.RP + 4;
+// A wave has 32 rows and 128 columns: lane 16 g + c columns 8 c .. 8 c + 7 of them, so that w, base and y go
+// 16 bytes at a time, and matrix instruction j makes columns 8 c + j.
+template <int WD, int YD, bool WHOLE>
+__device__ __forceinline__ void expand_block(const ExpandArgs& a, int t, int e, int64_t n0, int lane) {
+  const int c = lane & 15, g = lane >> 4;
+  const int64_t n = n0 + 8 * c;
   const bool none = e >= a.o.L;
-  if (none && a.base == a.y && (!a.h || blockIdx.y)) return;
-  if (threadIdx.x < kTile) rows[threadIdx.x] = a.o.order[static_cast<int64_t>(t) * kTile + threadIdx.x];
-  const float f = a.scale && !none ? a.scale[e] : 1.0f;
-  for (int i = threadIdx.x; i < kTile * a.RP; i += 256) {
-    const int m = i / a.RP, r = i % a.RP;
-    float v = 0.0f;
-    if (!none)
-      for (int s = 0; s < a.splits; ++s) v += a.c[(s * a.o.rows + static_cast<int64_t>(t) * kTile + m) * a.RP + r];
-    if (a.h && blockIdx.y == 0 && r < a.R) {
-      const int row = a.o.order[static_cast<int64_t>(t) * kTile + m];
-      if (row >= 0) a.h[static_cast<int64_t>(row) * a.R + r] = v;
-    }
-    cl[m * pitch + r] = v * f;
-  }
-  __syncthreads();
-  const int64_t n0 = (static_cast<int64_t>(blockIdx.y) * 4 + wave) * 128, n = n0 + 8 * c;
-  if (n0 >= a.N) return;
+  const int32_t* order = a.o.order + static_cast<int64_t>(t) * kTile;
   using W = typename Elem<WD>::type;
   using Y = typename Elem<YD>::type;
+  int row[2][4];
+  Eight<YD> base[2][4] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int l = 0; l < 4; ++l) {
+      row[i][l] = order[16 * i + 4 * g + l];
+      if (a.base && row[i][l] >= 0)
+        base[i][l] = load8<YD, WHOLE>(static_cast<const Y*>(a.base) + row[i][l] * a.ldbase, n, a.N);
+    }
   f32x4 acc[2][8] = {};
   if (!none) {
     const W* w = static_cast<const W*>(a.w) + static_cast<int64_t>(e) * a.R * a.N;
-    for (int r0 = 0; r0 < a.RP; r0 += 16) {
-      Eight<WD> wv[4];
+    if constexpr (WD == BL_F32) {
+      const float* co = a.c.f + static_cast<int64_t>(t) * kTile * a.RP;
+      for (int r0 = 0; r0 < a.RP; r0 += 16) {
+        Eight<WD> wv[4];
+        float cv[2][4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int r = r0 + 4 * s + g;
-        wv[s] = load8<WD, VEC>(w + static_cast<int64_t>(min(r, a.R - 1)) * a.N, n, r < a.R ? a.N : 0);
+        for (int s = 0; s < 4; ++s) {
+          const int r = r0 + 4 * s + g;
+          wv[s] = zero_unless(r < a.R, load8<WD, WHOLE>(w + static_cast<int64_t>(min(r, a.R - 1)) * a.N, n, a.N));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) cv[i][s] = co[(16 * i + c) * a.RP + r];
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[i][s], value<WD>(wv[s], j), acc[i][j], 0, 0, 0);
       }
+    } else {
+      constexpr int P = Parts<WD>::n;
+      const int RK = (a.RP + 31) / 32 * 32;
+      const uint16_t* co = a.c.by_row + static_cast<int64_t>(t) * kTile * RK;
+      for (int r0 = 0; r0 < RK; r0 += 32) {
+        u32x4 wv[8], cv[P][2];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float c0 = cl[c * pitch + r0 + 4 * s + g], c1 = cl[(16 + c) * pitch + r0 + 4 * s + g];
+        for (int s = 0; s < 8; ++s) {
+          const int r = r0 + 8 * g + s;
+          wv[s] = zero_unless(r < a.R, load8<WD, WHOLE>(w + static_cast<int64_t>(min(r, a.R - 1)) * a.N, n, a.N)).w;
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            cv[p][i] = *reinterpret_cast<const u32x4*>(co + (p * a.o.rows + 16 * i + c) * RK + r0 + 8 * g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float v = value<WD>(wv[s], j);
-          acc[0][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(c0, v, acc[0][j], 0, 0, 0);
-          acc[1][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(c1, v, acc[1][j], 0, 0, 0);
+          const u32x4 v = column(wv, j);
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) acc[i][j] = dot32<WD>(cv[p][i], v, acc[i][j]);
         }
       }
     }
@@ -384,105 +656,159 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int l = 0; l < 4; ++l) {
-      const int row = rows[16 * i + 4 * g + l];
-      if (row < 0) continue;
+      if (row[i][l] < 0) continue;
       float v[8];
+      int ex = 0;
+      if constexpr (WD == BL_F16) ex = none ? 0 : a.c.row_e[static_cast<int64_t>(t) * kTile + 16 * i + 4 * g + l];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = acc[i][j][l];
-      if (a.base) {
-        const Eight<YD> b = load8<YD, VEC>(static_cast<const Y*>(a.base) + row * a.ldbase, n, a.N);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = none ? value<YD>(b, j) : value<YD>(b, j) + v[j];
+      for (int j = 0; j < 8; ++j) {
+        v[j] = acc[i][j][l];
+        if constexpr (WD == BL_F16) v[j] = ldexpf(v[j], ex);
+        if (a.base) v[j] = none ? value<YD>(base[i][l], j) : value<YD>(base[i][l], j) + v[j];
       }
-      store8<YD, VEC>(static_cast<Y*>(a.y) + row * a.ldy, n, a.N, v);
+      store8<YD, WHOLE>(static_cast<Y*>(a.y) + row[i][l] * a.ldy, n, a.N, v);
     }
 }
 
-// ------------------------------------------------------------------------------------------
-// dh and the scaled h, sorted; places without a row are 0
-// ------------------------------------------------------------------------------------------
-struct FinishArgs {
-  Sorted o;
-  const float* part;      // [splits, rows, RP]
-  int splits, R, RP;
-  const float* scale;
-  const float* h;         // [M, R]
-  float* dh;              // [rows, RP]
-  float* hs;              // [rows, RP]
-};
-
-__global__ __launch_bounds__(256) void adapter_finish_kernel(FinishArgs a) {
+template <int WD, int YD>
+__global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
   const int t = blockIdx.x;
-  if (t >= a.o.start[a.o.L]) return;
-  const int e = a.o.tile[t];
-  const float f = a.scale ? a.scale[e] : 1.0f;
-  const int64_t at = static_cast<int64_t>(t) * kTile;
-  for (int i = threadIdx.x; i < kTile * a.RP; i += 256) {
-    const int m = i / a.RP, r = i % a.RP;
-    const int row = a.o.order[at + m];
-    float v = 0.0f, h = 0.0f;
-    if (row >= 0 && r < a.R) {
-      for (int s = 0; s < a.splits; ++s) v += a.part[(s * a.o.rows + at + m) * a.RP + r];
-      h = a.h[static_cast<int64_t>(row) * a.R + r];
-    }
-    a.dh[at * a.RP + i] = v * f;
-    a.hs[at * a.RP + i] = h * f;
+  if (t >= a.o.start[a.o.L + 1]) return;
+  const int e = a.o.tile[t], lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (e >= a.o.L) {
+    if (a.h && blockIdx.y == 0)
+      for (int i = threadIdx.x; i < kTile * a.R; i += 256) {
+        const int row = a.o.order[static_cast<int64_t>(t) * kTile + i / a.R];
+        if (row >= 0) a.h[static_cast<int64_t>(row) * a.R + i % a.R] = 0.0f;
+      }
+    if (a.base == a.y) return;
   }
+  const int64_t n0 = (static_cast<int64_t>(blockIdx.y) * 4 + wave) * 128;
+  if (n0 + 128 <= a.N) expand_block<WD, YD, true>(a, t, e, n0, lane);
+  else if (n0 < a.N) expand_block<WD, YD, false>(a, t, e, n0, lane);
 }
 
 // ------------------------------------------------------------------------------------------
 // outer: grad[e, r, d] = sum over the adapter's rows of c[row, r] S[row, d]
 // ------------------------------------------------------------------------------------------
-// Tiles are split evenly over workgroups. An adapter that lies within one split is written at
-// once; the pieces of the others go to sum[2 split], where the adapter began in an earlier split,
-// or sum[2 split + 1], and meet in adapter_gather_kernel in their order.
+// A workgroup has 128 columns, up to 64 ranks and an even share of the tiles, which its waves take in
+// turn. An adapter that lies within one share is written at once. The pieces of one that does
+// not go to sum[2 share], where the adapter began in an earlier share, or sum[2 share + 1]; the
+// workgroup that ends last adds them in their order. Each share has at most one adapter that
+// goes on after it, so the share where an adapter begins names its counter.
 struct OuterArgs {
   Sorted o;
-  const float* c;         // [rows, RP]
+  Coefs c;
   const void* s;
   int64_t D, ld;
   int R, RP, splits;
   float* sum;             // [2 splits, R, D]
+  uint32_t* arrived;      // [splits, z, x]
   float* grad;            // [L, R, D]
   int add;
 };
 
-template <int SD, int NR, bool VEC>
+template <int SD, int NR, bool WHOLE>
+__device__ __forceinline__ void outer_tile(const OuterArgs& a, int64_t t, int64_t d, int r0, int c, int g, f32x4 (&acc)[NR][8]) {
+  using S = typename Elem<SD>::type;
+  const S* s = static_cast<const S*>(a.s);
+  const int32_t* order = a.o.order + t * kTile;
+  if constexpr (SD == BL_F32) {
+    Eight<SD> sv[8];
+    float cv[8][NR];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = order[4 * i + g];
+      sv[i] = zero_unless(row >= 0, load8<SD, WHOLE>(s + static_cast<int64_t>(max(row, 0)) * a.ld, d, a.D));
+#pragma unroll
+      for (int q = 0; q < NR; ++q) {
+        const int r = r0 + 16 * q + c;
+        cv[i][q] = r < a.RP ? a.c.f[(t * kTile + 4 * i + g) * a.RP + r] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int q = 0; q < NR; ++q)
+          acc[q][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[i][q], value<SD>(sv[i], j), acc[q][j], 0, 0, 0);
+  } else {
+    constexpr int P = Parts<SD>::n;
+    const int64_t tiles = a.o.rows / kTile;
+    u32x4 sv[8], cv[P][NR];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = order[8 * g + i];
+      sv[i] = zero_unless(row >= 0, load8<SD, WHOLE>(s + static_cast<int64_t>(max(row, 0)) * a.ld, d, a.D)).w;
+    }
+#pragma unroll
+    for (int q = 0; q < NR; ++q) {
+      const int r = min(r0 + 16 * q + c, a.RP - 1);   // past the last rank: not used
+#pragma unroll
+      for (int p = 0; p < P; ++p) cv[p][q] = *reinterpret_cast<const u32x4*>(a.c.by_rank + ((p * tiles + t) * a.RP + r) * 32 + 8 * g);
+    }
+    if constexpr (SD == BL_F16) {
+      int ex[NR][4];
+#pragma unroll
+      for (int q = 0; q < NR; ++q)
+#pragma unroll
+        for (int l = 0; l < 4; ++l) ex[q][l] = a.c.rank_e[t * a.RP + min(r0 + 16 * q + 4 * g + l, a.RP - 1)];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const u32x4 v = column(sv, j);
+#pragma unroll
+        for (int q = 0; q < NR; ++q) {
+          f32x4 one = {};
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p) one = dot32<SD>(cv[p][q], v, one);
+#pragma unroll
+          for (int l = 0; l < 4; ++l) acc[q][j][l] += ldexpf(one[l], ex[q][l]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const u32x4 v = column(sv, j);
+#pragma unroll
+        for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+          for (int q = 0; q < NR; ++q) acc[q][j] = dot32<SD>(cv[p][q], v, acc[q][j]);
+      }
+    }
+  }
+}
+
+template <int SD, int NR>
 __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a) {
-  __shared__ float red[16 * NR][128];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+  __shared__ f32x4 red[16 * NR][32];
+  __shared__ int last_one;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
   const int64_t d0 = static_cast<int64_t>(blockIdx.x) * 128;
   const int r0 = blockIdx.z * 16 * NR;
-  const int64_t tiles = a.o.start[a.o.L];
+  const int64_t tiles = a.o.start[a.o.L], n = static_cast<int64_t>(a.R) * a.D;
+  const auto each = [&](auto f) {                   // of this workgroup's values: (row and column in red, place in [R, D])
+    for (int i = tid; i < 16 * NR * 128; i += 256) {
+      const int r = r0 + i / 128;
+      const int64_t d = d0 + i % 128;
+      if (r < a.R && d < a.D) f(i, r * a.D + d);
+    }
+  };
+  float* flat = reinterpret_cast<float*>(red);
+  // adapters without rows, shared out over the shares
+  if (!a.add)
+    for (int e = blockIdx.y; e < a.o.L; e += a.splits)
+      if (a.o.start[e] == a.o.start[e + 1]) each([&](int, int64_t at) { a.grad[e * n + at] = 0.0f; });
+
   const int t1 = static_cast<int>(tiles * (blockIdx.y + 1) / a.splits);
-  using S = typename Elem<SD>::type;
   for (int t = static_cast<int>(tiles * blockIdx.y / a.splits); t < t1;) {
     const int e = a.o.tile[t], first = a.o.start[e], last = a.o.start[e + 1];
     const int end = min(last, t1);
     f32x4 acc[NR][8] = {};
-    for (int i = t + wave; i < end; i += 4) {
-      const int64_t at = static_cast<int64_t>(i) * kTile;
-      Eight<SD> sv[8];
-      float cv[8][NR];
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const int row = a.o.order[at + 4 * s + g];
-        sv[s] = load8<SD, VEC>(static_cast<const S*>(a.s) + static_cast<int64_t>(row < 0 ? 0 : row) * a.ld, d0 + 8 * c, row < 0 ? 0 : a.D);
-#pragma unroll
-        for (int q = 0; q < NR; ++q) {
-          const int r = r0 + 16 * q + c;
-          cv[s][q] = r < a.RP ? a.c[(at + 4 * s + g) * a.RP + r] : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float v = value<SD>(sv[s], j);
-#pragma unroll
-          for (int q = 0; q < NR; ++q) acc[q][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[s][q], v, acc[q][j], 0, 0, 0);
-        }
-    }
+    if (d0 + 128 <= a.D)
+      for (int i = t + wave; i < end; i += 4) outer_tile<SD, NR, true>(a, i, d0 + 8 * c, r0, c, g, acc);
+    else
+      for (int i = t + wave; i < end; i += 4) outer_tile<SD, NR, false>(a, i, d0 + 8 * c, r0, c, g, acc);
     // the waves' sums, one after another
     for (int w = 0; w < 4; ++w) {
       if (wave == w) {
@@ -491,52 +817,37 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a) {
 #pragma unroll
           for (int l = 0; l < 4; ++l)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float& p = red[16 * q + 4 * g + l][8 * c + j];
-              p = w ? p + acc[q][j][l] : acc[q][j][l];
+            for (int j = 0; j < 2; ++j) {
+              f32x4& p = red[16 * q + 4 * g + l][2 * c + j];
+              const f32x4 v = {acc[q][4 * j][l], acc[q][4 * j + 1][l], acc[q][4 * j + 2][l], acc[q][4 * j + 3][l]};
+              p = w ? p + v : v;
             }
       }
       __syncthreads();
     }
-    const bool whole = first >= t && last <= end;
-    float* out = whole ? a.grad + static_cast<int64_t>(e) * a.R * a.D
-                       : a.sum + (2 * static_cast<int64_t>(blockIdx.y) + (first >= t ? 1 : 0)) * a.R * a.D;
-    for (int i = threadIdx.x; i < 16 * NR * 128; i += 256) {
-      const int r = r0 + i / 128;
-      const int64_t d = d0 + i % 128;
-      if (r < a.R && d < a.D) {
-        float* p = out + r * a.D + d;
-        *p = whole && a.add ? *p + red[i / 128][i % 128] : red[i / 128][i % 128];
-      }
+    float* grad = a.grad + e * n;
+    if (first >= t && last <= end) {
+      each([&](int i, int64_t at) { grad[at] = a.add ? grad[at] + flat[i] : flat[i]; });
+    } else {
+      float* out = a.sum + (2 * static_cast<int64_t>(blockIdx.y) + (first >= t ? 1 : 0)) * n;
+      each([&](int i, int64_t at) { atomic_store_agent(out + at, flat[i]); });
+      wait_own_memory_ops();
+      __syncthreads();
+      // the share of tile t is the largest s whose first tile, floor(s tiles / splits), is not past t
+      const int64_t s0 = ((first + 1ll) * a.splits - 1) / tiles, s1 = (static_cast<int64_t>(last) * a.splits - 1) / tiles;
+      if (tid == 0)
+        last_one = arrive_agent(a.arrived + (s0 * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x) == static_cast<uint32_t>(s1 - s0);
+      __syncthreads();
+      if (last_one)
+        each([&](int, int64_t at) {
+          float v = atomic_load_agent(a.sum + (2 * s0 + 1) * n + at);
+#pragma unroll 8
+          for (int64_t s = s0 + 1; s <= s1; ++s) v += atomic_load_agent(a.sum + 2 * s * n + at);
+          grad[at] = a.add ? grad[at] + v : v;
+        });
     }
     __syncthreads();
     t = end;
-  }
-}
-
-__global__ __launch_bounds__(256) void adapter_gather_kernel(OuterArgs a) {
-  const int64_t n = static_cast<int64_t>(a.R) * a.D;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x;
-  const int64_t tiles = a.o.start[a.o.L];
-  for (int e = blockIdx.y; e < a.o.L; e += gridDim.y) {
-    const int64_t first = a.o.start[e], last = a.o.start[e + 1];
-    float* grad = a.grad + e * n;
-    if (first == last) {
-      if (!a.add)
-        for (int i = 0; i < 4; ++i)
-          if (at + 256 * i < n) grad[at + 256 * i] = 0.0f;
-      continue;
-    }
-    // the split of tile t is the largest s whose first tile, floor(s tiles / splits), is not past t
-    const int64_t s0 = ((first + 1) * a.splits - 1) / tiles, s1 = (last * a.splits - 1) / tiles;
-    if (s0 == s1) continue;
-    for (int i = 0; i < 4; ++i) {
-      const int64_t d = at + 256 * i;
-      if (d >= n) break;
-      float v = a.sum[(2 * s0 + 1) * n + d];
-      for (int64_t s = s0 + 1; s <= s1; ++s) v += a.sum[2 * s * n + d];
-      grad[d] = a.add ? grad[d] + v : v;
-    }
   }
 }
 
@@ -549,7 +860,18 @@ int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
 }
 int outer_splits(int64_t M, int64_t R, int64_t D) {
   const int64_t groups = div_up(D, 128) * div_up(rank_pad(R), 64);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({1024 / groups, div_up(M, 4 * kTile), 32})));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({512 / groups, div_up(M, 4 * kTile), 32})));
+}
+int64_t outer_counters(int64_t M, int64_t R, int64_t D) { return outer_splits(M, R, D) * div_up(D, 128) * div_up(rank_pad(R), 64); }
+
+// Bytes of each layout of the coefficients.
+struct CoefBytes {
+  size_t f, by_row, row_e, by_rank, rank_e;
+};
+CoefBytes coef_bytes(int64_t M, int64_t L, int64_t R) {
+  const int64_t tiles = max_tiles(M, L), rows = tiles * kTile, RP = rank_pad(R), RK = div_up(R, 32) * 32;
+  return {static_cast<size_t>(rows * RP * 4), static_cast<size_t>(3 * rows * RK * 2), static_cast<size_t>(rows * 4),
+          static_cast<size_t>(3 * rows * RP * 2), static_cast<size_t>(tiles * RP * 4)};
 }
 
 struct Scratch {
@@ -558,7 +880,9 @@ struct Scratch {
   int32_t* tile;
   int32_t* start;
   int32_t* counts;
-  float *part, *c, *sum;
+  uint32_t* arrived;
+  float *part, *sum;
+  Coefs c, hc;
 };
 Scratch scratch(const AdapterWs& L, char* ws, const AdapterRows& r) {
   Scratch s{};
@@ -566,15 +890,23 @@ Scratch scratch(const AdapterWs& L, char* ws, const AdapterRows& r) {
   s.tile = reinterpret_cast<int32_t*>(ws + L.tile_off);
   s.start = reinterpret_cast<int32_t*>(ws + L.start_off);
   s.counts = reinterpret_cast<int32_t*>(ws + L.count_off);
+  s.arrived = reinterpret_cast<uint32_t*>(ws + L.arrived_off);
   s.part = reinterpret_cast<float*>(ws + L.part_off);
-  s.c = reinterpret_cast<float*>(ws + L.c_off);
   s.sum = reinterpret_cast<float*>(ws + L.sum_off);
   s.o = Sorted{s.order, s.tile, s.start, static_cast<int>(r.L), max_tiles(r.M, r.L) * kTile};
+  const auto coefs = [&](const size_t (&at)[5]) {
+    return Coefs{reinterpret_cast<float*>(ws + at[0]), reinterpret_cast<uint16_t*>(ws + at[1]), reinterpret_cast<int32_t*>(ws + at[2]),
+                 reinterpret_cast<uint16_t*>(ws + at[3]), reinterpret_cast<int32_t*>(ws + at[4])};
+  };
+  s.c = coefs(L.c_off);
+  s.hc = coefs(L.hc_off);
   return s;
 }
 
-hipError_t sort_rows(const AdapterRows& r, const Scratch& w, hipStream_t s) {
-  SortArgs a{r.index, r.M, static_cast<int>(r.L), static_cast<int>(div_up(r.M, kSortChunk)), w.order, w.tile, w.start, w.counts};
+hipError_t sort_rows(const AdapterRows& r, const Scratch& w, int64_t counters, hipStream_t s) {
+  const int chunks = static_cast<int>(div_up(r.M, kSortChunk));
+  const int steps = chunks > 1 ? kSortSteps : static_cast<int>(div_up(r.M, 64 * kSortWaves));
+  const SortArgs a{r.index, r.M, static_cast<int>(r.L), chunks, steps, w.order, w.tile, w.start, w.counts, w.arrived, counters};
   const size_t lds = sort_lds(r.L);
   if (a.chunks == 1) {
     adapter_sort_kernel<0><<<1, 64 * kSortWaves, lds, s>>>(a);
@@ -586,69 +918,62 @@ hipError_t sort_rows(const AdapterRows& r, const Scratch& w, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Whether rows of n values of either type are whole, aligned pieces of eight.
-bool vec_rows(const void* p, int64_t n, int64_t ld) {
-  return !p || (n % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0);
-}
-
-template <int SD, int WD, bool VEC>
-hipError_t start_shrink_nr(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
-  const int nr = std::min(a.RP / 16, 4);
+template <int SD, int WD, int NR, int CD, int HD>
+hipError_t start_shrink_as(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(tiles), a.splits, static_cast<uint32_t>(div_up(a.RP, 64)));
-  if (nr == 1) adapter_shrink_kernel<SD, WD, 1, VEC><<<grid, 256, 0, s>>>(a);
-  else if (nr == 2) adapter_shrink_kernel<SD, WD, 2, VEC><<<grid, 256, 0, s>>>(a);
-  else if (nr == 3) adapter_shrink_kernel<SD, WD, 3, VEC><<<grid, 256, 0, s>>>(a);
-  else adapter_shrink_kernel<SD, WD, 4, VEC><<<grid, 256, 0, s>>>(a);
+  const size_t lds = static_cast<size_t>(kTile) * std::max(64 * NR, a.RP + 1) * 4;
+  adapter_shrink_kernel<SD, WD, NR, CD, HD><<<grid, 256, lds, s>>>(a);
   return hipGetLastError();
 }
-template <int SD, int WD>
-hipError_t start_shrink_vec(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
-  return vec_rows(a.s, a.D, a.ld) && vec_rows(a.w, a.D, a.D) ? start_shrink_nr<SD, WD, true>(a, tiles, s)
-                                                              : start_shrink_nr<SD, WD, false>(a, tiles, s);
+template <int SD, int WD, int CD, int HD>
+hipError_t start_shrink_nr(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
+  const int nr = std::min(a.RP / 16, 4);
+  if (nr == 1) return start_shrink_as<SD, WD, 1, CD, HD>(a, tiles, s);
+  if (nr == 2) return start_shrink_as<SD, WD, 2, CD, HD>(a, tiles, s);
+  if (nr == 3) return start_shrink_as<SD, WD, 3, CD, HD>(a, tiles, s);
+  return start_shrink_as<SD, WD, 4, CD, HD>(a, tiles, s);
 }
-// sd is wd, or fp32.
+// sd is wd, or fp32. The sums' coefficients multiply values of wd, h_in's values of sd.
 hipError_t start_shrink(const ShrinkArgs& a, int sd, int wd, int64_t tiles, hipStream_t s) {
-  if (wd == BL_F16) return sd == BL_F16 ? start_shrink_vec<BL_F16, BL_F16>(a, tiles, s) : start_shrink_vec<BL_F32, BL_F16>(a, tiles, s);
-  if (wd == BL_BF16) return sd == BL_BF16 ? start_shrink_vec<BL_BF16, BL_BF16>(a, tiles, s) : start_shrink_vec<BL_F32, BL_BF16>(a, tiles, s);
-  return start_shrink_vec<BL_F32, BL_F32>(a, tiles, s);
+  if (wd == BL_F16) return sd == BL_F16 ? start_shrink_nr<BL_F16, BL_F16, BL_F16, BL_F16>(a, tiles, s) : start_shrink_nr<BL_F32, BL_F16, BL_F16, BL_F32>(a, tiles, s);
+  if (wd == BL_BF16) return sd == BL_BF16 ? start_shrink_nr<BL_BF16, BL_BF16, BL_BF16, BL_BF16>(a, tiles, s) : start_shrink_nr<BL_F32, BL_BF16, BL_BF16, BL_F32>(a, tiles, s);
+  return start_shrink_nr<BL_F32, BL_F32, BL_F32, BL_F32>(a, tiles, s);
 }
 
 template <int WD, int YD>
-hipError_t start_expand_vec(const ExpandArgs& a, int64_t tiles, hipStream_t s) {
+hipError_t start_expand_as(const ExpandArgs& a, int64_t tiles, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(div_up(a.N, 512)));
-  const size_t lds = static_cast<size_t>(kTile) * (a.RP + 4) * 4;
-  if (vec_rows(a.w, a.N, a.N) && vec_rows(a.base, a.N, a.ldbase) && vec_rows(a.y, a.N, a.ldy))
-    adapter_expand_kernel<WD, YD, true><<<grid, 256, lds, s>>>(a);
-  else
-    adapter_expand_kernel<WD, YD, false><<<grid, 256, lds, s>>>(a);
+  adapter_expand_kernel<WD, YD><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 // yd is wd, or fp32.
 hipError_t start_expand(const ExpandArgs& a, int wd, int yd, int64_t tiles, hipStream_t s) {
-  if (wd == BL_F16) return yd == BL_F16 ? start_expand_vec<BL_F16, BL_F16>(a, tiles, s) : start_expand_vec<BL_F16, BL_F32>(a, tiles, s);
-  if (wd == BL_BF16) return yd == BL_BF16 ? start_expand_vec<BL_BF16, BL_BF16>(a, tiles, s) : start_expand_vec<BL_BF16, BL_F32>(a, tiles, s);
-  return start_expand_vec<BL_F32, BL_F32>(a, tiles, s);
+  if (wd == BL_F16) return yd == BL_F16 ? start_expand_as<BL_F16, BL_F16>(a, tiles, s) : start_expand_as<BL_F16, BL_F32>(a, tiles, s);
+  if (wd == BL_BF16) return yd == BL_BF16 ? start_expand_as<BL_BF16, BL_BF16>(a, tiles, s) : start_expand_as<BL_BF16, BL_F32>(a, tiles, s);
+  return start_expand_as<BL_F32, BL_F32>(a, tiles, s);
 }
 
-template <int SD, bool VEC>
-hipError_t start_outer_nr(const OuterArgs& a, hipStream_t s) {
+template <int SD>
+hipError_t start_outer_as(const OuterArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(div_up(a.D, 128)), a.splits, static_cast<uint32_t>(div_up(a.RP, 64)));
   const int nr = std::min(a.RP / 16, 4);
-  if (nr == 1) adapter_outer_kernel<SD, 1, VEC><<<grid, 256, 0, s>>>(a);
-  else if (nr == 2) adapter_outer_kernel<SD, 2, VEC><<<grid, 256, 0, s>>>(a);
-  else if (nr == 3) adapter_outer_kernel<SD, 3, VEC><<<grid, 256, 0, s>>>(a);
-  else adapter_outer_kernel<SD, 4, VEC><<<grid, 256, 0, s>>>(a);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  const dim3 each(static_cast<uint32_t>(div_up(static_cast<int64_t>(a.R) * a.D, 1024)), static_cast<uint32_t>(a.o.L));
-  adapter_gather_kernel<<<each, 256, 0, s>>>(a);
+  if (nr == 1) adapter_outer_kernel<SD, 1><<<grid, 256, 0, s>>>(a);
+  else if (nr == 2) adapter_outer_kernel<SD, 2><<<grid, 256, 0, s>>>(a);
+  else if (nr == 3) adapter_outer_kernel<SD, 3><<<grid, 256, 0, s>>>(a);
+  else adapter_outer_kernel<SD, 4><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
-template <int SD>
-hipError_t start_outer_vec(const OuterArgs& a, hipStream_t s) {
-  return vec_rows(a.s, a.D, a.ld) ? start_outer_nr<SD, true>(a, s) : start_outer_nr<SD, false>(a, s);
-}
 hipError_t start_outer(const OuterArgs& a, int sd, hipStream_t s) {
-  return sd == BL_F16 ? start_outer_vec<BL_F16>(a, s) : sd == BL_BF16 ? start_outer_vec<BL_BF16>(a, s) : start_outer_vec<BL_F32>(a, s);
+  return sd == BL_F16 ? start_outer_as<BL_F16>(a, s) : sd == BL_BF16 ? start_outer_as<BL_BF16>(a, s) : start_outer_as<BL_F32>(a, s);
+}
+
+// The layouts that a value of type dt is multiplied by: fp32 for fp32, else parts.
+Coefs only(const Coefs& c, int dt, bool rows, bool ranks) {
+  Coefs o{};
+  if (dt == BL_F32) o.f = c.f;
+  else if (rows) o.by_row = c.by_row, o.row_e = c.row_e;
+  if (dt != BL_F32 && ranks) o.by_rank = c.by_rank, o.rank_e = c.rank_e;
+  return o;
 }
 
 }  // namespace
@@ -662,49 +987,61 @@ AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool
     return at;
   };
   const int64_t tiles = max_tiles(M, L), rows = tiles * kTile, RP = rank_pad(R), D = backward ? N : K;
+  const CoefBytes b = coef_bytes(M, L, R);
   w.order_off = take(rows * 4);
   w.tile_off = take(tiles * 4);
   w.start_off = take((L + 2) * 4);
   w.count_off = take(M > kSortChunk ? div_up(M, kSortChunk) * (L + 1) * 4 : 0);
+  w.counters = tiles + (backward ? outer_counters(M, R, K) + outer_counters(M, R, N) : 0);
+  w.arrived_off = take(w.counters * 4);
   w.part_off = take(shrink_splits(M, L, R, D) * rows * RP * 4);
-  w.c_off = take(backward ? 2 * rows * RP * 4 : 0);
-  w.sum_off = take(backward ? 2 * std::max(outer_splits(M, R, K) * R * K, outer_splits(M, R, N) * R * N) * 4 : 0);
+  const size_t each[5] = {b.f, b.by_row, b.row_e, backward ? b.by_rank : 0, backward ? b.rank_e : 0};
+  for (int i = 0; i < 5; ++i) w.c_off[i] = take(each[i]);
+  if (backward) {
+    w.hc_off[0] = take(b.f);
+    w.hc_off[3] = take(b.by_rank);
+    w.hc_off[4] = take(b.rank_e);
+    w.sum_off = take(2 * std::max(outer_splits(M, R, K) * R * K, outer_splits(M, R, N) * R * N) * 4);
+  }
   w.total = off;
   return w;
 }
 
 hipError_t launch_adapter_forward(const AdapterForwardArgs& a, char* ws, hipStream_t s) {
   const AdapterRows& r = a.rows;
-  const Scratch w = scratch(adapter_ws(r.M, r.L, r.R, a.K, a.N, false), ws, r);
+  const AdapterWs L = adapter_ws(r.M, r.L, r.R, a.K, a.N, false);
+  const Scratch w = scratch(L, ws, r);
   const int64_t tiles = max_tiles(r.M, r.L);
   const int R = static_cast<int>(r.R), RP = rank_pad(r.R), splits = shrink_splits(r.M, r.L, r.R, a.K);
-  hipError_t e = sort_rows(r, w, s);
+  hipError_t e = sort_rows(r, w, L.counters, s);
   if (e != hipSuccess) return e;
-  e = start_shrink(ShrinkArgs{w.o, a.x, a.K, a.ldx, a.a, R, RP, splits, w.part}, a.dtype, a.dtype, tiles, s);
+  ShrinkArgs p{w.o, a.x, a.K, a.ldx, a.a, R, RP, splits, w.part, w.arrived, a.scale, a.h, nullptr, only(w.c, a.dtype, true, false), {}};
+  e = start_shrink(p, a.dtype, a.dtype, tiles, s);
   if (e != hipSuccess) return e;
-  return start_expand(ExpandArgs{w.o, w.part, splits, R, RP, a.scale, a.h, a.b, a.N, a.base, a.ldbase, a.y, a.ldy},
-                      a.dtype, a.ydtype, tiles, s);
+  return start_expand(ExpandArgs{w.o, w.c, R, RP, a.h, a.b, a.N, a.base, a.ldbase, a.y, a.ldy}, a.dtype, a.ydtype, tiles, s);
 }
 
 hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipStream_t s) {
   const AdapterRows& r = a.rows;
-  const Scratch w = scratch(adapter_ws(r.M, r.L, r.R, a.K, a.N, true), ws, r);
+  const AdapterWs L = adapter_ws(r.M, r.L, r.R, a.K, a.N, true);
+  const Scratch w = scratch(L, ws, r);
   const int64_t tiles = max_tiles(r.M, r.L);
   const int R = static_cast<int>(r.R), RP = rank_pad(r.R), splits = shrink_splits(r.M, r.L, r.R, a.N);
-  float *dh = w.c, *hs = w.c + w.o.rows * RP;
-  hipError_t e = sort_rows(r, w, s);
+  hipError_t e = sort_rows(r, w, L.counters, s);
   if (e != hipSuccess) return e;
-  e = start_shrink(ShrinkArgs{w.o, a.dy, a.N, a.lddy, a.b, R, RP, splits, w.part}, a.dydtype, a.dtype, tiles, s);
+  ShrinkArgs p{w.o, a.dy, a.N, a.lddy, a.b, R, RP, splits, w.part, w.arrived, a.scale, nullptr, a.h,
+               only(w.c, a.dtype, a.dx != nullptr, true), only(w.hc, a.dydtype, false, true)};
+  e = start_shrink(p, a.dydtype, a.dtype, tiles, s);
   if (e != hipSuccess) return e;
-  adapter_finish_kernel<<<static_cast<uint32_t>(tiles), 256, 0, s>>>(FinishArgs{w.o, w.part, splits, R, RP, a.scale, a.h, dh, hs});
-  if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.dx) {
-    e = start_expand(ExpandArgs{w.o, dh, 1, R, RP, nullptr, nullptr, a.a, a.K, a.base, a.ldbase, a.dx, a.lddx}, a.dtype, a.dxdtype, tiles, s);
+    e = start_expand(ExpandArgs{w.o, w.c, R, RP, nullptr, a.a, a.K, a.base, a.ldbase, a.dx, a.lddx}, a.dtype, a.dxdtype, tiles, s);
     if (e != hipSuccess) return e;
   }
-  e = start_outer(OuterArgs{w.o, dh, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.R, a.K), w.sum, a.da, a.add}, a.dtype, s);
+  uint32_t* arrived = w.arrived + tiles;
+  e = start_outer(OuterArgs{w.o, w.c, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.R, a.K), w.sum, arrived, a.da, a.add}, a.dtype, s);
   if (e != hipSuccess) return e;
-  return start_outer(OuterArgs{w.o, hs, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.R, a.N), w.sum, a.db, a.add}, a.dydtype, s);
+  arrived += outer_counters(r.M, r.R, a.K);
+  return start_outer(OuterArgs{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.R, a.N), w.sum, arrived, a.db, a.add}, a.dydtype, s);
 }
 
 }  // namespace bl

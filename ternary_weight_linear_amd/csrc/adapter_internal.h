@@ -60,8 +60,11 @@ struct AdapterWs {
   size_t tile_off;       // int32 [tiles] adapter of each tile, L for rows without one
   size_t start_off;      // int32 [L + 2] first tile of each adapter, of the rows without one, and the end
   size_t count_off;      // int32 [chunks, L + 1], more than one chunk of the sort
+  size_t arrived_off;    // uint32 [counters] workgroups that have ended, cleared by the sort
+  int64_t counters;
   size_t part_off;       // fp32 [splits, rows, RP] partial sums of the products over K or N
-  size_t c_off;          // fp32 [2, rows, RP] dh and the scaled h, sorted (backward)
+  size_t c_off[5];       // the scaled h (forward) or dh, sorted, in each layout that is needed
+  size_t hc_off[5];      // the scaled h (backward)
   size_t sum_off;        // fp32 [2 splits, R, D] partial sums over rows (backward)
   size_t total;
 };
