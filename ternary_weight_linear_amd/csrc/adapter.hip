@@ -337,6 +337,15 @@ __global__ __launch_bounds__(64 * kSortWaves) void adapter_sort_kernel(SortArgs 
   }
 }
 
+// Values that are loaded together, before a branch on one of them: the loads of the others would wait
+// for its answer otherwise.
+__device__ __forceinline__ void loaded() {}
+template <typename... T>
+__device__ __forceinline__ void loaded(int& v, T&... more) {
+  asm volatile("" : "+v"(v));
+  loaded(more...);
+}
+
 struct Sorted {
   const int32_t* order;
   const int32_t* tile;
@@ -352,6 +361,7 @@ struct Sorted {
 // blocks of 64 values in turn, straight from memory in the matrix operands' layout (any order of
 // k serves that both operands share). Where there are several workgroups to a tile, the last one
 // that ends adds their sums, in order, and makes the coefficients.
+constexpr int kShrinkWaves = 8;
 struct ShrinkArgs {
   Sorted o;
   const void* s;
@@ -371,21 +381,21 @@ template <int DT>
 __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int64_t rows, int64_t tiles, int RP, const float* v) {
   const int pitch = RP + 1, tid = threadIdx.x;
   if (c.f)
-    for (int i = tid; i < kTile * RP; i += 256) c.f[t * kTile * RP + i] = v[i / RP * pitch + i % RP];
+    for (int i = tid; i < kTile * RP; i += 64 * kShrinkWaves) c.f[t * kTile * RP + i] = v[i / RP * pitch + i % RP];
   if constexpr (DT != BL_F32) {
     constexpr int P = Parts<DT>::n;
     if (c.by_row) {
-      const int RK = (RP + 31) / 32 * 32, m = tid / 8, q = tid % 8;
+      const int RK = (RP + 31) / 32 * 32, m = tid / 16, q = tid % 16;
       int e = 0;
       if constexpr (DT == BL_F16) {
         uint32_t top = 0;
-        for (int r = q; r < RP; r += 8) top = max(top, finite_bits(v[m * pitch + r]));
+        for (int r = q; r < RP; r += 16) top = max(top, finite_bits(v[m * pitch + r]));
 #pragma unroll
-        for (int off = 1; off < 8; off <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off)));
+        for (int off = 1; off < 16; off <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off)));
         e = scale_exponent(top);
         if (q == 0) c.row_e[t * kTile + m] = -e;
       }
-      for (int k = q; k < RK / 8; k += 8) {
+      for (int k = q; k < RK / 8; k += 16) {
         u32x4 w[3] = {};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -400,7 +410,7 @@ __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int64_t r
     }
     if (c.by_rank) {
       const int q = tid % 4;
-      for (int r = tid / 4; r < RP; r += 64) {
+      for (int r = tid / 4; r < RP; r += 16 * kShrinkWaves) {
         int e = 0;
         if constexpr (DT == BL_F16) {
           uint32_t top = 0;
@@ -428,24 +438,22 @@ __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int64_t r
 
 // CD: the type of what the coefficients will multiply, HD: of what h_in's will.
 template <int SD, int WD, int NR, int CD, int HD>
-__global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
+__global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(ShrinkArgs a) {
   extern __shared__ float lds[];                    // [4][32][16 NR], then [32][RP + 1]
   __shared__ int last;
-  const int t = blockIdx.x;
-  if (t >= a.o.start[a.o.L]) return;
-  const int e = a.o.tile[t];
+  const int t = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
   const int r0 = blockIdx.z * 16 * NR;
   using S = typename Elem<SD>::type;
   using W = typename Elem<WD>::type;
   const int32_t* order = a.o.order + static_cast<int64_t>(t) * kTile;
+  int end = a.o.start[a.o.L], e = a.o.tile[t], some = order[0], m0 = order[c], m1 = order[16 + c];
+  loaded(end, e, some, m0, m1);
+  if (t >= end) return;
+  e = __builtin_amdgcn_readfirstlane(e);
   // places without a row and ranks past the last one repeat another: their sums are not used
-  const S* row[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int m = order[16 * i + c];
-    row[i] = static_cast<const S*>(a.s) + static_cast<int64_t>(m < 0 ? order[0] : m) * a.ld;
-  }
+  const S* row[2] = {static_cast<const S*>(a.s) + static_cast<int64_t>(m0 < 0 ? some : m0) * a.ld,
+                     static_cast<const S*>(a.s) + static_cast<int64_t>(m1 < 0 ? some : m1) * a.ld};
   const W* w[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i)
@@ -482,45 +490,55 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
         }
   };
   const int64_t units = (a.D + 63) / 64, full = a.D / 64;
-  const int64_t u0 = units * blockIdx.y / a.splits, u1 = units * (blockIdx.y + 1) / a.splits, uf = min(u1, full);
+  const int64_t u0 = units * blockIdx.x / a.splits, u1 = units * (blockIdx.x + 1) / a.splits, uf = min(u1, full);
   int64_t u = u0 + wave;
   // two blocks in flight
   Unit v0, v1;
+  constexpr int V = kShrinkWaves;
   if (u < uf) load(v0, u, std::true_type{});
-  for (; u < uf; u += 8) {
-    if (u + 4 < uf) load(v1, u + 4, std::true_type{});
+  for (; u < uf; u += 2 * V) {
+    if (u + V < uf) load(v1, u + V, std::true_type{});
     multiply(v0);
-    if (u + 4 < uf) {
-      if (u + 8 < uf) load(v0, u + 8, std::true_type{});
+    if (u + V < uf) {
+      if (u + 2 * V < uf) load(v0, u + 2 * V, std::true_type{});
       multiply(v1);
     }
   }
-  if (u1 > full && (full - u0) % 4 == wave) {       // the block that is not whole
+  if (u1 > full && (full - u0) % V == wave) {       // the block that is not whole
     load(v0, full, std::false_type{});
     multiply(v0);
   }
 
+  // the sums of waves w and w + 4, then of the four pairs
+  const auto mine = [&](int i, int q, int l) -> float& {
+    return lds[((wave & 3) * kTile + 16 * i + 4 * g + l) * 16 * NR + 16 * q + c];
+  };
+  for (int h = 1; h >= 0; --h) {
+    if (wave / 4 == h) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int q = 0; q < NR; ++q)
+        for (int q = 0; q < NR; ++q)
 #pragma unroll
-      for (int l = 0; l < 4; ++l) lds[(wave * kTile + 16 * i + 4 * g + l) * 16 * NR + 16 * q + c] = acc[i][q][l];
-  __syncthreads();
-  constexpr int kEach = kTile * 16 * NR / 256;
+          for (int l = 0; l < 4; ++l) mine(i, q, l) = h ? acc[i][q][l] : acc[i][q][l] + mine(i, q, l);
+    }
+    __syncthreads();
+  }
+  constexpr int kThreads = 64 * kShrinkWaves;
+  constexpr int kEach = kTile * 16 * NR / kThreads;
   float sum[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int at = tid + 256 * i;
+    const int at = tid + kThreads * i;
     sum[i] = lds[at] + lds[at + kTile * 16 * NR] + lds[at + 2 * kTile * 16 * NR] + lds[at + 3 * kTile * 16 * NR];
   }
   const int groups = a.splits * static_cast<int>(gridDim.z), pitch = a.RP + 1;
   const float f = a.scale ? a.scale[e] : 1.0f;
   if (groups > 1) {
-    float* out = a.part + (blockIdx.y * a.o.rows + static_cast<int64_t>(t) * kTile) * a.RP;
+    float* out = a.part + (blockIdx.x * a.o.rows + static_cast<int64_t>(t) * kTile) * a.RP;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int at = tid + 256 * i, m = at / (16 * NR), r = r0 + at % (16 * NR);
+      const int at = tid + kThreads * i, m = at / (16 * NR), r = r0 + at % (16 * NR);
       if (r < a.RP) atomic_store_agent(out + m * a.RP + r, sum[i]);
     }
     wait_own_memory_ops();
@@ -530,7 +548,7 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
     if (!last) return;
     const float* in = a.part + static_cast<int64_t>(t) * kTile * a.RP;
     const int64_t step = a.o.rows * a.RP;
-    for (int i = tid; i < kTile * a.RP; i += 256) {
+    for (int i = tid; i < kTile * a.RP; i += kThreads) {
       float v = 0.0f;
 #pragma unroll 8
       for (int s = 0; s < a.splits; ++s) v += atomic_load_agent(in + s * step + i);
@@ -540,12 +558,12 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int at = tid + 256 * i, m = at / (16 * NR), r = at % (16 * NR);
+      const int at = tid + kThreads * i, m = at / (16 * NR), r = at % (16 * NR);
       if (r < a.RP) lds[m * pitch + r] = sum[i];
     }
   }
   __syncthreads();
-  for (int i = tid; i < kTile * a.RP; i += 256) {
+  for (int i = tid; i < kTile * a.RP; i += kThreads) {
     const int m = i / a.RP, r = i % a.RP, at = order[m];
     float& v = lds[m * pitch + r];
     const bool there = at >= 0 && r < a.R;
@@ -557,7 +575,7 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
   write_coefs<CD>(a.c, t, a.o.rows, tiles, a.RP, lds);
   if (a.h_in) {
     __syncthreads();
-    for (int i = tid; i < kTile * a.RP; i += 256) {
+    for (int i = tid; i < kTile * a.RP; i += kThreads) {
       const int m = i / a.RP, r = i % a.RP, at = order[m];
       lds[m * pitch + r] = at >= 0 && r < a.R ? a.h_in[static_cast<int64_t>(at) * a.R + r] * f : 0.0f;
     }
@@ -582,110 +600,105 @@ struct ExpandArgs {
   int64_t ldy;
 };
 
-// A wave has 32 rows and 128 columns: lane 16 g + c columns 8 c .. 8 c + 7 of them, so that w, base and y go
+// A wave has 16 rows and 128 columns: lane 16 g + c columns 8 c .. 8 c + 7 of them, so that w, base and y go
 // 16 bytes at a time, and matrix instruction j makes columns 8 c + j.
 template <int WD, int YD, bool WHOLE>
-__device__ __forceinline__ void expand_block(const ExpandArgs& a, int t, int e, int64_t n0, int lane) {
+__device__ __forceinline__ void expand_block(const ExpandArgs& a, int64_t at, const int (&row)[4], int e, int64_t n0, int lane) {
   const int c = lane & 15, g = lane >> 4;
   const int64_t n = n0 + 8 * c;
   const bool none = e >= a.o.L;
-  const int32_t* order = a.o.order + static_cast<int64_t>(t) * kTile;
   using W = typename Elem<WD>::type;
   using Y = typename Elem<YD>::type;
-  int row[2][4];
-  Eight<YD> base[2][4] = {};
+  Eight<YD> base[4] = {};
+  if (a.base) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int l = 0; l < 4; ++l) {
-      row[i][l] = order[16 * i + 4 * g + l];
-      if (a.base && row[i][l] >= 0)
-        base[i][l] = load8<YD, WHOLE>(static_cast<const Y*>(a.base) + row[i][l] * a.ldbase, n, a.N);
-    }
-  f32x4 acc[2][8] = {};
+    for (int l = 0; l < 4; ++l)
+      if (row[l] >= 0) base[l] = load8<YD, WHOLE>(static_cast<const Y*>(a.base) + row[l] * a.ldbase, n, a.N);
+  }
+  int ex[4] = {};
+  f32x4 acc[8] = {};
   if (!none) {
     const W* w = static_cast<const W*>(a.w) + static_cast<int64_t>(e) * a.R * a.N;
     if constexpr (WD == BL_F32) {
-      const float* co = a.c.f + static_cast<int64_t>(t) * kTile * a.RP;
+      const float* co = a.c.f + at * a.RP;
       for (int r0 = 0; r0 < a.RP; r0 += 16) {
         Eight<WD> wv[4];
-        float cv[2][4];
+        float cv[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const int r = r0 + 4 * s + g;
           wv[s] = zero_unless(r < a.R, load8<WD, WHOLE>(w + static_cast<int64_t>(min(r, a.R - 1)) * a.N, n, a.N));
-#pragma unroll
-          for (int i = 0; i < 2; ++i) cv[i][s] = co[(16 * i + c) * a.RP + r];
+          cv[s] = co[c * a.RP + r];
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[i][s], value<WD>(wv[s], j), acc[i][j], 0, 0, 0);
+          for (int j = 0; j < 8; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[s], value<WD>(wv[s], j), acc[j], 0, 0, 0);
       }
     } else {
       constexpr int P = Parts<WD>::n;
       const int RK = (a.RP + 31) / 32 * 32;
-      const uint16_t* co = a.c.by_row + static_cast<int64_t>(t) * kTile * RK;
+      const uint16_t* co = a.c.by_row + at * RK;
+      if constexpr (WD == BL_F16) {
+#pragma unroll
+        for (int l = 0; l < 4; ++l) ex[l] = a.c.row_e[at + 4 * g + l];
+      }
       for (int r0 = 0; r0 < RK; r0 += 32) {
-        u32x4 wv[8], cv[P][2];
+        u32x4 wv[8], cv[P];
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           const int r = r0 + 8 * g + s;
           wv[s] = zero_unless(r < a.R, load8<WD, WHOLE>(w + static_cast<int64_t>(min(r, a.R - 1)) * a.N, n, a.N)).w;
         }
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            cv[p][i] = *reinterpret_cast<const u32x4*>(co + (p * a.o.rows + 16 * i + c) * RK + r0 + 8 * g);
+        for (int p = 0; p < P; ++p) cv[p] = *reinterpret_cast<const u32x4*>(co + (p * a.o.rows + c) * RK + r0 + 8 * g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const u32x4 v = column(wv, j);
 #pragma unroll
-          for (int p = P - 1; p >= 0; --p)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) acc[i][j] = dot32<WD>(cv[p][i], v, acc[i][j]);
+          for (int p = P - 1; p >= 0; --p) acc[j] = dot32<WD>(cv[p], v, acc[j]);
         }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int l = 0; l < 4; ++l) {
+    if (row[l] < 0) continue;
+    float v[8];
 #pragma unroll
-    for (int l = 0; l < 4; ++l) {
-      if (row[i][l] < 0) continue;
-      float v[8];
-      int ex = 0;
-      if constexpr (WD == BL_F16) ex = none ? 0 : a.c.row_e[static_cast<int64_t>(t) * kTile + 16 * i + 4 * g + l];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = acc[i][j][l];
-        if constexpr (WD == BL_F16) v[j] = ldexpf(v[j], ex);
-        if (a.base) v[j] = none ? value<YD>(base[i][l], j) : value<YD>(base[i][l], j) + v[j];
-      }
-      store8<YD, WHOLE>(static_cast<Y*>(a.y) + row[i][l] * a.ldy, n, a.N, v);
+    for (int j = 0; j < 8; ++j) {
+      v[j] = acc[j][l];
+      if constexpr (WD == BL_F16) v[j] = ldexpf(v[j], ex[l]);
+      if (a.base) v[j] = none ? value<YD>(base[l], j) : value<YD>(base[l], j) + v[j];
     }
+    store8<YD, WHOLE>(static_cast<Y*>(a.y) + row[l] * a.ldy, n, a.N, v);
+  }
 }
 
+// A workgroup has a tile and 256 columns, its waves the tile's halves. Tiles come after the columns: rows
+// are read and written whole by workgroups that run together.
 template <int WD, int YD>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
-  const int t = blockIdx.x;
-  if (t >= a.o.start[a.o.L + 1]) return;
-  const int e = a.o.tile[t], lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t at = static_cast<int64_t>(t) * kTile + 16 * (wave & 1);
+  int end = a.o.start[a.o.L + 1], e = a.o.tile[t], first = a.o.order[at], row[4];
+#pragma unroll
+  for (int l = 0; l < 4; ++l) row[l] = a.o.order[at + 4 * (lane >> 4) + l];
+  loaded(end, e, first, row[0], row[1], row[2], row[3]);
+  if (t >= end) return;
   if (e >= a.o.L) {
-    if (a.h && blockIdx.y == 0)
+    if (a.h && blockIdx.x == 0)
       for (int i = threadIdx.x; i < kTile * a.R; i += 256) {
-        const int row = a.o.order[static_cast<int64_t>(t) * kTile + i / a.R];
-        if (row >= 0) a.h[static_cast<int64_t>(row) * a.R + i % a.R] = 0.0f;
+        const int m = a.o.order[static_cast<int64_t>(t) * kTile + i / a.R];
+        if (m >= 0) a.h[static_cast<int64_t>(m) * a.R + i % a.R] = 0.0f;
       }
     if (a.base == a.y) return;
   }
-  const int64_t n0 = (static_cast<int64_t>(blockIdx.y) * 4 + wave) * 128;
-  if (n0 + 128 <= a.N) expand_block<WD, YD, true>(a, t, e, n0, lane);
-  else if (n0 < a.N) expand_block<WD, YD, false>(a, t, e, n0, lane);
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * 2 + (wave >> 1)) * 128;
+  if (first < 0 || n0 >= a.N) return;               // a half without rows
+  if (n0 + 128 <= a.N) expand_block<WD, YD, true>(a, at, row, e, n0, lane);
+  else expand_block<WD, YD, false>(a, at, row, e, n0, lane);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -708,74 +721,101 @@ struct OuterArgs {
   int add;
 };
 
-template <int SD, int NR, bool WHOLE>
-__device__ __forceinline__ void outer_tile(const OuterArgs& a, int64_t t, int64_t d, int r0, int c, int g, f32x4 (&acc)[NR][8]) {
-  using S = typename Elem<SD>::type;
-  const S* s = static_cast<const S*>(a.s);
-  const int32_t* order = a.o.order + t * kTile;
-  if constexpr (SD == BL_F32) {
-    Eight<SD> sv[8];
-    float cv[8][NR];
+// What a wave takes of a tile: lane 16 g + c rows 8 g .. 8 g + 7 (fp32: 4 i + g), columns 8 c .. 8 c + 7.
+template <int SD, int NR>
+struct OuterTile {
+  static constexpr int P = Parts<SD>::n;
+  int row[8];
+  Eight<SD> s[8];
+  u32x4 c[P][NR];                                   // 16-bit parts
+  float f[SD == BL_F32 ? 8 : 1][NR];
+  int ex[SD == BL_F16 ? NR : 1][4];
+
+  __device__ __forceinline__ void load_rows(const OuterArgs& a, int64_t t, int g) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = order[4 * i + g];
-      sv[i] = zero_unless(row >= 0, load8<SD, WHOLE>(s + static_cast<int64_t>(max(row, 0)) * a.ld, d, a.D));
-#pragma unroll
-      for (int q = 0; q < NR; ++q) {
-        const int r = r0 + 16 * q + c;
-        cv[i][q] = r < a.RP ? a.c.f[(t * kTile + 4 * i + g) * a.RP + r] : 0.0f;
-      }
-    }
+    for (int i = 0; i < 8; ++i) row[i] = a.o.order[t * kTile + (SD == BL_F32 ? 4 * i + g : 8 * g + i)];
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const OuterArgs& a, int64_t t, int64_t d, int r0, int c16, int g) {
+    using S = typename Elem<SD>::type;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
+      s[i] = load8<SD, WHOLE>(static_cast<const S*>(a.s) + static_cast<int64_t>(max(row[i], 0)) * a.ld, d, a.D);
+    if constexpr (SD == BL_F32) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int q = 0; q < NR; ++q)
-          acc[q][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[i][q], value<SD>(sv[i], j), acc[q][j], 0, 0, 0);
-  } else {
-    constexpr int P = Parts<SD>::n;
-    const int64_t tiles = a.o.rows / kTile;
-    u32x4 sv[8], cv[P][NR];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = order[8 * g + i];
-      sv[i] = zero_unless(row >= 0, load8<SD, WHOLE>(s + static_cast<int64_t>(max(row, 0)) * a.ld, d, a.D)).w;
-    }
-#pragma unroll
-    for (int q = 0; q < NR; ++q) {
-      const int r = min(r0 + 16 * q + c, a.RP - 1);   // past the last rank: not used
-#pragma unroll
-      for (int p = 0; p < P; ++p) cv[p][q] = *reinterpret_cast<const u32x4*>(a.c.by_rank + ((p * tiles + t) * a.RP + r) * 32 + 8 * g);
-    }
-    if constexpr (SD == BL_F16) {
-      int ex[NR][4];
-#pragma unroll
-      for (int q = 0; q < NR; ++q)
-#pragma unroll
-        for (int l = 0; l < 4; ++l) ex[q][l] = a.c.rank_e[t * a.RP + min(r0 + 16 * q + 4 * g + l, a.RP - 1)];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const u32x4 v = column(sv, j);
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int q = 0; q < NR; ++q) {
-          f32x4 one = {};
+          const int r = r0 + 16 * q + c16;
+          f[i][q] = r < a.RP ? a.c.f[(t * kTile + 4 * i + g) * a.RP + r] : 0.0f;
+        }
+    } else {
+      const int64_t tiles = a.o.rows / kTile;
 #pragma unroll
-          for (int p = P - 1; p >= 0; --p) one = dot32<SD>(cv[p][q], v, one);
+      for (int q = 0; q < NR; ++q) {
+        const int r = min(r0 + 16 * q + c16, a.RP - 1);   // past the last rank: not used
 #pragma unroll
-          for (int l = 0; l < 4; ++l) acc[q][j][l] += ldexpf(one[l], ex[q][l]);
+        for (int p = 0; p < P; ++p) c[p][q] = *reinterpret_cast<const u32x4*>(a.c.by_rank + ((p * tiles + t) * a.RP + r) * 32 + 8 * g);
+        if constexpr (SD == BL_F16) {
+#pragma unroll
+          for (int l = 0; l < 4; ++l) ex[q][l] = a.c.rank_e[t * a.RP + min(r0 + 16 * q + 4 * g + l, a.RP - 1)];
         }
       }
+    }
+  }
+  // A place without a row holds row 0's values, which the sums must not see.
+  __device__ __forceinline__ void multiply(const int (&rows)[8], f32x4 (&acc)[NR][8]) {
+    if constexpr (SD == BL_F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const Eight<SD> v = zero_unless(rows[i] >= 0, s[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int q = 0; q < NR; ++q)
+            acc[q][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[i][q], value<SD>(v, j), acc[q][j], 0, 0, 0);
+      }
     } else {
+      u32x4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = zero_unless(rows[i] >= 0, s[i]).w;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const u32x4 v = column(sv, j);
+        const u32x4 v = column(w, j);
 #pragma unroll
-        for (int p = P - 1; p >= 0; --p)
+        for (int q = 0; q < NR; ++q) {
+          if constexpr (SD == BL_F16) {
+            f32x4 one = {};
 #pragma unroll
-          for (int q = 0; q < NR; ++q) acc[q][j] = dot32<SD>(cv[p][q], v, acc[q][j]);
+            for (int p = P - 1; p >= 0; --p) one = dot32<SD>(c[p][q], v, one);
+#pragma unroll
+            for (int l = 0; l < 4; ++l) acc[q][j][l] += ldexpf(one[l], ex[q][l]);
+          } else {
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p) acc[q][j] = dot32<SD>(c[p][q], v, acc[q][j]);
+          }
+        }
       }
     }
+  }
+};
+
+// Tiles t, t + 4 .. before end, each loaded while the one before is multiplied, its rows' numbers one
+// tile earlier still.
+template <int SD, int NR, bool WHOLE>
+__device__ __forceinline__ void outer_tiles(const OuterArgs& a, int t, int end, int64_t d, int r0, int c, int g, f32x4 (&acc)[NR][8]) {
+  if (t >= end) return;
+  OuterTile<SD, NR> v;
+  int rows[8];
+  v.load_rows(a, t, g);
+  for (;;) {
+    v.template load<WHOLE>(a, t, d, r0, c, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rows[i] = v.row[i];
+    t += 4;
+    if (t < end) v.load_rows(a, t, g);
+    v.multiply(rows, acc);
+    if (t >= end) return;
   }
 }
 
@@ -805,10 +845,8 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a) {
     const int e = a.o.tile[t], first = a.o.start[e], last = a.o.start[e + 1];
     const int end = min(last, t1);
     f32x4 acc[NR][8] = {};
-    if (d0 + 128 <= a.D)
-      for (int i = t + wave; i < end; i += 4) outer_tile<SD, NR, true>(a, i, d0 + 8 * c, r0, c, g, acc);
-    else
-      for (int i = t + wave; i < end; i += 4) outer_tile<SD, NR, false>(a, i, d0 + 8 * c, r0, c, g, acc);
+    if (d0 + 128 <= a.D) outer_tiles<SD, NR, true>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
+    else outer_tiles<SD, NR, false>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
     // the waves' sums, one after another
     for (int w = 0; w < 4; ++w) {
       if (wave == w) {
@@ -856,7 +894,7 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a) {
 // ------------------------------------------------------------------------------------------
 int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
   const int64_t groups = max_tiles(M, L) * div_up(rank_pad(R), 64);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({1024 / groups, div_up(D, 64) / 8, 16})));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({div_up(256, groups), div_up(D, 64) / (2 * kShrinkWaves), 16})));
 }
 int outer_splits(int64_t M, int64_t R, int64_t D) {
   const int64_t groups = div_up(D, 128) * div_up(rank_pad(R), 64);
@@ -920,9 +958,9 @@ hipError_t sort_rows(const AdapterRows& r, const Scratch& w, int64_t counters, h
 
 template <int SD, int WD, int NR, int CD, int HD>
 hipError_t start_shrink_as(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
-  const dim3 grid(static_cast<uint32_t>(tiles), a.splits, static_cast<uint32_t>(div_up(a.RP, 64)));
+  const dim3 grid(a.splits, static_cast<uint32_t>(tiles), static_cast<uint32_t>(div_up(a.RP, 64)));
   const size_t lds = static_cast<size_t>(kTile) * std::max(64 * NR, a.RP + 1) * 4;
-  adapter_shrink_kernel<SD, WD, NR, CD, HD><<<grid, 256, lds, s>>>(a);
+  adapter_shrink_kernel<SD, WD, NR, CD, HD><<<grid, 64 * kShrinkWaves, lds, s>>>(a);
   return hipGetLastError();
 }
 template <int SD, int WD, int CD, int HD>
@@ -942,7 +980,7 @@ hipError_t start_shrink(const ShrinkArgs& a, int sd, int wd, int64_t tiles, hipS
 
 template <int WD, int YD>
 hipError_t start_expand_as(const ExpandArgs& a, int64_t tiles, hipStream_t s) {
-  const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(div_up(a.N, 512)));
+  const dim3 grid(static_cast<uint32_t>(div_up(a.N, 256)), static_cast<uint32_t>(tiles));
   adapter_expand_kernel<WD, YD><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
