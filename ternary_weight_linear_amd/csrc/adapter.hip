@@ -465,6 +465,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
   };
   const auto load = [&](Unit& v, int64_t u, auto whole) {
     const int64_t k = u * 64 + g * 16;
+    __builtin_amdgcn_sched_barrier(0);              // or the loads sink to where they are used
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -472,6 +473,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
 #pragma unroll
       for (int i = 0; i < NR; ++i) v.w[j][i] = load8<WD, decltype(whole)::value>(w[i], k + 8 * j, a.D);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   const auto multiply = [&](const Unit& v) {
 #pragma unroll
@@ -491,17 +493,31 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
   };
   const int64_t units = (a.D + 63) / 64, full = a.D / 64;
   const int64_t u0 = units * blockIdx.x / a.splits, u1 = units * (blockIdx.x + 1) / a.splits, uf = min(u1, full);
-  int64_t u = u0 + wave;
-  // two blocks in flight
-  Unit v0, v1;
   constexpr int V = kShrinkWaves;
-  if (u < uf) load(v0, u, std::true_type{});
-  for (; u < uf; u += 2 * V) {
-    if (u + V < uf) load(v1, u + V, std::true_type{});
-    multiply(v0);
-    if (u + V < uf) {
-      if (u + 2 * V < uf) load(v0, u + 2 * V, std::true_type{});
+  int64_t u = u0 + wave;
+  int64_t n = u < uf ? (uf - u + V - 1) / V : 0;    // whole blocks of this wave
+  Unit v0;
+  if constexpr (NR > 2 || SD == BL_F32) {
+    for (; n; --n, u += V) {
+      load(v0, u, std::true_type{});
+      multiply(v0);
+    }
+  } else if (n) {
+    // two blocks in flight; no load is under a condition of its own, so each wait is for the older ones alone
+    Unit v1;
+    load(v0, u, std::true_type{});
+    for (; n > 2; n -= 2, u += 2 * V) {
+      load(v1, u + V, std::true_type{});
+      multiply(v0);
+      load(v0, u + 2 * V, std::true_type{});
       multiply(v1);
+    }
+    if (n == 2) {
+      load(v1, u + V, std::true_type{});
+      multiply(v0);
+      multiply(v1);
+    } else {
+      multiply(v0);
     }
   }
   if (u1 > full && (full - u0) % V == wave) {       // the block that is not whole
