@@ -191,6 +191,14 @@ struct Coefs {
 // ------------------------------------------------------------------------------------------
 // rows sorted by adapter
 // ------------------------------------------------------------------------------------------
+// A tile's word: its adapter (L: none), which of the adapter's tiles it is, modulo 16, and how many follow
+// it, up to 15. So a kernel can take several tiles of an adapter at a time: the workgroups of the others
+// end at once.
+__host__ __device__ __forceinline__ int tile_word(int e, int pos, int left) { return e | (pos & 15) << 16 | (left < 15 ? left : 15) << 20; }
+__device__ __forceinline__ int tile_adapter(int w) { return w & 0xFFFF; }
+__device__ __forceinline__ int tile_pos(int w) { return w >> 16 & 15; }
+__device__ __forceinline__ int tile_left(int w) { return w >> 20; }
+
 // The sort is stable, so that sums over an adapter's rows have one order. A chunk of up to 8192 rows
 // per workgroup; more than one chunk: a first launch counts, the second places. Bucket L holds the
 // rows without an adapter. Each bucket starts a tile of its own. The counters of the call's later
@@ -328,7 +336,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void adapter_sort_kernel(SortArgs 
         if (start[mid] <= t) lo = mid;
         else hi = mid - 1;
       }
-      a.tile[t] = lo;
+      a.tile[t] = tile_word(lo, t - start[lo], start[lo + 1] - 1 - t);
     }
     for (int i = threadIdx.x; i < B * kTile; i += blockDim.x) {
       const int b = i / kTile, p = total[b] + i % kTile;
@@ -361,13 +369,13 @@ struct Sorted {
 // blocks of 64 values in turn, straight from memory in the matrix operands' layout (any order of
 // k serves that both operands share). Where there are several workgroups to a tile, the last one
 // that ends adds their sums, in order, and makes the coefficients.
-constexpr int kShrinkWaves = 8;
+constexpr int kShrinkWaves = 4;
 struct ShrinkArgs {
   Sorted o;
   const void* s;
   int64_t D, ld;
   const void* w;          // [L, R, D]
-  int R, RP, splits;
+  int R, RP, splits, by_chip;
   float* part;            // [splits, rows, RP]
   uint32_t* arrived;      // [max_tiles]
   const float* scale;     // [L] or null
@@ -385,17 +393,17 @@ __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int64_t r
   if constexpr (DT != BL_F32) {
     constexpr int P = Parts<DT>::n;
     if (c.by_row) {
-      const int RK = (RP + 31) / 32 * 32, m = tid / 16, q = tid % 16;
+      const int RK = (RP + 31) / 32 * 32, m = tid / 8, q = tid % 8;
       int e = 0;
       if constexpr (DT == BL_F16) {
         uint32_t top = 0;
-        for (int r = q; r < RP; r += 16) top = max(top, finite_bits(v[m * pitch + r]));
+        for (int r = q; r < RP; r += 8) top = max(top, finite_bits(v[m * pitch + r]));
 #pragma unroll
-        for (int off = 1; off < 16; off <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off)));
+        for (int off = 1; off < 8; off <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off)));
         e = scale_exponent(top);
         if (q == 0) c.row_e[t * kTile + m] = -e;
       }
-      for (int k = q; k < RK / 8; k += 16) {
+      for (int k = q; k < RK / 8; k += 8) {
         u32x4 w[3] = {};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -441,16 +449,25 @@ template <int SD, int WD, int NR, int CD, int HD>
 __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(ShrinkArgs a) {
   extern __shared__ float lds[];                    // [4][32][16 NR], then [32][RP + 1]
   __shared__ int last;
-  const int t = blockIdx.y;
+  constexpr int V = kShrinkWaves, kThreads = 64 * V;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
   const int r0 = blockIdx.z * 16 * NR;
   using S = typename Elem<SD>::type;
   using W = typename Elem<WD>::type;
+  int end = a.o.start[a.o.L], t = blockIdx.y, part = blockIdx.x;
+  if (a.by_chip) {
+    // workgroups go to the eight chips in turn: each gets a run of the tiles, and so few adapters
+    const int all = end * a.splits, per = (all + 7) / 8, id = t * a.splits + part;
+    const int mine = id % 8 * per + id / 8;
+    if (id / 8 >= per || mine >= all) return;
+    t = mine / a.splits;
+    part = mine % a.splits;
+  }
   const int32_t* order = a.o.order + static_cast<int64_t>(t) * kTile;
-  int end = a.o.start[a.o.L], e = a.o.tile[t], some = order[0], m0 = order[c], m1 = order[16 + c];
-  loaded(end, e, some, m0, m1);
+  int word = a.o.tile[t], some = order[0], m0 = order[c], m1 = order[16 + c];
+  loaded(end, word, some, m0, m1);
   if (t >= end) return;
-  e = __builtin_amdgcn_readfirstlane(e);
+  const int e = tile_adapter(__builtin_amdgcn_readfirstlane(word));
   // places without a row and ranks past the last one repeat another: their sums are not used
   const S* row[2] = {static_cast<const S*>(a.s) + static_cast<int64_t>(m0 < 0 ? some : m0) * a.ld,
                      static_cast<const S*>(a.s) + static_cast<int64_t>(m1 < 0 ? some : m1) * a.ld};
@@ -459,11 +476,11 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
   for (int i = 0; i < NR; ++i)
     w[i] = static_cast<const W*>(a.w) + (static_cast<int64_t>(e) * a.R + min(r0 + 16 * i + c, a.R - 1)) * a.D;
   f32x4 acc[2][NR] = {};
-  struct Unit {
+  struct Block {
     Eight<SD> s[2][2];
     Eight<WD> w[2][NR];
   };
-  const auto load = [&](Unit& v, int64_t u, auto whole) {
+  const auto load = [&](Block& v, int64_t u, auto whole) {
     const int64_t k = u * 64 + g * 16;
     __builtin_amdgcn_sched_barrier(0);              // or the loads sink to where they are used
 #pragma unroll
@@ -475,7 +492,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  const auto multiply = [&](const Unit& v) {
+  const auto multiply = [&](const Block& v) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -492,19 +509,18 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
         }
   };
   const int64_t units = (a.D + 63) / 64, full = a.D / 64;
-  const int64_t u0 = units * blockIdx.x / a.splits, u1 = units * (blockIdx.x + 1) / a.splits, uf = min(u1, full);
-  constexpr int V = kShrinkWaves;
+  const int64_t u0 = units * part / a.splits, u1 = units * (part + 1) / a.splits, uf = min(u1, full);
   int64_t u = u0 + wave;
   int64_t n = u < uf ? (uf - u + V - 1) / V : 0;    // whole blocks of this wave
-  Unit v0;
-  if constexpr (NR > 2 || SD == BL_F32) {
+  Block v0;
+  if constexpr (SD == BL_F32) {
     for (; n; --n, u += V) {
       load(v0, u, std::true_type{});
       multiply(v0);
     }
   } else if (n) {
     // two blocks in flight; no load is under a condition of its own, so each wait is for the older ones alone
-    Unit v1;
+    Block v1;
     load(v0, u, std::true_type{});
     for (; n > 2; n -= 2, u += 2 * V) {
       load(v1, u + V, std::true_type{});
@@ -525,22 +541,14 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
     multiply(v0);
   }
 
-  // the sums of waves w and w + 4, then of the four pairs
-  const auto mine = [&](int i, int q, int l) -> float& {
-    return lds[((wave & 3) * kTile + 16 * i + 4 * g + l) * 16 * NR + 16 * q + c];
-  };
-  for (int h = 1; h >= 0; --h) {
-    if (wave / 4 == h) {
+  // the waves' sums
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int q = 0; q < NR; ++q)
+    for (int q = 0; q < NR; ++q)
 #pragma unroll
-          for (int l = 0; l < 4; ++l) mine(i, q, l) = h ? acc[i][q][l] : acc[i][q][l] + mine(i, q, l);
-    }
-    __syncthreads();
-  }
-  constexpr int kThreads = 64 * kShrinkWaves;
+      for (int l = 0; l < 4; ++l) lds[(wave * kTile + 16 * i + 4 * g + l) * 16 * NR + 16 * q + c] = acc[i][q][l];
+  __syncthreads();
   constexpr int kEach = kTile * 16 * NR / kThreads;
   float sum[kEach];
 #pragma unroll
@@ -551,37 +559,52 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
   const int groups = a.splits * static_cast<int>(gridDim.z), pitch = a.RP + 1;
   const float f = a.scale ? a.scale[e] : 1.0f;
   if (groups > 1) {
-    float* out = a.part + (blockIdx.x * a.o.rows + static_cast<int64_t>(t) * kTile) * a.RP;
+    float* out = a.part + (part * a.o.rows + static_cast<int64_t>(t) * kTile) * a.RP;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int at = tid + kThreads * i, m = at / (16 * NR), r = r0 + at % (16 * NR);
-      if (r < a.RP) atomic_store_agent(out + m * a.RP + r, sum[i]);
+      const int at = tid + kThreads * i, r = r0 + at % (16 * NR);
+      if (r < a.RP) atomic_store_agent(out + at / (16 * NR) * a.RP + r, sum[i]);
     }
     wait_own_memory_ops();
     __syncthreads();
     if (tid == 0) last = arrive_agent(a.arrived + t) + 1 == static_cast<uint32_t>(groups);
     __syncthreads();
     if (!last) return;
+    // four splits' values in flight at a time, those of up to eight places
     const float* in = a.part + static_cast<int64_t>(t) * kTile * a.RP;
     const int64_t step = a.o.rows * a.RP;
-    for (int i = tid; i < kTile * a.RP; i += kThreads) {
-      float v = 0.0f;
-#pragma unroll 8
-      for (int s = 0; s < a.splits; ++s) v += atomic_load_agent(in + s * step + i);
-      lds[i / a.RP * pitch + i % a.RP] = v;
+    for (int i0 = tid; i0 < kTile * a.RP; i0 += 8 * kThreads) {
+      float v[8] = {};
+      for (int s0 = 0; s0 < a.splits; s0 += 4) {
+        float p[4][8];
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            p[s][i] = atomic_load_agent(in + min(s0 + s, a.splits - 1) * step + min(i0 + i * kThreads, kTile * a.RP - 1));
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += s0 + s < a.splits ? p[s][i] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = i0 + i * kThreads;
+        if (at < kTile * a.RP) lds[at / a.RP * pitch + at % a.RP] = v[i];
+      }
     }
   } else {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int at = tid + kThreads * i, m = at / (16 * NR), r = at % (16 * NR);
-      if (r < a.RP) lds[m * pitch + r] = sum[i];
+      const int at = tid + kThreads * i, r = at % (16 * NR);
+      if (r < a.RP) lds[at / (16 * NR) * pitch + r] = sum[i];
     }
   }
   __syncthreads();
   for (int i = tid; i < kTile * a.RP; i += kThreads) {
-    const int m = i / a.RP, r = i % a.RP, at = order[m];
-    float& v = lds[m * pitch + r];
+    const int r = i % a.RP, at = order[i / a.RP];
+    float& v = lds[i / a.RP * pitch + r];
     const bool there = at >= 0 && r < a.R;
     if (there && a.h_out) a.h_out[static_cast<int64_t>(at) * a.R + r] = v;
     v = there ? v * f : 0.0f;
@@ -592,8 +615,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
   if (a.h_in) {
     __syncthreads();
     for (int i = tid; i < kTile * a.RP; i += kThreads) {
-      const int m = i / a.RP, r = i % a.RP, at = order[m];
-      lds[m * pitch + r] = at >= 0 && r < a.R ? a.h_in[static_cast<int64_t>(at) * a.R + r] * f : 0.0f;
+      const int r = i % a.RP, at = order[i / a.RP];
+      lds[i / a.RP * pitch + r] = at >= 0 && r < a.R ? a.h_in[static_cast<int64_t>(at) * a.R + r] * f : 0.0f;
     }
     __syncthreads();
     write_coefs<HD>(a.hc, t, a.o.rows, tiles, a.RP, lds);
@@ -614,69 +637,23 @@ struct ExpandArgs {
   int64_t ldbase;
   void* y;
   int64_t ldy;
+  int tiles;              // 1, 2 or 4
 };
 
-// A wave has 16 rows and 128 columns: lane 16 g + c columns 8 c .. 8 c + 7 of them, so that w, base and y go
-// 16 bytes at a time, and matrix instruction j makes columns 8 c + j.
-template <int WD, int YD, bool WHOLE>
-__device__ __forceinline__ void expand_block(const ExpandArgs& a, int64_t at, const int (&row)[4], int e, int64_t n0, int lane) {
-  const int c = lane & 15, g = lane >> 4;
-  const int64_t n = n0 + 8 * c;
-  const bool none = e >= a.o.L;
-  using W = typename Elem<WD>::type;
+// A wave has 16 rows and 128 columns at a time: lane 16 g + c columns 8 c .. 8 c + 7 of them, so that w, base and
+// y go 16 bytes at a time, and matrix instruction j makes columns 8 c + j.
+template <int YD, bool WHOLE>
+__device__ __forceinline__ void load_base(const ExpandArgs& a, const int (&row)[4], int64_t n, Eight<YD> (&base)[4]) {
   using Y = typename Elem<YD>::type;
-  Eight<YD> base[4] = {};
-  if (a.base) {
+  if (!a.base) return;
 #pragma unroll
-    for (int l = 0; l < 4; ++l)
-      if (row[l] >= 0) base[l] = load8<YD, WHOLE>(static_cast<const Y*>(a.base) + row[l] * a.ldbase, n, a.N);
-  }
-  int ex[4] = {};
-  f32x4 acc[8] = {};
-  if (!none) {
-    const W* w = static_cast<const W*>(a.w) + static_cast<int64_t>(e) * a.R * a.N;
-    if constexpr (WD == BL_F32) {
-      const float* co = a.c.f + at * a.RP;
-      for (int r0 = 0; r0 < a.RP; r0 += 16) {
-        Eight<WD> wv[4];
-        float cv[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int r = r0 + 4 * s + g;
-          wv[s] = zero_unless(r < a.R, load8<WD, WHOLE>(w + static_cast<int64_t>(min(r, a.R - 1)) * a.N, n, a.N));
-          cv[s] = co[c * a.RP + r];
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[s], value<WD>(wv[s], j), acc[j], 0, 0, 0);
-      }
-    } else {
-      constexpr int P = Parts<WD>::n;
-      const int RK = (a.RP + 31) / 32 * 32;
-      const uint16_t* co = a.c.by_row + at * RK;
-      if constexpr (WD == BL_F16) {
-#pragma unroll
-        for (int l = 0; l < 4; ++l) ex[l] = a.c.row_e[at + 4 * g + l];
-      }
-      for (int r0 = 0; r0 < RK; r0 += 32) {
-        u32x4 wv[8], cv[P];
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const int r = r0 + 8 * g + s;
-          wv[s] = zero_unless(r < a.R, load8<WD, WHOLE>(w + static_cast<int64_t>(min(r, a.R - 1)) * a.N, n, a.N)).w;
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p) cv[p] = *reinterpret_cast<const u32x4*>(co + (p * a.o.rows + c) * RK + r0 + 8 * g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const u32x4 v = column(wv, j);
-#pragma unroll
-          for (int p = P - 1; p >= 0; --p) acc[j] = dot32<WD>(cv[p], v, acc[j]);
-        }
-      }
-    }
-  }
+  for (int l = 0; l < 4; ++l)                       // a place without a row reads row 0
+    base[l] = load8<YD, WHOLE>(static_cast<const Y*>(a.base) + max(row[l], 0) * a.ldbase, n, a.N);
+}
+template <int WD, int YD, bool WHOLE>
+__device__ __forceinline__ void store_rows(const ExpandArgs& a, const int (&row)[4], int64_t n, const Eight<YD> (&base)[4],
+                                           const f32x4 (&acc)[8], const int (&ex)[4]) {
+  using Y = typename Elem<YD>::type;
 #pragma unroll
   for (int l = 0; l < 4; ++l) {
     if (row[l] < 0) continue;
@@ -685,36 +662,156 @@ __device__ __forceinline__ void expand_block(const ExpandArgs& a, int64_t at, co
     for (int j = 0; j < 8; ++j) {
       v[j] = acc[j][l];
       if constexpr (WD == BL_F16) v[j] = ldexpf(v[j], ex[l]);
-      if (a.base) v[j] = none ? value<YD>(base[l], j) : value<YD>(base[l], j) + v[j];
+      if (a.base) v[j] = value<YD>(base[l], j) + v[j];
     }
     store8<YD, WHOLE>(static_cast<Y*>(a.y) + row[l] * a.ldy, n, a.N, v);
   }
 }
+// Rows without an adapter are base's.
+template <int YD, bool WHOLE>
+__device__ __forceinline__ void copy_rows(const ExpandArgs& a, const int (&row)[4], int64_t n) {
+  using Y = typename Elem<YD>::type;
+  Eight<YD> base[4] = {};
+  load_base<YD, WHOLE>(a, row, n, base);
+#pragma unroll
+  for (int l = 0; l < 4; ++l) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = value<YD>(base[l], j);
+    if (row[l] >= 0) store8<YD, WHOLE>(static_cast<Y*>(a.y) + row[l] * a.ldy, n, a.N, v);
+  }
+}
 
-// A workgroup has a tile and 256 columns, its waves the tile's halves. Tiles come after the columns: rows
-// are read and written whole by workgroups that run together.
-template <int WD, int YD>
+// The rows of up to `count` tiles. KB blocks of 32 ranks of w stay in registers over them; 0: any rank, w is
+// loaded again for each tile (fp32: always so).
+template <int WD, int YD, int KB, bool WHOLE>
+__device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, int count, int e, int64_t n0, int lane) {
+  const int c = lane & 15, g = lane >> 4;
+  const int64_t n = n0 + 8 * c;
+  using W = typename Elem<WD>::type;
+  constexpr int P = Parts<WD>::n;
+  const W* w = static_cast<const W*>(a.w) + static_cast<int64_t>(e) * a.R * a.N;
+  const int RK = (a.RP + 31) / 32 * 32;
+  int row[4], ex[4] = {};
+  const auto rows = [&](int64_t p, int (&r)[4]) {
+#pragma unroll
+    for (int l = 0; l < 4; ++l) r[l] = a.o.order[p + 4 * g + l];
+  };
+  const auto load_w = [&](int r0, u32x4 (&v)[8]) {  // 32 ranks: rows 8 g .. 8 g + 7 of them
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int r = r0 + 8 * g + s;
+      if constexpr (WD != BL_F32)
+        v[s] = zero_unless(r < a.R, load8<WD, WHOLE>(w + static_cast<int64_t>(min(r, a.R - 1)) * a.N, n, a.N)).w;
+    }
+  };
+  Eight<YD> base[4] = {};
+  rows(at, row);
+  load_base<YD, WHOLE>(a, row, n, base);
+  u32x4 wv[KB ? KB : 1][8];                         // as operands: column j of block k
+  if constexpr (KB > 0) {
+    u32x4 raw[KB][8];
+#pragma unroll
+    for (int k = 0; k < KB; ++k) load_w(32 * k, raw[k]);
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wv[k][j] = column(raw[k], j);
+  }
+  for (int i = 0; i < count; ++i, at += kTile) {
+    f32x4 acc[8] = {};
+    int next[4];
+    rows(i + 1 < count ? at + kTile : at, next);
+    if constexpr (WD == BL_F16) {
+#pragma unroll
+      for (int l = 0; l < 4; ++l) ex[l] = a.c.row_e[at + 4 * g + l];
+    }
+    if constexpr (WD == BL_F32) {
+      const float* co = a.c.f + at * a.RP;
+      for (int r0 = 0; r0 < a.RP; r0 += 16) {
+        Eight<WD> v[4];
+        float cv[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int r = r0 + 4 * s + g;
+          v[s] = zero_unless(r < a.R, load8<WD, WHOLE>(w + static_cast<int64_t>(min(r, a.R - 1)) * a.N, n, a.N));
+          cv[s] = co[c * a.RP + r];
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[s], value<WD>(v[s], j), acc[j], 0, 0, 0);
+      }
+    } else {
+      const uint16_t* co = a.c.by_row + at * RK;
+      if constexpr (KB > 0) {
+        u32x4 cv[KB][P];
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+          for (int p = 0; p < P; ++p) cv[k][p] = *reinterpret_cast<const u32x4*>(co + (p * a.o.rows + c) * RK + 32 * k + 8 * g);
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = dot32<WD>(cv[k][p], wv[k][j], acc[j]);
+      } else {
+        for (int r0 = 0; r0 < RK; r0 += 32) {
+          u32x4 raw[8], cv[P];
+          load_w(r0, raw);
+#pragma unroll
+          for (int p = 0; p < P; ++p) cv[p] = *reinterpret_cast<const u32x4*>(co + (p * a.o.rows + c) * RK + r0 + 8 * g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const u32x4 v = column(raw, j);
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p) acc[j] = dot32<WD>(cv[p], v, acc[j]);
+          }
+        }
+      }
+    }
+    Eight<YD> more[4] = {};
+    load_base<YD, WHOLE>(a, next, n, more);
+    store_rows<WD, YD, WHOLE>(a, row, n, base, acc, ex);
+#pragma unroll
+    for (int l = 0; l < 4; ++l) {
+      row[l] = next[l];
+      base[l] = more[l];
+    }
+  }
+}
+
+// A workgroup has up to `tiles` tiles and 256 columns, its waves the tiles' halves. Tiles come after the
+// columns: rows are read and written whole by workgroups that run together.
+template <int WD, int YD, int KB>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
   const int t = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t at = static_cast<int64_t>(t) * kTile + 16 * (wave & 1);
-  int end = a.o.start[a.o.L + 1], e = a.o.tile[t], first = a.o.order[at], row[4];
+  int end = a.o.start[a.o.L + 1], word = a.o.tile[t], first = a.o.order[at], row[4];
 #pragma unroll
   for (int l = 0; l < 4; ++l) row[l] = a.o.order[at + 4 * (lane >> 4) + l];
-  loaded(end, e, first, row[0], row[1], row[2], row[3]);
+  loaded(end, word, first, row[0], row[1], row[2], row[3]);
   if (t >= end) return;
+  word = __builtin_amdgcn_readfirstlane(word);
+  const int e = tile_adapter(word);
+  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * 2 + (wave >> 1)) * 128, n = n0 + 8 * (lane & 15);
   if (e >= a.o.L) {
     if (a.h && blockIdx.x == 0)
       for (int i = threadIdx.x; i < kTile * a.R; i += 256) {
         const int m = a.o.order[static_cast<int64_t>(t) * kTile + i / a.R];
         if (m >= 0) a.h[static_cast<int64_t>(m) * a.R + i % a.R] = 0.0f;
       }
-    if (a.base == a.y) return;
+    if (a.base == a.y || n0 >= a.N) return;
+    if (n0 + 128 <= a.N) copy_rows<YD, true>(a, row, n);
+    else copy_rows<YD, false>(a, row, n);
+    return;
   }
-  e = __builtin_amdgcn_readfirstlane(e);
-  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * 2 + (wave >> 1)) * 128;
-  if (first < 0 || n0 >= a.N) return;               // a half without rows
-  if (n0 + 128 <= a.N) expand_block<WD, YD, true>(a, at, row, e, n0, lane);
-  else expand_block<WD, YD, false>(a, at, row, e, n0, lane);
+  if (tile_pos(word) % a.tiles) return;
+  const int count = min(a.tiles, tile_left(word) + 1);
+  if (n0 >= a.N || (count == 1 && first < 0)) return;   // a half without rows
+  if (n0 + 128 <= a.N) expand_tiles<WD, YD, KB, true>(a, at, count, e, n0, lane);
+  else expand_tiles<WD, YD, KB, false>(a, at, count, e, n0, lane);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -858,7 +955,7 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a) {
 
   const int t1 = static_cast<int>(tiles * (blockIdx.y + 1) / a.splits);
   for (int t = static_cast<int>(tiles * blockIdx.y / a.splits); t < t1;) {
-    const int e = a.o.tile[t], first = a.o.start[e], last = a.o.start[e + 1];
+    const int e = tile_adapter(a.o.tile[t]), first = a.o.start[e], last = a.o.start[e + 1];
     const int end = min(last, t1);
     f32x4 acc[NR][8] = {};
     if (d0 + 128 <= a.D) outer_tiles<SD, NR, true>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
@@ -908,10 +1005,14 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a) {
 // ------------------------------------------------------------------------------------------
 // launches
 // ------------------------------------------------------------------------------------------
+// Splits for about 448 workgroups: the 512 that the chip holds at once of the largest rank, less
+// what an uneven spread over its CUs needs (a workgroup that starts after the others doubles the time).
 int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
   const int64_t groups = max_tiles(M, L) * div_up(rank_pad(R), 64);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({div_up(256, groups), div_up(D, 64) / (2 * kShrinkWaves), 16})));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({448 / groups, div_up(D, 64) / (2 * kShrinkWaves), 16})));
 }
+int expand_tiles_of(int64_t M) { return M >= 2048 ? 4 : 1; }
+int by_chip(const AdapterRows& r) { return r.M >= 64 * kTile; }
 int outer_splits(int64_t M, int64_t R, int64_t D) {
   const int64_t groups = div_up(D, 128) * div_up(rank_pad(R), 64);
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({512 / groups, div_up(M, 4 * kTile), 32})));
@@ -974,7 +1075,7 @@ hipError_t sort_rows(const AdapterRows& r, const Scratch& w, int64_t counters, h
 
 template <int SD, int WD, int NR, int CD, int HD>
 hipError_t start_shrink_as(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
-  const dim3 grid(a.splits, static_cast<uint32_t>(tiles), static_cast<uint32_t>(div_up(a.RP, 64)));
+  const dim3 grid(a.splits, static_cast<uint32_t>(tiles) + (a.by_chip ? 7 : 0), static_cast<uint32_t>(div_up(a.RP, 64)));
   const size_t lds = static_cast<size_t>(kTile) * std::max(64 * NR, a.RP + 1) * 4;
   adapter_shrink_kernel<SD, WD, NR, CD, HD><<<grid, 64 * kShrinkWaves, lds, s>>>(a);
   return hipGetLastError();
@@ -997,7 +1098,9 @@ hipError_t start_shrink(const ShrinkArgs& a, int sd, int wd, int64_t tiles, hipS
 template <int WD, int YD>
 hipError_t start_expand_as(const ExpandArgs& a, int64_t tiles, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(div_up(a.N, 256)), static_cast<uint32_t>(tiles));
-  adapter_expand_kernel<WD, YD><<<grid, 256, 0, s>>>(a);
+  if (WD == BL_F32 || a.RP > 64) adapter_expand_kernel<WD, YD, 0><<<grid, 256, 0, s>>>(a);
+  else if (a.RP > 32) adapter_expand_kernel<WD, YD, WD == BL_F32 ? 0 : 2><<<grid, 256, 0, s>>>(a);
+  else adapter_expand_kernel<WD, YD, WD == BL_F32 ? 0 : 1><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 // yd is wd, or fp32.
@@ -1069,10 +1172,10 @@ hipError_t launch_adapter_forward(const AdapterForwardArgs& a, char* ws, hipStre
   const int R = static_cast<int>(r.R), RP = rank_pad(r.R), splits = shrink_splits(r.M, r.L, r.R, a.K);
   hipError_t e = sort_rows(r, w, L.counters, s);
   if (e != hipSuccess) return e;
-  ShrinkArgs p{w.o, a.x, a.K, a.ldx, a.a, R, RP, splits, w.part, w.arrived, a.scale, a.h, nullptr, only(w.c, a.dtype, true, false), {}};
+  ShrinkArgs p{w.o, a.x, a.K, a.ldx, a.a, R, RP, splits, by_chip(r), w.part, w.arrived, a.scale, a.h, nullptr, only(w.c, a.dtype, true, false), {}};
   e = start_shrink(p, a.dtype, a.dtype, tiles, s);
   if (e != hipSuccess) return e;
-  return start_expand(ExpandArgs{w.o, w.c, R, RP, a.h, a.b, a.N, a.base, a.ldbase, a.y, a.ldy}, a.dtype, a.ydtype, tiles, s);
+  return start_expand(ExpandArgs{w.o, w.c, R, RP, a.h, a.b, a.N, a.base, a.ldbase, a.y, a.ldy, expand_tiles_of(r.M)}, a.dtype, a.ydtype, tiles, s);
 }
 
 hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipStream_t s) {
@@ -1083,12 +1186,12 @@ hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipSt
   const int R = static_cast<int>(r.R), RP = rank_pad(r.R), splits = shrink_splits(r.M, r.L, r.R, a.N);
   hipError_t e = sort_rows(r, w, L.counters, s);
   if (e != hipSuccess) return e;
-  ShrinkArgs p{w.o, a.dy, a.N, a.lddy, a.b, R, RP, splits, w.part, w.arrived, a.scale, nullptr, a.h,
+  ShrinkArgs p{w.o, a.dy, a.N, a.lddy, a.b, R, RP, splits, by_chip(r), w.part, w.arrived, a.scale, nullptr, a.h,
                only(w.c, a.dtype, a.dx != nullptr, true), only(w.hc, a.dydtype, false, true)};
   e = start_shrink(p, a.dydtype, a.dtype, tiles, s);
   if (e != hipSuccess) return e;
   if (a.dx) {
-    e = start_expand(ExpandArgs{w.o, w.c, R, RP, nullptr, a.a, a.K, a.base, a.ldbase, a.dx, a.lddx}, a.dtype, a.dxdtype, tiles, s);
+    e = start_expand(ExpandArgs{w.o, w.c, R, RP, nullptr, a.a, a.K, a.base, a.ldbase, a.dx, a.lddx, expand_tiles_of(r.M)}, a.dtype, a.dxdtype, tiles, s);
     if (e != hipSuccess) return e;
   }
   uint32_t* arrived = w.arrived + tiles;
