@@ -73,6 +73,20 @@ __device__ __forceinline__ Eight<DT> load8(const typename Elem<DT>::type* row, i
   }
   return v;
 }
+// A piece of 16 bytes of a row, its first value at `at`; values from n on are 0.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ u32x4 load16(const typename Elem<DT>::type* row, int64_t at, int64_t n) {
+  constexpr int V = 16 / sizeof(*row);
+  if (WHOLE || at + V <= n) return *reinterpret_cast<const u32x4_any*>(row + at);
+  u32x4 v{};
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (at + j < n) {
+      if constexpr (DT == BL_F32) v[j] = __float_as_uint(row[at + j]);
+      else v[j / 2] |= static_cast<uint32_t>(row[at + j]) << (16 * (j & 1));
+    }
+  return v;
+}
 template <int DT>
 __device__ __forceinline__ Eight<DT> zero_unless(bool keep, Eight<DT> v) {
   return keep ? v : Eight<DT>{};
@@ -177,9 +191,10 @@ __device__ __forceinline__ void split(float v, int e, uint16_t (&part)[3]) {
   }
 }
 
-// Coefficients of the sorted rows, in what the passes after it need of: fp32 [rows, RP]; parts row by
-// row [n, rows, RK] (RK: R up to 32) with exponents [rows]; parts by columns [n, tiles, RP, 32] with exponents
-// [tiles, RP]. What a row or a rank has not is 0.
+// Coefficients of the sorted rows, in what the passes after it need of: fp32 [rows, RP]; parts as operands
+// whose rows are rows, [rows / 16, RK / 32, n, 64 lanes, 8] (RK: R up to 32), with exponents [rows]; parts as operands
+// whose rows are ranks, [tiles, RP / 16, n, 64 lanes, 8], with exponents [tiles, RP]. So an operand is
+// 1 KB in one piece. What a row or a rank has not is 0.
 struct Coefs {
   float* f;
   uint16_t* by_row;
@@ -366,8 +381,9 @@ struct Sorted {
 // shrink: sums[row, r] = sum over k of S[row, k] w[e, r, k], and the coefficients made of them
 // ------------------------------------------------------------------------------------------
 // A workgroup has a tile of 32 rows, up to 64 ranks and one of the splits of k; its waves take
-// blocks of 64 values in turn, straight from memory in the matrix operands' layout (any order of
-// k serves that both operands share). Where there are several workgroups to a tile, the last one
+// blocks of 128 bytes of a row in turn. An operand's lanes 0 .. 15 are 16 rows, and a load whose lanes
+// touch so many lines gets 16 bytes a clock: so eight lanes load a row's 128 bytes, and the operand is
+// picked up from LDS of the wave's own. Where there are several workgroups to a tile, the last one
 // that ends adds their sums, in order, and makes the coefficients.
 constexpr int kShrinkWaves = 4;
 struct ShrinkArgs {
@@ -386,7 +402,7 @@ struct ShrinkArgs {
 
 // Values of a tile in LDS, v [32][RP + 1], as the coefficients that the later passes take.
 template <int DT>
-__device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int64_t rows, int64_t tiles, int RP, const float* v) {
+__device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int RP, const float* v) {
   const int pitch = RP + 1, tid = threadIdx.x;
   if (c.f)
     for (int i = tid; i < kTile * RP; i += 64 * kShrinkWaves) c.f[t * kTile * RP + i] = v[i / RP * pitch + i % RP];
@@ -413,7 +429,7 @@ __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int64_t r
           for (int p = 0; p < P; ++p) w[p][j / 2] |= static_cast<uint32_t>(part[p]) << (16 * (j & 1));
         }
 #pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(c.by_row + ((p * rows + t * kTile + m) * RK + 8 * k)) = w[p];
+        for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(c.by_row + (((t * 2 + m / 16) * (RK / 32) + k / 4) * P + p) * 512 + (k % 4 * 16 + m % 16) * 8) = w[p];
       }
     }
     if (c.by_rank) {
@@ -438,7 +454,7 @@ __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int64_t r
           for (int p = 0; p < P; ++p) w[p][j / 2] |= static_cast<uint32_t>(part[p]) << (16 * (j & 1));
         }
 #pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(c.by_rank + ((p * tiles + t) * RP + r) * 32 + 8 * q) = w[p];
+        for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(c.by_rank + ((t * (RP / 16) + r / 16) * P + p) * 512 + (q * 16 + r % 16) * 8) = w[p];
       }
     }
   }
@@ -446,9 +462,9 @@ __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int64_t r
 
 // CD: the type of what the coefficients will multiply, HD: of what h_in's will.
 template <int SD, int WD, int NR, int CD, int HD>
-__global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(ShrinkArgs a) {
-  extern __shared__ float lds[];                    // [4][32][16 NR], then [32][RP + 1]
-  __shared__ int last;
+__global__ __launch_bounds__(64 * kShrinkWaves, 2) void adapter_shrink_kernel(ShrinkArgs a) {
+  extern __shared__ __align__(16) float lds[];      // the waves' rooms, [4][32][16 NR], then [32][RP + 1]
+  __shared__ int last, place_row[kTile];
   constexpr int V = kShrinkWaves, kThreads = 64 * V;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
   const int r0 = blockIdx.z * 16 * NR;
@@ -464,82 +480,111 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
     part = mine % a.splits;
   }
   const int32_t* order = a.o.order + static_cast<int64_t>(t) * kTile;
-  int word = a.o.tile[t], some = order[0], m0 = order[c], m1 = order[16 + c];
-  loaded(end, word, some, m0, m1);
+  int word = a.o.tile[t], some = order[0], m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = order[8 * i + lane / 8];
+  loaded(end, word, some, m[0], m[1], m[2], m[3]);
   if (t >= end) return;
   const int e = tile_adapter(__builtin_amdgcn_readfirstlane(word));
-  // places without a row and ranks past the last one repeat another: their sums are not used
-  const S* row[2] = {static_cast<const S*>(a.s) + static_cast<int64_t>(m0 < 0 ? some : m0) * a.ld,
-                     static_cast<const S*>(a.s) + static_cast<int64_t>(m1 < 0 ? some : m1) * a.ld};
-  const W* w[NR];
+  if (wave == 0 && lane % 8 == 0) {
 #pragma unroll
-  for (int i = 0; i < NR; ++i)
-    w[i] = static_cast<const W*>(a.w) + (static_cast<int64_t>(e) * a.R + min(r0 + 16 * i + c, a.R - 1)) * a.D;
+    for (int i = 0; i < 4; ++i) place_row[8 * i + lane / 8] = m[i];
+  }
+  // Places without a row and ranks past the last one repeat another: their sums are not used. Load i
+  // of a block brings rows 8 i + lane / 8 (16-bit w beside fp32 rows: 16 i + lane / 4).
+  constexpr int KU = SD == BL_F32 ? 32 : 64;        // values of a block
+  constexpr int WL = SD == BL_F32 && WD != BL_F32 ? 4 : 8;   // lanes of a row of w
+  constexpr int WN = 16 * NR * WL / 64;             // loads of a block of w
+  constexpr int SV = 16 / sizeof(S), WV = 16 / sizeof(W);    // values of a lane's piece
+  const S* row[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) row[i] = static_cast<const S*>(a.s) + static_cast<int64_t>(m[i] < 0 ? some : m[i]) * a.ld;
+  const W* w[WN];
+#pragma unroll
+  for (int i = 0; i < WN; ++i)
+    w[i] = static_cast<const W*>(a.w) + (static_cast<int64_t>(e) * a.R + min(r0 + 64 / WL * i + lane / WL, a.R - 1)) * a.D;
   f32x4 acc[2][NR] = {};
   struct Block {
-    Eight<SD> s[2][2];
-    Eight<WD> w[2][NR];
+    u32x4 s[4], w[WN];
   };
   const auto load = [&](Block& v, int64_t u, auto whole) {
-    const int64_t k = u * 64 + g * 16;
     __builtin_amdgcn_sched_barrier(0);              // or the loads sink to where they are used
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int i = 0; i < 4; ++i) v.s[i] = load16<SD, decltype(whole)::value>(row[i], u * KU + lane % 8 * SV, a.D);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) v.s[j][i] = load8<SD, decltype(whole)::value>(row[i], k + 8 * j, a.D);
-#pragma unroll
-      for (int i = 0; i < NR; ++i) v.w[j][i] = load8<WD, decltype(whole)::value>(w[i], k + 8 * j, a.D);
-    }
+    for (int i = 0; i < WN; ++i) v.w[i] = load16<WD, decltype(whole)::value>(w[i], u * KU + lane % WL * WV, a.D);
     __builtin_amdgcn_sched_barrier(0);
   };
-  const auto multiply = [&](const Block& v) {
+  // pieces of 16 bytes, [32][8] and [16 NR][WL], in an XOR order that spreads 16 rows over all banks
+  u32x4* room = reinterpret_cast<u32x4*>(lds) + wave * (kTile * 8 + 16 * NR * WL);
+  u32x4* wroom = room + kTile * 8;
+  const auto place = [](int r, int p, int lanes) { return r * lanes + (p ^ (lanes == 8 ? r >> 1 & 7 : r >> 2 & 3)); };
+  const auto spread = [&](const Block& v) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int i = 0; i < 4; ++i) room[place(8 * i + lane / 8, lane % 8, 8)] = v.s[i];
+#pragma unroll
+    for (int i = 0; i < WN; ++i) wroom[place(64 / WL * i + lane / WL, lane % WL, WL)] = v.w[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  const auto multiply = [&]() {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u32x4 sv[2], wv[NR];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sv[i] = room[place(16 * i + c, 4 * j + g, 8)];
+#pragma unroll
+      for (int q = 0; q < NR; ++q) wv[q] = wroom[WL == 8 ? place(16 * q + c, 4 * j + g, 8) : place(16 * q + c, 2 * j + (g >> 1), 4)];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < NR; ++q) {
-          if constexpr (SD == WD && SD != BL_F32) {
-            acc[i][q] = dot32<SD>(v.s[j][i].w, v.w[j][q].w, acc[i][q]);
+          if constexpr (SD != BL_F32) {
+            acc[i][q] = dot32<SD>(sv[i], wv[q], acc[i][q]);
           } else {
 #pragma unroll
-            for (int l = 0; l < 8; ++l)
-              acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(value<SD>(v.s[j][i], l), value<WD>(v.w[j][q], l), acc[i][q], 0, 0, 0);
+            for (int l = 0; l < 4; ++l) {
+              float wl;
+              if constexpr (WD == BL_F32) wl = __uint_as_float(wv[q][l]);
+              else wl = to_float<WD>(static_cast<uint16_t>((g & 1 ? wv[q][2 + l / 2] : wv[q][l / 2]) >> (16 * (l & 1))));
+              acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(sv[i][l]), wl, acc[i][q], 0, 0, 0);
+            }
           }
         }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   };
-  const int64_t units = (a.D + 63) / 64, full = a.D / 64;
+  const int64_t units = (a.D + KU - 1) / KU, full = a.D / KU;
   const int64_t u0 = units * part / a.splits, u1 = units * (part + 1) / a.splits, uf = min(u1, full);
   int64_t u = u0 + wave;
   int64_t n = u < uf ? (uf - u + V - 1) / V : 0;    // whole blocks of this wave
-  Block v0;
-  if constexpr (SD == BL_F32) {
-    for (; n; --n, u += V) {
-      load(v0, u, std::true_type{});
-      multiply(v0);
-    }
-  } else if (n) {
+  Block v0, v1;
+  if (n) {
     // two blocks in flight; no load is under a condition of its own, so each wait is for the older ones alone
-    Block v1;
     load(v0, u, std::true_type{});
-    for (; n > 2; n -= 2, u += 2 * V) {
-      load(v1, u + V, std::true_type{});
-      multiply(v0);
-      load(v0, u + 2 * V, std::true_type{});
-      multiply(v1);
+    load(v1, n > 1 ? u + V : u, std::true_type{});
+    for (; n > 2; n -= 2) {
+      spread(v0);
+      load(v0, u += 2 * V, std::true_type{});
+      multiply();
+      spread(v1);
+      load(v1, n > 3 ? u + V : u, std::true_type{});
+      multiply();
     }
+    spread(v0);
+    multiply();
     if (n == 2) {
-      load(v1, u + V, std::true_type{});
-      multiply(v0);
-      multiply(v1);
-    } else {
-      multiply(v0);
+      spread(v1);
+      multiply();
     }
   }
   if (u1 > full && (full - u0) % V == wave) {       // the block that is not whole
     load(v0, full, std::false_type{});
-    multiply(v0);
+    spread(v0);
+    multiply();
   }
+  __syncthreads();
 
   // the waves' sums
 #pragma unroll
@@ -602,24 +647,39 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
     }
   }
   __syncthreads();
+#pragma unroll 4
   for (int i = tid; i < kTile * a.RP; i += kThreads) {
-    const int r = i % a.RP, at = order[i / a.RP];
+    const int r = i % a.RP, at = place_row[i / a.RP];
     float& v = lds[i / a.RP * pitch + r];
     const bool there = at >= 0 && r < a.R;
     if (there && a.h_out) a.h_out[static_cast<int64_t>(at) * a.R + r] = v;
     v = there ? v * f : 0.0f;
   }
+  // h_in: eight loads in flight, under way while the sums' coefficients are made
+  float h[8];
+  const auto load_h = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = min(i0 + i * kThreads, kTile * a.RP - 1), r = k % a.RP, at = place_row[k / a.RP];
+      h[i] = a.h_in[static_cast<int64_t>(max(at, 0)) * a.R + min(r, a.R - 1)];
+      h[i] = at >= 0 && r < a.R ? h[i] * f : 0.0f;
+    }
+  };
+  if (a.h_in) load_h(tid);
   __syncthreads();
-  const int64_t tiles = a.o.rows / kTile;
-  write_coefs<CD>(a.c, t, a.o.rows, tiles, a.RP, lds);
+  write_coefs<CD>(a.c, t, a.RP, lds);
   if (a.h_in) {
     __syncthreads();
-    for (int i = tid; i < kTile * a.RP; i += kThreads) {
-      const int r = i % a.RP, at = order[i / a.RP];
-      lds[i / a.RP * pitch + r] = at >= 0 && r < a.R ? a.h_in[static_cast<int64_t>(at) * a.R + r] * f : 0.0f;
+    for (int i0 = tid; i0 < kTile * a.RP; i0 += 8 * kThreads) {
+      if (i0 != tid) load_h(i0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = i0 + i * kThreads;
+        if (k < kTile * a.RP) lds[k / a.RP * pitch + k % a.RP] = h[i];
+      }
     }
     __syncthreads();
-    write_coefs<HD>(a.hc, t, a.o.rows, tiles, a.RP, lds);
+    write_coefs<HD>(a.hc, t, a.RP, lds);
   }
 }
 
@@ -743,13 +803,13 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
           for (int j = 0; j < 8; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[s], value<WD>(v[s], j), acc[j], 0, 0, 0);
       }
     } else {
-      const uint16_t* co = a.c.by_row + at * RK;
+      const u32x4* co = reinterpret_cast<const u32x4*>(a.c.by_row) + at / 16 * (RK / 32) * P * 64 + lane;
       if constexpr (KB > 0) {
         u32x4 cv[KB][P];
 #pragma unroll
         for (int k = 0; k < KB; ++k)
 #pragma unroll
-          for (int p = 0; p < P; ++p) cv[k][p] = *reinterpret_cast<const u32x4*>(co + (p * a.o.rows + c) * RK + 32 * k + 8 * g);
+          for (int p = 0; p < P; ++p) cv[k][p] = co[(k * P + p) * 64];
 #pragma unroll
         for (int k = 0; k < KB; ++k)
 #pragma unroll
@@ -761,7 +821,7 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
           u32x4 raw[8], cv[P];
           load_w(r0, raw);
 #pragma unroll
-          for (int p = 0; p < P; ++p) cv[p] = *reinterpret_cast<const u32x4*>(co + (p * a.o.rows + c) * RK + r0 + 8 * g);
+          for (int p = 0; p < P; ++p) cv[p] = co[(r0 / 32 * P + p) * 64];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const u32x4 v = column(raw, j);
@@ -817,7 +877,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
 // ------------------------------------------------------------------------------------------
 // outer: grad[e, r, d] = sum over the adapter's rows of c[row, r] S[row, d]
 // ------------------------------------------------------------------------------------------
-// A workgroup has 128 columns, up to 64 ranks and an even share of the tiles, which its waves take in
+// A workgroup has 128 columns, up to 32 ranks and an even share of the tiles, which its waves take in
 // turn. An adapter that lies within one share is written at once. The pieces of one that does
 // not go to sum[2 share], where the adapter began in an earlier share, or sum[2 share + 1]; the
 // workgroup that ends last adds them in their order. Each share has at most one adapter that
@@ -863,12 +923,12 @@ struct OuterTile {
           f[i][q] = r < a.RP ? a.c.f[(t * kTile + 4 * i + g) * a.RP + r] : 0.0f;
         }
     } else {
-      const int64_t tiles = a.o.rows / kTile;
 #pragma unroll
       for (int q = 0; q < NR; ++q) {
-        const int r = min(r0 + 16 * q + c16, a.RP - 1);   // past the last rank: not used
+        const int rb = min(r0 / 16 + q, a.RP / 16 - 1);   // past the last rank: not used
 #pragma unroll
-        for (int p = 0; p < P; ++p) c[p][q] = *reinterpret_cast<const u32x4*>(a.c.by_rank + ((p * tiles + t) * a.RP + r) * 32 + 8 * g);
+        for (int p = 0; p < P; ++p)
+          c[p][q] = reinterpret_cast<const u32x4*>(a.c.by_rank)[((t * (a.RP / 16) + rb) * P + p) * 64 + 16 * g + c16];
         if constexpr (SD == BL_F16) {
 #pragma unroll
           for (int l = 0; l < 4; ++l) ex[q][l] = a.c.rank_e[t * a.RP + min(r0 + 16 * q + 4 * g + l, a.RP - 1)];
@@ -913,27 +973,47 @@ struct OuterTile {
   }
 };
 
-// Tiles t, t + 4 .. before end, each loaded while the one before is multiplied, its rows' numbers one
-// tile earlier still.
+// Tiles t, t + 4 .. before end: each is loaded while the one before is multiplied, its rows' numbers one
+// tile earlier still. Past the last tile the loads repeat it, so that none is under a condition.
 template <int SD, int NR, bool WHOLE>
 __device__ __forceinline__ void outer_tiles(const OuterArgs& a, int t, int end, int64_t d, int r0, int c, int g, f32x4 (&acc)[NR][8]) {
   if (t >= end) return;
-  OuterTile<SD, NR> v;
-  int rows[8];
-  v.load_rows(a, t, g);
-  for (;;) {
-    v.template load<WHOLE>(a, t, d, r0, c, g);
+  const int last = t + (end - 1 - t) / 4 * 4;
+  if constexpr (SD == BL_F32) {                     // no registers for two tiles
+    OuterTile<SD, NR> v;
+    int rows[8];
+    v.load_rows(a, t, g);
+    for (; t <= last; t += 4) {
+      v.template load<WHOLE>(a, t, d, r0, c, g);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rows[i] = v.row[i];
-    t += 4;
-    if (t < end) v.load_rows(a, t, g);
-    v.multiply(rows, acc);
-    if (t >= end) return;
+      for (int k = 0; k < 8; ++k) rows[k] = v.row[k];
+      v.load_rows(a, min(t + 4, last), g);
+      v.multiply(rows, acc);
+    }
+    return;
   }
+  OuterTile<SD, NR> v[2];
+  v[0].load_rows(a, t, g);
+  v[1].load_rows(a, min(t + 4, last), g);
+  v[0].template load<WHOLE>(a, t, d, r0, c, g);
+  for (;;)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      OuterTile<SD, NR>&now = v[i], &next = v[1 - i];
+      int rows[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) rows[k] = now.row[k];
+      __builtin_amdgcn_sched_barrier(0);
+      next.template load<WHOLE>(a, min(t + 4, last), d, r0, c, g);
+      now.load_rows(a, min(t + 8, last), g);
+      __builtin_amdgcn_sched_barrier(0);
+      now.multiply(rows, acc);
+      if ((t += 4) > last) return;
+    }
 }
 
 template <int SD, int NR>
-__global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a) {
+__global__ __launch_bounds__(256, SD == BL_F32 ? 2 : 1) void adapter_outer_kernel(OuterArgs a) {
   __shared__ f32x4 red[16 * NR][32];
   __shared__ int last_one;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
@@ -989,13 +1069,39 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a) {
       if (tid == 0)
         last_one = arrive_agent(a.arrived + (s0 * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x) == static_cast<uint32_t>(s1 - s0);
       __syncthreads();
-      if (last_one)
-        each([&](int, int64_t at) {
-          float v = atomic_load_agent(a.sum + (2 * s0 + 1) * n + at);
-#pragma unroll 8
-          for (int64_t s = s0 + 1; s <= s1; ++s) v += atomic_load_agent(a.sum + 2 * s * n + at);
-          grad[at] = a.add ? grad[at] + v : v;
-        });
+      if (last_one) {
+        // eight places' values of four shares in flight at a time
+        const int parts = static_cast<int>(s1 - s0) + 1;
+        for (int i0 = tid; i0 < 16 * NR * 128; i0 += 8 * 256) {
+          int64_t at[8];
+          bool here[8];
+          float v[8] = {};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int k = i0 + 256 * i, r = r0 + k / 128;
+            const int64_t d = d0 + k % 128;
+            here[i] = r < a.R && d < a.D;
+            at[i] = here[i] ? r * a.D + d : static_cast<int64_t>(min(r0, a.R - 1)) * a.D;
+          }
+          for (int q = 0; q < parts; q += 4) {
+            float p[4][8];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const int64_t share = s0 + min(q + s, parts - 1);
+              const float* in = a.sum + (2 * share + (share == s0 ? 1 : 0)) * n;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) p[s][i] = atomic_load_agent(in + at[i]);
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] += q + s < parts ? p[s][i] : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (here[i]) grad[at[i]] = a.add ? grad[at[i]] + v[i] : v[i];
+        }
+      }
     }
     __syncthreads();
     t = end;
@@ -1003,8 +1109,151 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a) {
 }
 
 // ------------------------------------------------------------------------------------------
+// few rows: each by itself, nothing sorted
+// ------------------------------------------------------------------------------------------
+struct RowsArgs {
+  AdapterForwardArgs f;
+  int R;
+};
+
+// h[m, r] for RW ranks of a row: every thread has pieces of eight values of the row and of each rank.
+template <int DT, int RW>
+__global__ __launch_bounds__(256) void adapter_rows_shrink_kernel(RowsArgs p) {
+  __shared__ float red[4][RW];
+  const AdapterForwardArgs& a = p.f;
+  using T = typename Elem<DT>::type;
+  const int tid = threadIdx.x, r0 = blockIdx.y * RW;
+  const int64_t m = blockIdx.x;
+  const int e = a.rows.index[m];
+  float* h = a.h + m * p.R + r0;
+  if (e < 0 || e >= a.rows.L) {
+    if (tid < RW && r0 + tid < p.R) h[tid] = 0.0f;
+    return;
+  }
+  const T* x = static_cast<const T*>(a.x) + m * a.ldx;
+  const T* w[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) w[i] = static_cast<const T*>(a.a) + (static_cast<int64_t>(e) * p.R + min(r0 + i, p.R - 1)) * a.K;
+  float sum[RW] = {};
+  const auto add = [&](int64_t k, auto whole) {
+    const Eight<DT> xv = load8<DT, decltype(whole)::value>(x, k, a.K);
+    Eight<DT> wv[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) wv[i] = load8<DT, decltype(whole)::value>(w[i], k, a.K);
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[i] += value<DT>(xv, j) * value<DT>(wv[i], j);
+  };
+  const int64_t full = a.K / 2048 * 2048;
+#pragma unroll 4
+  for (int64_t k = 0; k < full; k += 2048) add(k + 8 * tid, std::true_type{});
+  if (full + 8 * tid < a.K) add(full + 8 * tid, std::false_type{});
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum[i] += __shfl_xor(sum[i], off);
+    if (tid % 64 == 0) red[tid / 64][i] = sum[i];
+  }
+  __syncthreads();
+  if (tid < RW && r0 + tid < p.R) h[tid] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+}
+
+// 512 columns of a row of y: each wave takes every fourth rank.
+template <int WD, int YD>
+__global__ __launch_bounds__(256) void adapter_rows_expand_kernel(RowsArgs p) {
+  __shared__ f32x4 red[4][64][2];
+  const AdapterForwardArgs& a = p.f;
+  using W = typename Elem<WD>::type;
+  using Y = typename Elem<YD>::type;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t m = blockIdx.y, n0 = static_cast<int64_t>(blockIdx.x) * 512, n = n0 + 8 * lane, at = n0 + 2 * tid;
+  const int e = a.rows.index[m];
+  const bool none = e < 0 || e >= a.rows.L;
+  if (none && a.base == a.y) return;
+  const Y* base = static_cast<const Y*>(a.base) + m * a.ldbase;
+  float b[2] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (a.base && at + i < a.N) b[i] = to_float<YD>(base[at + i]);
+  float v[2] = {};
+  if (!none) {
+    const W* w = static_cast<const W*>(a.b) + static_cast<int64_t>(e) * p.R * a.N;
+    const float* h = a.h + m * p.R;
+    float sum[8] = {};
+    const auto ranks = [&](auto whole) {
+#pragma unroll 8
+      for (int r = wave; r < p.R; r += 4) {
+        const float c = h[r];
+        const Eight<WD> wv = load8<WD, decltype(whole)::value>(w + r * a.N, n, a.N);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += c * value<WD>(wv, j);
+      }
+    };
+    if (n0 + 512 <= a.N) ranks(std::true_type{});
+    else ranks(std::false_type{});
+    red[wave][lane][0] = f32x4{sum[0], sum[1], sum[2], sum[3]};
+    red[wave][lane][1] = f32x4{sum[4], sum[5], sum[6], sum[7]};
+    __syncthreads();
+    const float f = a.scale ? a.scale[e] : 1.0f;
+    const float* flat = reinterpret_cast<const float*>(red);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = 2 * tid + i;
+      v[i] = f * (flat[k] + flat[512 + k] + flat[1024 + k] + flat[1536 + k]);
+      if (a.base) v[i] = b[i] + v[i];
+    }
+  } else {
+    v[0] = b[0];
+    v[1] = b[1];
+  }
+  Y* y = static_cast<Y*>(a.y) + m * a.ldy;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (at + i < a.N) {
+      if constexpr (YD == BL_F32) y[at + i] = v[i];
+      else y[at + i] = bits16<YD>(v[i]);
+    }
+}
+
+// ------------------------------------------------------------------------------------------
 // launches
 // ------------------------------------------------------------------------------------------
+// Bytes of the adapters that the rows read if each reads its own: up to this they are done so, in two launches
+// that wait for nothing. (us from a graph, this way / sorted, bf16: 1 row of 8192 x 8192, rank 16 6.5 / 17, 64 rows of 16
+// adapters 10 / 21; 134 MB: 512 rows of 4096 x 4096, rank 16 of 2 / 64 adapters 16.5 / 19.4 and 20.0 / 22.7, 64 rows of
+// 8192 x 8192, rank 64 of 16 19.7 / 26.2; 268 MB: 512 rows of 8192 x 8192, rank 16 of 16 27.2 / 25.8, 128, rank 64 of 16
+// 26.5 / 26.6; 604 MB: 512 rows of 8192 x 28672, rank 16 of 16 65 / 39.)
+constexpr int64_t kRowsMost = int64_t(3) << 26;
+bool by_rows(const AdapterForwardArgs& a) {
+  return a.rows.M <= 65535 && a.rows.M * a.rows.R * (a.K + a.N) * static_cast<int64_t>(dtype_bytes(a.dtype)) <= kRowsMost;
+}
+
+template <int DT>
+hipError_t start_rows_shrink(const RowsArgs& p, hipStream_t s) {
+  const auto M = static_cast<uint32_t>(p.f.rows.M);
+  // one rank to a workgroup while that makes few of them, else four, which share the row's reads
+  if (p.f.rows.M * p.R <= 1024) adapter_rows_shrink_kernel<DT, 1><<<dim3(M, p.R), 256, 0, s>>>(p);
+  else adapter_rows_shrink_kernel<DT, 4><<<dim3(M, static_cast<uint32_t>(div_up(p.R, 4))), 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+template <int WD, int YD>
+hipError_t start_rows_expand(const RowsArgs& p, hipStream_t s) {
+  const dim3 grid(static_cast<uint32_t>(div_up(p.f.N, 512)), static_cast<uint32_t>(p.f.rows.M));
+  adapter_rows_expand_kernel<WD, YD><<<grid, 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+hipError_t forward_by_rows(const AdapterForwardArgs& a, hipStream_t s) {
+  const RowsArgs p{a, static_cast<int>(a.rows.R)};
+  const hipError_t e = a.dtype == BL_F16    ? start_rows_shrink<BL_F16>(p, s)
+                       : a.dtype == BL_BF16 ? start_rows_shrink<BL_BF16>(p, s)
+                                            : start_rows_shrink<BL_F32>(p, s);
+  if (e != hipSuccess) return e;
+  if (a.dtype == BL_F16) return a.ydtype == BL_F16 ? start_rows_expand<BL_F16, BL_F16>(p, s) : start_rows_expand<BL_F16, BL_F32>(p, s);
+  if (a.dtype == BL_BF16) return a.ydtype == BL_BF16 ? start_rows_expand<BL_BF16, BL_BF16>(p, s) : start_rows_expand<BL_BF16, BL_F32>(p, s);
+  return start_rows_expand<BL_F32, BL_F32>(p, s);
+}
+
 // Splits for about 448 workgroups: the 512 that the chip holds at once of the largest rank, less
 // what an uneven spread over its CUs needs (a workgroup that starts after the others doubles the time).
 int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
@@ -1013,11 +1262,13 @@ int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
 }
 int expand_tiles_of(int64_t M) { return M >= 2048 ? 4 : 1; }
 int by_chip(const AdapterRows& r) { return r.M >= 64 * kTile; }
-int outer_splits(int64_t M, int64_t R, int64_t D) {
-  const int64_t groups = div_up(D, 128) * div_up(rank_pad(R), 64);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({512 / groups, div_up(M, 4 * kTile), 32})));
+// Two workgroups to a CU, or the one that two tiles' registers of 16-bit values leave beyond rank 16. (us,
+// 4096 rows of 8192, bf16, rank 32: 22 for 256 workgroups, 32 for 384, 30 for 512, 44 for 1024.)
+int outer_splits(int64_t M, int64_t R, int64_t D, int dt) {
+  const int64_t most = dt != BL_F32 && R > 16 ? 256 : 512, groups = div_up(D, 128) * div_up(rank_pad(R), 32);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most / groups, div_up(M, 4 * kTile), 32})));
 }
-int64_t outer_counters(int64_t M, int64_t R, int64_t D) { return outer_splits(M, R, D) * div_up(D, 128) * div_up(rank_pad(R), 64); }
+int64_t outer_counters(int64_t M, int64_t R, int64_t D) { return outer_splits(M, R, D, BL_F32) * div_up(D, 128) * div_up(rank_pad(R), 32); }
 
 // Bytes of each layout of the coefficients.
 struct CoefBytes {
@@ -1076,7 +1327,7 @@ hipError_t sort_rows(const AdapterRows& r, const Scratch& w, int64_t counters, h
 template <int SD, int WD, int NR, int CD, int HD>
 hipError_t start_shrink_as(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
   const dim3 grid(a.splits, static_cast<uint32_t>(tiles) + (a.by_chip ? 7 : 0), static_cast<uint32_t>(div_up(a.RP, 64)));
-  const size_t lds = static_cast<size_t>(kTile) * std::max(64 * NR, a.RP + 1) * 4;
+  const size_t lds = std::max<size_t>(kShrinkWaves * (kTile * 8 + 16 * NR * 8) * 16, kTile * static_cast<size_t>(a.RP + 1) * 4);
   adapter_shrink_kernel<SD, WD, NR, CD, HD><<<grid, 64 * kShrinkWaves, lds, s>>>(a);
   return hipGetLastError();
 }
@@ -1112,12 +1363,9 @@ hipError_t start_expand(const ExpandArgs& a, int wd, int yd, int64_t tiles, hipS
 
 template <int SD>
 hipError_t start_outer_as(const OuterArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<uint32_t>(div_up(a.D, 128)), a.splits, static_cast<uint32_t>(div_up(a.RP, 64)));
-  const int nr = std::min(a.RP / 16, 4);
-  if (nr == 1) adapter_outer_kernel<SD, 1><<<grid, 256, 0, s>>>(a);
-  else if (nr == 2) adapter_outer_kernel<SD, 2><<<grid, 256, 0, s>>>(a);
-  else if (nr == 3) adapter_outer_kernel<SD, 3><<<grid, 256, 0, s>>>(a);
-  else adapter_outer_kernel<SD, 4><<<grid, 256, 0, s>>>(a);
+  const dim3 grid(static_cast<uint32_t>(div_up(a.D, 128)), a.splits, static_cast<uint32_t>(div_up(a.RP, 32)));
+  if (a.RP == 16) adapter_outer_kernel<SD, 1><<<grid, 256, 0, s>>>(a);
+  else adapter_outer_kernel<SD, 2><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 hipError_t start_outer(const OuterArgs& a, int sd, hipStream_t s) {
@@ -1158,7 +1406,7 @@ AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool
     w.hc_off[0] = take(b.f);
     w.hc_off[3] = take(b.by_rank);
     w.hc_off[4] = take(b.rank_e);
-    w.sum_off = take(2 * std::max(outer_splits(M, R, K) * R * K, outer_splits(M, R, N) * R * N) * 4);
+    w.sum_off = take(2 * std::max(outer_splits(M, R, K, BL_F32) * R * K, outer_splits(M, R, N, BL_F32) * R * N) * 4);
   }
   w.total = off;
   return w;
@@ -1166,6 +1414,7 @@ AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool
 
 hipError_t launch_adapter_forward(const AdapterForwardArgs& a, char* ws, hipStream_t s) {
   const AdapterRows& r = a.rows;
+  if (by_rows(a)) return forward_by_rows(a, s);
   const AdapterWs L = adapter_ws(r.M, r.L, r.R, a.K, a.N, false);
   const Scratch w = scratch(L, ws, r);
   const int64_t tiles = max_tiles(r.M, r.L);
@@ -1195,10 +1444,10 @@ hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipSt
     if (e != hipSuccess) return e;
   }
   uint32_t* arrived = w.arrived + tiles;
-  e = start_outer(OuterArgs{w.o, w.c, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.R, a.K), w.sum, arrived, a.da, a.add}, a.dtype, s);
+  e = start_outer(OuterArgs{w.o, w.c, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.R, a.K, a.dtype), w.sum, arrived, a.da, a.add}, a.dtype, s);
   if (e != hipSuccess) return e;
   arrived += outer_counters(r.M, r.R, a.K);
-  return start_outer(OuterArgs{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.R, a.N), w.sum, arrived, a.db, a.add}, a.dydtype, s);
+  return start_outer(OuterArgs{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.R, a.N, a.dydtype), w.sum, arrived, a.db, a.add}, a.dydtype, s);
 }
 
 }  // namespace bl
