@@ -64,6 +64,11 @@ __device__ __forceinline__ void load_logits(const typename Elem<DT>::type* row, 
   for (int i = 0; i < NE; ++i) l[i] = l[i] > -INFINITY ? fminf(l[i], kMost) : -INFINITY;   // NaN compares false
 }
 
+// exp and 1 / v by the hardware's instructions: the first errs by two units and one of its argument's
+// rounding, |v| 2^-24, the second by one unit.
+__device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504088896341f); }
+__device__ __forceinline__ float fast_inv(float v) { return __builtin_amdgcn_rcpf(v); }
+
 // l becomes the normalised scores t (0 for what is left out). Sigmoid scores also give p and
 // 1 - p, each without a difference. A row whose sigmoids are all below a half is normalised as
 // exp(l - max) / (1 + exp(l)), so that none of them has to be large enough for fp32.
@@ -78,15 +83,15 @@ __device__ __forceinline__ void normalise(float (&l)[NE], float (&p)[NE], float 
   for (int i = 0; i < NE; ++i) {
     const float v = l[i];
     if constexpr (SIGMOID) {
-      const float z = expf(-fabsf(v)), inv = 1.0f / (1.0f + z);      // z = 0 for -inf
+      const float z = fast_exp(-fabsf(v)), inv = fast_inv(1.0f + z);  // z = 0 for -inf
       const float ps = v >= 0.0f ? inv : z * inv;
       if constexpr (SCORES) {
         p[i] = ps;
         q[i] = v >= 0.0f ? z * inv : inv;
       }
-      l[i] = mx > 0.0f ? ps : v > -INFINITY ? expf(v - mx) * inv : 0.0f;
+      l[i] = mx > 0.0f ? ps : v > -INFINITY ? fast_exp(v - mx) * inv : 0.0f;
     } else {
-      l[i] = v > -INFINITY ? expf(v - mx) : 0.0f;
+      l[i] = v > -INFINITY ? fast_exp(v - mx) : 0.0f;
     }
     sum += l[i];
   }
@@ -100,8 +105,20 @@ __device__ __forceinline__ int64_t bounded(const int32_t* offsets, int64_t i, in
   const int64_t o = offsets[i];
   return o < 0 ? 0 : o > M ? M : o;
 }
-// The first sequence that ends past row m; S if none does.
-__device__ __forceinline__ int64_t sequence_of(const int32_t* offsets, int64_t S, int64_t m) {
+// The first sequence that ends past row m; S if none does. Few sequences: the group's lanes count those
+// that end before, all at once.
+template <int LANES>
+__device__ __forceinline__ int64_t sequence_of(const int32_t* offsets, int64_t S, int64_t m, int lane) {
+  if (S <= 2 * LANES) {
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int s = lane + LANES * i;
+      const uint64_t all = __ballot(s < S && offsets[s < S ? s + 1 : 0] <= m);
+      before += __popcll(LANES == 64 ? all : all >> (threadIdx.x & 48) & 0xFFFF);
+    }
+    return before;
+  }
   int64_t lo = 0, hi = S;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
@@ -123,20 +140,22 @@ struct BalanceParts {
   int32_t* rows;          // [chunks + S - 1]
 };
 
+constexpr int balance_threads(int lanes) { return lanes == 16 ? 1024 : 256; }
+
 template <int DT, int LANES, int NE, int V, bool SIGMOID>
-__global__ __launch_bounds__(256) void route_balance_kernel(RouteRows r, BalanceParts w) {
-  constexpr int G = 256 / LANES;
-  __shared__ float sums[G][LANES * NE];
+__global__ __launch_bounds__(balance_threads(LANES)) void route_balance_kernel(RouteRows r, BalanceParts w) {
+  constexpr int T = balance_threads(LANES), G = T / LANES, W = T / 64;
+  __shared__ float sums[W][LANES * NE];
   __shared__ int count[LANES * NE];
-  __shared__ int counted[G];
-  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, E = static_cast<int>(r.E);
+  __shared__ int counted[W];
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, wave = threadIdx.x / 64, E = static_cast<int>(r.E);
   const int64_t c0 = blockIdx.x * w.chunk, c1 = min(c0 + w.chunk, r.M);
-  for (int64_t s = r.offsets ? sequence_of(r.offsets, r.S, c0) : 0; s < r.S; ++s) {
+  for (int64_t s = r.offsets ? sequence_of<64>(r.offsets, r.S, c0, threadIdx.x & 63) : 0; s < r.S; ++s) {
     const int64_t begin = r.offsets ? bounded(r.offsets, s, r.M) : 0, end = r.offsets ? bounded(r.offsets, s + 1, r.M) : r.M;
     if (begin >= c1) break;
     const int64_t m0 = max(begin, c0), m1 = min(end, c1);
     if (m0 >= m1) continue;
-    for (int i = threadIdx.x; i < E; i += 256) count[i] = 0;
+    for (int i = threadIdx.x; i < E; i += T) count[i] = 0;
     __syncthreads();
     float acc[NE] = {};
     int n = 0;
@@ -153,56 +172,68 @@ __global__ __launch_bounds__(256) void route_balance_kernel(RouteRows r, Balance
       }
       any = group_any<LANES>(any);
       normalise<LANES, NE, SIGMOID, false>(l, none, none);
-      n += any;
+      n += any && lane == 0;
 #pragma unroll
       for (int i = 0; i < NE; ++i) acc[i] += any ? l[i] : 0.0f;
     }
+    // the wave's groups, then the waves
 #pragma unroll
-    for (int i = 0; i < NE; ++i) sums[group][expert_of<LANES, V>(lane, i)] = acc[i];
-    if (lane == 0) counted[group] = n;
+    for (int off = LANES; off < 64; off <<= 1) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) acc[i] += __shfl_xor(acc[i], off);
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off);
+    if (threadIdx.x % 64 < LANES) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) sums[wave][expert_of<LANES, V>(lane, i)] = acc[i];
+    }
+    if (threadIdx.x % 64 == 0) counted[wave] = n;
     __syncthreads();
     const int64_t slot = blockIdx.x + s;
-    for (int e = threadIdx.x; e < E; e += 256) {
+    for (int e = threadIdx.x; e < E; e += T) {
       float v = 0.0f;
 #pragma unroll
-      for (int g = 0; g < G; ++g) v += sums[g][e];
+      for (int g = 0; g < W; ++g) v += sums[g][e];
       w.t[slot * E + e] = v;
       w.count[slot * E + e] = count[e];
     }
     if (threadIdx.x == 0) {
       int rows = 0;
-      for (int g = 0; g < G; ++g) rows += counted[g];
+#pragma unroll
+      for (int g = 0; g < W; ++g) rows += counted[g];
       w.rows[slot] = rows;
     }
     __syncthreads();
   }
 }
 
+// Sums of two values over the 1024 threads, in every thread.
 template <typename T>
 __device__ __forceinline__ T block_sum(T v, T* lds) {
-  lds[threadIdx.x] = v;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = v;
   __syncthreads();
-  for (int off = 512; off > 0; off >>= 1) {
-    if (threadIdx.x < off) lds[threadIdx.x] += lds[threadIdx.x + off];
-    __syncthreads();
-  }
-  const T all = lds[0];
+  T all = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) all += lds[i];
   __syncthreads();
   return all;
 }
 
-// One workgroup per sequence: `parts` threads share an expert's partial sums.
+// One workgroup per sequence: `parts` threads share an expert's partial sums, eight loads of each in
+// flight at a time.
 __global__ __launch_bounds__(1024) void route_balance_finish_kernel(RouteRows r, BalanceParts w, float* loss, int32_t* count, float* coef) {
   __shared__ double sum[1024];
   __shared__ int cnt[1024];
-  __shared__ int64_t whole[1024];
+  __shared__ int64_t whole[16];
   const int64_t s = blockIdx.x;
   const int E = static_cast<int>(r.E);
   const int64_t begin = r.offsets ? bounded(r.offsets, s, r.M) : 0, end = r.offsets ? bounded(r.offsets, s + 1, r.M) : r.M;
   const int64_t first = begin / w.chunk + s, last = begin < end ? (end - 1) / w.chunk + s + 1 : first;   // slots
   int64_t n = 0;
   for (int64_t i = first + threadIdx.x; i < last; i += 1024) n += w.rows[i];
-  const int64_t rows = block_sum(n, whole);
   const int width = E < 1024 ? E : 1024, parts = 1024 / width;
   const int part = threadIdx.x / width, e0 = threadIdx.x % width;
   double mine[2] = {};                              // of expert e0 and e0 + 1024
@@ -213,9 +244,21 @@ __global__ __launch_bounds__(1024) void route_balance_finish_kernel(RouteRows r,
     double v = 0.0;
     int c = 0;
     if (part < parts && e < E)
-      for (int64_t i = first + part; i < last; i += parts) {
-        v += w.t[i * E + e];
-        c += w.count[i * E + e];
+      for (int64_t i = first + part; i < last; i += 8 * parts) {
+        float tv[8];
+        int cv[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int64_t at = min(i + k * parts, last - 1) * E + e;
+          tv[k] = w.t[at];
+          cv[k] = w.count[at];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i + k * parts < last) {
+            v += tv[k];
+            c += cv[k];
+          }
       }
     sum[threadIdx.x] = v;
     cnt[threadIdx.x] = c;
@@ -226,7 +269,9 @@ __global__ __launch_bounds__(1024) void route_balance_finish_kernel(RouteRows r,
         slots[q] += cnt[i * width + e0];
       }
     __syncthreads();
+    if (E <= 1024) break;
   }
+  const int64_t rows = block_sum(n, whole);
   const double all = static_cast<double>(block_sum(static_cast<int64_t>(slots[0]) + slots[1], whole)) * static_cast<double>(rows);
   double v = 0.0;
 #pragma unroll
@@ -323,7 +368,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs a
     int64_t s = 0;
     bool inside = any;
     if (r.offsets) {
-      s = sequence_of(r.offsets, r.S, mc);
+      s = sequence_of<LANES>(r.offsets, r.S, mc, lane);
       inside = any && s < r.S && r.offsets[s < r.S ? s : 0] <= mc;
     }
     if (inside) {
@@ -417,10 +462,11 @@ bool vec_experts(const void* p, int64_t E, int64_t ld, size_t size) {
   return E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * size) == 0;
 }
 
-// Rows of a chunk: about 512 workgroups, a row for every group of lanes at least.
+// Rows of a chunk: about 128 workgroups of 64 rows at a time (512 of 4 beyond 512 experts), a row for every
+// group of lanes at least.
 int64_t balance_chunk(int64_t M, int64_t E) {
-  const int64_t groups = E <= 512 ? 16 : 4;
-  return (std::max<int64_t>(M / 512, 1) + groups - 1) / groups * groups;
+  const int64_t groups = E <= 512 ? 64 : 4, most = E <= 512 ? 128 : 512;
+  return (std::max<int64_t>(M / most, 1) + groups - 1) / groups * groups;
 }
 struct BalanceWs {
   int64_t chunk, chunks;
@@ -440,8 +486,9 @@ BalanceWs balance_ws(int64_t M, int64_t E, int64_t S) {
 template <int DT, int LANES, int NE, int V>
 hipError_t start_balance(const RouteRows& r, const BalanceParts& w, hipStream_t s) {
   const auto grid = static_cast<uint32_t>(w.chunks);
-  if (r.sigmoid) route_balance_kernel<DT, LANES, NE, V, true><<<grid, 256, 0, s>>>(r, w);
-  else route_balance_kernel<DT, LANES, NE, V, false><<<grid, 256, 0, s>>>(r, w);
+  constexpr int T = balance_threads(LANES);
+  if (r.sigmoid) route_balance_kernel<DT, LANES, NE, V, true><<<grid, T, 0, s>>>(r, w);
+  else route_balance_kernel<DT, LANES, NE, V, false><<<grid, T, 0, s>>>(r, w);
   return hipGetLastError();
 }
 template <int DT, int V>
