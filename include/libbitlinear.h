@@ -449,7 +449,7 @@ int bl_fp8_experts(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
  * dxdtype) is x's dtype or BL_F32. 1 <= M <= 2^20, 1 <= K, N <= 2^24, 1 <= R <= 256, 1 <= L <= 1024.
  * Sums are fp32 sums of exact products (a 16-bit value times an fp32 one is rounded to fp32 once), in
  * a fixed order for a given shape and index. Uses ws (bl_adapter_workspace_bytes; the last argument says
- * which call it is for). */
+ * which call it is for; 0 where a forward pass of few rows needs none, and for sizes that are refused). */
 size_t bl_adapter_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t R,
                                   int backward);
 

@@ -781,10 +781,11 @@ def bl_adapter_forward(x, a, b, index, scale=None, base=None, out_dtype=None, ou
     d = _dev(x, a, b, index, scale, base, out)
     y = _out(out, (M, N), out_dtype, d)
     h = torch.empty((M, R), dtype=torch.float32, device=d)
-    ws = _scratch(_lib.bl_adapter_workspace_bytes(M, K, N, L, R, 0), d, f"M={M} K={K} N={N} L={L} R={R}")
+    nbytes = _lib.bl_adapter_workspace_bytes(M, K, N, L, R, 0)   # 0 for few rows: the call needs none
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=d) if nbytes else None
     _check(_lib.bl_adapter_forward(_ptr(x), dt, M, K, ld, _ptr(a), _ptr(b), L, R, N, _ptr(index), _ptr(scale),
                                    _ptr(base), ldbase, _ptr(y), _DTYPES[out_dtype], _row_stride(y, "out"), _ptr(h),
-                                   _ptr(ws), ws.numel(), _stream(d)), "bl_adapter_forward")
+                                   _ptr(ws), nbytes, _stream(d)), "bl_adapter_forward")
     return y, h
 
 

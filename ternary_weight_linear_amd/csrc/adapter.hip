@@ -1219,15 +1219,13 @@ __global__ __launch_bounds__(256) void adapter_rows_expand_kernel(RowsArgs p) {
 // ------------------------------------------------------------------------------------------
 // launches
 // ------------------------------------------------------------------------------------------
-// Bytes of the adapters that the rows read if each reads its own: up to this they are done so, in two launches
-// that wait for nothing. (us from a graph, this way / sorted, bf16: 1 row of 8192 x 8192, rank 16 6.5 / 17, 64 rows of 16
+// Values of the adapters that the rows read if each reads its own: up to this they are done so, in two launches
+// that wait for nothing and need no scratch. (us from a graph, this way / sorted, bf16: 1 row of 8192 x 8192, rank 16 6.5 / 17, 64 rows of 16
 // adapters 10 / 21; 134 MB: 512 rows of 4096 x 4096, rank 16 of 2 / 64 adapters 16.5 / 19.4 and 20.0 / 22.7, 64 rows of
 // 8192 x 8192, rank 64 of 16 19.7 / 26.2; 268 MB: 512 rows of 8192 x 8192, rank 16 of 16 27.2 / 25.8, 128, rank 64 of 16
 // 26.5 / 26.6; 604 MB: 512 rows of 8192 x 28672, rank 16 of 16 65 / 39.)
-constexpr int64_t kRowsMost = int64_t(3) << 26;
-bool by_rows(const AdapterForwardArgs& a) {
-  return a.rows.M <= 65535 && a.rows.M * a.rows.R * (a.K + a.N) * static_cast<int64_t>(dtype_bytes(a.dtype)) <= kRowsMost;
-}
+constexpr int64_t kRowsMost = int64_t(3) << 25;
+bool by_rows(int64_t M, int64_t R, int64_t K, int64_t N) { return M <= 65535 && M * R * (K + N) <= kRowsMost; }
 
 template <int DT>
 hipError_t start_rows_shrink(const RowsArgs& p, hipStream_t s) {
@@ -1254,11 +1252,12 @@ hipError_t forward_by_rows(const AdapterForwardArgs& a, hipStream_t s) {
   return start_rows_expand<BL_F32, BL_F32>(p, s);
 }
 
-// Splits for about 448 workgroups: the 512 that the chip holds at once of the largest rank, less
-// what an uneven spread over its CUs needs (a workgroup that starts after the others doubles the time).
+// Splits for about 300 workgroups, 448 beyond rank 32, where the matrices' reads take as long as the rows': less
+// than the 512 that the chip holds at once, since one that starts after the others doubles the time. (us, 300 /
+// 448, bf16: 777 x 8640, rank 12 11.9 / 13.6, 4096 x 8192, rank 32 27.9 / 30.4, rank 64 38.5 / 31.3.)
 int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
-  const int64_t groups = max_tiles(M, L) * div_up(rank_pad(R), 64);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({448 / groups, div_up(D, 64) / (2 * kShrinkWaves), 16})));
+  const int64_t groups = max_tiles(M, L) * div_up(rank_pad(R), 64), most = R <= 32 ? 300 : 448;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most / groups, div_up(D, 64) / (2 * kShrinkWaves), 16})));
 }
 int expand_tiles_of(int64_t M) { return M >= 2048 ? 4 : 1; }
 int by_chip(const AdapterRows& r) { return r.M >= 64 * kTile; }
@@ -1385,6 +1384,7 @@ Coefs only(const Coefs& c, int dt, bool rows, bool ranks) {
 
 AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool backward) {
   AdapterWs w{};
+  if (!backward && by_rows(M, R, K, N)) return w;
   size_t off = 0;
   auto take = [&](int64_t bytes) {
     const size_t at = off;
@@ -1414,7 +1414,7 @@ AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool
 
 hipError_t launch_adapter_forward(const AdapterForwardArgs& a, char* ws, hipStream_t s) {
   const AdapterRows& r = a.rows;
-  if (by_rows(a)) return forward_by_rows(a, s);
+  if (by_rows(r.M, r.R, a.K, a.N)) return forward_by_rows(a, s);
   const AdapterWs L = adapter_ws(r.M, r.L, r.R, a.K, a.N, false);
   const Scratch w = scratch(L, ws, r);
   const int64_t tiles = max_tiles(r.M, r.L);

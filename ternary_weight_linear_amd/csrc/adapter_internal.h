@@ -54,7 +54,7 @@ struct AdapterBackwardArgs {
 };
 
 // Scratch of one call: the rows sorted by adapter, and what passes hand on. 256-byte aligned
-// regions, no fill needed.
+// regions, no fill needed; nothing at all for few rows (forward).
 struct AdapterWs {
   size_t order_off;      // int32 [rows] row of each sorted place, -1 for none
   size_t tile_off;       // int32 [tiles] adapter of each tile, L for rows without one

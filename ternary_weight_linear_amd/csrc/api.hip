@@ -863,7 +863,7 @@ int bl_adapter_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t l
   if (base)
     if (int st = check_rows_out(base, ydtype, N, ldbase)) return st;
   const size_t need = adapter_ws(M, L, R, K, N, false).total, size = dtype_bytes(dtype);
-  if (!ws || ws_bytes < need) return BL_ERR_WORKSPACE;
+  if (need && (!ws || ws_bytes < need)) return BL_ERR_WORKSPACE;
   if (!aligned_to(a, size) || !aligned_to(b, size) || !aligned_to(index, 4) || !aligned_to(scale, 4) ||
       !aligned_to(h, 4) || !aligned16(ws))
     return BL_ERR_ALIGN;

@@ -130,12 +130,15 @@ def test_adapter_checks(call):
     assert call(dtype=3) == ARG
     for name in ("ydtype",) if call is forward else ("dydtype", "dxdtype"):
         assert call(**{name: 0}) == ARG and call(**{name: 7}) == ARG         # neither x's type nor fp32
-    assert call(wsb=16) == WS and call(ws=None) == WS
-    for name, off in (("x", 1), ("a", 1), ("b", 1), ("index", 2), ("scale", 2), ("h", 2), ("base", 1), ("ws", 8)):
+    many = {} if call is backward else dict(M=1 << 17, wsb=1 << 28)       # a forward pass of few rows needs no workspace
+    assert call(**many | dict(wsb=16)) == WS and call(ws=None, **many) == WS
+    for name, off in (("x", 1), ("a", 1), ("b", 1), ("index", 2), ("scale", 2), ("h", 2), ("base", 1)):
         assert call(**{name: at[name] + off}) == ALIGN, name
+    assert call(ws=at["ws"] + 8, **many) == ALIGN
     out, ld = ("y", "ldy") if call is forward else ("dx", "lddx")
-    for name in ("x", "a", "b", "index", "scale", "h", "ws"):
+    for name in ("x", "a", "b", "index", "scale", "h"):
         assert call(**{out: at[name]}) == ALIAS, name
+    assert call(**{out: at["ws"]}, **many) == ALIAS
     assert call(base=at[out] + 2) == ALIAS                                   # neither out itself nor apart from it
     assert call(base=at[out], ldbase=128, **{ld: 64}) == ALIAS
 
@@ -175,7 +178,9 @@ def test_route_checks():
 def test_workspace_sizes():
     f = lib.bl_adapter_workspace_bytes
     assert f(0, 64, 64, 1, 1, 0) == 0 and f(1, 64, 64, 1, 257, 0) == 0 and f(1, 64, 64, 1025, 1, 1) == 0
-    assert 0 < f(1, 64, 64, 1, 1, 0) < f(4096, 64, 64, 1, 1, 0) < f(4096, 64, 64, 1, 1, 1)
+    assert f(1, 64, 64, 1, 1, 0) == 0 and f(4096, 64, 64, 1, 1, 0) == 0      # few rows, each by itself
+    assert 0 < f(1, 64, 64, 1, 1, 1) < f(4096, 64, 64, 1, 1, 1)
+    assert 0 < f(70000, 64, 64, 1, 1, 0) < f(70000, 64, 64, 1, 1, 1)
     # sorted places of 32 rows for each adapter at most, padded to tiles, with a rank of 16 or more
     assert f(4096, 8192, 8192, 64, 16, 0) >= (4096 + 32 * 65) * 17 * 4
     for R in (1, 15, 16, 17, 64, 65, 256):

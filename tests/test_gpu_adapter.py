@@ -22,6 +22,9 @@ u = 2.0 ** -24
 SHAPES = [(1, 1, 1, 1, 1), (1, 64, 128, 3, 16), (2, 8, 8, 1, 5), (5, 100, 36, 2, 3), (16, 4096, 1032, 6, 16), (31, 256, 130, 4, 8),
           (33, 129, 257, 3, 17), (64, 512, 384, 1, 33), (100, 72, 1000, 7, 48), (257, 640, 264, 5, 64), (300, 1001, 777, 3, 5),
           (500, 64, 96, 9, 65), (130, 200, 136, 2, 100), (70, 96, 80, 2, 256), (513, 2056, 512, 40, 12), (1100, 320, 1000, 2, 32)]
+# Enough values of adapters that the rows are sorted, tiles of few and many rows among them.
+SORTED = [(65600, 17, 9, 3, 2), (65536, 40, 130, 700, 5), (2100, 1001, 777, 5, 33), (900, 3000, 1544, 300, 40), (700, 2056, 1100, 2, 64),
+          (450, 1032, 400, 2, 256), (3000, 520, 520, 9, 48), (4100, 640, 1000, 3, 16), (2500, 4104, 1031, 1, 10)]
 PAIRS = [("fp16", "fp16"), ("fp16", "fp32"), ("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")]
 
 
@@ -103,7 +106,7 @@ class Case:
 
 
 @pytest.mark.parametrize("dtype,out", PAIRS)
-@pytest.mark.parametrize("M,K,N,L,R", SHAPES)
+@pytest.mark.parametrize("M,K,N,L,R", SHAPES + SORTED)
 def test_forward_and_backward(M, K, N, L, R, dtype, out):
     say("adapter", M, K, N, L, R, dtype, out)
     c = Case(M, K, N, L, R, dtype, out, M + 3 * K + 5 * N)
@@ -126,7 +129,7 @@ def test_without_base_scale_or_dx(dtype, out):
 
 
 @pytest.mark.parametrize("dtype,out", PAIRS)
-@pytest.mark.parametrize("M", [3, 90])
+@pytest.mark.parametrize("M", [3, 90, 66000])
 def test_in_place_equals_apart(dtype, out, M):
     say("adapter in place", dtype, out, M)
     c = Case(M, 264, 200, 3, 20, dtype, out, 2)
@@ -140,7 +143,7 @@ def test_in_place_equals_apart(dtype, out, M):
     assert torch.equal(dx, room) and torch.equal(da, da2) and torch.equal(db, db2)
 
 
-@pytest.mark.parametrize("M", [4, 77])
+@pytest.mark.parametrize("M", [4, 77, 66000])
 @pytest.mark.parametrize("shift", [8, 3])
 @pytest.mark.parametrize("dtype,out", PAIRS)
 def test_strided_and_unaligned_rows(dtype, out, shift, M):
@@ -180,7 +183,7 @@ def test_gradients_are_added_onto():
     assert np.array_equal(host(da)[2], dah[2]) and np.array_equal(host(db)[2], dbh[2])
 
 
-@pytest.mark.parametrize("M", [1, 40, 200])
+@pytest.mark.parametrize("M", [1, 40, 200, 70000])
 def test_no_row_has_an_adapter(M):
     say("adapter none", M)
     c = Case(M, 64, 72, 2, 8, "bf16", "bf16", 5)
@@ -192,7 +195,7 @@ def test_no_row_has_an_adapter(M):
     assert torch.equal(y, c.base) and torch.equal(dx, c.dbase) and not h.any() and not da.any() and not db.any()
 
 
-@pytest.mark.parametrize("M", [2, 70, 400])
+@pytest.mark.parametrize("M", [2, 70, 400, 66000])
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_nan_and_infinity_stay_in_their_rows_and_adapters(M, dtype):
     say("adapter nan", M, dtype)
@@ -227,7 +230,7 @@ def test_many_rows_and_adapters(M, L, kind):
     c.check_backward(c.backward(h), h)
 
 
-@pytest.mark.parametrize("M,K,N,L,R", [(3, 1024, 300, 2, 16), (48, 512, 264, 5, 16), (200, 640, 512, 1, 40), (700, 256, 136, 3, 8)])
+@pytest.mark.parametrize("M,K,N,L,R", [(3, 1024, 300, 2, 16), (48, 512, 264, 5, 16), (200, 640, 512, 1, 40), (700, 256, 136, 3, 8), (66000, 48, 40, 40, 8)])
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_exact_on_small_integers(M, K, N, L, R, dtype):
     """Sums of small whole numbers stay below 2^24 and come back exactly, whatever the order."""
@@ -252,7 +255,7 @@ def test_exact_on_small_integers(M, K, N, L, R, dtype):
 
 
 @pytest.mark.parametrize("dtype,out", PAIRS)
-@pytest.mark.parametrize("M", [9, 600])
+@pytest.mark.parametrize("M", [9, 600, 1300])
 def test_results_keep_the_precision_of_their_type(dtype, out, M):
     """Far below the worst case: errors of n roundings add up as their square root, so fp32 sums stay
     within 2^-19 of the root of their summed squares, and 16-bit results within 1.01 of their rounding."""
@@ -289,7 +292,7 @@ def test_same_bits_on_every_run_and_stream(M, L):
     assert all(torch.equal(a, b) for g in got for a, b in zip(first, g))
 
 
-@pytest.mark.parametrize("M", [1, 16, 300])
+@pytest.mark.parametrize("M", [1, 16, 300, 66000])
 def test_replayed_from_a_graph(M):
     """Two graphs and eager calls in turn, with new inputs and new adapters' rows between replays."""
     say("adapter graph", M)
