@@ -56,36 +56,73 @@ __device__ __forceinline__ Eight<DT> load_whole(const typename Elem<DT>::type* p
   }
   return v;
 }
+// Dwords v moved down by s (of N) dwords, zeros behind them.
+template <int N>
+__device__ __forceinline__ void move_down(uint32_t (&v)[N], int s) {
+#pragma unroll
+  for (int step = N / 2; step > 0; step >>= 1)
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = s & step ? (j + step < N ? v[j + step] : 0) : v[j];
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = s < N ? v[j] : 0;
+}
+// Values at .. at + N - 1 of a row of n as dwords; those from n on are 0. Where the row ends inside, its
+// last N values are loaded and moved down, so that no load is under a condition.
+template <int DT, int N>
+__device__ __forceinline__ void load_end(const typename Elem<DT>::type* row, int64_t at, int64_t n, uint32_t (&v)[N * sizeof(typename Elem<DT>::type) / 4]) {
+  constexpr int W = N * sizeof(*row) / 4;           // dwords
+  if (n < N) {                                      // uniform: a row shorter than a piece
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (at + j < n) {
+        if constexpr (DT == BL_F32) v[j] = __float_as_uint(row[at + j]);
+        else v[j / 2] |= static_cast<uint32_t>(row[at + j]) << (16 * (j & 1));
+      }
+    return;
+  }
+  const int64_t from = min(at, n - N);
+  const int s = static_cast<int>(min(at - from, static_cast<int64_t>(2 * N)));
+#pragma unroll
+  for (int j = 0; j < W; j += 4) {
+    const u32x4 w = *reinterpret_cast<const u32x4_any*>(row + from + 4 * j / static_cast<int>(sizeof(*row)));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[j + k] = w[k];
+  }
+  if constexpr (DT == BL_F32) {
+    move_down<W>(v, s);
+  } else {
+    move_down<W>(v, s / 2);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const uint32_t next = j + 1 < W ? v[j + 1] : 0;
+      v[j] = s & 1 ? __builtin_amdgcn_alignbit(next, v[j], 16) : v[j];
+    }
+  }
+}
 // Values at .. at + 7 of a row of n; those from n on are 0. WHOLE: there are none.
 template <int DT, bool WHOLE>
 __device__ __forceinline__ Eight<DT> load8(const typename Elem<DT>::type* row, int64_t at, int64_t n) {
   if constexpr (WHOLE) return load_whole<DT>(row + at);
-  Eight<DT> v{};
-  if (at + 8 <= n) {
-    v = load_whole<DT>(row + at);
-  } else if (at < n) {
+  uint32_t w[sizeof(Eight<DT>) / 4];
+  load_end<DT, 8>(row, at, n, w);
+  Eight<DT> v;
+  if constexpr (DT == BL_F32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (at + j < n) {
-        if constexpr (DT == BL_F32) v.w[j / 4][j % 4] = row[at + j];
-        else v.w[j / 2] |= static_cast<uint32_t>(row[at + j]) << (16 * (j & 1));
-      }
+    for (int j = 0; j < 8; ++j) v.w[j / 4][j % 4] = __uint_as_float(w[j]);
+  } else {
+    v.w = u32x4{w[0], w[1], w[2], w[3]};
   }
   return v;
 }
 // A piece of 16 bytes of a row, its first value at `at`; values from n on are 0.
 template <int DT, bool WHOLE>
 __device__ __forceinline__ u32x4 load16(const typename Elem<DT>::type* row, int64_t at, int64_t n) {
-  constexpr int V = 16 / sizeof(*row);
-  if (WHOLE || at + V <= n) return *reinterpret_cast<const u32x4_any*>(row + at);
-  u32x4 v{};
-#pragma unroll
-  for (int j = 0; j < V; ++j)
-    if (at + j < n) {
-      if constexpr (DT == BL_F32) v[j] = __float_as_uint(row[at + j]);
-      else v[j / 2] |= static_cast<uint32_t>(row[at + j]) << (16 * (j & 1));
-    }
-  return v;
+  if constexpr (WHOLE) return *reinterpret_cast<const u32x4_any*>(row + at);
+  uint32_t w[4];
+  load_end<DT, 16 / sizeof(*row)>(row, at, n, w);
+  return u32x4{w[0], w[1], w[2], w[3]};
 }
 template <int DT>
 __device__ __forceinline__ Eight<DT> zero_unless(bool keep, Eight<DT> v) {
@@ -845,7 +882,7 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
 // A workgroup has up to `tiles` tiles and 256 columns, its waves the tiles' halves. Tiles come after the
 // columns: rows are read and written whole by workgroups that run together.
 template <int WD, int YD, int KB>
-__global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
+__global__ __launch_bounds__(256, YD == BL_F32 ? 2 : 3) void adapter_expand_kernel(ExpandArgs a) {
   const int t = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t at = static_cast<int64_t>(t) * kTile + 16 * (wave & 1);
   int end = a.o.start[a.o.L + 1], word = a.o.tile[t], first = a.o.order[at], row[4];
@@ -871,7 +908,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
   const int count = min(a.tiles, tile_left(word) + 1);
   if (n0 >= a.N || (count == 1 && first < 0)) return;   // a half without rows
   if (n0 + 128 <= a.N) expand_tiles<WD, YD, KB, true>(a, at, count, e, n0, lane);
-  else expand_tiles<WD, YD, KB, false>(a, at, count, e, n0, lane);
+  else expand_tiles<WD, YD, 0, false>(a, at, count, e, n0, lane);   // the last columns: fewer registers
 }
 
 // ------------------------------------------------------------------------------------------
@@ -973,28 +1010,35 @@ struct OuterTile {
   }
 };
 
-// Tiles t, t + 4 .. before end: each is loaded while the one before is multiplied, its rows' numbers one
+// Tiles t, t + STEP .. before end: each is loaded while the one before is multiplied, its rows' numbers one
 // tile earlier still. Past the last tile the loads repeat it, so that none is under a condition.
-template <int SD, int NR, bool WHOLE>
+template <int SD, int NR, bool WHOLE, int STEP>
 __device__ __forceinline__ void outer_tiles(const OuterArgs& a, int t, int end, int64_t d, int r0, int c, int g, f32x4 (&acc)[NR][8]) {
   if (t >= end) return;
-  const int last = t + (end - 1 - t) / 4 * 4;
-  if constexpr (SD == BL_F32) {                     // no registers for two tiles
+  const int last = t + (end - 1 - t) / STEP * STEP;
+  if constexpr (SD == BL_F32 || !WHOLE) {           // no registers for two tiles
     OuterTile<SD, NR> v;
     int rows[8];
     v.load_rows(a, t, g);
-    for (; t <= last; t += 4) {
+    for (; t <= last; t += STEP) {
       v.template load<WHOLE>(a, t, d, r0, c, g);
 #pragma unroll
       for (int k = 0; k < 8; ++k) rows[k] = v.row[k];
-      v.load_rows(a, min(t + 4, last), g);
+      v.load_rows(a, min(t + STEP, last), g);
       v.multiply(rows, acc);
     }
     return;
   }
+  if (t == last) {                                  // the only one
+    OuterTile<SD, NR> v;
+    v.load_rows(a, t, g);
+    v.template load<WHOLE>(a, t, d, r0, c, g);
+    v.multiply(v.row, acc);
+    return;
+  }
   OuterTile<SD, NR> v[2];
   v[0].load_rows(a, t, g);
-  v[1].load_rows(a, min(t + 4, last), g);
+  v[1].load_rows(a, min(t + STEP, last), g);
   v[0].template load<WHOLE>(a, t, d, r0, c, g);
   for (;;)
 #pragma unroll
@@ -1004,16 +1048,16 @@ __device__ __forceinline__ void outer_tiles(const OuterArgs& a, int t, int end, 
 #pragma unroll
       for (int k = 0; k < 8; ++k) rows[k] = now.row[k];
       __builtin_amdgcn_sched_barrier(0);
-      next.template load<WHOLE>(a, min(t + 4, last), d, r0, c, g);
-      now.load_rows(a, min(t + 8, last), g);
+      next.template load<WHOLE>(a, min(t + STEP, last), d, r0, c, g);
+      now.load_rows(a, min(t + 2 * STEP, last), g);
       __builtin_amdgcn_sched_barrier(0);
       now.multiply(rows, acc);
-      if ((t += 4) > last) return;
+      if ((t += STEP) > last) return;
     }
 }
 
 template <int SD, int NR>
-__global__ __launch_bounds__(256, SD == BL_F32 ? 2 : 1) void adapter_outer_kernel(OuterArgs a) {
+__global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_outer_kernel(OuterArgs a) {
   __shared__ f32x4 red[16 * NR][32];
   __shared__ int last_one;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
@@ -1034,12 +1078,39 @@ __global__ __launch_bounds__(256, SD == BL_F32 ? 2 : 1) void adapter_outer_kerne
       if (a.o.start[e] == a.o.start[e + 1]) each([&](int, int64_t at) { a.grad[e * n + at] = 0.0f; });
 
   const int t1 = static_cast<int>(tiles * (blockIdx.y + 1) / a.splits);
+  int turn = 0;
   for (int t = static_cast<int>(tiles * blockIdx.y / a.splits); t < t1;) {
     const int e = tile_adapter(a.o.tile[t]), first = a.o.start[e], last = a.o.start[e + 1];
     const int end = min(last, t1);
+    float* grad = a.grad + e * n;
     f32x4 acc[NR][8] = {};
-    if (d0 + 128 <= a.D) outer_tiles<SD, NR, true>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
-    else outer_tiles<SD, NR, false>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
+    if (first >= t && last <= end && end - t <= 4) {
+      // an adapter of few tiles is one wave's, which writes it from its registers
+      if (turn++ % 4 == wave) {
+        if (d0 + 128 <= a.D) outer_tiles<SD, NR, true, 1>(a, t, end, d0 + 8 * c, r0, c, g, acc);
+        else outer_tiles<SD, NR, false, 1>(a, t, end, d0 + 8 * c, r0, c, g, acc);
+#pragma unroll
+        for (int q = 0; q < NR; ++q)
+#pragma unroll
+          for (int l = 0; l < 4; ++l) {
+            const int r = r0 + 16 * q + 4 * g + l;
+            if (r >= a.R) continue;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = acc[q][j][l];
+            if (a.add) {
+              const Eight<BL_F32> old = load8<BL_F32, false>(grad + r * a.D, d0 + 8 * c, a.D);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = value<BL_F32>(old, j) + v[j];
+            }
+            store8<BL_F32, false>(grad + r * a.D, d0 + 8 * c, a.D, v);
+          }
+      }
+      t = end;
+      continue;
+    }
+    if (d0 + 128 <= a.D) outer_tiles<SD, NR, true, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
+    else outer_tiles<SD, NR, false, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
     // the waves' sums, one after another
     for (int w = 0; w < 4; ++w) {
       if (wave == w) {
@@ -1056,7 +1127,6 @@ __global__ __launch_bounds__(256, SD == BL_F32 ? 2 : 1) void adapter_outer_kerne
       }
       __syncthreads();
     }
-    float* grad = a.grad + e * n;
     if (first >= t && last <= end) {
       each([&](int i, int64_t at) { grad[at] = a.add ? grad[at] + flat[i] : flat[i]; });
     } else {
@@ -1263,11 +1333,13 @@ int expand_tiles_of(int64_t M) { return M >= 2048 ? 4 : 1; }
 int by_chip(const AdapterRows& r) { return r.M >= 64 * kTile; }
 // Two workgroups to a CU, or the one that two tiles' registers of 16-bit values leave beyond rank 16. (us,
 // 4096 rows of 8192, bf16, rank 32: 22 for 256 workgroups, 32 for 384, 30 for 512, 44 for 1024.)
-int outer_splits(int64_t M, int64_t R, int64_t D, int dt) {
+int outer_splits(int64_t M, int64_t L, int64_t R, int64_t D, int dt) {
   const int64_t most = dt != BL_F32 && R > 16 ? 256 : 512, groups = div_up(D, 128) * div_up(rank_pad(R), 32);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most / groups, div_up(M, 4 * kTile), 32})));
+  // four tiles to a share at least, or four adapters, whose gradients are written even if they have no rows
+  const int64_t enough = std::max(div_up(M / kTile + std::min(M, L), 4), div_up(L, 4));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most / groups, enough, 32})));
 }
-int64_t outer_counters(int64_t M, int64_t R, int64_t D) { return outer_splits(M, R, D, BL_F32) * div_up(D, 128) * div_up(rank_pad(R), 32); }
+int64_t outer_counters(int64_t M, int64_t L, int64_t R, int64_t D) { return outer_splits(M, L, R, D, BL_F32) * div_up(D, 128) * div_up(rank_pad(R), 32); }
 
 // Bytes of each layout of the coefficients.
 struct CoefBytes {
@@ -1397,7 +1469,7 @@ AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool
   w.tile_off = take(tiles * 4);
   w.start_off = take((L + 2) * 4);
   w.count_off = take(M > kSortChunk ? div_up(M, kSortChunk) * (L + 1) * 4 : 0);
-  w.counters = tiles + (backward ? outer_counters(M, R, K) + outer_counters(M, R, N) : 0);
+  w.counters = tiles + (backward ? outer_counters(M, L, R, K) + outer_counters(M, L, R, N) : 0);
   w.arrived_off = take(w.counters * 4);
   w.part_off = take(shrink_splits(M, L, R, D) * rows * RP * 4);
   const size_t each[5] = {b.f, b.by_row, b.row_e, backward ? b.by_rank : 0, backward ? b.rank_e : 0};
@@ -1406,7 +1478,7 @@ AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool
     w.hc_off[0] = take(b.f);
     w.hc_off[3] = take(b.by_rank);
     w.hc_off[4] = take(b.rank_e);
-    w.sum_off = take(2 * std::max(outer_splits(M, R, K, BL_F32) * R * K, outer_splits(M, R, N, BL_F32) * R * N) * 4);
+    w.sum_off = take(2 * std::max(outer_splits(M, L, R, K, BL_F32) * R * K, outer_splits(M, L, R, N, BL_F32) * R * N) * 4);
   }
   w.total = off;
   return w;
@@ -1444,10 +1516,10 @@ hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipSt
     if (e != hipSuccess) return e;
   }
   uint32_t* arrived = w.arrived + tiles;
-  e = start_outer(OuterArgs{w.o, w.c, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.R, a.K, a.dtype), w.sum, arrived, a.da, a.add}, a.dtype, s);
+  e = start_outer(OuterArgs{w.o, w.c, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.L, r.R, a.K, a.dtype), w.sum, arrived, a.da, a.add}, a.dtype, s);
   if (e != hipSuccess) return e;
-  arrived += outer_counters(r.M, r.R, a.K);
-  return start_outer(OuterArgs{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.R, a.N, a.dydtype), w.sum, arrived, a.db, a.add}, a.dydtype, s);
+  arrived += outer_counters(r.M, r.L, r.R, a.K);
+  return start_outer(OuterArgs{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.L, r.R, a.N, a.dydtype), w.sum, arrived, a.db, a.add}, a.dydtype, s);
 }
 
 }  // namespace bl
