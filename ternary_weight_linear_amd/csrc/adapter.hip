@@ -140,15 +140,16 @@ __device__ __forceinline__ uint16_t bits16(float v) {
   return DT == BL_BF16 ? bf16_bits(v) : half_bits(v);
 }
 
-template <int DT, bool WHOLE>
-__device__ __forceinline__ void store8(typename Elem<DT>::type* row, int64_t at, int64_t n, const float (&v)[8]) {
+// Places lo .. n - 1 of a row alone.
+template <int DT>
+__device__ __forceinline__ void store8(typename Elem<DT>::type* row, int64_t at, int64_t lo, int64_t n, const float (&v)[8]) {
   if constexpr (DT == BL_F32) {
-    if (WHOLE || at + 8 <= n) {
+    if (at >= lo && at + 8 <= n) {
       *reinterpret_cast<f32x4_any*>(row + at) = f32x4{v[0], v[1], v[2], v[3]};
       *reinterpret_cast<f32x4_any*>(row + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
       return;
     }
-  } else if (WHOLE || at + 8 <= n) {
+  } else if (at >= lo && at + 8 <= n) {
     u32x4 w;
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = bits16<DT>(v[2 * j]) | static_cast<uint32_t>(bits16<DT>(v[2 * j + 1])) << 16;
@@ -157,7 +158,7 @@ __device__ __forceinline__ void store8(typename Elem<DT>::type* row, int64_t at,
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (at + j < n) {
+    if (at + j >= lo && at + j < n) {
       if constexpr (DT == BL_F32) row[at + j] = v[j];
       else row[at + j] = bits16<DT>(v[j]);
     }
@@ -747,8 +748,8 @@ __device__ __forceinline__ void load_base(const ExpandArgs& a, const int (&row)[
   for (int l = 0; l < 4; ++l)                       // a place without a row reads row 0
     base[l] = load8<YD, WHOLE>(static_cast<const Y*>(a.base) + max(row[l], 0) * a.ldbase, n, a.N);
 }
-template <int WD, int YD, bool WHOLE>
-__device__ __forceinline__ void store_rows(const ExpandArgs& a, const int (&row)[4], int64_t n, const Eight<YD> (&base)[4],
+template <int WD, int YD>
+__device__ __forceinline__ void store_rows(const ExpandArgs& a, const int (&row)[4], int64_t n, int64_t lo, const Eight<YD> (&base)[4],
                                            const f32x4 (&acc)[8], const int (&ex)[4]) {
   using Y = typename Elem<YD>::type;
 #pragma unroll
@@ -761,12 +762,12 @@ __device__ __forceinline__ void store_rows(const ExpandArgs& a, const int (&row)
       if constexpr (WD == BL_F16) v[j] = ldexpf(v[j], ex[l]);
       if (a.base) v[j] = value<YD>(base[l], j) + v[j];
     }
-    store8<YD, WHOLE>(static_cast<Y*>(a.y) + row[l] * a.ldy, n, a.N, v);
+    store8<YD>(static_cast<Y*>(a.y) + row[l] * a.ldy, n, lo, a.N, v);
   }
 }
 // Rows without an adapter are base's.
 template <int YD, bool WHOLE>
-__device__ __forceinline__ void copy_rows(const ExpandArgs& a, const int (&row)[4], int64_t n) {
+__device__ __forceinline__ void copy_rows(const ExpandArgs& a, const int (&row)[4], int64_t n, int64_t lo) {
   using Y = typename Elem<YD>::type;
   Eight<YD> base[4] = {};
   load_base<YD, WHOLE>(a, row, n, base);
@@ -775,14 +776,14 @@ __device__ __forceinline__ void copy_rows(const ExpandArgs& a, const int (&row)[
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = value<YD>(base[l], j);
-    if (row[l] >= 0) store8<YD, WHOLE>(static_cast<Y*>(a.y) + row[l] * a.ldy, n, a.N, v);
+    if (row[l] >= 0) store8<YD>(static_cast<Y*>(a.y) + row[l] * a.ldy, n, lo, a.N, v);
   }
 }
 
 // The rows of up to `count` tiles. KB blocks of 32 ranks of w stay in registers over them; 0: any rank, w is
 // loaded again for each tile (fp32: always so).
 template <int WD, int YD, int KB, bool WHOLE>
-__device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, int count, int e, int64_t n0, int lane) {
+__device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, int count, int e, int64_t n0, int64_t lo, int lane) {
   const int c = lane & 15, g = lane >> 4;
   const int64_t n = n0 + 8 * c;
   using W = typename Elem<WD>::type;
@@ -870,7 +871,7 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
     }
     Eight<YD> more[4] = {};
     load_base<YD, WHOLE>(a, next, n, more);
-    store_rows<WD, YD, WHOLE>(a, row, n, base, acc, ex);
+    store_rows<WD, YD>(a, row, n, lo, base, acc, ex);
 #pragma unroll
     for (int l = 0; l < 4; ++l) {
       row[l] = next[l];
@@ -892,23 +893,25 @@ __global__ __launch_bounds__(256, YD == BL_F32 ? 2 : 3) void adapter_expand_kern
   if (t >= end) return;
   word = __builtin_amdgcn_readfirstlane(word);
   const int e = tile_adapter(word);
-  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * 2 + (wave >> 1)) * 128, n = n0 + 8 * (lane & 15);
+  // the last columns are taken with those before them, to be 128, and stored alone
+  const int64_t lo = (static_cast<int64_t>(blockIdx.x) * 2 + (wave >> 1)) * 128, n0 = max(min(lo, a.N - 128), int64_t(0));
+  const int64_t n = n0 + 8 * (lane & 15);
   if (e >= a.o.L) {
     if (a.h && blockIdx.x == 0)
       for (int i = threadIdx.x; i < kTile * a.R; i += 256) {
         const int m = a.o.order[static_cast<int64_t>(t) * kTile + i / a.R];
         if (m >= 0) a.h[static_cast<int64_t>(m) * a.R + i % a.R] = 0.0f;
       }
-    if (a.base == a.y || n0 >= a.N) return;
-    if (n0 + 128 <= a.N) copy_rows<YD, true>(a, row, n);
-    else copy_rows<YD, false>(a, row, n);
+    if (a.base == a.y || lo >= a.N) return;
+    if (a.N >= 128) copy_rows<YD, true>(a, row, n, lo);
+    else copy_rows<YD, false>(a, row, n, lo);
     return;
   }
   if (tile_pos(word) % a.tiles) return;
   const int count = min(a.tiles, tile_left(word) + 1);
-  if (n0 >= a.N || (count == 1 && first < 0)) return;   // a half without rows
-  if (n0 + 128 <= a.N) expand_tiles<WD, YD, KB, true>(a, at, count, e, n0, lane);
-  else expand_tiles<WD, YD, 0, false>(a, at, count, e, n0, lane);   // the last columns: fewer registers
+  if (lo >= a.N || (count == 1 && first < 0)) return;   // a half without rows
+  if (a.N >= 128) expand_tiles<WD, YD, KB, true>(a, at, count, e, n0, lo, lane);
+  else expand_tiles<WD, YD, 0, false>(a, at, count, e, n0, lo, lane);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -1061,14 +1064,15 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
   __shared__ f32x4 red[16 * NR][32];
   __shared__ int last_one;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
-  const int64_t d0 = static_cast<int64_t>(blockIdx.x) * 128;
+  // the last columns are taken with those before them, to be 128, and written alone
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * 128, d0 = max(min(lo, a.D - 128), int64_t(0));
   const int r0 = blockIdx.z * 16 * NR;
   const int64_t tiles = a.o.start[a.o.L], n = static_cast<int64_t>(a.R) * a.D;
   const auto each = [&](auto f) {                   // of this workgroup's values: (row and column in red, place in [R, D])
     for (int i = tid; i < 16 * NR * 128; i += 256) {
       const int r = r0 + i / 128;
       const int64_t d = d0 + i % 128;
-      if (r < a.R && d < a.D) f(i, r * a.D + d);
+      if (r < a.R && d >= lo && d < a.D) f(i, r * a.D + d);
     }
   };
   float* flat = reinterpret_cast<float*>(red);
@@ -1077,17 +1081,18 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
     for (int e = blockIdx.y; e < a.o.L; e += a.splits)
       if (a.o.start[e] == a.o.start[e + 1]) each([&](int, int64_t at) { a.grad[e * n + at] = 0.0f; });
 
-  const int t1 = static_cast<int>(tiles * (blockIdx.y + 1) / a.splits);
+  const int t0 = static_cast<int>(tiles * blockIdx.y / a.splits), t1 = static_cast<int>(tiles * (blockIdx.y + 1) / a.splits);
+  const int few = max(4, (t1 - t0) / 4);
   int turn = 0;
-  for (int t = static_cast<int>(tiles * blockIdx.y / a.splits); t < t1;) {
+  for (int t = t0; t < t1;) {
     const int e = tile_adapter(a.o.tile[t]), first = a.o.start[e], last = a.o.start[e + 1];
     const int end = min(last, t1);
     float* grad = a.grad + e * n;
     f32x4 acc[NR][8] = {};
-    if (first >= t && last <= end && end - t <= 4) {
-      // an adapter of few tiles is one wave's, which writes it from its registers
+    if (first >= t && last <= end && end - t <= few) {
+      // an adapter of few of the share's tiles is one wave's, which writes it from its registers
       if (turn++ % 4 == wave) {
-        if (d0 + 128 <= a.D) outer_tiles<SD, NR, true, 1>(a, t, end, d0 + 8 * c, r0, c, g, acc);
+        if (a.D >= 128) outer_tiles<SD, NR, true, 1>(a, t, end, d0 + 8 * c, r0, c, g, acc);
         else outer_tiles<SD, NR, false, 1>(a, t, end, d0 + 8 * c, r0, c, g, acc);
 #pragma unroll
         for (int q = 0; q < NR; ++q)
@@ -1103,13 +1108,13 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
 #pragma unroll
               for (int j = 0; j < 8; ++j) v[j] = value<BL_F32>(old, j) + v[j];
             }
-            store8<BL_F32, false>(grad + r * a.D, d0 + 8 * c, a.D, v);
+            store8<BL_F32>(grad + r * a.D, d0 + 8 * c, lo, a.D, v);
           }
       }
       t = end;
       continue;
     }
-    if (d0 + 128 <= a.D) outer_tiles<SD, NR, true, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
+    if (a.D >= 128) outer_tiles<SD, NR, true, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
     else outer_tiles<SD, NR, false, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
     // the waves' sums, one after another
     for (int w = 0; w < 4; ++w) {
@@ -1150,7 +1155,7 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
           for (int i = 0; i < 8; ++i) {
             const int k = i0 + 256 * i, r = r0 + k / 128;
             const int64_t d = d0 + k % 128;
-            here[i] = r < a.R && d < a.D;
+            here[i] = r < a.R && d >= lo && d < a.D;
             at[i] = here[i] ? r * a.D + d : static_cast<int64_t>(min(r0, a.R - 1)) * a.D;
           }
           for (int q = 0; q < parts; q += 4) {
@@ -1329,7 +1334,8 @@ int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
   const int64_t groups = max_tiles(M, L) * div_up(rank_pad(R), 64), most = R <= 32 ? 300 : 448;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most / groups, div_up(D, 64) / (2 * kShrinkWaves), 16})));
 }
-int expand_tiles_of(int64_t M) { return M >= 2048 ? 4 : 1; }
+// Tiles of a workgroup of the product along the long axis: as many as leave 1024 workgroups or so.
+int expand_tiles_of(int64_t M, int64_t N) { return M * N >= int64_t(1) << 25 ? 4 : M * N >= int64_t(1) << 24 ? 2 : 1; }
 int by_chip(const AdapterRows& r) { return r.M >= 64 * kTile; }
 // Two workgroups to a CU, or the one that two tiles' registers of 16-bit values leave beyond rank 16. (us,
 // 4096 rows of 8192, bf16, rank 32: 22 for 256 workgroups, 32 for 384, 30 for 512, 44 for 1024.)
@@ -1496,7 +1502,7 @@ hipError_t launch_adapter_forward(const AdapterForwardArgs& a, char* ws, hipStre
   ShrinkArgs p{w.o, a.x, a.K, a.ldx, a.a, R, RP, splits, by_chip(r), w.part, w.arrived, a.scale, a.h, nullptr, only(w.c, a.dtype, true, false), {}};
   e = start_shrink(p, a.dtype, a.dtype, tiles, s);
   if (e != hipSuccess) return e;
-  return start_expand(ExpandArgs{w.o, w.c, R, RP, a.h, a.b, a.N, a.base, a.ldbase, a.y, a.ldy, expand_tiles_of(r.M)}, a.dtype, a.ydtype, tiles, s);
+  return start_expand(ExpandArgs{w.o, w.c, R, RP, a.h, a.b, a.N, a.base, a.ldbase, a.y, a.ldy, expand_tiles_of(r.M, a.N)}, a.dtype, a.ydtype, tiles, s);
 }
 
 hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipStream_t s) {
@@ -1512,7 +1518,7 @@ hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipSt
   e = start_shrink(p, a.dydtype, a.dtype, tiles, s);
   if (e != hipSuccess) return e;
   if (a.dx) {
-    e = start_expand(ExpandArgs{w.o, w.c, R, RP, nullptr, a.a, a.K, a.base, a.ldbase, a.dx, a.lddx, expand_tiles_of(r.M)}, a.dtype, a.dxdtype, tiles, s);
+    e = start_expand(ExpandArgs{w.o, w.c, R, RP, nullptr, a.a, a.K, a.base, a.ldbase, a.dx, a.lddx, expand_tiles_of(r.M, a.K)}, a.dtype, a.dxdtype, tiles, s);
     if (e != hipSuccess) return e;
   }
   uint32_t* arrived = w.arrived + tiles;
