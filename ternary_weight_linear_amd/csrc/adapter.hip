@@ -929,9 +929,14 @@ struct OuterArgs {
   int64_t D, ld;
   int R, RP, splits;
   float* sum;             // [2 splits, R, D]
-  uint32_t* arrived;      // [splits, z, x]
+  uint32_t* arrived;      // [splits, blocks of ranks, blocks of columns]
   float* grad;            // [L, R, D]
   int add;
+};
+// One launch takes both sums where x and dy have one type: the first `columns` workgroups along x are p[0]'s.
+struct OuterPair {
+  OuterArgs p[2];
+  uint32_t columns;
 };
 
 // What a wave takes of a tile: lane 16 g + c rows 8 g .. 8 g + 7 (fp32: 4 i + g), columns 8 c .. 8 c + 7.
@@ -1060,12 +1065,16 @@ __device__ __forceinline__ void outer_tiles(const OuterArgs& a, int t, int end, 
 }
 
 template <int SD, int NR>
-__global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_outer_kernel(OuterArgs a) {
+__global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_outer_kernel(OuterPair pair) {
   __shared__ f32x4 red[16 * NR][32];
   __shared__ int last_one;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
+  const bool second = blockIdx.x >= pair.columns;
+  const OuterArgs& a = pair.p[second];
+  const uint32_t column = second ? blockIdx.x - pair.columns : blockIdx.x;
+  if (static_cast<int>(blockIdx.y) >= a.splits) return;
   // the last columns are taken with those before them, to be 128, and written alone
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * 128, d0 = max(min(lo, a.D - 128), int64_t(0));
+  const int64_t lo = static_cast<int64_t>(column) * 128, d0 = max(min(lo, a.D - 128), int64_t(0));
   const int r0 = blockIdx.z * 16 * NR;
   const int64_t tiles = a.o.start[a.o.L], n = static_cast<int64_t>(a.R) * a.D;
   const auto each = [&](auto f) {                   // of this workgroup's values: (row and column in red, place in [R, D])
@@ -1142,7 +1151,7 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
       // the share of tile t is the largest s whose first tile, floor(s tiles / splits), is not past t
       const int64_t s0 = ((first + 1ll) * a.splits - 1) / tiles, s1 = (static_cast<int64_t>(last) * a.splits - 1) / tiles;
       if (tid == 0)
-        last_one = arrive_agent(a.arrived + (s0 * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x) == static_cast<uint32_t>(s1 - s0);
+        last_one = arrive_agent(a.arrived + (s0 * gridDim.z + blockIdx.z) * ((a.D + 127) / 128) + column) == static_cast<uint32_t>(s1 - s0);
       __syncthreads();
       if (last_one) {
         // eight places' values of four shares in flight at a time
@@ -1339,13 +1348,16 @@ int expand_tiles_of(int64_t M, int64_t N) { return M * N >= int64_t(1) << 25 ? 4
 int by_chip(const AdapterRows& r) { return r.M >= 64 * kTile; }
 // Two workgroups to a CU, or the one that two tiles' registers of 16-bit values leave beyond rank 16. (us,
 // 4096 rows of 8192, bf16, rank 32: 22 for 256 workgroups, 32 for 384, 30 for 512, 44 for 1024.)
-int outer_splits(int64_t M, int64_t L, int64_t R, int64_t D, int dt) {
-  const int64_t most = dt != BL_F32 && R > 16 ? 256 : 512, groups = div_up(D, 128) * div_up(rank_pad(R), 32);
+// `blocks`: of 128 columns, of all that one launch takes.
+int outer_splits(int64_t M, int64_t L, int64_t R, int64_t blocks, int dt) {
+  const int64_t most = dt != BL_F32 && R > 16 ? 256 : 512, groups = blocks * div_up(rank_pad(R), 32);
   // four tiles to a share at least, or four adapters, whose gradients are written even if they have no rows
   const int64_t enough = std::max(div_up(M / kTile + std::min(M, L), 4), div_up(L, 4));
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most / groups, enough, 32})));
 }
-int64_t outer_counters(int64_t M, int64_t L, int64_t R, int64_t D) { return outer_splits(M, L, R, D, BL_F32) * div_up(D, 128) * div_up(rank_pad(R), 32); }
+// The most that either sum takes by itself.
+int64_t outer_shares(int64_t M, int64_t L, int64_t R, int64_t D) { return outer_splits(M, L, R, div_up(D, 128), BL_F32); }
+int64_t outer_counters(int64_t M, int64_t L, int64_t R, int64_t D) { return outer_shares(M, L, R, D) * div_up(D, 128) * div_up(rank_pad(R), 32); }
 
 // Bytes of each layout of the coefficients.
 struct CoefBytes {
@@ -1364,7 +1376,7 @@ struct Scratch {
   int32_t* start;
   int32_t* counts;
   uint32_t* arrived;
-  float *part, *sum;
+  float *part, *sum[2];
   Coefs c, hc;
 };
 Scratch scratch(const AdapterWs& L, char* ws, const AdapterRows& r) {
@@ -1375,7 +1387,7 @@ Scratch scratch(const AdapterWs& L, char* ws, const AdapterRows& r) {
   s.counts = reinterpret_cast<int32_t*>(ws + L.count_off);
   s.arrived = reinterpret_cast<uint32_t*>(ws + L.arrived_off);
   s.part = reinterpret_cast<float*>(ws + L.part_off);
-  s.sum = reinterpret_cast<float*>(ws + L.sum_off);
+  for (int i = 0; i < 2; ++i) s.sum[i] = reinterpret_cast<float*>(ws + L.sum_off[i]);
   s.o = Sorted{s.order, s.tile, s.start, static_cast<int>(r.L), max_tiles(r.M, r.L) * kTile};
   const auto coefs = [&](const size_t (&at)[5]) {
     return Coefs{reinterpret_cast<float*>(ws + at[0]), reinterpret_cast<uint16_t*>(ws + at[1]), reinterpret_cast<int32_t*>(ws + at[2]),
@@ -1439,14 +1451,14 @@ hipError_t start_expand(const ExpandArgs& a, int wd, int yd, int64_t tiles, hipS
 }
 
 template <int SD>
-hipError_t start_outer_as(const OuterArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<uint32_t>(div_up(a.D, 128)), a.splits, static_cast<uint32_t>(div_up(a.RP, 32)));
-  if (a.RP == 16) adapter_outer_kernel<SD, 1><<<grid, 256, 0, s>>>(a);
+hipError_t start_outer_as(const OuterPair& a, uint32_t columns, hipStream_t s) {
+  const dim3 grid(columns, std::max(a.p[0].splits, a.p[1].splits), static_cast<uint32_t>(div_up(a.p[0].RP, 32)));
+  if (a.p[0].RP == 16) adapter_outer_kernel<SD, 1><<<grid, 256, 0, s>>>(a);
   else adapter_outer_kernel<SD, 2><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
-hipError_t start_outer(const OuterArgs& a, int sd, hipStream_t s) {
-  return sd == BL_F16 ? start_outer_as<BL_F16>(a, s) : sd == BL_BF16 ? start_outer_as<BL_BF16>(a, s) : start_outer_as<BL_F32>(a, s);
+hipError_t start_outer(const OuterPair& a, uint32_t columns, int sd, hipStream_t s) {
+  return sd == BL_F16 ? start_outer_as<BL_F16>(a, columns, s) : sd == BL_BF16 ? start_outer_as<BL_BF16>(a, columns, s) : start_outer_as<BL_F32>(a, columns, s);
 }
 
 // The layouts that a value of type dt is multiplied by: fp32 for fp32, else parts.
@@ -1484,7 +1496,8 @@ AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool
     w.hc_off[0] = take(b.f);
     w.hc_off[3] = take(b.by_rank);
     w.hc_off[4] = take(b.rank_e);
-    w.sum_off = take(2 * std::max(outer_splits(M, L, R, K, BL_F32) * R * K, outer_splits(M, L, R, N, BL_F32) * R * N) * 4);
+    w.sum_off[0] = take(2 * outer_shares(M, L, R, K) * R * K * 4);
+    w.sum_off[1] = take(2 * outer_shares(M, L, R, N) * R * N * 4);
   }
   w.total = off;
   return w;
@@ -1522,10 +1535,15 @@ hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipSt
     if (e != hipSuccess) return e;
   }
   uint32_t* arrived = w.arrived + tiles;
-  e = start_outer(OuterArgs{w.o, w.c, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.L, r.R, a.K, a.dtype), w.sum, arrived, a.da, a.add}, a.dtype, s);
+  const int64_t kb = div_up(a.K, 128), nb = div_up(a.N, 128);
+  const bool one = a.dtype == a.dydtype;            // one launch
+  OuterArgs da{w.o, w.c, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.L, r.R, one ? kb + nb : kb, a.dtype), w.sum[0], arrived, a.da, a.add};
+  OuterArgs db{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.L, r.R, one ? kb + nb : nb, a.dydtype), w.sum[1],
+               arrived + outer_counters(r.M, r.L, r.R, a.K), a.db, a.add};
+  if (one) return start_outer(OuterPair{{da, db}, static_cast<uint32_t>(kb)}, static_cast<uint32_t>(kb + nb), a.dtype, s);
+  e = start_outer(OuterPair{{da, da}, static_cast<uint32_t>(kb)}, static_cast<uint32_t>(kb), a.dtype, s);
   if (e != hipSuccess) return e;
-  arrived += outer_counters(r.M, r.L, r.R, a.K);
-  return start_outer(OuterArgs{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.L, r.R, a.N, a.dydtype), w.sum, arrived, a.db, a.add}, a.dydtype, s);
+  return start_outer(OuterPair{{db, db}, static_cast<uint32_t>(nb)}, static_cast<uint32_t>(nb), a.dydtype, s);
 }
 
 }  // namespace bl

@@ -65,7 +65,7 @@ struct AdapterWs {
   size_t part_off;       // fp32 [splits, rows, RP] partial sums of the products over K or N
   size_t c_off[5];       // the scaled h (forward) or dh, sorted, in each layout that is needed
   size_t hc_off[5];      // the scaled h (backward)
-  size_t sum_off;        // fp32 [2 splits, R, D] partial sums over rows (backward)
+  size_t sum_off[2];     // fp32 [2 shares, R, D] partial sums over rows, of da and of db (backward)
   size_t total;
 };
 AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool backward);

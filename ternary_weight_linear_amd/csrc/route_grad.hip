@@ -131,7 +131,7 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* offsets, int64_t S
 // ------------------------------------------------------------------------------------------
 // balance loss
 // ------------------------------------------------------------------------------------------
-// A workgroup sums a chunk of rows, sequence by sequence. Going from chunk to chunk and sequence
+// A workgroup sums a chunk of rows, sequence by sequence (those of a chunk are shared out over up to 16). Going from chunk to chunk and sequence
 // to sequence, either number grows at each step: chunk + sequence numbers the partial sums.
 struct BalanceParts {
   int64_t chunk, chunks;
@@ -150,7 +150,8 @@ __global__ __launch_bounds__(balance_threads(LANES)) void route_balance_kernel(R
   __shared__ int counted[W];
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, wave = threadIdx.x / 64, E = static_cast<int>(r.E);
   const int64_t c0 = blockIdx.x * w.chunk, c1 = min(c0 + w.chunk, r.M);
-  for (int64_t s = r.offsets ? sequence_of<64>(r.offsets, r.S, c0, threadIdx.x & 63) : 0; s < r.S; ++s) {
+  const int64_t s0 = r.offsets ? sequence_of<64>(r.offsets, r.S, c0, threadIdx.x & 63) : 0;
+  for (int64_t s = s0 + blockIdx.y; s < r.S; s += gridDim.y) {
     const int64_t begin = r.offsets ? bounded(r.offsets, s, r.M) : 0, end = r.offsets ? bounded(r.offsets, s + 1, r.M) : r.M;
     if (begin >= c1) break;
     const int64_t m0 = max(begin, c0), m1 = min(end, c1);
@@ -486,7 +487,7 @@ BalanceWs balance_ws(int64_t M, int64_t E, int64_t S) {
 
 template <int DT, int LANES, int NE, int V>
 hipError_t start_balance(const RouteRows& r, const BalanceParts& w, hipStream_t s) {
-  const auto grid = static_cast<uint32_t>(w.chunks);
+  const dim3 grid(static_cast<uint32_t>(w.chunks), static_cast<uint32_t>(std::min<int64_t>(r.S, 16)));
   constexpr int T = balance_threads(LANES);
   if (r.sigmoid) route_balance_kernel<DT, LANES, NE, V, true><<<grid, T, 0, s>>>(r, w);
   else route_balance_kernel<DT, LANES, NE, V, false><<<grid, T, 0, s>>>(r, w);
