@@ -1,7 +1,8 @@
 /*
- * libbitlinear — ternary (BitNet b1.58) and sign-only (OneBit) linear layers, and 8-bit
- * floating point ones with the routing to experts built on them, for AMD Instinct MI355X
- * (gfx950), as a C ABI over hand-written HIP kernels.
+ * libbitlinear — ternary (BitNet b1.58) and sign-only (OneBit) linear layers, 8-bit floating
+ * point ones with the routing to experts built on them, and the low-rank adapters and router's
+ * gradients that train beside such frozen weights, for AMD Instinct MI355X (gfx950), as a C ABI
+ * over hand-written HIP kernels.
  *
  * Sources (cited by page title and section):
  *  [b158]   "微软、国科大开启1Bit时代：大模型转三进制，速度快4倍能耗降至1/41" — BitNet b1.58
@@ -447,8 +448,9 @@ int bl_fp8_experts(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
  * holds the transpose of an nn.Linear weight [N, R]; an adapter of a lower rank has rows of zeros.
  * scale fp32 [L], or NULL for 1. A row whose index is outside [0, L) has no adapter. ydtype (dydtype,
  * dxdtype) is x's dtype or BL_F32. 1 <= M <= 2^20, 1 <= K, N <= 2^24, 1 <= R <= 256, 1 <= L <= 1024.
- * Sums are fp32 sums of exact products (a 16-bit value times an fp32 one is rounded to fp32 once), in
- * a fixed order for a given shape and index. Uses ws (bl_adapter_workspace_bytes; the last argument says
+ * Sums are fp32 sums, in a fixed order for a given shape and index, of products rounded to fp32 at
+ * most; h and dh go into their second product whole (fp32, bf16) or, for fp16, with 22 bits or more below
+ * the largest of their row (dx, y) or of their rank in 32 rows (da, db). Uses ws (bl_adapter_workspace_bytes; the last argument says
  * which call it is for; 0 where a forward pass of few rows needs none, and for sizes that are refused). */
 size_t bl_adapter_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t R,
                                   int backward);
@@ -483,8 +485,8 @@ int bl_adapter_backward(const void* x, int dtype, int64_t M, int64_t K, int64_t 
  * row's p, and for each sequence count[e] slots of expert e, C slots in all, T rows that count:
  *   coef[e] = E count[e] / (C T),   loss = sum over e of coef[e] times the sum of t[m, e] over those rows
  * (1 for an even load; an empty sequence gives zeros). Outputs: loss fp32 [S], count int32 [S, E],
- * coef fp32 [S, E], which is the loss's derivative by t. Sums over rows are fp32 within about M / 512
- * rows and fp64 over those, in a fixed order. E <= 2048, k <= 64, M k < 2^31, S <= 2^20. Uses ws. */
+ * coef fp32 [S, E], which is the loss's derivative by t. Sums over rows are fp32 within a chunk of about
+ * M / 128 rows and fp64 over chunks, in a fixed order. E <= 2048, k <= 64, M k < 2^31, S <= 2^20. Uses ws. */
 size_t bl_route_balance_workspace_bytes(int64_t M, int64_t E, int64_t S);
 int bl_route_balance(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
                      const int32_t* index, int64_t k, int score, const int32_t* offsets, int64_t S,

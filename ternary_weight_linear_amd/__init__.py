@@ -1,6 +1,6 @@
 """Python binding of libbitlinear: BitNet b1.58 ternary, OneBit sign-only,
 residual-binarised and 8-bit floating point linear layers, expert routing and experts'
-products on MI355X (gfx950).
+products, and low-rank adapters and the router's training beside them on MI355X (gfx950).
 
 Every function here only marshals arguments: it checks tensor dtypes, devices and
 contiguity, allocates outputs with torch (device memory is PyTorch's job) and calls the

@@ -132,7 +132,9 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* offsets, int64_t S
 // balance loss
 // ------------------------------------------------------------------------------------------
 // A workgroup sums a chunk of rows, sequence by sequence (those of a chunk are shared out over up to 16). Going from chunk to chunk and sequence
-// to sequence, either number grows at each step: chunk + sequence numbers the partial sums.
+// to sequence, either number grows at each step: chunk + sequence numbers the partial sums. 16384 x
+// 256, sigmoid, 11 sequences: 11 us in the trace (17 MB; scores are an exponential and a quotient each), its finish
+// 7; 4096 x 60: 4.6 and 6.3, two chains of waits.
 struct BalanceParts {
   int64_t chunk, chunks;
   float* t;               // [chunks + S - 1, E]
@@ -297,7 +299,9 @@ __global__ __launch_bounds__(1024) void route_balance_finish_kernel(RouteRows r,
 //   softmax   u_j (g_j - sum u g)    sigmoid   u_j (1 - p_j) (g_j - sum u g)       renormalised
 //   softmax   p_j g_j                sigmoid   p_j (1 - p_j) g_j                   else,
 // a softmax that is not renormalised takes p_e sum_j p_j g_j from every expert, and the balance
-// loss adds t_e (c_e - sum t c), times 1 - p_e for sigmoid scores, with c = dloss coef.
+// loss adds t_e (c_e - sum t c), times 1 - p_e for sigmoid scores, with c = dloss coef. A row is read and
+// written once: 16384 x 256, sigmoid, 12 us (33.5 MB, 2.8 TB/s; the scores' VALU work and three passes through
+// LDS beside it), 4096 x 60 4.
 template <int DT, int LANES, int NE, int V, bool SIGMOID, int KS>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs a) {
   constexpr int G = 256 / LANES;
