@@ -1354,7 +1354,9 @@ int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
   const int64_t groups = max_tiles(M, L) * div_up(rank_pad(R), 64), most = R <= 32 ? 300 : 448;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most / groups, div_up(D, 64) / (2 * kShrinkWaves), 16})));
 }
-// Tiles of a workgroup of the product along the long axis: as many as leave 1024 workgroups or so.
+// Tiles of a workgroup of the product along the long axis: as many as leave 1024 workgroups or so. (us for 1 / 2 / 4 / 8,
+// bf16: 4096 x 8192, rank 64 42 / 38 / 38 / 42, rank 32 34 / 31 / 32 / 36; 777 x 3200, rank 12, fp32 results 7.4 / 9.2 for
+// 1 / 2.)
 int expand_tiles_of(int64_t M, int64_t N) { return M * N >= int64_t(1) << 25 ? 4 : M * N >= int64_t(1) << 24 ? 2 : 1; }
 int by_chip(const AdapterRows& r) { return r.M >= 64 * kTile; }
 // Two workgroups to a CU, or the one that two tiles' registers of 16-bit values leave beyond rank 16. (us,
@@ -1541,20 +1543,23 @@ hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipSt
                only(w.c, a.dtype, a.dx != nullptr, true), only(w.hc, a.dydtype, false, true)};
   e = start_shrink(p, a.dydtype, a.dtype, tiles, s);
   if (e != hipSuccess) return e;
-  if (a.dx) {
-    e = start_expand(ExpandArgs{w.o, w.c, R, RP, nullptr, a.a, a.K, a.base, a.ldbase, a.dx, a.lddx, expand_tiles_of(r.M, a.K)}, a.dtype, a.dxdtype, tiles, s);
-    if (e != hipSuccess) return e;
-  }
   uint32_t* arrived = w.arrived + tiles;
   const int64_t kb = div_up(a.K, 128), nb = div_up(a.N, 128);
   const bool one = a.dtype == a.dydtype;            // one launch
   OuterArgs da{w.o, w.c, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.L, r.R, one ? kb + nb : kb, a.dtype), w.sum[0], arrived, a.da, a.add};
   OuterArgs db{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.L, r.R, one ? kb + nb : nb, a.dydtype), w.sum[1],
                arrived + outer_counters(r.M, r.L, r.R, a.K), a.db, a.add};
-  if (one) return start_outer(OuterPair{{da, db}, static_cast<uint32_t>(kb)}, static_cast<uint32_t>(kb + nb), a.dtype, s);
-  e = start_outer(OuterPair{{da, da}, static_cast<uint32_t>(kb)}, static_cast<uint32_t>(kb), a.dtype, s);
-  if (e != hipSuccess) return e;
-  return start_outer(OuterPair{{db, db}, static_cast<uint32_t>(nb)}, static_cast<uint32_t>(nb), a.dydtype, s);
+  // before dx, whose traffic would turn dy out of the caches
+  if (one) {
+    e = start_outer(OuterPair{{da, db}, static_cast<uint32_t>(kb)}, static_cast<uint32_t>(kb + nb), a.dtype, s);
+  } else {
+    e = start_outer(OuterPair{{db, db}, static_cast<uint32_t>(nb)}, static_cast<uint32_t>(nb), a.dydtype, s);
+    if (e != hipSuccess) return e;
+    e = start_outer(OuterPair{{da, da}, static_cast<uint32_t>(kb)}, static_cast<uint32_t>(kb), a.dtype, s);
+  }
+  if (e != hipSuccess || !a.dx) return e;
+  return start_expand(ExpandArgs{w.o, w.c, R, RP, nullptr, a.a, a.K, a.base, a.ldbase, a.dx, a.lddx, expand_tiles_of(r.M, a.K)}, a.dtype,
+                      a.dxdtype, tiles, s);
 }
 
 }  // namespace bl
