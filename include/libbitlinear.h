@@ -486,7 +486,7 @@ int bl_adapter_backward(const void* x, int dtype, int64_t M, int64_t K, int64_t 
  *   coef[e] = E count[e] / (C T),   loss = sum over e of coef[e] times the sum of t[m, e] over those rows
  * (1 for an even load; an empty sequence gives zeros). Outputs: loss fp32 [S], count int32 [S, E],
  * coef fp32 [S, E], which is the loss's derivative by t. Sums over rows are fp32 within a chunk of about
- * M / 128 rows and fp64 over chunks, in a fixed order. E <= 2048, k <= 64, M k < 2^31, S <= 2^20. Uses ws. */
+ * M / 128 rows, 8192 at most, and fp64 over chunks, in a fixed order. E <= 2048, k <= 64, M k < 2^31, S <= 2^20. Uses ws. */
 size_t bl_route_balance_workspace_bytes(int64_t M, int64_t E, int64_t S);
 int bl_route_balance(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
                      const int32_t* index, int64_t k, int score, const int32_t* offsets, int64_t S,

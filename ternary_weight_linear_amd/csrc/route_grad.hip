@@ -467,12 +467,14 @@ bool vec_experts(const void* p, int64_t E, int64_t ld, size_t size) {
   return E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * size) == 0;
 }
 
+// An fp32 sum of one group of lanes has 128 rows at most (2048 beyond 512 experts).
+constexpr int64_t kMostChunk = 8192;
 // Rows of a chunk: about 128 workgroups of 64 rows at a time (256 of many rows, 512 of 4 rows beyond 512
 // experts), a row for every group of lanes at least. More chunks shorten the sums and lengthen their
 // finish (us from a graph, 128 / 256, one sequence: 16384 x 256 18.9 / 22.6, 65536 x 256 32.9 / 31.4).
 int64_t balance_chunk(int64_t M, int64_t E) {
   const int64_t groups = E <= 512 ? 64 : 4, most = E > 512 ? 512 : M >= 32768 ? 256 : 128;
-  return (std::max<int64_t>(M / most, 1) + groups - 1) / groups * groups;
+  return (std::clamp<int64_t>(M / most, 1, kMostChunk) + groups - 1) / groups * groups;
 }
 struct BalanceWs {
   int64_t chunk, chunks;

@@ -342,3 +342,59 @@ def test_offsets_past_32_bits():
     wide[:, 4096:4096 + N] = c.base
     y2, h2 = tw.bl_adapter_forward(c.x, c.a, c.b, c.index, scale=c.scale, base=wide[:, 4096:4096 + N], out=wide[:, 4096:4096 + N])
     assert torch.equal(y2, y)
+
+
+def test_most_rows():
+    """2^20 rows, 128 chunks of the sort, against 64 bits on the GPU."""
+    say("adapter most rows")
+    M, K, N, L, R = 1 << 20, 16, 12, 7, 2
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    x = torch.randn(M, K, generator=gen, device=DEV).bfloat16()
+    a, b = (torch.randn(L, R, n, generator=gen, device=DEV).bfloat16() for n in (K, N))
+    index = torch.randint(-1, L, (M,), generator=gen, device=DEV, dtype=torch.int32)
+    dy = torch.randn(M, N, generator=gen, device=DEV).bfloat16()
+    y, h = tw.bl_adapter_forward(x, a, b, index)
+    dx, da, db = tw.bl_adapter_backward(x, a, b, index, h, dy)
+    at, held = index.long().clamp_min(0), (index >= 0).double()[:, None]
+    xd, dyd = x.double(), dy.double()
+    hd = (a.double()[at] * xd[:, None]).sum(2) * held
+    assert torch.all((h - hd).abs() <= 20 * u * (a.double().abs()[at] * xd.abs()[:, None]).sum(2) * held)
+    yd = (b.double()[at] * h.double()[:, :, None]).sum(1)
+    assert torch.all((y - yd).abs() <= 20 * u * (b.double().abs()[at] * h.double().abs()[:, :, None]).sum(1) + u * yd.abs())
+    dh = (b.double()[at] * dyd[:, None]).sum(2) * held
+    mag = (b.double().abs()[at] * dyd.abs()[:, None]).sum(2) * held
+    dxd = (a.double()[at] * dh[:, :, None]).sum(1)
+    assert torch.all((dx - dxd).abs() <= 40 * u * (a.double().abs()[at] * mag[:, :, None]).sum(1) + u * dxd.abs())
+    for e in range(L):
+        rows = (index == e).nonzero()[:, 0]
+        # the roundings of M / L additions add up as their square root: 400, and three times that
+        for got, c, cm, s in ((da[e], dh[rows], mag[rows], xd[rows]), (db[e], h[rows].double(), h[rows].double().abs(), dyd[rows])):
+            ref, size = c.t() @ s, (cm.t() @ s.abs())
+            assert torch.all((got - ref).abs() <= 1200 * u * size)
+
+
+def test_adapters_past_32_bits():
+    """Matrices of 2^32 values: the last adapter's lie far past 2^31 from the first's."""
+    say("adapter large matrices")
+    M, K, N, L, R = 70, 16384, 40, 1024, 256
+    a = torch.zeros((L, R, K), dtype=torch.bfloat16, device=DEV)
+    b = torch.zeros((L, R, N), dtype=torch.bfloat16, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    for e in (0, 1023):
+        a[e] = torch.randn(R, K, generator=gen, device=DEV).bfloat16() * K ** -0.5
+        b[e] = torch.randn(R, N, generator=gen, device=DEV).bfloat16()
+    x, dy = torch.randn(M, K, generator=gen, device=DEV).bfloat16(), torch.randn(M, N, generator=gen, device=DEV).bfloat16()
+    index = torch.where(torch.arange(M, device=DEV) % 3 == 0, 0, 1023).int()
+    few = torch.where(index == 0, 0, 1).int()
+    pair = [t[[0, 1023]].contiguous() for t in (a, b)]
+    for rows in (M, 5):                             # sorted, and each row by itself
+        y, h = tw.bl_adapter_forward(x[:rows], a, b, index[:rows])
+        y2, h2 = tw.bl_adapter_forward(x[:rows], *pair, few[:rows])
+        size = (pair[0].double().abs()[few[:rows].long()] * x[:rows].double().abs()[:, None]).sum(2)
+        bound = 2 * (K / 4 + 64) * u * size
+        assert torch.all((h - h2).abs() <= bound)
+        assert torch.all((y - y2).abs() <= (pair[1].double().abs()[few[:rows].long()] * (bound + 2 * R * u * h.abs())[:, :, None]).sum(1))
+    dx, da, db = tw.bl_adapter_backward(x, a, b, index, h := tw.bl_adapter_forward(x, a, b, index)[1], dy)
+    dx2, da2, db2 = tw.bl_adapter_backward(x, *pair, few, h, dy)
+    assert torch.equal(dx, dx2) and torch.equal(db[[0, 1023]], db2) and not db[1:1023].any()
+    assert torch.equal(da[[0, 1023]], da2) and not any(da[e].any() for e in (1, 2, 511, 1022))

@@ -240,3 +240,25 @@ def test_the_choice_of_bl_route_experts_and_its_gradient_by_differences():
 
         want = (f(lh + 1e-5 * v) - f(lh - 1e-5 * v)) / 2e-5
         assert abs((host(d) * v).sum() - want) <= 1e-5 * np.abs(host(d) * v).sum()
+
+
+def test_more_rows_than_a_grid_has_work_items_along_x():
+    """2^28 rows of 16 lanes each are 2^32 work-items; the last rows and all counts."""
+    say("route many rows")
+    M, E = (1 << 28) + 5, 2
+    logits = torch.zeros((M, E), dtype=torch.bfloat16, device=DEV)
+    index = torch.zeros((M, 1), dtype=torch.int32, device=DEV)
+    index[1::4] = 1
+    index[3::4] = -1
+    tail, lh, _ = make(37, E, 1, "bf16", 13)
+    logits[-37:] = tail
+    dweight = torch.ones((M, 1), device=DEV)
+    loss, count, coef = tw.bl_route_balance(logits, index)
+    n = [(index == e).sum().item() for e in range(E)]
+    assert count[0].tolist() == n
+    # even scores but for the last rows: the loss is E (n_0 + n_1) / (2 C) = 1 to a few of 2^28 rows
+    assert abs(loss.item() - 1) <= 2.0 ** -17
+    d = tw.bl_route_backward(logits, index, dweight, renorm=False, coef=coef, dloss=torch.ones_like(loss), out_dtype=torch.float32)
+    ih = index[-37:].cpu().numpy()
+    check_gradient(d[-37:], lh, ih, "softmax", False, 1.0, "fp32", dweight=np.ones((37, 1), np.float32), coef=host(coef), dloss=np.ones(1))
+    assert torch.equal(d[:4096], d[4096:8192]) and torch.equal(d[:4096], d[(1 << 27):(1 << 27) + 4096])
