@@ -1078,7 +1078,7 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
   __shared__ int last_one;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
   const bool second = blockIdx.x >= pair.columns;
-  const OuterArgs& a = pair.p[second];
+  const OuterArgs a = second ? pair.p[1] : pair.p[0];   // in registers: not loaded again at every use
   const uint32_t column = second ? blockIdx.x - pair.columns : blockIdx.x;
   if (static_cast<int>(blockIdx.y) >= a.splits) return;
   // the last columns are taken with those before them, to be 128, and written alone
@@ -1086,10 +1086,12 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
   const int r0 = blockIdx.z * 16 * NR;
   const int64_t tiles = a.o.start[a.o.L], n = static_cast<int64_t>(a.R) * a.D;
   const auto each = [&](auto f) {                   // of this workgroup's values: (row and column in red, place in [R, D])
-    for (int i = tid; i < 16 * NR * 128; i += 256) {
-      const int r = r0 + i / 128;
-      const int64_t d = d0 + i % 128;
-      if (r < a.R && d >= lo && d < a.D) f(i, r * a.D + d);
+    const int64_t d = d0 + tid % 128;
+    if (d < lo || d >= a.D) return;
+#pragma unroll
+    for (int i = 0; i < 8 * NR; ++i) {
+      const int r = r0 + 2 * i + tid / 128;
+      if (r < a.R) f(tid + 256 * i, r * a.D + d);
     }
   };
   float* flat = reinterpret_cast<float*>(red);
