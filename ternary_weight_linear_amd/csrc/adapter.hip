@@ -1100,7 +1100,10 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
     for (int e = blockIdx.y; e < a.o.L; e += a.splits)
       if (a.o.start[e] == a.o.start[e + 1]) each([&](int, int64_t at) { a.grad[e * n + at] = 0.0f; });
 
-  const int t0 = static_cast<int>(tiles * blockIdx.y / a.splits), t1 = static_cast<int>(tiles * (blockIdx.y + 1) / a.splits);
+  // no share without a tile: the last to end is known by how many shares an adapter lies in
+  const int64_t shares = min(static_cast<int64_t>(a.splits), tiles);
+  if (blockIdx.y >= shares) return;
+  const int t0 = static_cast<int>(tiles * blockIdx.y / shares), t1 = static_cast<int>(tiles * (blockIdx.y + 1) / shares);
   const int few = max(4, (t1 - t0) / 4);
   int turn = 0;
   for (int t = t0; t < t1;) {
@@ -1158,8 +1161,8 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
       each([&](int i, int64_t at) { atomic_store_agent(out + at, flat[i]); });
       wait_own_memory_ops();
       __syncthreads();
-      // the share of tile t is the largest s whose first tile, floor(s tiles / splits), is not past t
-      const int64_t s0 = ((first + 1ll) * a.splits - 1) / tiles, s1 = (static_cast<int64_t>(last) * a.splits - 1) / tiles;
+      // the share of tile t is the largest s whose first tile, floor(s tiles / shares), is not past t
+      const int64_t s0 = ((first + 1) * shares - 1) / tiles, s1 = (last * shares - 1) / tiles;
       if (tid == 0)
         last_one = arrive_agent(a.arrived + (s0 * gridDim.z + blockIdx.z) * ((a.D + 127) / 128) + column) == static_cast<uint32_t>(s1 - s0);
       __syncthreads();

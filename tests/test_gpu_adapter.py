@@ -195,6 +195,28 @@ def test_no_row_has_an_adapter(M):
     assert torch.equal(y, c.base) and torch.equal(dx, c.dbase) and not h.any() and not da.any() and not db.any()
 
 
+@pytest.mark.parametrize("M,L,rows", [(70, 64, 70), (300, 1024, 300), (2048, 1, 40), (2048, 3, 70), (20000, 5, 97), (66000, 2, 200), (513, 700, 33)])
+@pytest.mark.parametrize("K,N,R", [(96, 264, 9), (1032, 130, 33)])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_few_tiles_of_many_possible_ones(M, L, rows, K, N, R, dtype):
+    """One adapter of many for all rows, or few rows of many with one: far fewer tiles than a call of its
+    sizes may have, and less than it has shares for them."""
+    say("adapter few tiles", M, L, rows, K, N, R, dtype)
+    c = Case(M, K, N, L, R, dtype, dtype, 11)
+    c.indexh[:] = -1
+    c.indexh[np.sort(np.random.default_rng(12).permutation(M)[:rows])] = L // 2
+    c.index = gpu(c.indexh)
+    y, h = c.forward()
+    c.check_forward(y, h)
+    nan = lambda *shape: torch.full(shape, float("nan"), device=DEV)      # what fresh memory may hold
+    room = [nan(L, R, K), nan(L, R, N)]
+    del room
+    c.check_backward(c.backward(h), h)
+    da, dah = values((L, R, K), "fp32", 13)
+    db, dbh = values((L, R, N), "fp32", 14)
+    c.check_backward(c.backward(h, da=da, db=db), h, add=(dah, dbh))
+
+
 @pytest.mark.parametrize("M", [2, 70, 400, 66000])
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_nan_and_infinity_stay_in_their_rows_and_adapters(M, dtype):
