@@ -242,6 +242,29 @@ def test_nan_and_infinity_stay_in_their_rows_and_adapters(M, dtype):
     assert torch.equal(da[0][:, keep], g0[1][0][:, keep])
 
 
+@pytest.mark.parametrize("M", [3, 70, 66000])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_infinities_give_nothing_finite(M, dtype):
+    """Coefficients that 16 bits hold whole, whose further parts are zeros, times infinities."""
+    say("adapter infinity", M, dtype)
+    K, N, L, R = 40, 136, 2, 5
+    t = lambda v: v.to(DEV).to(TYPES[dtype])
+    x, a, b, dy = torch.zeros(M, K), torch.ones(L, R, K), torch.ones(L, R, N), torch.zeros(M, N)
+    x[:, 0], dy[:, 0] = 1.0, 1.0
+    b[0, 2, 77] = float("inf")
+    index = torch.arange(M, dtype=torch.int32, device=DEV) % 2
+    y, h = tw.bl_adapter_forward(t(x), t(a), t(b), index)
+    mine = index == 0
+    assert torch.all(h == 1) and not torch.isfinite(y[mine][:, 77]).any()
+    y[mine.nonzero()[:, 0], 77] = 5.0
+    assert torch.all(y == 5)
+    x[2, 7], dy[1, 9] = float("inf"), float("inf")
+    dx, da, db = tw.bl_adapter_backward(t(x), t(a), t(torch.ones(L, R, N)), index, h, t(dy))
+    assert not torch.isfinite(da[0, :, 7]).any() and not torch.isfinite(db[1, :, 9]).any() and not torch.isfinite(dx[1]).any()
+    assert torch.isfinite(da[0, :, 8:]).all() and torch.isfinite(db[0]).all() and torch.isfinite(db[1, :, 10:]).all()
+    assert torch.all(dx[0] == R) and torch.all(dx[2:] == R)
+
+
 @pytest.mark.parametrize("M,L", [(8192, 3), (8193, 5), (20000, 1024), (16384, 1), (1000, 1024), (9000, 700)])
 @pytest.mark.parametrize("kind", ["mixed", "runs"])
 def test_many_rows_and_adapters(M, L, kind):
