@@ -658,25 +658,26 @@ __global__ __launch_bounds__(64 * kShrinkWaves, 2) void adapter_shrink_kernel(Sh
     if (tid == 0) last = arrive_agent(a.arrived + t) + 1 == static_cast<uint32_t>(groups);
     __syncthreads();
     if (!last) return;
-    // four splits' values in flight at a time, those of up to eight places
+    // about 32 loads in flight at a time: of PL places (all of a thread's, up to rank 64) those of NS splits
+    constexpr int PL = 2 * NR, NS = 32 / PL;
     const float* in = a.part + static_cast<int64_t>(t) * kTile * a.RP;
     const int64_t step = a.o.rows * a.RP;
-    for (int i0 = tid; i0 < kTile * a.RP; i0 += 8 * kThreads) {
-      float v[8] = {};
-      for (int s0 = 0; s0 < a.splits; s0 += 4) {
-        float p[4][8];
+    for (int i0 = tid; i0 < kTile * a.RP; i0 += PL * kThreads) {
+      float v[PL] = {};
+      for (int s0 = 0; s0 < a.splits; s0 += NS) {
+        float p[NS][PL];
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < PL; ++i)
             p[s][i] = atomic_load_agent(in + min(s0 + s, a.splits - 1) * step + min(i0 + i * kThreads, kTile * a.RP - 1));
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += s0 + s < a.splits ? p[s][i] : 0.0f;
+          for (int i = 0; i < PL; ++i) v[i] += s0 + s < a.splits ? p[s][i] : 0.0f;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < PL; ++i) {
         const int at = i0 + i * kThreads;
         if (at < kTile * a.RP) lds[at / a.RP * pitch + at % a.RP] = v[i];
       }
