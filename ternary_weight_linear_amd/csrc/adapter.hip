@@ -1029,11 +1029,11 @@ struct OuterTile {
 
 // Tiles t, t + STEP .. before end: each is loaded while the one before is multiplied, its rows' numbers one
 // tile earlier still. Past the last tile the loads repeat it, so that none is under a condition.
-template <int SD, int NR, bool WHOLE, int STEP>
+template <int SD, int NR, bool TWO, bool WHOLE, int STEP>
 __device__ __forceinline__ void outer_tiles(const OuterArgs& a, int t, int end, int64_t d, int r0, int c, int g, f32x4 (&acc)[NR][8]) {
   if (t >= end) return;
   const int last = t + (end - 1 - t) / STEP * STEP;
-  if constexpr (SD == BL_F32 || !WHOLE) {           // no registers for two tiles
+  if constexpr (!TWO || !WHOLE) {
     OuterTile<SD, NR> v;
     int rows[8];
     v.load_rows(a, t, g);
@@ -1073,14 +1073,10 @@ __device__ __forceinline__ void outer_tiles(const OuterArgs& a, int t, int end, 
     }
 }
 
-template <int SD, int NR>
-__global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_outer_kernel(OuterPair pair) {
-  __shared__ f32x4 red[16 * NR][32];
-  __shared__ int last_one;
+// red [16 NR][32].
+template <int SD, int NR, bool TWO>
+__device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4 (*red)[32], int& last_one) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
-  const bool second = blockIdx.x >= pair.columns;
-  const OuterArgs a = second ? pair.p[1] : pair.p[0];   // in registers: not loaded again at every use
-  const uint32_t column = second ? blockIdx.x - pair.columns : blockIdx.x;
   if (static_cast<int>(blockIdx.y) >= a.splits) return;
   // the last columns are taken with those before them, to be 128, and written alone
   const int64_t lo = static_cast<int64_t>(column) * 128, d0 = max(min(lo, a.D - 128), int64_t(0));
@@ -1115,8 +1111,8 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
     if (first >= t && last <= end && end - t <= few) {
       // an adapter of few of the share's tiles is one wave's, which writes it from its registers
       if (turn++ % 4 == wave) {
-        if (a.D >= 128) outer_tiles<SD, NR, true, 1>(a, t, end, d0 + 8 * c, r0, c, g, acc);
-        else outer_tiles<SD, NR, false, 1>(a, t, end, d0 + 8 * c, r0, c, g, acc);
+        if (a.D >= 128) outer_tiles<SD, NR, TWO, true, 1>(a, t, end, d0 + 8 * c, r0, c, g, acc);
+        else outer_tiles<SD, NR, TWO, false, 1>(a, t, end, d0 + 8 * c, r0, c, g, acc);
 #pragma unroll
         for (int q = 0; q < NR; ++q)
 #pragma unroll
@@ -1137,8 +1133,8 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
       t = end;
       continue;
     }
-    if (a.D >= 128) outer_tiles<SD, NR, true, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
-    else outer_tiles<SD, NR, false, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
+    if (a.D >= 128) outer_tiles<SD, NR, TWO, true, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
+    else outer_tiles<SD, NR, TWO, false, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
     // the waves' sums, one after another
     for (int w = 0; w < 4; ++w) {
       if (wave == w) {
@@ -1203,6 +1199,27 @@ __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_
     }
     __syncthreads();
     t = end;
+  }
+}
+
+// Types of the first and the second sum of a pair. Registers: two workgroups to a CU, or one with two tiles of 16-bit
+// values in flight beyond rank 16; fp32 leaves none for a second tile.
+template <int SD, int TD, int NR>
+__global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_outer_kernel(OuterPair pair) {
+  __shared__ f32x4 red[16 * NR][32];
+  __shared__ int last_one;
+  constexpr bool kTwo = SD != BL_F32;
+  const bool second = blockIdx.x >= pair.columns;
+  const uint32_t column = second ? blockIdx.x - pair.columns : blockIdx.x;
+  if constexpr (SD == TD) {
+    const OuterArgs a = second ? pair.p[1] : pair.p[0];   // in registers: not loaded again at every use
+    outer<SD, NR, kTwo>(a, column, red, last_one);
+  } else if (second) {
+    const OuterArgs a = pair.p[1];
+    outer<TD, NR, NR == 1>(a, column, red, last_one);
+  } else {
+    const OuterArgs a = pair.p[0];
+    outer<SD, NR, kTwo>(a, column, red, last_one);
   }
 }
 
@@ -1469,15 +1486,17 @@ hipError_t start_expand(const ExpandArgs& a, int wd, int yd, int64_t tiles, hipS
   return start_expand_as<BL_F32, BL_F32>(a, tiles, s);
 }
 
-template <int SD>
+template <int SD, int TD>
 hipError_t start_outer_as(const OuterPair& a, uint32_t columns, hipStream_t s) {
   const dim3 grid(columns, std::max(a.p[0].splits, a.p[1].splits), static_cast<uint32_t>(div_up(a.p[0].RP, 32)));
-  if (a.p[0].RP == 16) adapter_outer_kernel<SD, 1><<<grid, 256, 0, s>>>(a);
-  else adapter_outer_kernel<SD, 2><<<grid, 256, 0, s>>>(a);
+  if (a.p[0].RP == 16) adapter_outer_kernel<SD, TD, 1><<<grid, 256, 0, s>>>(a);
+  else adapter_outer_kernel<SD, TD, 2><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
-hipError_t start_outer(const OuterPair& a, uint32_t columns, int sd, hipStream_t s) {
-  return sd == BL_F16 ? start_outer_as<BL_F16>(a, columns, s) : sd == BL_BF16 ? start_outer_as<BL_BF16>(a, columns, s) : start_outer_as<BL_F32>(a, columns, s);
+// Types of the sums: the same, or fp32 and another.
+hipError_t start_outer(const OuterPair& a, uint32_t columns, int sd, int td, hipStream_t s) {
+  if (sd == td) return sd == BL_F16 ? start_outer_as<BL_F16, BL_F16>(a, columns, s) : sd == BL_BF16 ? start_outer_as<BL_BF16, BL_BF16>(a, columns, s) : start_outer_as<BL_F32, BL_F32>(a, columns, s);
+  return td == BL_F16 ? start_outer_as<BL_F32, BL_F16>(a, columns, s) : start_outer_as<BL_F32, BL_BF16>(a, columns, s);
 }
 
 // The layouts that a value of type dt is multiplied by: fp32 for fp32, else parts.
@@ -1551,18 +1570,11 @@ hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipSt
   if (e != hipSuccess) return e;
   uint32_t* arrived = w.arrived + tiles;
   const int64_t kb = div_up(a.K, 128), nb = div_up(a.N, 128);
-  const bool one = a.dtype == a.dydtype;            // one launch
-  OuterArgs da{w.o, w.c, a.x, a.K, a.ldx, R, RP, outer_splits(r.M, r.L, r.R, one ? kb + nb : kb, a.dtype), w.sum[0], arrived, a.da, a.add};
-  OuterArgs db{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, outer_splits(r.M, r.L, r.R, one ? kb + nb : nb, a.dydtype), w.sum[1],
-               arrived + outer_counters(r.M, r.L, r.R, a.K), a.db, a.add};
-  // before dx, whose traffic would turn dy out of the caches
-  if (one) {
-    e = start_outer(OuterPair{{da, db}, static_cast<uint32_t>(kb)}, static_cast<uint32_t>(kb + nb), a.dtype, s);
-  } else {
-    e = start_outer(OuterPair{{db, db}, static_cast<uint32_t>(nb)}, static_cast<uint32_t>(nb), a.dydtype, s);
-    if (e != hipSuccess) return e;
-    e = start_outer(OuterPair{{da, da}, static_cast<uint32_t>(kb)}, static_cast<uint32_t>(kb), a.dtype, s);
-  }
+  const int shares = outer_splits(r.M, r.L, r.R, kb + nb, a.dydtype);
+  const OuterArgs da{w.o, w.c, a.x, a.K, a.ldx, R, RP, shares, w.sum[0], arrived, a.da, a.add};
+  const OuterArgs db{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, shares, w.sum[1], arrived + outer_counters(r.M, r.L, r.R, a.K), a.db, a.add};
+  // before dx, whose traffic would turn dy out of the caches; fp32, which takes longer, first
+  e = start_outer(OuterPair{{db, da}, static_cast<uint32_t>(nb)}, static_cast<uint32_t>(kb + nb), a.dydtype, a.dtype, s);
   if (e != hipSuccess || !a.dx) return e;
   return start_expand(ExpandArgs{w.o, w.c, R, RP, nullptr, a.a, a.K, a.base, a.ldbase, a.dx, a.lddx, expand_tiles_of(r.M, a.K)}, a.dtype,
                       a.dxdtype, tiles, s);
