@@ -1073,7 +1073,7 @@ __device__ __forceinline__ void outer_tiles(const OuterArgs& a, int t, int end, 
     }
 }
 
-// red [16 NR][32].
+// red [4 waves][16 NR][32].
 template <int SD, int NR, bool TWO>
 __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4 (*red)[32], int& last_one) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
@@ -1091,7 +1091,8 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
       if (r < a.R) f(tid + 256 * i, r * a.D + d);
     }
   };
-  float* flat = reinterpret_cast<float*>(red);
+  const float* flat = reinterpret_cast<const float*>(red);
+  const auto sum = [&](int i) { return flat[i] + flat[i + 2048 * NR] + flat[i + 2 * 2048 * NR] + flat[i + 3 * 2048 * NR]; };
   // adapters without rows, shared out over the shares
   if (!a.add)
     for (int e = blockIdx.y; e < a.o.L; e += a.splits)
@@ -1135,27 +1136,20 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
     }
     if (a.D >= 128) outer_tiles<SD, NR, TWO, true, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
     else outer_tiles<SD, NR, TWO, false, 4>(a, t + wave, end, d0 + 8 * c, r0, c, g, acc);
-    // the waves' sums, one after another
-    for (int w = 0; w < 4; ++w) {
-      if (wave == w) {
+    // the waves' sums, added in their order as they are read
 #pragma unroll
-        for (int q = 0; q < NR; ++q)
+    for (int q = 0; q < NR; ++q)
 #pragma unroll
-          for (int l = 0; l < 4; ++l)
+      for (int l = 0; l < 4; ++l)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              f32x4& p = red[16 * q + 4 * g + l][2 * c + j];
-              const f32x4 v = {acc[q][4 * j][l], acc[q][4 * j + 1][l], acc[q][4 * j + 2][l], acc[q][4 * j + 3][l]};
-              p = w ? p + v : v;
-            }
-      }
-      __syncthreads();
-    }
+        for (int j = 0; j < 2; ++j)
+          red[wave * 16 * NR + 16 * q + 4 * g + l][2 * c + j] = f32x4{acc[q][4 * j][l], acc[q][4 * j + 1][l], acc[q][4 * j + 2][l], acc[q][4 * j + 3][l]};
+    __syncthreads();
     if (first >= t && last <= end) {
-      each([&](int i, int64_t at) { grad[at] = a.add ? grad[at] + flat[i] : flat[i]; });
+      each([&](int i, int64_t at) { grad[at] = a.add ? grad[at] + sum(i) : sum(i); });
     } else {
       float* out = a.sum + (2 * static_cast<int64_t>(blockIdx.y) + (first >= t ? 1 : 0)) * n;
-      each([&](int i, int64_t at) { atomic_store_agent(out + at, flat[i]); });
+      each([&](int i, int64_t at) { atomic_store_agent(out + at, sum(i)); });
       wait_own_memory_ops();
       __syncthreads();
       // the share of tile t is the largest s whose first tile, floor(s tiles / shares), is not past t
@@ -1206,7 +1200,7 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
 // values in flight beyond rank 16; fp32 leaves none for a second tile.
 template <int SD, int TD, int NR>
 __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_outer_kernel(OuterPair pair) {
-  __shared__ f32x4 red[16 * NR][32];
+  __shared__ f32x4 red[4 * 16 * NR][32];
   __shared__ int last_one;
   constexpr bool kTwo = SD != BL_F32;
   const bool second = blockIdx.x >= pair.columns;
