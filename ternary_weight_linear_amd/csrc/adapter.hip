@@ -1095,8 +1095,14 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
   const auto sum = [&](int i) { return flat[i] + flat[i + 2048 * NR] + flat[i + 2 * 2048 * NR] + flat[i + 3 * 2048 * NR]; };
   // adapters without rows, shared out over the shares
   if (!a.add)
-    for (int e = blockIdx.y; e < a.o.L; e += a.splits)
-      if (a.o.start[e] == a.o.start[e + 1]) each([&](int, int64_t at) { a.grad[e * n + at] = 0.0f; });
+    for (int e0 = blockIdx.y; e0 < a.o.L; e0 += 64 * a.splits) {
+      const int mine = min(e0 + lane * a.splits, a.o.L - 1);
+      uint64_t empty = __ballot(e0 + lane * a.splits < a.o.L && a.o.start[mine] == a.o.start[mine + 1]);
+      for (; empty; empty &= empty - 1) {
+        const int64_t e = e0 + __builtin_ctzll(empty) * a.splits;
+        each([&](int, int64_t at) { a.grad[e * n + at] = 0.0f; });
+      }
+    }
 
   // no share without a tile: the last to end is known by how many shares an adapter lies in
   const int64_t shares = min(static_cast<int64_t>(a.splits), tiles);
@@ -1104,8 +1110,12 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
   const int t0 = static_cast<int>(tiles * blockIdx.y / shares), t1 = static_cast<int>(tiles * (blockIdx.y + 1) / shares);
   const int few = max(4, (t1 - t0) / 4);
   int turn = 0;
+  int words = 0, words_at = t0 - 64;                // of 64 tiles, one a lane
   for (int t = t0; t < t1;) {
-    const int e = tile_adapter(a.o.tile[t]), first = a.o.start[e], last = a.o.start[e + 1];
+    if (t - words_at >= 64) words = a.o.tile[min(static_cast<int64_t>((words_at = t) + lane), tiles - 1)];
+    const int word = __builtin_amdgcn_readlane(words, t - words_at), e = tile_adapter(word);
+    // its first tile and the one after its last: known but at the share's start, and of long ones
+    const int first = t == t0 ? a.o.start[e] : t, last = tile_left(word) < 15 ? t + tile_left(word) + 1 : a.o.start[e + 1];
     const int end = min(last, t1);
     float* grad = a.grad + e * n;
     f32x4 acc[NR][8] = {};
