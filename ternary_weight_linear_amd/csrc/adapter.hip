@@ -426,8 +426,8 @@ struct Sorted {
 // touch so many lines gets 16 bytes a clock: so eight lanes load a row's 128 bytes, and the operand is
 // picked up from LDS of the wave's own. Where there are several workgroups to a tile, the last one
 // that ends adds their sums, in order, and makes the coefficients (memory-side stores, no cache
-// write-back: about 1 us to arrive, 1.5 to gather, 1.5 to 4.5 for the coefficients). 4096 x 8192, bf16, rank 32:
-// 28 us, of which 15 are the loop at 4.5 TB/s of rows; rank 64 31 us (operands straight from memory 39).
+// write-back: about 1 us to arrive, 1 to gather, 1.5 to 4.5 for the coefficients). 4096 x 8192, bf16, rank 32:
+// 24 us, of which 15 are the loop at 4.5 TB/s of rows; rank 64 31 us (operands straight from memory 39).
 constexpr int kShrinkWaves = 4;
 struct ShrinkArgs {
   Sorted o;
@@ -929,8 +929,9 @@ __global__ __launch_bounds__(256, YD == BL_F32 ? 2 : 3) void adapter_expand_kern
 // not go to sum[2 share], where the adapter began in an earlier share, or sum[2 share + 1]; the
 // workgroup that ends last adds them in their order. Each share has at most one adapter that
 // goes on after it, so the share where an adapter begins names its counter. A wave has two tiles' loads in
-// flight, which bounds it: 4096 rows of 8192 and 8192, bf16, rank 32 38 us for both sums (134 MB, 3.6
-// TB/s; with one tile at a time 100), fp32 rows of 8640, rank 8, 1024 of them 19 us (fp32 instructions).
+// flight, which bounds it: 4096 rows of 8192 and 8192, bf16, rank 32 34 us for both sums (134 MB, 3.9
+// TB/s; with one tile at a time 100). fp32 rows have one in flight and the fp32 instruction: 1024 of 3200 beside
+// fp16 ones of 8640, rank 8, 19 us (31 MB) where each sum by itself takes 19 and 15.
 struct OuterArgs {
   Sorted o;
   Coefs c;
@@ -942,7 +943,7 @@ struct OuterArgs {
   float* grad;            // [L, R, D]
   int add;
 };
-// One launch takes both sums where x and dy have one type: the first `columns` workgroups along x are p[0]'s.
+// One launch takes both sums: the first `columns` workgroups along x are p[0]'s.
 struct OuterPair {
   OuterArgs p[2];
   uint32_t columns;
