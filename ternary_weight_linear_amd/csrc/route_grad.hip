@@ -64,9 +64,8 @@ __device__ __forceinline__ void load_logits(const typename Elem<DT>::type* row, 
   for (int i = 0; i < NE; ++i) l[i] = l[i] > -INFINITY ? fminf(l[i], kMost) : -INFINITY;   // NaN compares false
 }
 
-// exp and 1 / v by the hardware's instructions: the first errs by two units and one of its argument's
-// rounding, |v| 2^-24, the second by one unit.
-__device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504088896341f); }
+// 1 / v by the hardware's instruction, which errs by one unit. Exponentials are the routing's own
+// expf: the hardware's instruction alone is off by |v| 2^-24 more, and gives 0 below 2^-126.
 __device__ __forceinline__ float fast_inv(float v) { return __builtin_amdgcn_rcpf(v); }
 
 // l becomes the normalised scores t (0 for what is left out). Sigmoid scores also give p and
@@ -83,15 +82,15 @@ __device__ __forceinline__ void normalise(float (&l)[NE], float (&p)[NE], float 
   for (int i = 0; i < NE; ++i) {
     const float v = l[i];
     if constexpr (SIGMOID) {
-      const float z = fast_exp(-fabsf(v)), inv = fast_inv(1.0f + z);  // z = 0 for -inf
+      const float z = expf(-fabsf(v)), inv = fast_inv(1.0f + z);  // z = 0 for -inf
       const float ps = v >= 0.0f ? inv : z * inv;
       if constexpr (SCORES) {
         p[i] = ps;
         q[i] = v >= 0.0f ? z * inv : inv;
       }
-      l[i] = mx > 0.0f ? ps : v > -INFINITY ? fast_exp(v - mx) * inv : 0.0f;
+      l[i] = mx > 0.0f ? ps : v > -INFINITY ? expf(v - mx) * inv : 0.0f;
     } else {
-      l[i] = v > -INFINITY ? fast_exp(v - mx) : 0.0f;
+      l[i] = v > -INFINITY ? expf(v - mx) : 0.0f;
     }
     sum += l[i];
   }
@@ -346,14 +345,17 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs a
       sum += ps[j];
     }
     if (a.renorm) {
+      // quotients, as the routing has them: 1 / sum is infinite where the slots have next to no score
       sum = group_sum<LANES>(sum);
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
       float mean = 0.0f;
 #pragma unroll
-      for (int j = 0; j < KS; ++j) mean += ps[j] * inv * g[j];
+      for (int j = 0; j < KS; ++j) {
+        ps[j] = sum > 0.0f ? ps[j] / sum : 0.0f;
+        mean += ps[j] * g[j];
+      }
       mean = group_sum<LANES>(mean);
 #pragma unroll
-      for (int j = 0; j < KS; ++j) v[j] = ps[j] * inv * (g[j] - mean);
+      for (int j = 0; j < KS; ++j) v[j] = ps[j] * (g[j] - mean);
     } else {
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
