@@ -1,5 +1,5 @@
 """Scores far below the largest: gradients of the router where what was chosen has next to no score,
-as a choice by bias or by another routing leaves it.
+as a choice by bias or by another routing leaves it, and the balance loss of logits far apart.
 
 Bounds. u = 2^-24 is half a unit of fp32. An exponential errs by two units, and by u |l - max| of its
 argument's rounding; results below 2^-126 are multiples of 2^-149, off by at most one each for the
@@ -50,3 +50,29 @@ def test_renormalised_weights_of_scores_that_fp32_hardly_holds(E, k, score):
     # products and quotients of a few roundings each
     each = (2 * 94 + E / 8 + 40) * u + 2 * step / least
     assert np.all(np.abs(d - ref) <= 6 * each[:, None] * mag + step)
+
+
+@pytest.mark.parametrize("E", [6, 64, 600])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_expert_far_above_the_others(E, score):
+    """A logit of 3e38: softmax scores are one and zeros exactly, so the loss is that expert's
+    coefficient and no logit has a gradient. Sigmoid scores are one there, and one half and less elsewhere."""
+    say("route far apart", E, score)
+    g = np.random.default_rng(E)
+    lh = (-np.abs(g.standard_normal((1, E)))).astype(np.float32)
+    lh[0, 0] = 3e38
+    index = np.array([[0, 1, E - 1]], np.int32)
+    loss, count, coef = tw.bl_route_balance(gpu(lh), gpu(index), score=score)
+    rloss, rcount, rcoef = oa.balance(lh, index, score)
+    assert np.array_equal(count.cpu().numpy(), rcount) and np.all(np.abs(host(coef) - rcoef) <= 2 * u * rcoef)
+    dweight = g.standard_normal((1, 3)).astype(np.float32)
+    one = torch.ones(1, device=DEV)
+    for renorm in (True, False):
+        d = host(tw.bl_route_backward(gpu(lh), gpu(index), gpu(dweight), score=score, renorm=renorm, coef=coef, dloss=one))
+        ref, mag = oa.route_backward(lh, index, score, renorm, 1.0, dweight, host(coef), np.ones(1))
+        if score == "softmax":
+            assert loss.item() == coef[0, 0].item() and not d.any() and not ref.any()
+        else:
+            # exponentials of at most 5 in size, sums of E terms in chains of E / 16 + 4
+            bound = (2 * 5 + E / 8 + 40) * u
+            assert abs(loss.item() - rloss[0]) <= bound * rloss[0] and np.all(np.abs(d - ref) <= 2 * bound * mag + step)
