@@ -449,8 +449,9 @@ int bl_fp8_experts(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
  * scale fp32 [L], or NULL for 1. A row whose index is outside [0, L) has no adapter. ydtype (dydtype,
  * dxdtype) is x's dtype or BL_F32. 1 <= M <= 2^20, 1 <= K, N <= 2^24, 1 <= R <= 256, 1 <= L <= 1024.
  * Sums are fp32 sums, in a fixed order for a given shape and index, of products rounded to fp32 at
- * most; h and dh go into their second product whole (fp32, bf16) or, for fp16, with 22 bits or more below
- * the largest of their row (dx, y) or of their rank in 32 rows (da, db). What NaN or an infinity reaches is not
+ * most (where x or dy and the matrices are fp16, values below 2^-14 count as 2^-14 in a sum's error); h and
+ * dh go into their second product whole, but for what lies below 2^-133 where that is one of 16-bit
+ * values. What NaN or an infinity reaches is not
  * finite, and may be NaN where the formula has an infinity; it reaches its own row and its own adapter's matrices alone.
  * Uses ws (bl_adapter_workspace_bytes; the last argument says which call it is for; 0 where a forward pass of few
  * rows needs none, and for sizes that are refused). */

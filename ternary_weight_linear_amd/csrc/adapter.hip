@@ -188,59 +188,65 @@ __device__ __forceinline__ f32x4 dot32(u32x4 a, u32x4 b, f32x4 acc) {
 // ------------------------------------------------------------------------------------------
 // fp32 coefficients as 16-bit parts
 // ------------------------------------------------------------------------------------------
-// h and dh are fp32, and what they are multiplied by has 16 bits. The 16-bit matrix instructions
-// are 16 times as fast as the fp32 one, so a coefficient is split into parts that they take: three bf16
-// parts, cut at 8 bits each, hold all 24 bits; two fp16 parts hold 22 bits or more, after
-// a power of two has brought the largest of the row (or column) to 2^14 .. 2^15.
+// h and dh are fp32, and what they are multiplied by has 16 bits. The 16-bit matrix instructions are 16
+// times as fast as the fp32 one, so a coefficient is cut into three bf16 parts of 8 bits each, which hold
+// all of its 24 bits that are not below 2^-133. fp16 values are cut into two bf16 parts, of 8 and 3 bits, so
+// that their products are whole too: six instructions where fp16 parts would take two, but those have no
+// range for rows or ranks far quieter than the loudest beside them. (4096 x 8192, fp16, six / two: rank 64 86 us / 82, gradients,
+// rank 32, 105 / 107, where two need exponents.)
+constexpr int kParts = 3;
 template <int DT>
-struct Parts;
-template <>
-struct Parts<BL_BF16> { static constexpr int n = 3; };
-template <>
-struct Parts<BL_F16> { static constexpr int n = 2; };
-template <>
-struct Parts<BL_F32> { static constexpr int n = 1; };
+constexpr int kValueParts = DT == BL_F16 ? 2 : 1;
 
-// |v| of what is finite, else 0.
-__device__ __forceinline__ uint32_t finite_bits(float v) {
-  const uint32_t b = abs_bits(v);
-  return b < 0x7F800000u ? b : 0;
+// Infinities and NaN are in the first part alone.
+__device__ __forceinline__ void split(float v, uint16_t (&part)[kParts]) {
+  const bool odd = abs_bits(v) >= 0x7F800000u;
+  const uint32_t hi = odd ? static_cast<uint32_t>(bf16_bits(v)) << 16 : __float_as_uint(v) & 0xFFFF0000u;
+  const float r = odd ? 0.0f : v - __uint_as_float(hi);
+  const uint32_t mid = __float_as_uint(r) & 0xFFFF0000u;
+  const float lo = r - __uint_as_float(mid);
+  part[0] = static_cast<uint16_t>(hi >> 16);
+  part[1] = static_cast<uint16_t>(mid >> 16);
+  part[2] = static_cast<uint16_t>(__float_as_uint(lo) >> 16);
 }
-// Exponent e that brings a maximum (its bits) to 2^14 .. 2^15 as v 2^e; 0 for a maximum of 0.
-__device__ __forceinline__ int scale_exponent(uint32_t max_bits) {
-  return max_bits ? min(14 - (static_cast<int>(max_bits >> 23) - 127), 126) : 0;
-}
-// Parts of v (fp16: of v 2^e). Infinities and NaN are in the first part alone.
+// Eight 16-bit values as bf16 parts. What is infinite or NaN is NaN in the second part.
 template <int DT>
-__device__ __forceinline__ void split(float v, int e, uint16_t (&part)[3]) {
-  if constexpr (DT == BL_BF16) {
-    const bool odd = abs_bits(v) >= 0x7F800000u;
-    const uint32_t hi = odd ? static_cast<uint32_t>(bf16_bits(v)) << 16 : __float_as_uint(v) & 0xFFFF0000u;
-    const float r = odd ? 0.0f : v - __uint_as_float(hi);
-    const uint32_t mid = __float_as_uint(r) & 0xFFFF0000u;
-    const float lo = r - __uint_as_float(mid);
-    part[0] = static_cast<uint16_t>(hi >> 16);
-    part[1] = static_cast<uint16_t>(mid >> 16);
-    part[2] = static_cast<uint16_t>(__float_as_uint(lo) >> 16);
+__device__ __forceinline__ void value_parts(u32x4 v, u32x4 (&part)[kValueParts<DT>]) {
+  if constexpr (DT == BL_F16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f[2] = {to_float<BL_F16>(static_cast<uint16_t>(v[i])), to_float<BL_F16>(static_cast<uint16_t>(v[i] >> 16))};
+      uint32_t b[2], r[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        b[j] = __float_as_uint(f[j]);
+        r[j] = __float_as_uint(f[j] - __uint_as_float(b[j] & 0xFFFF0000u));
+      }
+      part[0][i] = __builtin_amdgcn_perm(b[1], b[0], 0x07060302u);
+      part[1][i] = __builtin_amdgcn_perm(r[1], r[0], 0x07060302u);
+    }
   } else {
-    const bool odd = abs_bits(v) >= 0x7F800000u;
-    const float s = ldexpf(v, e);
-    part[0] = half_bits(s);
-    part[1] = odd ? 0 : half_bits(s - static_cast<float>(__builtin_bit_cast(_Float16, part[0])));
-    part[2] = 0;
+    part[0] = v;
   }
+}
+// acc += the product of coefficients and values, the least parts first.
+template <int DT>
+__device__ __forceinline__ f32x4 dot_parts(const u32x4 (&c)[kParts], const u32x4 (&v)[kValueParts<DT>], f32x4 acc) {
+#pragma unroll
+  for (int p = kParts - 1; p >= 0; --p)
+#pragma unroll
+    for (int q = kValueParts<DT> - 1; q >= 0; --q) acc = dot32<BL_BF16>(c[p], v[q], acc);
+  return acc;
 }
 
 // Coefficients of the sorted rows, in what the passes after it need of: fp32 [rows, RP]; parts as operands
-// whose rows are rows, [rows / 16, RK / 32, n, 64 lanes, 8] (RK: R up to 32), with exponents [rows]; parts as operands
-// whose rows are ranks, [tiles, RP / 16, n, 64 lanes, 8], with exponents [tiles, RP]. So an operand is
-// 1 KB in one piece. What a row or a rank has not is 0.
+// whose rows are rows, [rows / 16, RK / 32, 3, 64 lanes, 8] (RK: R up to 32); parts as operands whose rows
+// are ranks, [tiles, RP / 16, 3, 64 lanes, 8]. So an operand is 1 KB in one piece. What a row or a rank
+// has not is 0.
 struct Coefs {
   float* f;
   uint16_t* by_row;
-  int32_t* row_e;
   uint16_t* by_rank;
-  int32_t* rank_e;
 };
 
 // ------------------------------------------------------------------------------------------
@@ -450,54 +456,31 @@ __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int RP, c
   if (c.f)
     for (int i = tid; i < kTile * RP; i += 64 * kShrinkWaves) c.f[t * kTile * RP + i] = v[i / RP * pitch + i % RP];
   if constexpr (DT != BL_F32) {
-    constexpr int P = Parts<DT>::n;
-    if (c.by_row) {
-      const int RK = (RP + 31) / 32 * 32, m = tid / 8, q = tid % 8;
-      int e = 0;
-      if constexpr (DT == BL_F16) {
-        uint32_t top = 0;
-        for (int r = q; r < RP; r += 8) top = max(top, finite_bits(v[m * pitch + r]));
+    const auto parts_of = [&](auto at, u32x4 (&w)[kParts]) {   // of eight values
 #pragma unroll
-        for (int off = 1; off < 8; off <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off)));
-        e = scale_exponent(top);
-        if (q == 0) c.row_e[t * kTile + m] = -e;
+      for (int j = 0; j < 8; ++j) {
+        uint16_t part[kParts];
+        split(at(j), part);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) w[p][j / 2] |= static_cast<uint32_t>(part[p]) << (16 * (j & 1));
       }
-      for (int k = q; k < RK / 8; k += 8) {
-        u32x4 w[3] = {};
+    };
+    if (c.by_row) {
+      const int RK = (RP + 31) / 32 * 32, m = tid / 8;
+      for (int k = tid % 8; k < RK / 8; k += 8) {
+        u32x4 w[kParts] = {};
+        parts_of([&](int j) { return 8 * k + j < RP ? v[m * pitch + 8 * k + j] : 0.0f; }, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint16_t part[3];
-          split<DT>(8 * k + j < RP ? v[m * pitch + 8 * k + j] : 0.0f, e, part);
-#pragma unroll
-          for (int p = 0; p < P; ++p) w[p][j / 2] |= static_cast<uint32_t>(part[p]) << (16 * (j & 1));
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(c.by_row + (((t * 2 + m / 16) * (RK / 32) + k / 4) * P + p) * 512 + (k % 4 * 16 + m % 16) * 8) = w[p];
+        for (int p = 0; p < kParts; ++p) *reinterpret_cast<u32x4*>(c.by_row + (((t * 2 + m / 16) * (RK / 32) + k / 4) * kParts + p) * 512 + (k % 4 * 16 + m % 16) * 8) = w[p];
       }
     }
     if (c.by_rank) {
       const int q = tid % 4;
       for (int r = tid / 4; r < RP; r += 16 * kShrinkWaves) {
-        int e = 0;
-        if constexpr (DT == BL_F16) {
-          uint32_t top = 0;
+        u32x4 w[kParts] = {};
+        parts_of([&](int j) { return v[(8 * q + j) * pitch + r]; }, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top = max(top, finite_bits(v[(8 * q + j) * pitch + r]));
-#pragma unroll
-          for (int off = 1; off < 4; off <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off)));
-          e = scale_exponent(top);
-          if (q == 0) c.rank_e[t * RP + r] = -e;
-        }
-        u32x4 w[3] = {};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint16_t part[3];
-          split<DT>(v[(8 * q + j) * pitch + r], e, part);
-#pragma unroll
-          for (int p = 0; p < P; ++p) w[p][j / 2] |= static_cast<uint32_t>(part[p]) << (16 * (j & 1));
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(c.by_rank + ((t * (RP / 16) + r / 16) * P + p) * 512 + (q * 16 + r % 16) * 8) = w[p];
+        for (int p = 0; p < kParts; ++p) *reinterpret_cast<u32x4*>(c.by_rank + ((t * (RP / 16) + r / 16) * kParts + p) * 512 + (q * 16 + r % 16) * 8) = w[p];
       }
     }
   }
@@ -754,9 +737,9 @@ __device__ __forceinline__ void load_base(const ExpandArgs& a, const int (&row)[
   for (int l = 0; l < 4; ++l)                       // a place without a row reads row 0
     base[l] = load8<YD, WHOLE>(static_cast<const Y*>(a.base) + max(row[l], 0) * a.ldbase, n, a.N);
 }
-template <int WD, int YD>
+template <int YD>
 __device__ __forceinline__ void store_rows(const ExpandArgs& a, const int (&row)[4], int64_t n, int64_t lo, const Eight<YD> (&base)[4],
-                                           const f32x4 (&acc)[8], const int (&ex)[4]) {
+                                           const f32x4 (&acc)[8]) {
   using Y = typename Elem<YD>::type;
 #pragma unroll
   for (int l = 0; l < 4; ++l) {
@@ -765,7 +748,6 @@ __device__ __forceinline__ void store_rows(const ExpandArgs& a, const int (&row)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       v[j] = acc[j][l];
-      if constexpr (WD == BL_F16) v[j] = ldexpf(v[j], ex[l]);
       if (a.base) v[j] = value<YD>(base[l], j) + v[j];
     }
     store8<YD>(static_cast<Y*>(a.y) + row[l] * a.ldy, n, lo, a.N, v);
@@ -794,10 +776,10 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
   const int c = lane & 15, g = lane >> 4;
   const int64_t n = n0 + 8 * c;
   using W = typename Elem<WD>::type;
-  constexpr int P = Parts<WD>::n;
+  constexpr int VP = kValueParts<WD>;
   const W* w = static_cast<const W*>(a.w) + static_cast<int64_t>(e) * a.R * a.N;
   const int RK = (a.RP + 31) / 32 * 32;
-  int row[4], ex[4] = {};
+  int row[4];
   const auto rows = [&](int64_t p, int (&r)[4]) {
 #pragma unroll
     for (int l = 0; l < 4; ++l) r[l] = a.o.order[p + 4 * g + l];
@@ -813,7 +795,10 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
   Eight<YD> base[4] = {};
   rows(at, row);
   load_base<YD, WHOLE>(a, row, n, base);
-  u32x4 wv[KB ? KB : 1][8];                         // as operands: column j of block k
+  // as operands: column j of block k. Two blocks of fp16 columns in parts would take 128 registers: they are
+  // cut for each tile (4096 x 8192, rank 64: 86 us for the whole call where 93)
+  constexpr bool kCut = WD != BL_F16 || KB == 1;
+  u32x4 wv[KB ? KB : 1][8][kCut ? VP : 1];
   if constexpr (KB > 0) {
     u32x4 raw[KB][8];
 #pragma unroll
@@ -821,16 +806,16 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
 #pragma unroll
     for (int k = 0; k < KB; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wv[k][j] = column(raw[k], j);
+      for (int j = 0; j < 8; ++j) {
+        const u32x4 v = column(raw[k], j);
+        if constexpr (kCut) value_parts<WD>(v, wv[k][j]);
+        else wv[k][j][0] = v;
+      }
   }
   for (int i = 0; i < count; ++i, at += kTile) {
     f32x4 acc[8] = {};
     int next[4];
     rows(i + 1 < count ? at + kTile : at, next);
-    if constexpr (WD == BL_F16) {
-#pragma unroll
-      for (int l = 0; l < 4; ++l) ex[l] = a.c.row_e[at + 4 * g + l];
-    }
     if constexpr (WD == BL_F32) {
       const float* co = a.c.f + at * a.RP;
       for (int r0 = 0; r0 < a.RP; r0 += 16) {
@@ -848,37 +833,43 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
           for (int j = 0; j < 8; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[s], value<WD>(v[s], j), acc[j], 0, 0, 0);
       }
     } else {
-      const u32x4* co = reinterpret_cast<const u32x4*>(a.c.by_row) + at / 16 * (RK / 32) * P * 64 + lane;
+      const u32x4* co = reinterpret_cast<const u32x4*>(a.c.by_row) + at / 16 * (RK / 32) * kParts * 64 + lane;
       if constexpr (KB > 0) {
-        u32x4 cv[KB][P];
+        u32x4 cv[KB][kParts];
 #pragma unroll
         for (int k = 0; k < KB; ++k)
 #pragma unroll
-          for (int p = 0; p < P; ++p) cv[k][p] = co[(k * P + p) * 64];
+          for (int p = 0; p < kParts; ++p) cv[k][p] = co[(k * kParts + p) * 64];
 #pragma unroll
         for (int k = 0; k < KB; ++k)
-#pragma unroll
-          for (int p = P - 1; p >= 0; --p)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = dot32<WD>(cv[k][p], wv[k][j], acc[j]);
-      } else {
-        for (int r0 = 0; r0 < RK; r0 += 32) {
-          u32x4 raw[8], cv[P];
-          load_w(r0, raw);
-#pragma unroll
-          for (int p = 0; p < P; ++p) cv[p] = co[(r0 / 32 * P + p) * 64];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const u32x4 v = column(raw, j);
+            if constexpr (kCut) {
+              acc[j] = dot_parts<WD>(cv[k], wv[k][j], acc[j]);
+            } else {
+              u32x4 v[VP];
+              value_parts<WD>(wv[k][j][0], v);
+              acc[j] = dot_parts<WD>(cv[k], v, acc[j]);
+            }
+          }
+      } else {
+        for (int r0 = 0; r0 < RK; r0 += 32) {
+          u32x4 raw[8], cv[kParts];
+          load_w(r0, raw);
 #pragma unroll
-            for (int p = P - 1; p >= 0; --p) acc[j] = dot32<WD>(cv[p], v, acc[j]);
+          for (int p = 0; p < kParts; ++p) cv[p] = co[(r0 / 32 * kParts + p) * 64];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            u32x4 v[VP];
+            value_parts<WD>(column(raw, j), v);
+            acc[j] = dot_parts<WD>(cv, v, acc[j]);
           }
         }
       }
     }
     Eight<YD> more[4] = {};
     load_base<YD, WHOLE>(a, next, n, more);
-    store_rows<WD, YD>(a, row, n, lo, base, acc, ex);
+    store_rows<YD>(a, row, n, lo, base, acc);
 #pragma unroll
     for (int l = 0; l < 4; ++l) {
       row[l] = next[l];
@@ -890,7 +881,7 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
 // A workgroup has up to `tiles` tiles and 256 columns, its waves the tiles' halves. Tiles come after the
 // columns: rows are read and written whole by workgroups that run together.
 template <int WD, int YD, int KB>
-__global__ __launch_bounds__(256, YD == BL_F32 ? 2 : 3) void adapter_expand_kernel(ExpandArgs a) {
+__global__ __launch_bounds__(256, YD == BL_F32 || (WD == BL_F16 && KB == 2) ? 2 : 3) void adapter_expand_kernel(ExpandArgs a) {
   const int t = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t at = static_cast<int64_t>(t) * kTile + 16 * (wave & 1);
   int end = a.o.start[a.o.L + 1], word = a.o.tile[t], first = a.o.order[at], row[4];
@@ -952,12 +943,10 @@ struct OuterPair {
 // What a wave takes of a tile: lane 16 g + c rows 8 g .. 8 g + 7 (fp32: 4 i + g), columns 8 c .. 8 c + 7.
 template <int SD, int NR>
 struct OuterTile {
-  static constexpr int P = Parts<SD>::n;
   int row[8];
   Eight<SD> s[8];
-  u32x4 c[P][NR];                                   // 16-bit parts
+  u32x4 c[NR][kParts];                              // 16-bit parts
   float f[SD == BL_F32 ? 8 : 1][NR];
-  int ex[SD == BL_F16 ? NR : 1][4];
 
   __device__ __forceinline__ void load_rows(const OuterArgs& a, int64_t t, int g) {
 #pragma unroll
@@ -982,12 +971,8 @@ struct OuterTile {
       for (int q = 0; q < NR; ++q) {
         const int rb = min(r0 / 16 + q, a.RP / 16 - 1);   // past the last rank: not used
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-          c[p][q] = reinterpret_cast<const u32x4*>(a.c.by_rank)[((t * (a.RP / 16) + rb) * P + p) * 64 + 16 * g + c16];
-        if constexpr (SD == BL_F16) {
-#pragma unroll
-          for (int l = 0; l < 4; ++l) ex[q][l] = a.c.rank_e[t * a.RP + min(r0 + 16 * q + 4 * g + l, a.RP - 1)];
-        }
+        for (int p = 0; p < kParts; ++p)
+          c[q][p] = reinterpret_cast<const u32x4*>(a.c.by_rank)[((t * (a.RP / 16) + rb) * kParts + p) * 64 + 16 * g + c16];
       }
     }
   }
@@ -1009,20 +994,10 @@ struct OuterTile {
       for (int i = 0; i < 8; ++i) w[i] = zero_unless(rows[i] >= 0, s[i]).w;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const u32x4 v = column(w, j);
+        u32x4 v[kValueParts<SD>];
+        value_parts<SD>(column(w, j), v);
 #pragma unroll
-        for (int q = 0; q < NR; ++q) {
-          if constexpr (SD == BL_F16) {
-            f32x4 one = {};
-#pragma unroll
-            for (int p = P - 1; p >= 0; --p) one = dot32<SD>(c[p][q], v, one);
-#pragma unroll
-            for (int l = 0; l < 4; ++l) acc[q][j][l] += ldexpf(one[l], ex[q][l]);
-          } else {
-#pragma unroll
-            for (int p = P - 1; p >= 0; --p) acc[q][j] = dot32<SD>(c[p][q], v, acc[q][j]);
-          }
-        }
+        for (int q = 0; q < NR; ++q) acc[q][j] = dot_parts<SD>(c[q], v, acc[q][j]);
       }
     }
   }
@@ -1402,12 +1377,11 @@ int64_t outer_counters(int64_t M, int64_t L, int64_t R, int64_t D) { return oute
 
 // Bytes of each layout of the coefficients.
 struct CoefBytes {
-  size_t f, by_row, row_e, by_rank, rank_e;
+  size_t f, by_row, by_rank;
 };
 CoefBytes coef_bytes(int64_t M, int64_t L, int64_t R) {
-  const int64_t tiles = max_tiles(M, L), rows = tiles * kTile, RP = rank_pad(R), RK = div_up(R, 32) * 32;
-  return {static_cast<size_t>(rows * RP * 4), static_cast<size_t>(3 * rows * RK * 2), static_cast<size_t>(rows * 4),
-          static_cast<size_t>(3 * rows * RP * 2), static_cast<size_t>(tiles * RP * 4)};
+  const int64_t rows = max_tiles(M, L) * kTile, RP = rank_pad(R), RK = div_up(R, 32) * 32;
+  return {static_cast<size_t>(rows * RP * 4), static_cast<size_t>(kParts * rows * RK * 2), static_cast<size_t>(kParts * rows * RP * 2)};
 }
 
 struct Scratch {
@@ -1430,9 +1404,8 @@ Scratch scratch(const AdapterWs& L, char* ws, const AdapterRows& r) {
   s.part = reinterpret_cast<float*>(ws + L.part_off);
   for (int i = 0; i < 2; ++i) s.sum[i] = reinterpret_cast<float*>(ws + L.sum_off[i]);
   s.o = Sorted{s.order, s.tile, s.start, static_cast<int>(r.L), max_tiles(r.M, r.L) * kTile};
-  const auto coefs = [&](const size_t (&at)[5]) {
-    return Coefs{reinterpret_cast<float*>(ws + at[0]), reinterpret_cast<uint16_t*>(ws + at[1]), reinterpret_cast<int32_t*>(ws + at[2]),
-                 reinterpret_cast<uint16_t*>(ws + at[3]), reinterpret_cast<int32_t*>(ws + at[4])};
+  const auto coefs = [&](const size_t (&at)[3]) {
+    return Coefs{reinterpret_cast<float*>(ws + at[0]), reinterpret_cast<uint16_t*>(ws + at[1]), reinterpret_cast<uint16_t*>(ws + at[2])};
   };
   s.c = coefs(L.c_off);
   s.hc = coefs(L.hc_off);
@@ -1508,8 +1481,8 @@ hipError_t start_outer(const OuterPair& a, uint32_t columns, int sd, int td, hip
 Coefs only(const Coefs& c, int dt, bool rows, bool ranks) {
   Coefs o{};
   if (dt == BL_F32) o.f = c.f;
-  else if (rows) o.by_row = c.by_row, o.row_e = c.row_e;
-  if (dt != BL_F32 && ranks) o.by_rank = c.by_rank, o.rank_e = c.rank_e;
+  else if (rows) o.by_row = c.by_row;
+  if (dt != BL_F32 && ranks) o.by_rank = c.by_rank;
   return o;
 }
 
@@ -1533,12 +1506,11 @@ AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool
   w.counters = tiles + (backward ? outer_counters(M, L, R, K) + outer_counters(M, L, R, N) : 0);
   w.arrived_off = take(w.counters * 4);
   w.part_off = take(shrink_splits(M, L, R, D) * rows * RP * 4);
-  const size_t each[5] = {b.f, b.by_row, b.row_e, backward ? b.by_rank : 0, backward ? b.rank_e : 0};
-  for (int i = 0; i < 5; ++i) w.c_off[i] = take(each[i]);
+  const size_t each[3] = {b.f, b.by_row, backward ? b.by_rank : 0};
+  for (int i = 0; i < 3; ++i) w.c_off[i] = take(each[i]);
   if (backward) {
     w.hc_off[0] = take(b.f);
-    w.hc_off[3] = take(b.by_rank);
-    w.hc_off[4] = take(b.rank_e);
+    w.hc_off[2] = take(b.by_rank);
     w.sum_off[0] = take(2 * outer_shares(M, L, R, K) * R * K * 4);
     w.sum_off[1] = take(2 * outer_shares(M, L, R, N) * R * N * 4);
   }

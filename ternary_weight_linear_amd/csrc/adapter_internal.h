@@ -63,8 +63,8 @@ struct AdapterWs {
   size_t arrived_off;    // uint32 [counters] workgroups that have ended, cleared by the sort
   int64_t counters;
   size_t part_off;       // fp32 [splits, rows, RP] partial sums of the products over K or N
-  size_t c_off[5];       // the scaled h (forward) or dh, sorted, in each layout that is needed
-  size_t hc_off[5];      // the scaled h (backward)
+  size_t c_off[3];       // the scaled h (forward) or dh, sorted, in each layout that is needed
+  size_t hc_off[3];      // the scaled h (backward)
   size_t sum_off[2];     // fp32 [2 shares, R, D] partial sums over rows, of da and of db (backward)
   size_t total;
 };
