@@ -1371,9 +1371,9 @@ int outer_splits(int64_t M, int64_t L, int64_t R, int64_t blocks, int dt) {
   const int64_t enough = std::max(div_up(M / kTile + std::min(M, L), 4), div_up(L, 4));
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most / groups, enough, 32})));
 }
-// The most that either sum takes by itself.
-int64_t outer_shares(int64_t M, int64_t L, int64_t R, int64_t D) { return outer_splits(M, L, R, div_up(D, 128), BL_F32); }
-int64_t outer_counters(int64_t M, int64_t L, int64_t R, int64_t D) { return outer_shares(M, L, R, D) * div_up(D, 128) * div_up(rank_pad(R), 32); }
+// The most shares that a call's sums have, and the counters of one of them.
+int64_t outer_shares(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N) { return outer_splits(M, L, R, div_up(K, 128) + div_up(N, 128), BL_F32); }
+int64_t outer_counters(int64_t shares, int64_t R, int64_t D) { return shares * div_up(D, 128) * div_up(rank_pad(R), 32); }
 
 // Bytes of each layout of the coefficients.
 struct CoefBytes {
@@ -1503,16 +1503,17 @@ AdapterWs adapter_ws(int64_t M, int64_t L, int64_t R, int64_t K, int64_t N, bool
   w.tile_off = take(tiles * 4);
   w.start_off = take((L + 2) * 4);
   w.count_off = take(M > kSortChunk ? div_up(M, kSortChunk) * (L + 1) * 4 : 0);
-  w.counters = tiles + (backward ? outer_counters(M, L, R, K) + outer_counters(M, L, R, N) : 0);
+  const int64_t shares = outer_shares(M, L, R, K, N), splits = shrink_splits(M, L, R, D);
+  w.counters = tiles + (backward ? outer_counters(shares, R, K) + outer_counters(shares, R, N) : 0);
   w.arrived_off = take(w.counters * 4);
-  w.part_off = take(shrink_splits(M, L, R, D) * rows * RP * 4);
+  w.part_off = take(splits * div_up(RP, 64) > 1 ? splits * rows * RP * 4 : 0);   // a workgroup that has a tile alone meets none
   const size_t each[3] = {b.f, b.by_row, backward ? b.by_rank : 0};
   for (int i = 0; i < 3; ++i) w.c_off[i] = take(each[i]);
   if (backward) {
     w.hc_off[0] = take(b.f);
     w.hc_off[2] = take(b.by_rank);
-    w.sum_off[0] = take(2 * outer_shares(M, L, R, K) * R * K * 4);
-    w.sum_off[1] = take(2 * outer_shares(M, L, R, N) * R * N * 4);
+    w.sum_off[0] = take(shares > 1 ? 2 * shares * R * K * 4 : 0);   // every adapter lies within the one share
+    w.sum_off[1] = take(shares > 1 ? 2 * shares * R * N * 4 : 0);
   }
   w.total = off;
   return w;
@@ -1549,7 +1550,7 @@ hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipSt
   const int64_t kb = div_up(a.K, 128), nb = div_up(a.N, 128);
   const int shares = outer_splits(r.M, r.L, r.R, kb + nb, a.dydtype);
   const OuterArgs da{w.o, w.c, a.x, a.K, a.ldx, R, RP, shares, w.sum[0], arrived, a.da, a.add};
-  const OuterArgs db{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, shares, w.sum[1], arrived + outer_counters(r.M, r.L, r.R, a.K), a.db, a.add};
+  const OuterArgs db{w.o, w.hc, a.dy, a.N, a.lddy, R, RP, shares, w.sum[1], arrived + outer_counters(shares, r.R, a.K), a.db, a.add};
   // before dx, whose traffic would turn dy out of the caches; fp32, which takes longer, first
   e = start_outer(OuterPair{{db, da}, static_cast<uint32_t>(nb)}, static_cast<uint32_t>(kb + nb), a.dydtype, a.dtype, s);
   if (e != hipSuccess || !a.dx) return e;
