@@ -1317,13 +1317,20 @@ __global__ __launch_bounds__(256) void adapter_rows_expand_kernel(RowsArgs p) {
 // ------------------------------------------------------------------------------------------
 // launches
 // ------------------------------------------------------------------------------------------
-// Values of the adapters that the rows read if each reads its own: up to this they are done so, in two launches
-// that wait for nothing and need no scratch. (us from a graph, this way / sorted, bf16: 1 row of 8192 x 8192, rank 16 6.5 / 17, 64 rows of 16
-// adapters 10 / 21; 134 MB: 512 rows of 4096 x 4096, rank 16 of 2 / 64 adapters 16.5 / 19.4 and 20.0 / 22.7, 64 rows of
-// 8192 x 8192, rank 64 of 16 19.7 / 26.2; 268 MB: 512 rows of 8192 x 8192, rank 16 of 16 27.2 / 25.8, 128, rank 64 of 16
-// 26.5 / 26.6; 604 MB: 512 rows of 8192 x 28672, rank 16 of 16 65 / 39.)
-constexpr int64_t kRowsMost = int64_t(3) << 25;
-bool by_rows(int64_t M, int64_t R, int64_t K, int64_t N) { return M <= 65535 && M * R * (K + N) <= kRowsMost; }
+// Rows each by itself, in two launches that wait for nothing and need no scratch, or sorted. Each by itself
+// a row reads its own copy of its adapter, R (K + N) values; a workgroup of four ranks takes as
+// long as 8192 values whatever it reads, and a row's other workgroups as long as 12288. Sorted,
+// the waits of three launches are most of the time until the rows themselves are. Up to kRowsMost by
+// this count each goes by itself. (us from a graph, by itself / sorted, bf16, eight adapters: 64 rows of 8192 x 8192, rank 16
+// 9.9 / 17.6, rank 64 17.9 / 23.5; 256 rows of 4096 x 4096, rank 64 21.7 / 23.0; 256 of 8192 x 28672, rank 8
+// 28.8 / 24.5; 1024 of 1024 x 1024, rank 16 16.8 / 17.8, rank 64 38 / 22; 1024 of 512 x 512, rank 8 9.5 / 14.7; 4096 of
+// 128 x 128, rank 8 21.6 / 16.3, rank 64 104 / 19. fp32 reads twice as much on both ways: 256 of 4096 x 4096, rank 64
+// 33.5 / 34.2, 64 of 8192 x 8192, rank 64 27.2 / 33.7. Over 464 shapes 1.1 % from the better way, 42 % at most; by
+// R (K + N) alone 28 %, and 13 times its time at most.)
+constexpr int64_t kRowsMost = int64_t(11) << 23;
+bool by_rows(int64_t M, int64_t R, int64_t K, int64_t N) {
+  return M <= 65535 && M * (div_up(R, 4) * std::max<int64_t>(4 * K, 8192) + R * N + 12288) <= kRowsMost;
+}
 
 template <int DT>
 hipError_t start_rows_shrink(const RowsArgs& p, hipStream_t s) {
