@@ -433,7 +433,10 @@ struct Sorted {
 // picked up from LDS of the wave's own. Where there are several workgroups to a tile, the last one
 // that ends adds their sums, in order, and makes the coefficients (memory-side stores, no cache
 // write-back: about 1 us to arrive, 1 to gather, 1.5 to 4.5 for the coefficients). 4096 x 8192, bf16, rank 32:
-// 24 us, of which 15 are the loop at 4.5 TB/s of rows; rank 64 31 us (operands straight from memory 39).
+// 24 us, of which 15 are the loop at 4.5 TB/s of rows; rank 64 31 us (operands straight from memory 39). 64 ranks to
+// a workgroup, since each block of ranks reads the rows again (with 32, the whole call, bf16: 4096 x 8192, rank 64 80 -> 82 us, rank
+// 128 131 -> 135, 2000 x 8640, rank 40 37 -> 41). Registers for two workgroups to a CU: for one 79 -> 83, for three,
+// which spill, 140 (rank 64).
 constexpr int kShrinkWaves = 4;
 struct ShrinkArgs {
   Sorted o;
@@ -879,7 +882,9 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
 }
 
 // A workgroup has up to `tiles` tiles and 256 columns, its waves the tiles' halves. Tiles come after the
-// columns: rows are read and written whole by workgroups that run together.
+// columns: rows are read and written whole by workgroups that run together. Registers for three
+// workgroups to a CU (two of fp32 results, and of two blocks of fp16): for two the same within 1 us, for four, which
+// spill, 4096 x 8192, rank 64 79 -> 140 us.
 template <int WD, int YD, int KB>
 __global__ __launch_bounds__(256, YD == BL_F32 || (WD == BL_F16 && KB == 2) ? 2 : 3) void adapter_expand_kernel(ExpandArgs a) {
   const int t = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -1084,7 +1089,10 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
   const int64_t shares = min(static_cast<int64_t>(a.splits), tiles);
   if (blockIdx.y >= shares) return;
   const int t0 = static_cast<int>(tiles * blockIdx.y / shares), t1 = static_cast<int>(tiles * (blockIdx.y + 1) / shares);
-  const int few = max(4, (t1 - t0) / 4);
+  // (us of the gradients, bf16, for a quarter / third / half of the share: 4096 x 4096, rank 32, 16 adapters 92 / 84 /
+  // 83, 32 of rank 16 85 / 80 / 80; 12000 x 4096, rank 32, 8 adapters 163 / 163 / 184, 16 188 / 165 / 165; none: 2048 x 2048,
+  // rank 8, 200 adapters 47 -> 68)
+  const int few = max(4, (t1 - t0) / 3);
   int turn = 0;
   int words = 0, words_at = t0 - 64;                // of 64 tiles, one a lane
   for (int t = t0; t < t1;) {
@@ -1183,7 +1191,9 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
 }
 
 // Types of the first and the second sum of a pair. Registers: two workgroups to a CU, or one with two tiles of 16-bit
-// values in flight beyond rank 16; fp32 leaves none for a second tile.
+// values in flight beyond rank 16; fp32 leaves none for a second tile. (us of the gradients of 4096 x 8192, rank 32, for one /
+// two: bf16 100 / 127, fp32 223 / 207; 1024 x 4096, rank 8, bf16 44 / 41.) 32 ranks to a workgroup: with 16, whose rows are
+// read twice as often, 4096 x 8192, rank 32 101 -> 115 us, 8 adapters of rank 64 142 -> 156.
 template <int SD, int TD, int NR>
 __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_outer_kernel(OuterPair pair) {
   __shared__ f32x4 red[4 * 16 * NR][32];
@@ -1335,7 +1345,9 @@ bool by_rows(int64_t M, int64_t R, int64_t K, int64_t N) {
 template <int DT>
 hipError_t start_rows_shrink(const RowsArgs& p, hipStream_t s) {
   const auto M = static_cast<uint32_t>(p.f.rows.M);
-  // one rank to a workgroup while that makes few of them, else four, which share the row's reads
+  // one rank to a workgroup while that makes few of them, else four, which share the row's reads (us, one / four,
+  // bf16: 16 rows of 8192, rank 16 7.9 / 8.9, 64 rows 11.0 / 12.4, 128 rows 13.3 / 14.7, of 4096 11.2 / 11.2; 256 rows of
+  // 4096, rank 16 14.5 / 13.3, 320, rank 32 22.1 / 17.8, 900 of 1024, rank 8 13.3 / 11.1)
   if (p.f.rows.M * p.R <= 1024) adapter_rows_shrink_kernel<DT, 1><<<dim3(M, p.R), 256, 0, s>>>(p);
   else adapter_rows_shrink_kernel<DT, 4><<<dim3(M, static_cast<uint32_t>(div_up(p.R, 4))), 256, 0, s>>>(p);
   return hipGetLastError();
@@ -1368,6 +1380,9 @@ int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
 // bf16: 4096 x 8192, rank 64 42 / 38 / 38 / 42, rank 32 34 / 31 / 32 / 36; 777 x 3200, rank 12, fp32 results 7.4 / 9.2 for
 // 1 / 2.)
 int expand_tiles_of(int64_t M, int64_t N) { return M * N >= int64_t(1) << 25 ? 4 : M * N >= int64_t(1) << 24 ? 2 : 1; }
+// A run of tiles to each of the eight chips, or neighbours to different ones (us, by chip / not, bf16, 4096 rows of
+// 8192: 64 adapters of rank 64 103 / 108, 8 79.1 / 80.6, of rank 32 70.5 / 71.0; fewer rows gain or lose as often: 1024 of
+// 8192, rank 32 28.9 / 30.8, 1024 of 3200, rank 8 26.0 / 25.3, 400 of 8640, rank 64 27.7 / 27.1).
 int by_chip(const AdapterRows& r) { return r.M >= 64 * kTile; }
 // Two workgroups to a CU, or the one that two tiles' registers of 16-bit values leave beyond rank 16. (us,
 // 4096 rows of 8192, bf16, rank 32: 22 for 256 workgroups, 32 for 384, 30 for 512, 44 for 1024.)
