@@ -136,6 +136,7 @@ def _ptr(t):
 
 # The handle of torch's current stream without building a Stream object (2 us of a call's 10).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(device):
@@ -151,6 +152,10 @@ def _dev(*ts):
             raise ValueError(f"all tensors must be on one device, got {sorted({str(t.device) for t in ts if t is not None})}")
     if d.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {d}")
+    # the library launches on the current device, where another one's default stream and memory mean nothing
+    if d.index != _current_device():
+        raise ValueError(f"tensors are on {d}, but the current device is cuda:{_current_device()}: "
+                         f"call with torch.cuda.device({d.index})")
     return d
 
 
