@@ -76,3 +76,31 @@ def test_one_expert_far_above_the_others(E, score):
             # exponentials of at most 5 in size, sums of E terms in chains of E / 16 + 4
             bound = (2 * 5 + E / 8 + 40) * u
             assert abs(loss.item() - rloss[0]) <= bound * rloss[0] and np.all(np.abs(d - ref) <= 2 * bound * mag + step)
+
+
+def test_falling_offsets_write_nothing_outside_the_buffers():
+    """Offsets that fall are outside the contract: any numbers may come back, inside the outputs and the workspace,
+    which stand here between guards."""
+    say("route falling offsets, guarded")
+    M, E, k, S = 3000, 40, 2, 7
+    g = np.random.default_rng(7)
+    logits, index = gpu(g.standard_normal((M, E)).astype(np.float32)), gpu(g.integers(-1, E, (M, k)).astype(np.int32))
+    dloss, guard = torch.ones(S, device=DEV), 1 << 16
+    sizes = [S * 4, S * E * 4, S * E * 4, tw._lib.bl_route_balance_workspace_bytes(M, E, S), M * E * 4]
+    rows = [-5, 0, 1, 400, 1500, 2999, 3000, 3001, 2 ** 31 - 1, -2 ** 31]
+    for turn in range(40):
+        offsets = gpu(g.choice(rows, S + 1).astype(np.int32))
+        at, room = [], torch.full((sum(-(-n // 256) * 256 + guard for n in sizes) + guard,), 0xA5, dtype=torch.uint8, device=DEV)
+        kept = torch.ones(room.numel(), dtype=torch.bool, device=DEV)
+        where = guard
+        for n in sizes:
+            at.append(room.data_ptr() + where)
+            kept[where:where + n] = False
+            where += -(-n // 256) * 256 + guard
+        for score in (0, 1):
+            assert tw._lib.bl_route_balance(logits.data_ptr(), 2, M, E, E, index.data_ptr(), k, score, offsets.data_ptr(), S, at[0], at[1], at[2],
+                                            at[3], sizes[3], tw._stream(logits.device)) == 0
+            assert tw._lib.bl_route_backward(logits.data_ptr(), 2, M, E, E, index.data_ptr(), k, score, None, 0, 1.0, at[2], dloss.data_ptr(),
+                                             offsets.data_ptr(), S, at[4], 2, E, tw._stream(logits.device)) == 0
+        torch.cuda.synchronize()
+        assert torch.all(room[kept] == 0xA5), offsets.tolist()
