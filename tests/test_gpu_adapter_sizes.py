@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import oracle.adapters as oa
+import ternary_weight_linear_amd as tw
 from tests.gpu_util import say
 from tests.test_gpu_adapter import PAIRS, TYPES, Case, close, gpu, host, u
 
@@ -100,3 +101,38 @@ def test_matrices_of_subnormal_halves(M, least):
         # h is given, so no sum of db is one of fp16 products
         _, mag = oa.backward(c.xh, c.ah, c.bh, c.indexh, c.scaleh, host(h), c.dyh, none[1])
         close(got["db"], ref["db"], (M / 4 + 72) * u * mag["db"] + u * np.abs(ref["db"]), "fp32", "db")
+
+
+@pytest.mark.parametrize("M,K,N,L,R", [(1, 65536, 32768, 1, 256), (66000, 64, 72, 1, 64), (90, 1000, 136, 3, 9), (2048, 520, 264, 64, 33), (70000, 40, 24, 700, 100)])
+@pytest.mark.parametrize("dtype,out", PAIRS)
+def test_nothing_is_written_outside_the_outputs_and_the_workspace(M, K, N, L, R, dtype, out):
+    """Both calls with a workspace of just the size that they ask for, everything that they write between guards."""
+    say("adapter guarded", M, K, N, L, R, dtype, out)
+    c = Case(M, K, N, L, R, dtype, out, 5)
+    code, guard, lib, size = {"fp16": 0, "bf16": 1, "fp32": 2}, 1 << 12, tw._lib, TYPES[out].itemsize
+    ws = [lib.bl_adapter_workspace_bytes(M, K, N, L, R, b) for b in (0, 1)]
+    sizes = [M * N * size, M * R * 4, ws[0], M * K * size, L * R * K * 4, L * R * N * 4, ws[1]]
+    up = lambda n: -(-n // 256) * 256
+    room = torch.full((sum(up(n) + guard for n in sizes) + guard,), 0xA5, dtype=torch.uint8, device=c.x.device)
+    at, where, kept = [], guard, []
+    for n in sizes:
+        at.append(room.data_ptr() + where)
+        kept.append(room[where - guard:where])
+        kept.append(room[where + n:where + up(n)])
+        where += up(n) + guard
+    kept.append(room[where - guard:])
+    stream = tw._stream(c.x.device)
+    p = lambda t: t.data_ptr()
+    assert lib.bl_adapter_forward(p(c.x), code[dtype], M, K, K, p(c.a), p(c.b), L, R, N, p(c.index), p(c.scale), p(c.base), N, at[0], code[out], N,
+                                  at[1], at[2], ws[0], stream) == 0
+    assert lib.bl_adapter_backward(p(c.x), code[dtype], M, K, K, p(c.a), p(c.b), L, R, N, p(c.index), p(c.scale), at[1], p(c.dy), code[out], N,
+                                   p(c.dbase), K, at[3], code[out], K, at[4], at[5], 0, at[6], ws[1], stream) == 0
+    torch.cuda.synchronize()
+    assert all(torch.all(k == 0xA5) for k in kept)
+    y, h = c.forward()
+    for got, n, want in zip(at, sizes, (y, h)):
+        start = got - room.data_ptr()
+        assert torch.equal(room[start:start + n], want.contiguous().view(torch.uint8).flatten())
+    for i, want in zip((3, 4, 5), c.backward(h)):
+        start = at[i] - room.data_ptr()
+        assert torch.equal(room[start:start + sizes[i]], want.contiguous().view(torch.uint8).flatten())
