@@ -439,29 +439,31 @@ int bl_fp8_experts(const void* x, int dtype, int64_t M, int64_t H, int64_t ldx,
 /* ---- low-rank adapters beside a shared projection, and the router's training ----------------- */
 
 /* What can learn beside frozen weights. The conventions of the 8-bit section hold, but for
- * these: no size has to be a multiple of anything, and x and the adapters' matrices need the alignment
- * of their type alone (rows of whole 16-byte pieces at 16-byte addresses are read several times
- * faster).
+ * these: no size has to be a multiple of anything, and x and the adapters' matrices need the
+ * alignment of their type alone (rows of whole 16-byte pieces at 16-byte addresses are read
+ * several times faster).
  *
- * Row m has the adapter e = index[m] (int32 [M]) of the L adapters that a call is given, each of rank
- * R: a [L, R, K] and b [L, R, N], contiguous, in x's dtype. Both have their rows along the long axis, so b
- * holds the transpose of an nn.Linear weight [N, R]; an adapter of a lower rank has rows of zeros.
- * scale fp32 [L], or NULL for 1. A row whose index is outside [0, L) has no adapter. ydtype (dydtype,
- * dxdtype) is x's dtype or BL_F32. 1 <= M <= 2^20, 1 <= K, N <= 2^24, 1 <= R <= 256, 1 <= L <= 1024.
+ * Row m has the adapter e = index[m] (int32 [M]) of the L adapters that a call is given, each of
+ * rank R: a [L, R, K] and b [L, R, N], contiguous, in x's dtype. Both have their rows along the
+ * long axis, so b holds the transpose of an nn.Linear weight [N, R]; an adapter of a lower rank has
+ * rows of zeros. scale fp32 [L], or NULL for 1. A row whose index is outside [0, L) has no adapter.
+ * ydtype (dydtype, dxdtype) is x's dtype or BL_F32. 1 <= M <= 2^20, 1 <= K, N <= 2^24,
+ * 1 <= R <= 256, 1 <= L <= 1024.
  * Sums are fp32 sums, in a fixed order for a given shape and index, of products rounded to fp32 at
- * most (where x or dy and the matrices are fp16, values below 2^-14 count as 2^-14 in a sum's error); h and
- * dh go into their second product whole, but for what lies below 2^-133 where that is one of 16-bit
- * values. What NaN or an infinity reaches is not
- * finite, and may be NaN where the formula has an infinity; it reaches its own row and its own adapter's matrices alone.
- * Uses ws (bl_adapter_workspace_bytes; the last argument says which call it is for; 0 where a forward pass of few
- * rows needs none, and for sizes that are refused). */
+ * most. Where x (or dy) and the matrices are fp16, values below 2^-14 count as 2^-14 in a sum's
+ * error. h and dh go into their second product whole, but for what lies below 2^-133 where they
+ * meet 16-bit values. What NaN or an infinity reaches is not finite, and may be NaN where the
+ * formula has an infinity; it reaches its own row and its own adapter's matrices alone.
+ * Uses ws (bl_adapter_workspace_bytes; the last argument says which call it is for; 0 where a
+ * forward pass of few rows needs none, and for sizes that are refused). */
 size_t bl_adapter_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t R,
                                   int backward);
 
 /* h[m] = a[e] x[m] (fp32 [M, R], zeros without an adapter; the backward pass takes it) and
  *   y[m] = base[m] + scale[e] b[e]^T h[m],
- * rounded once to ydtype. base [M, N] of ydtype, rows ldbase apart: the shared projection's outputs.
- * It may be y itself (with ldbase = ldy: in place), or NULL for zeros; a row without an adapter is base's. */
+ * rounded once to ydtype. base [M, N] of ydtype, rows ldbase apart: the shared projection's
+ * outputs. It may be y itself (with ldbase = ldy: in place), or NULL for zeros; a row without an
+ * adapter is base's. */
 int bl_adapter_forward(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, const void* a,
                        const void* b, int64_t L, int64_t R, int64_t N, const int32_t* index,
                        const float* scale, const void* base, int64_t ldbase, void* y, int ydtype,
@@ -480,16 +482,18 @@ int bl_adapter_backward(const void* x, int dtype, int64_t M, int64_t K, int64_t 
                         int64_t lddx, float* da, float* db, int add, void* ws, size_t ws_bytes,
                         void* stream);
 
-/* Balance loss of a routing, and how many slots each expert got. Rows are packed sequences: sequence s
- * holds rows offsets[s] .. offsets[s + 1] - 1 (int32 [S + 1], not falling, on the device; cut at
- * 0 and M), rows before the first and behind the last count nowhere; NULL: one sequence of
+/* Balance loss of a routing, and how many slots each expert got. Rows are packed sequences:
+ * sequence s holds rows offsets[s] .. offsets[s + 1] - 1 (int32 [S + 1], not falling, on the device;
+ * cut at 0 and M), rows before the first and behind the last count nowhere; NULL: one sequence of
  * all rows, S = 1. index [M, k] as bl_route_experts gives it; a slot outside [0, E) is no slot, and
  * only rows with a slot count. With p the scores of bl_route_experts (no bias), t = p / sum of the
  * row's p, and for each sequence count[e] slots of expert e, C slots in all, T rows that count:
- *   coef[e] = E count[e] / (C T),   loss = sum over e of coef[e] times the sum of t[m, e] over those rows
+ *   coef[e] = E count[e] / (C T),
+ *   loss = sum over e of coef[e] times the sum of t[m, e] over those rows
  * (1 for an even load; an empty sequence gives zeros). Outputs: loss fp32 [S], count int32 [S, E],
- * coef fp32 [S, E], which is the loss's derivative by t. Sums over rows are fp32 within a chunk of about
- * M / 128 rows, 8192 at most, and fp64 over chunks, in a fixed order. E <= 2048, k <= 64, M k < 2^31, S <= 2^20. Uses ws. */
+ * coef fp32 [S, E], which is the loss's derivative by t. Sums over rows are fp32 within a chunk of
+ * at most 8192 rows and fp64 over chunks, in a fixed order. E <= 2048, k <= 64, M k < 2^31,
+ * S <= 2^20. Uses ws (bl_route_balance_workspace_bytes). */
 size_t bl_route_balance_workspace_bytes(int64_t M, int64_t E, int64_t S);
 int bl_route_balance(const void* logits, int dtype, int64_t M, int64_t E, int64_t ld,
                      const int32_t* index, int64_t k, int score, const int32_t* offsets, int64_t S,
