@@ -71,7 +71,8 @@ __device__ __forceinline__ void move_down(uint32_t (&v)[N], int s) {
 // Values at .. at + N - 1 of a row of n as dwords; those from n on are 0. Where the row ends inside, its
 // last N values are loaded and moved down, so that no load is under a condition.
 template <int DT, int N>
-__device__ __forceinline__ void load_end(const typename Elem<DT>::type* row, int64_t at, int64_t n, uint32_t (&v)[N * sizeof(typename Elem<DT>::type) / 4]) {
+__device__ __forceinline__ void load_end(const typename Elem<DT>::type* row, int64_t at, int64_t n,
+                                         uint32_t (&v)[N * sizeof(typename Elem<DT>::type) / 4]) {
   constexpr int W = N * sizeof(*row) / 4;           // dwords
   if (n < N) {                                      // uniform: a row shorter than a piece
 #pragma unroll
@@ -189,11 +190,11 @@ __device__ __forceinline__ f32x4 dot32(u32x4 a, u32x4 b, f32x4 acc) {
 // fp32 coefficients as 16-bit parts
 // ------------------------------------------------------------------------------------------
 // h and dh are fp32, and what they are multiplied by has 16 bits. The 16-bit matrix instructions are 16
-// times as fast as the fp32 one, so a coefficient is cut into three bf16 parts of 8 bits each, which hold
-// all of its 24 bits that are not below 2^-133. fp16 values are cut into two bf16 parts, of 8 and 3 bits, so
-// that their products are whole too: six instructions where fp16 parts would take two, but those have no
-// range for rows or ranks far quieter than the loudest beside them. (4096 x 8192, fp16, six / two: rank 64 86 us / 82, gradients,
-// rank 32, 105 / 107, where two need exponents.)
+// times as fast as the fp32 one, so a coefficient is cut into three bf16 parts of 8 bits each, which
+// hold all of its 24 bits that are not below 2^-133. fp16 values are cut into two bf16 parts, of 8 and
+// 3 bits, so that their products are whole too: six instructions where fp16 parts would take two, but
+// those have no range for rows or ranks far quieter than the loudest beside them. (4096 x 8192, fp16,
+// six / two: rank 64 86 us / 82, gradients, rank 32, 105 / 107, where two need exponents.)
 constexpr int kParts = 3;
 template <int DT>
 constexpr int kValueParts = DT == BL_F16 ? 2 : 1;
@@ -427,16 +428,16 @@ struct Sorted {
 // ------------------------------------------------------------------------------------------
 // shrink: sums[row, r] = sum over k of S[row, k] w[e, r, k], and the coefficients made of them
 // ------------------------------------------------------------------------------------------
-// A workgroup has a tile of 32 rows, up to 64 ranks and one of the splits of k; its waves take
-// blocks of 128 bytes of a row in turn. An operand's lanes 0 .. 15 are 16 rows, and a load whose lanes
-// touch so many lines gets 16 bytes a clock: so eight lanes load a row's 128 bytes, and the operand is
-// picked up from LDS of the wave's own. Where there are several workgroups to a tile, the last one
-// that ends adds their sums, in order, and makes the coefficients (memory-side stores, no cache
-// write-back: about 1 us to arrive, 1 to gather, 1.5 to 4.5 for the coefficients). 4096 x 8192, bf16, rank 32:
-// 24 us, of which 15 are the loop at 4.5 TB/s of rows; rank 64 31 us (operands straight from memory 39). 64 ranks to
-// a workgroup, since each block of ranks reads the rows again (with 32, the whole call, bf16: 4096 x 8192, rank 64 80 -> 82 us, rank
-// 128 131 -> 135, 2000 x 8640, rank 40 37 -> 41). Registers for two workgroups to a CU: for one 79 -> 83, for three,
-// which spill, 140 (rank 64).
+// A workgroup has a tile of 32 rows, up to 64 ranks and one of the splits of k; its waves take blocks
+// of 128 bytes of a row in turn. An operand's lanes 0 .. 15 are 16 rows, and a load whose lanes touch
+// so many lines gets 16 bytes a clock: so eight lanes load a row's 128 bytes, and the operand is picked
+// up from LDS of the wave's own. Where there are several workgroups to a tile, the last one that ends
+// adds their sums, in order, and makes the coefficients (memory-side stores, no cache write-back: about
+// 1 us to arrive, 1 to gather, 1.5 to 4.5 for the coefficients). 4096 x 8192, bf16, rank 32: 24 us, of
+// which 15 are the loop at 4.5 TB/s of rows; rank 64 31 us (operands straight from memory 39). 64 ranks
+// to a workgroup, since each block of ranks reads the rows again (with 32, the whole call, bf16: 4096 x
+// 8192, rank 64 80 -> 82 us, rank 128 131 -> 135, 2000 x 8640, rank 40 37 -> 41). Registers for two
+// workgroups to a CU: for one 79 -> 83, for three, which spill, 140 (rank 64).
 constexpr int kShrinkWaves = 4;
 struct ShrinkArgs {
   Sorted o;
@@ -474,7 +475,10 @@ __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int RP, c
         u32x4 w[kParts] = {};
         parts_of([&](int j) { return 8 * k + j < RP ? v[m * pitch + 8 * k + j] : 0.0f; }, w);
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) *reinterpret_cast<u32x4*>(c.by_row + (((t * 2 + m / 16) * (RK / 32) + k / 4) * kParts + p) * 512 + (k % 4 * 16 + m % 16) * 8) = w[p];
+        for (int p = 0; p < kParts; ++p) {
+          uint16_t* to = c.by_row + (((t * 2 + m / 16) * (RK / 32) + k / 4) * kParts + p) * 512;
+          *reinterpret_cast<u32x4*>(to + (k % 4 * 16 + m % 16) * 8) = w[p];
+        }
       }
     }
     if (c.by_rank) {
@@ -483,7 +487,10 @@ __device__ __forceinline__ void write_coefs(const Coefs& c, int64_t t, int RP, c
         u32x4 w[kParts] = {};
         parts_of([&](int j) { return v[(8 * q + j) * pitch + r]; }, w);
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) *reinterpret_cast<u32x4*>(c.by_rank + ((t * (RP / 16) + r / 16) * kParts + p) * 512 + (q * 16 + r % 16) * 8) = w[p];
+        for (int p = 0; p < kParts; ++p) {
+          uint16_t* to = c.by_rank + ((t * (RP / 16) + r / 16) * kParts + p) * 512;
+          *reinterpret_cast<u32x4*>(to + (q * 16 + r % 16) * 8) = w[p];
+        }
       }
     }
   }
@@ -590,7 +597,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves, 2) void adapter_shrink_kernel(Sh
   int64_t n = u < uf ? (uf - u + V - 1) / V : 0;    // whole blocks of this wave
   Block v0, v1;
   if (n) {
-    // two blocks in flight; no load is under a condition of its own, so each wait is for the older ones alone
+    // two blocks in flight; no load is under a condition of its own, so each wait is for the older ones
+    // alone
     load(v0, u, std::true_type{});
     load(v1, n > 1 ? u + V : u, std::true_type{});
     for (; n > 2; n -= 2) {
@@ -644,7 +652,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves, 2) void adapter_shrink_kernel(Sh
     if (tid == 0) last = arrive_agent(a.arrived + t) + 1 == static_cast<uint32_t>(groups);
     __syncthreads();
     if (!last) return;
-    // about 32 loads in flight at a time: of PL places (all of a thread's, up to rank 64) those of NS splits
+    // about 32 loads in flight at a time: of PL places (all of a thread's, up to rank 64) those of NS
+    // splits
     constexpr int PL = 2 * NR, NS = 32 / PL;
     const float* in = a.part + static_cast<int64_t>(t) * kTile * a.RP;
     const int64_t step = a.o.rows * a.RP;
@@ -730,8 +739,8 @@ struct ExpandArgs {
   int tiles;              // 1, 2 or 4
 };
 
-// A wave has 16 rows and 128 columns at a time: lane 16 g + c columns 8 c .. 8 c + 7 of them, so that w, base and
-// y go 16 bytes at a time, and matrix instruction j makes columns 8 c + j.
+// A wave has 16 rows and 128 columns at a time: lane 16 g + c columns 8 c .. 8 c + 7 of them, so that
+// w, base and y go 16 bytes at a time, and matrix instruction j makes columns 8 c + j.
 template <int YD, bool WHOLE>
 __device__ __forceinline__ void load_base(const ExpandArgs& a, const int (&row)[4], int64_t n, Eight<YD> (&base)[4]) {
   using Y = typename Elem<YD>::type;
@@ -771,9 +780,10 @@ __device__ __forceinline__ void copy_rows(const ExpandArgs& a, const int (&row)[
   }
 }
 
-// The rows of up to `count` tiles. KB blocks of 32 ranks of w stay in registers over them; 0: any rank, w is
-// loaded again for each tile (fp32: always so). Reading base and writing y bound it: 4096 x 8192, bf16,
-// rank 32 31 us (134 MB, 4.3 TB/s), rank 64 38; with two halves' rows per wave and w loaded by each tile 57.
+// The rows of up to `count` tiles. KB blocks of 32 ranks of w stay in registers over them; 0: any rank,
+// w is loaded again for each tile (fp32: always so). Reading base and writing y bound it: 4096 x 8192,
+// bf16, rank 32 31 us (134 MB, 4.3 TB/s), rank 64 38; with two halves' rows per wave and w loaded by
+// each tile 57.
 template <int WD, int YD, int KB, bool WHOLE>
 __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, int count, int e, int64_t n0, int64_t lo, int lane) {
   const int c = lane & 15, g = lane >> 4;
@@ -798,8 +808,8 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
   Eight<YD> base[4] = {};
   rows(at, row);
   load_base<YD, WHOLE>(a, row, n, base);
-  // as operands: column j of block k. Two blocks of fp16 columns in parts would take 128 registers: they are
-  // cut for each tile (4096 x 8192, rank 64: 86 us for the whole call where 93)
+  // as operands: column j of block k. Two blocks of fp16 columns in parts would take 128 registers:
+  // they are cut for each tile (4096 x 8192, rank 64: 86 us for the whole call where 93)
   constexpr bool kCut = WD != BL_F16 || KB == 1;
   u32x4 wv[KB ? KB : 1][8][kCut ? VP : 1];
   if constexpr (KB > 0) {
@@ -881,10 +891,10 @@ __device__ __forceinline__ void expand_tiles(const ExpandArgs& a, int64_t at, in
   }
 }
 
-// A workgroup has up to `tiles` tiles and 256 columns, its waves the tiles' halves. Tiles come after the
-// columns: rows are read and written whole by workgroups that run together. Registers for three
-// workgroups to a CU (two of fp32 results, and of two blocks of fp16): for two the same within 1 us, for four, which
-// spill, 4096 x 8192, rank 64 79 -> 140 us.
+// A workgroup has up to `tiles` tiles and 256 columns, its waves the tiles' halves. Tiles come after
+// the columns: rows are read and written whole by workgroups that run together. Registers for three
+// workgroups to a CU (two of fp32 results, and of two blocks of fp16): for two the same within 1 us,
+// for four, which spill, 4096 x 8192, rank 64 79 -> 140 us.
 template <int WD, int YD, int KB>
 __global__ __launch_bounds__(256, YD == BL_F32 || (WD == BL_F16 && KB == 2) ? 2 : 3) void adapter_expand_kernel(ExpandArgs a) {
   const int t = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -921,13 +931,13 @@ __global__ __launch_bounds__(256, YD == BL_F32 || (WD == BL_F16 && KB == 2) ? 2 
 // outer: grad[e, r, d] = sum over the adapter's rows of c[row, r] S[row, d]
 // ------------------------------------------------------------------------------------------
 // A workgroup has 128 columns, up to 32 ranks and an even share of the tiles, which its waves take in
-// turn. An adapter that lies within one share is written at once. The pieces of one that does
-// not go to sum[2 share], where the adapter began in an earlier share, or sum[2 share + 1]; the
-// workgroup that ends last adds them in their order. Each share has at most one adapter that
-// goes on after it, so the share where an adapter begins names its counter. A wave has two tiles' loads in
-// flight, which bounds it: 4096 rows of 8192 and 8192, bf16, rank 32 34 us for both sums (134 MB, 3.9
-// TB/s; with one tile at a time 100). fp32 rows have one in flight and the fp32 instruction: 1024 of 3200 beside
-// fp16 ones of 8640, rank 8, 19 us (31 MB) where each sum by itself takes 19 and 15.
+// turn. An adapter that lies within one share is written at once. The pieces of one that does not go to
+// sum[2 share], where the adapter began in an earlier share, or sum[2 share + 1]; the workgroup that
+// ends last adds them in their order. Each share has at most one adapter that goes on after it, so the
+// share where an adapter begins names its counter. A wave has two tiles' loads in flight, which bounds
+// it: 4096 rows of 8192 and 8192, bf16, rank 32 34 us for both sums (134 MB, 3.9 TB/s; with one tile at
+// a time 100). fp32 rows have one in flight and the fp32 instruction: 1024 rows of 8640 in fp32 beside 3200
+// in fp16, rank 8, 19 us (42 MB) where each sum by itself takes 19 and 15.
 struct OuterArgs {
   Sorted o;
   Coefs c;
@@ -1089,9 +1099,9 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
   const int64_t shares = min(static_cast<int64_t>(a.splits), tiles);
   if (blockIdx.y >= shares) return;
   const int t0 = static_cast<int>(tiles * blockIdx.y / shares), t1 = static_cast<int>(tiles * (blockIdx.y + 1) / shares);
-  // (us of the gradients, bf16, for a quarter / third / half of the share: 4096 x 4096, rank 32, 16 adapters 92 / 84 /
-  // 83, 32 of rank 16 85 / 80 / 80; 12000 x 4096, rank 32, 8 adapters 163 / 163 / 184, 16 188 / 165 / 165; none: 2048 x 2048,
-  // rank 8, 200 adapters 47 -> 68)
+  // (us of the gradients, bf16, for a quarter / third / half of the share: 4096 x 4096, rank 32, 16
+  // adapters 92 / 84 / 83, 32 of rank 16 85 / 80 / 80; 12000 x 4096, rank 32, 8 adapters 163 / 163 /
+  // 184, 16 188 / 165 / 165; none: 2048 x 2048, rank 8, 200 adapters 47 -> 68)
   const int few = max(4, (t1 - t0) / 3);
   int turn = 0;
   int words = 0, words_at = t0 - 64;                // of 64 tiles, one a lane
@@ -1137,7 +1147,8 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
       for (int l = 0; l < 4; ++l)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          red[wave * 16 * NR + 16 * q + 4 * g + l][2 * c + j] = f32x4{acc[q][4 * j][l], acc[q][4 * j + 1][l], acc[q][4 * j + 2][l], acc[q][4 * j + 3][l]};
+          red[wave * 16 * NR + 16 * q + 4 * g + l][2 * c + j] =
+              f32x4{acc[q][4 * j][l], acc[q][4 * j + 1][l], acc[q][4 * j + 2][l], acc[q][4 * j + 3][l]};
     __syncthreads();
     if (first >= t && last <= end) {
       each([&](int i, int64_t at) { grad[at] = a.add ? grad[at] + sum(i) : sum(i); });
@@ -1190,10 +1201,11 @@ __device__ __forceinline__ void outer(const OuterArgs& a, uint32_t column, f32x4
   }
 }
 
-// Types of the first and the second sum of a pair. Registers: two workgroups to a CU, or one with two tiles of 16-bit
-// values in flight beyond rank 16; fp32 leaves none for a second tile. (us of the gradients of 4096 x 8192, rank 32, for one /
-// two: bf16 100 / 127, fp32 223 / 207; 1024 x 4096, rank 8, bf16 44 / 41.) 32 ranks to a workgroup: with 16, whose rows are
-// read twice as often, 4096 x 8192, rank 32 101 -> 115 us, 8 adapters of rank 64 142 -> 156.
+// Types of the first and the second sum of a pair. Registers: two workgroups to a CU, or one with two
+// tiles of 16-bit values in flight beyond rank 16; fp32 leaves none for a second tile. (us of the
+// gradients of 4096 x 8192, rank 32, for one / two: bf16 100 / 127, fp32 223 / 207; 1024 x 4096, rank
+// 8, bf16 44 / 41.) 32 ranks to a workgroup: with 16, whose rows are read twice as often, 4096 x 8192,
+// rank 32 101 -> 115 us, 8 adapters of rank 64 142 -> 156.
 template <int SD, int TD, int NR>
 __global__ __launch_bounds__(256, SD == BL_F32 || NR == 1 ? 2 : 1) void adapter_outer_kernel(OuterPair pair) {
   __shared__ f32x4 red[4 * 16 * NR][32];
@@ -1266,8 +1278,8 @@ __global__ __launch_bounds__(256) void adapter_rows_shrink_kernel(RowsArgs p) {
   if (tid < RW && r0 + tid < p.R) h[tid] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
 }
 
-// 512 columns of a row of y: each wave takes every fourth rank. One row of 8192, rank 16: 3.6 us in the trace, 48
-// rows of 28672 9.5 (50 MB, 5.2 TB/s).
+// 512 columns of a row of y: each wave takes every fourth rank. One row of 8192, rank 16: 3.6 us in the
+// trace, 48 rows of 28672 9.5 (50 MB, 5.2 TB/s).
 template <int WD, int YD>
 __global__ __launch_bounds__(256) void adapter_rows_expand_kernel(RowsArgs p) {
   __shared__ f32x4 red[4][64][2];
@@ -1327,16 +1339,17 @@ __global__ __launch_bounds__(256) void adapter_rows_expand_kernel(RowsArgs p) {
 // ------------------------------------------------------------------------------------------
 // launches
 // ------------------------------------------------------------------------------------------
-// Rows each by itself, in two launches that wait for nothing and need no scratch, or sorted. Each by itself
-// a row reads its own copy of its adapter, R (K + N) values; a workgroup of four ranks takes as
-// long as 8192 values whatever it reads, and a row's other workgroups as long as 12288. Sorted,
-// the waits of three launches are most of the time until the rows themselves are. Up to kRowsMost by
-// this count each goes by itself. (us from a graph, by itself / sorted, bf16, eight adapters: 64 rows of 8192 x 8192, rank 16
-// 9.9 / 17.6, rank 64 17.9 / 23.5; 256 rows of 4096 x 4096, rank 64 21.7 / 23.0; 256 of 8192 x 28672, rank 8
-// 28.8 / 24.5; 1024 of 1024 x 1024, rank 16 16.8 / 17.8, rank 64 38 / 22; 1024 of 512 x 512, rank 8 9.5 / 14.7; 4096 of
-// 128 x 128, rank 8 21.6 / 16.3, rank 64 104 / 19. fp32 reads twice as much on both ways: 256 of 4096 x 4096, rank 64
-// 33.5 / 34.2, 64 of 8192 x 8192, rank 64 27.2 / 33.7. Over 464 shapes 1.1 % from the better way, 42 % at most; by
-// R (K + N) alone 28 %, and 13 times its time at most.)
+// Rows each by itself, in two launches that wait for nothing and need no scratch, or sorted. Each by
+// itself a row reads its own copy of its adapter, R (K + N) values; a workgroup of four ranks takes as
+// long as 8192 values whatever it reads, and a row's other workgroups as long as 12288. Sorted, the
+// waits of three launches are most of the time until the rows themselves are. Up to kRowsMost by this
+// count each goes by itself. (us from a graph, by itself / sorted, bf16, eight adapters: 64 rows of
+// 8192 x 8192, rank 16 9.9 / 17.6, rank 64 17.9 / 23.5; 256 rows of 4096 x 4096, rank 64 21.7 / 23.0;
+// 256 of 8192 x 28672, rank 8 28.8 / 24.5; 1024 of 1024 x 1024, rank 16 16.8 / 17.8, rank 64 38 / 22;
+// 1024 of 512 x 512, rank 8 9.5 / 14.7; 4096 of 128 x 128, rank 8 21.6 / 16.3, rank 64 104 / 19. fp32
+// reads twice as much on both ways: 256 of 4096 x 4096, rank 64 33.5 / 34.2, 64 of 8192 x 8192, rank 64
+// 27.2 / 33.7. Over 464 shapes 1.1 % from the better way, 42 % at most; by R (K + N) alone 28 %, and 13
+// times its time at most.)
 constexpr int64_t kRowsMost = int64_t(11) << 23;
 bool by_rows(int64_t M, int64_t R, int64_t K, int64_t N) {
   return M <= 65535 && M * (div_up(R, 4) * std::max<int64_t>(4 * K, 8192) + R * N + 12288) <= kRowsMost;
@@ -1345,9 +1358,10 @@ bool by_rows(int64_t M, int64_t R, int64_t K, int64_t N) {
 template <int DT>
 hipError_t start_rows_shrink(const RowsArgs& p, hipStream_t s) {
   const auto M = static_cast<uint32_t>(p.f.rows.M);
-  // one rank to a workgroup while that makes few of them, else four, which share the row's reads (us, one / four,
-  // bf16: 16 rows of 8192, rank 16 7.9 / 8.9, 64 rows 11.0 / 12.4, 128 rows 13.3 / 14.7, of 4096 11.2 / 11.2; 256 rows of
-  // 4096, rank 16 14.5 / 13.3, 320, rank 32 22.1 / 17.8, 900 of 1024, rank 8 13.3 / 11.1)
+  // one rank to a workgroup while that makes few of them, else four, which share the row's reads (us,
+  // one / four, bf16: 16 rows of 8192, rank 16 7.9 / 8.9, 64 rows 11.0 / 12.4, 128 rows 13.3 / 14.7, of
+  // 4096 11.2 / 11.2; 256 rows of 4096, rank 16 14.5 / 13.3, 320, rank 32 22.1 / 17.8, 900 of 1024,
+  // rank 8 13.3 / 11.1)
   if (p.f.rows.M * p.R <= 1024) adapter_rows_shrink_kernel<DT, 1><<<dim3(M, p.R), 256, 0, s>>>(p);
   else adapter_rows_shrink_kernel<DT, 4><<<dim3(M, static_cast<uint32_t>(div_up(p.R, 4))), 256, 0, s>>>(p);
   return hipGetLastError();
@@ -1369,20 +1383,22 @@ hipError_t forward_by_rows(const AdapterForwardArgs& a, hipStream_t s) {
   return start_rows_expand<BL_F32, BL_F32>(p, s);
 }
 
-// Splits for about 300 workgroups, 448 beyond rank 32, where the matrices' reads take as long as the rows': less
-// than the 512 that the chip holds at once, since one that starts after the others doubles the time. (us, 300 /
-// 448, bf16: 777 x 8640, rank 12 11.9 / 13.6, 4096 x 8192, rank 32 27.9 / 30.4, rank 64 38.5 / 31.3.)
+// Splits for about 300 workgroups, 448 beyond rank 32, where the matrices' reads take as long as the
+// rows': less than the 512 that the chip holds at once, since one that starts after the others doubles
+// the time. (us, 300 / 448, bf16: 777 x 8640, rank 12 11.9 / 13.6, 4096 x 8192, rank 32 27.9 / 30.4,
+// rank 64 38.5 / 31.3.)
 int shrink_splits(int64_t M, int64_t L, int64_t R, int64_t D) {
   const int64_t groups = max_tiles(M, L) * div_up(rank_pad(R), 64), most = R <= 32 ? 300 : 448;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most / groups, div_up(D, 64) / (2 * kShrinkWaves), 16})));
 }
-// Tiles of a workgroup of the product along the long axis: as many as leave 1024 workgroups or so. (us for 1 / 2 / 4 / 8,
-// bf16: 4096 x 8192, rank 64 42 / 38 / 38 / 42, rank 32 34 / 31 / 32 / 36; 777 x 3200, rank 12, fp32 results 7.4 / 9.2 for
-// 1 / 2.)
+// Tiles of a workgroup of the product along the long axis: as many as leave 1024 workgroups or so. (us
+// for 1 / 2 / 4 / 8, bf16: 4096 x 8192, rank 64 42 / 38 / 38 / 42, rank 32 34 / 31 / 32 / 36; 777 x
+// 3200, rank 12, fp32 results 7.4 / 9.2 for 1 / 2.)
 int expand_tiles_of(int64_t M, int64_t N) { return M * N >= int64_t(1) << 25 ? 4 : M * N >= int64_t(1) << 24 ? 2 : 1; }
-// A run of tiles to each of the eight chips, or neighbours to different ones (us, by chip / not, bf16, 4096 rows of
-// 8192: 64 adapters of rank 64 103 / 108, 8 79.1 / 80.6, of rank 32 70.5 / 71.0; fewer rows gain or lose as often: 1024 of
-// 8192, rank 32 28.9 / 30.8, 1024 of 3200, rank 8 26.0 / 25.3, 400 of 8640, rank 64 27.7 / 27.1).
+// A run of tiles to each of the eight chips, or neighbours to different ones (us, by chip / not, bf16,
+// 4096 rows of 8192: 64 adapters of rank 64 103 / 108, 8 79.1 / 80.6, of rank 32 70.5 / 71.0; fewer
+// rows gain or lose as often: 1024 of 8192, rank 32 28.9 / 30.8, 1024 of 3200, rank 8 26.0 / 25.3, 400
+// of 8640, rank 64 27.7 / 27.1).
 int by_chip(const AdapterRows& r) { return r.M >= 64 * kTile; }
 // Two workgroups to a CU, or the one that two tiles' registers of 16-bit values leave beyond rank 16. (us,
 // 4096 rows of 8192, bf16, rank 32: 22 for 256 workgroups, 32 for 384, 30 for 512, 44 for 1024.)
@@ -1466,8 +1482,12 @@ hipError_t start_shrink_nr(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
 }
 // sd is wd, or fp32. The sums' coefficients multiply values of wd, h_in's values of sd.
 hipError_t start_shrink(const ShrinkArgs& a, int sd, int wd, int64_t tiles, hipStream_t s) {
-  if (wd == BL_F16) return sd == BL_F16 ? start_shrink_nr<BL_F16, BL_F16, BL_F16, BL_F16>(a, tiles, s) : start_shrink_nr<BL_F32, BL_F16, BL_F16, BL_F32>(a, tiles, s);
-  if (wd == BL_BF16) return sd == BL_BF16 ? start_shrink_nr<BL_BF16, BL_BF16, BL_BF16, BL_BF16>(a, tiles, s) : start_shrink_nr<BL_F32, BL_BF16, BL_BF16, BL_F32>(a, tiles, s);
+  if (wd == BL_F16)
+    return sd == BL_F16 ? start_shrink_nr<BL_F16, BL_F16, BL_F16, BL_F16>(a, tiles, s)
+                       : start_shrink_nr<BL_F32, BL_F16, BL_F16, BL_F32>(a, tiles, s);
+  if (wd == BL_BF16)
+    return sd == BL_BF16 ? start_shrink_nr<BL_BF16, BL_BF16, BL_BF16, BL_BF16>(a, tiles, s)
+                        : start_shrink_nr<BL_F32, BL_BF16, BL_BF16, BL_F32>(a, tiles, s);
   return start_shrink_nr<BL_F32, BL_F32, BL_F32, BL_F32>(a, tiles, s);
 }
 
@@ -1495,7 +1515,10 @@ hipError_t start_outer_as(const OuterPair& a, uint32_t columns, hipStream_t s) {
 }
 // Types of the sums: the same, or fp32 and another.
 hipError_t start_outer(const OuterPair& a, uint32_t columns, int sd, int td, hipStream_t s) {
-  if (sd == td) return sd == BL_F16 ? start_outer_as<BL_F16, BL_F16>(a, columns, s) : sd == BL_BF16 ? start_outer_as<BL_BF16, BL_BF16>(a, columns, s) : start_outer_as<BL_F32, BL_F32>(a, columns, s);
+  if (sd == td)
+    return sd == BL_F16    ? start_outer_as<BL_F16, BL_F16>(a, columns, s)
+           : sd == BL_BF16 ? start_outer_as<BL_BF16, BL_BF16>(a, columns, s)
+                           : start_outer_as<BL_F32, BL_F32>(a, columns, s);
   return td == BL_F16 ? start_outer_as<BL_F32, BL_F16>(a, columns, s) : start_outer_as<BL_F32, BL_BF16>(a, columns, s);
 }
 
@@ -1553,7 +1576,8 @@ hipError_t launch_adapter_forward(const AdapterForwardArgs& a, char* ws, hipStre
   ShrinkArgs p{w.o, a.x, a.K, a.ldx, a.a, R, RP, splits, by_chip(r), w.part, w.arrived, a.scale, a.h, nullptr, only(w.c, a.dtype, true, false), {}};
   e = start_shrink(p, a.dtype, a.dtype, tiles, s);
   if (e != hipSuccess) return e;
-  return start_expand(ExpandArgs{w.o, w.c, R, RP, a.h, a.b, a.N, a.base, a.ldbase, a.y, a.ldy, expand_tiles_of(r.M, a.N)}, a.dtype, a.ydtype, tiles, s);
+  return start_expand(ExpandArgs{w.o, w.c, R, RP, a.h, a.b, a.N, a.base, a.ldbase, a.y, a.ldy, expand_tiles_of(r.M, a.N)}, a.dtype,
+                      a.ydtype, tiles, s);
 }
 
 hipError_t launch_adapter_backward(const AdapterBackwardArgs& a, char* ws, hipStream_t s) {

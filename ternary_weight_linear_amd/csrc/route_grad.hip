@@ -66,9 +66,9 @@ __device__ __forceinline__ void load_logits(const typename Elem<DT>::type* row, 
 
 // 1 / v by the hardware's instruction, which errs by one unit.
 __device__ __forceinline__ float fast_inv(float v) { return __builtin_amdgcn_rcpf(v); }
-// The gradient's scores are the routing's, by its expf. The loss's go into sums, which need no
-// score below 2^-126: the hardware's instruction gives 0 there, and errs by |v| 2^-24 more (65536 rows of 1024, sigmoid
-// 192 us where expf takes 222).
+// The gradient's scores are the routing's, by its expf. The loss's go into sums, which need no score
+// below 2^-126: the hardware's instruction gives 0 there, and errs by |v| 2^-24 more (65536 rows of
+// 1024, sigmoid 192 us where expf takes 222).
 template <bool OF_ROUTING>
 __device__ __forceinline__ float exponential(float v) {
   return OF_ROUTING ? expf(v) : __builtin_amdgcn_exp2f(v * 1.44269504088896341f);
@@ -136,10 +136,11 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* offsets, int64_t S
 // ------------------------------------------------------------------------------------------
 // balance loss
 // ------------------------------------------------------------------------------------------
-// A workgroup sums a chunk of rows, sequence by sequence (those of a chunk are shared out over up to 16). Going
-// from chunk to chunk and sequence to sequence, either number grows at each step: chunk + sequence
-// numbers the partial sums. 16384 x 256, sigmoid, 11 sequences: 11 us in the trace (17 MB; scores are an exponential and a
-// quotient each), its finish 7; 4096 x 60: 4.7 and 6.4, two chains of waits.
+// A workgroup sums a chunk of rows, sequence by sequence (those of a chunk are shared out over up to
+// 16). Going from chunk to chunk and sequence to sequence, either number grows at each step: chunk +
+// sequence numbers the partial sums. 16384 x 256, sigmoid, 11 sequences: 11 us in the trace (17 MB;
+// scores are an exponential and a quotient each), its finish 7; 4096 x 60: 4.7 and 6.4, two chains of
+// waits.
 struct BalanceParts {
   int64_t chunk, chunks;
   float* t;               // [chunks + S - 1, E]
@@ -303,10 +304,10 @@ __global__ __launch_bounds__(1024) void route_balance_finish_kernel(RouteRows r,
 // expert's gradient
 //   softmax   u_j (g_j - sum u g)    sigmoid   u_j (1 - p_j) (g_j - sum u g)       renormalised
 //   softmax   p_j g_j                sigmoid   p_j (1 - p_j) g_j                   else,
-// a softmax that is not renormalised takes p_e sum_j p_j g_j from every expert, and the balance
-// loss adds t_e (c_e - sum t c), times 1 - p_e for sigmoid scores, with c = dloss coef. A row is read and
-// written once: 16384 x 256, sigmoid, 12.6 us (33.5 MB, 2.7 TB/s; the scores' VALU work and three passes through
-// LDS beside it), 4096 x 60 4.
+// a softmax that is not renormalised takes p_e sum_j p_j g_j from every expert, and the balance loss
+// adds t_e (c_e - sum t c), times 1 - p_e for sigmoid scores, with c = dloss coef. A row is read and
+// written once: 16384 x 256, sigmoid, 12.6 us (33.5 MB, 2.7 TB/s; the scores' VALU work and three
+// passes through LDS beside it), 4096 x 60 4.
 template <int DT, int LANES, int NE, int V, bool SIGMOID, int KS>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs a) {
   constexpr int G = 256 / LANES;
@@ -478,10 +479,10 @@ bool vec_experts(const void* p, int64_t E, int64_t ld, size_t size) {
 // An fp32 sum of one group of lanes has 128 rows at most (2048 beyond 512 experts).
 constexpr int64_t kMostChunk = 8192;
 // Rows of a chunk, a row for every group of lanes at least: about 128 workgroups, 256 of many rows, and
-// beyond 512 experts 128, 256 or 512. More chunks shorten the sums and lengthen their finish, which is one
-// workgroup for each sequence. (us from a graph, one sequence, sigmoid, for 128 / 256 / 512: 16384 x 256
-// 20.5 / 23.7 / 23.6, 32768 x 256 25.3 / 26.0 / 38.6, 65536 x 256 36.4 / 32.4 / 44.2; 2048 x 1024 40 / 52 / 86,
-// 8192 x 1024 74 / 69 / 94, 16384 x 1024 127 / 96 / 108, 65536 x 1024 429 / 248 / 193.)
+// beyond 512 experts 128, 256 or 512. More chunks shorten the sums and lengthen their finish, which is
+// one workgroup for each sequence. (us from a graph, one sequence, sigmoid, for 128 / 256 / 512: 16384
+// x 256 20.5 / 23.7 / 23.6, 32768 x 256 25.3 / 26.0 / 38.6, 65536 x 256 36.4 / 32.4 / 44.2; 2048 x 1024
+// 40 / 52 / 86, 8192 x 1024 74 / 69 / 94, 16384 x 1024 127 / 96 / 108, 65536 x 1024 429 / 248 / 193.)
 int64_t balance_chunk(int64_t M, int64_t E) {
   const int64_t groups = E <= 512 ? 64 : 4;
   const int64_t most = M >= 32768 ? (E > 512 ? 512 : 256) : E > 512 && M >= 4096 ? 256 : 128;
